@@ -55,7 +55,9 @@ typedef enum {
   SP24_ERR_CUDA = 4,           /* a CUDA runtime/driver call failed           */
   SP24_ERR_ARCH = 5,           /* current device is not sm_103                */
   SP24_ERR_WORKSPACE = 6,      /* workspace missing or too small              */
-  SP24_ERR_DEVICE_TIMEOUT = 7  /* a kernel gave up waiting (device error word)*/
+  SP24_ERR_DEVICE_TIMEOUT = 7, /* a kernel gave up waiting (device error word)*/
+  SP24_ERR_DEVICE_INDEX = 8    /* a page, slot, position or length that a
+                                  kernel read was out of range (the same word) */
 } sp24_status;
 
 /* Human-readable name of a status code (static string). */
@@ -307,7 +309,9 @@ SP24_API int sp24_fp8_gemm_decomposition(int64_t M, int64_t N, int64_t K, int64_
  * sp24_last_device_error -- synchronise `stream`, then read and clear the
  * library's device error word on the current device.  Returns SP24_OK, or
  * SP24_ERR_DEVICE_TIMEOUT if any kernel of this library gave up on a bounded
- * wait since the last call (its results are then invalid), or SP24_ERR_CUDA.
+ * wait since the last call (its results are then invalid), or else
+ * SP24_ERR_DEVICE_INDEX if one met an index out of range in the device arrays
+ * of the attention entry points below, or SP24_ERR_CUDA.
  */
 SP24_API sp24_status sp24_last_device_error(void* stream);
 
@@ -358,6 +362,146 @@ SP24_API sp24_status sp24_int8_quantize_act(const float* X, int64_t M, int64_t K
 SP24_API sp24_status sp24_int8_gemm(const void* Xq, const float* sx, int64_t M, int64_t K, int64_t ldx,
                            const void* values, const void* meta, const float* sw, int64_t N, const void* bias,
                            void* Y, int64_t ldy, void* stream);
+
+/*
+ * --------------------------------------------------------------- attention
+ * What a transformer layer runs between its QKV and its output projection,
+ * around a paged cache of keys and values: sp24_qk_norm_rope fills the cache
+ * from the QKV projection's rows, sp24_attention_decode and
+ * sp24_attention_prompt read it.  (The reference pages stop at the linear
+ * layer; these have no counterpart there.)
+ *
+ * A sequence's token j sits in page page_table[j / page_size] of the cache,
+ * at place j % page_size.  Which pages a sequence has, and in which order, is
+ * the caller's; unused places may hold anything, NaN included.
+ *
+ * sp24_kv_cache describes it (host struct, read during the call only):
+ *   k, v    (device) [num_pages][heads][page_size][head_dim] with the three
+ *           strides below, in elements and the same for k and v; head_dim
+ *           has unit stride.  So pages may keep a head's tokens together
+ *           (token_stride = head_dim) or a token's heads (head_stride =
+ *           head_dim).
+ *   dtype   SP24_BF16, or SP24_E4M3: codes that stand for code * scale[head].
+ *   k_scale, v_scale (device) fp32 [heads], > 0, for SP24_E4M3; else NULL.
+ * Preconditions: head_dim 64 or 128; page_size 16, 32, 64 or 128; heads >= 1;
+ * num_pages >= 1; k and v 16-byte aligned; strides > 0 and times the element
+ * size a multiple of 16, below 2^40 bytes.
+ */
+enum { SP24_BF16 = 0, SP24_E4M3 = 1 };
+typedef struct sp24_kv_cache {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t num_pages;
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t token_stride;
+  int32_t heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t dtype;
+} sp24_kv_cache;
+
+/*
+ * sp24_qk_norm_rope -- per-head RMS norm and position rotation of the queries
+ * and keys, with keys and values appended to the cache, in one pass:
+ *
+ *   x      = a head of a QKV row (D = head_dim values)
+ *   y      = x / sqrt(mean(x^2) + eps) * weight      (y = x without weights)
+ *   a' = a cos - b sin, b' = b cos + a sin  for each of the rot/2 pairs (a, b):
+ *            (y[i], y[i + rot/2]), or (y[2i], y[2i + 1]) if `interleaved`;
+ *            the other D - rot values stay as they are.
+ * All of it in fp32; queries are rounded once to bf16, keys (and values,
+ * which are neither normed nor rotated) once to the cache's type:
+ * bf16, or e4m3_rn_satfinite(x / scale[head]) with a correctly rounded
+ * division.
+ *
+ *   qkv     (device) bf16 [T][(q_heads + 2 heads) * D], row stride ldqkv:
+ *           q_heads query heads, then the key heads, then the value heads.
+ *   q_weight, k_weight (device) bf16 [D] each, or both NULL for no norm.
+ *   cos_sin (device) fp32 [max_pos][rot]: rot/2 cosines, then rot/2 sines
+ *           of a position (NULL with rot = 0).  rot a multiple of 16, <= D.
+ *   positions (device) int32 [T], each in [0, max_pos) (NULL with rot = 0).
+ *   slots   (device) int64 [T]: page * page_size + place of each token, or a
+ *           negative number for a token that is not stored.  A slot given
+ *           to two tokens of a call holds a mixture of them afterwards.
+ *   q_out   (device, out) bf16 [T][q_heads * D], row stride ldq.
+ * A position out of range leaves its token's queries and cache slot unwritten,
+ * a slot out of range its token unstored; sp24_last_device_error then reports
+ * SP24_ERR_DEVICE_INDEX.
+ * Preconditions: T >= 0 (0: nothing to do); eps >= 0 and finite; qkv, q_out,
+ * cos_sin and weights 16-byte aligned; ldqkv and ldq multiples of 8.
+ */
+SP24_API sp24_status sp24_qk_norm_rope(const void* qkv, int64_t T, int64_t ldqkv, int q_heads, const void* q_weight,
+                                       const void* k_weight, float eps, const float* cos_sin, int64_t max_pos,
+                                       int rot, int interleaved, const int32_t* positions, const int64_t* slots,
+                                       void* q_out, int64_t ldq, const sp24_kv_cache* cache, void* stream);
+
+/*
+ * sp24_attention_decode -- attention of one new token per sequence over the
+ * cache, which already holds that token:
+ *
+ *   Y[b][h] = sum_j softmax_j(scale * q[b][h] . k[b][j]) v[b][j]
+ * over the keys j that the token at position p = seq_lens[b] - 1 sees: j <= p
+ * and (window = 0, or j > p - window, or j < sinks).  Head h reads the
+ * cache's head h / (q_heads / heads).  A sequence without a key gives zero.
+ * Scores, their running maximum and sum, and the weighted sum of values are
+ * fp32; the weights enter the tensor core rounded to bf16 (f16 for e4m3
+ * caches), and Y is rounded once to bf16.
+ *
+ *   q       (device) bf16 [B][q_heads * D], row stride ldq.
+ *   page_table (device) int32 [B][table_width], row stride ld_table: the
+ *           pages of each sequence.  Entries of pages without a visible key
+ *           are not read.
+ *   seq_lens (device) int32 [B].
+ *   window  0 for all, or how many of the latest tokens are seen, the new one
+ *           included; sinks: how many first tokens stay visible with it.
+ *   scale   finite and > 0 (usually 1 / sqrt(D)).
+ *   Y       (device, out) bf16 [B][q_heads * D], row stride ldy.
+ *   workspace: device scratch of sp24_attention_decode_workspace_size bytes,
+ *           16-byte aligned, zeroed once before its first use and then
+ *           consistent from call to call, whatever their shapes; calls that
+ *           overlap on the GPU must not share it.
+ * The keys of all sequences are dealt out in equal pieces to all SMs; the
+ * pieces of a sequence are joined in the launch, in a fixed order.
+ * A page out of [0, num_pages) is read as page 0, a length above table_width *
+ * page_size is cut to it and a negative one is 0; sp24_last_device_error
+ * then reports SP24_ERR_DEVICE_INDEX.
+ * Preconditions: B >= 0; q_heads a positive multiple of the cache's heads, at
+ * most 128 times it; q, Y 16-byte aligned; ldq, ldy multiples of 8.
+ * Errors: SP24_ERR_WORKSPACE for a workspace that is missing or too small.
+ */
+SP24_API sp24_status sp24_attention_decode(const void* q, int64_t B, int64_t ldq, int q_heads,
+                                           const sp24_kv_cache* cache, const int32_t* page_table, int64_t table_width,
+                                           int64_t ld_table, const int32_t* seq_lens, float scale, int window,
+                                           int sinks, void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/* Device scratch bytes sp24_attention_decode needs for this head layout on
+ * the current device (0 for an invalid one or without a usable device). */
+SP24_API size_t sp24_attention_decode_workspace_size(int q_heads, int heads, int head_dim);
+
+/*
+ * sp24_attention_prompt -- the same attention for a ragged batch of new
+ * tokens: sequence b has the query rows cu_q[b] .. cu_q[b + 1] - 1, m of
+ * them, which are the last m of the seq_lens[b] tokens that the cache holds
+ * for it (so a prompt may come in pieces); the i-th of them is at position
+ * p = seq_lens[b] - m + i and sees the keys that sp24_attention_decode
+ * defines.  A row that sees no key (p < 0) gives zero.
+ *
+ *   q       (device) bf16 [T][q_heads * D], row stride ldq.
+ *   cu_q    (device) int32 [B + 1], ascending from 0 to T.  Rows of Y that
+ *           belong to no sequence are not written.
+ *   Others as for sp24_attention_decode.
+ * Values of a sequence's own tokens are finite: a weight of zero times an
+ * infinite value is not a number.  (Places of the cache that no query of the
+ * call sees may hold anything.)
+ */
+SP24_API sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t ldq, int q_heads, const int32_t* cu_q,
+                                           int64_t B, const sp24_kv_cache* cache, const int32_t* page_table,
+                                           int64_t table_width, int64_t ld_table, const int32_t* seq_lens,
+                                           float scale, int window, int sinks, void* Y, int64_t ldy, void* stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,13 @@ is not an sm_103 GPU, every call raises.
     values, meta, sw = compress(w_bf16, gN=1, gK=None)        # prune + e4m3 + pack
     xq, sx          = quantize_act(x_fp32, gK=None)            # per-token / 1x128 e4m3
     y               = gemm(xq, sx, values, meta, sw, gM=1, gN=1, gK=None, x2=None, w2=None)
+
+Between a layer's QKV and output projections (attention over a paged cache):
+
+    cache = KVCache(k, v)                                      # bf16, or e4m3 codes with scales
+    q     = qk_norm_rope(qkv, heads, cache, positions, slots, cos_sin)
+    y     = attention_decode(q, cache, page_table, seq_lens)   # one new token per sequence
+    y     = attention_prompt(q, cu_q, cache, page_table, seq_lens)
 """
 import contextlib
 import ctypes
@@ -23,10 +30,11 @@ _lib = None
 SP24_STATUS = {
     0: "SP24_OK", 1: "SP24_ERR_INVALID_ARG", 2: "SP24_ERR_UNSUPPORTED", 3: "SP24_ERR_ALIGNMENT",
     4: "SP24_ERR_CUDA", 5: "SP24_ERR_ARCH", 6: "SP24_ERR_WORKSPACE", 7: "SP24_ERR_DEVICE_TIMEOUT",
+    8: "SP24_ERR_DEVICE_INDEX",
 }
 
 # Every entry point the C header declares, with its ctypes signature.
-_P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_P, _I64, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "sp24_status_string": ([_I], ctypes.c_char_p),
     "sp24_meta_bytes": ([_I64, _I64], _SZ),
@@ -47,6 +55,10 @@ SIGNATURES = {
     "sp24_int8_compress": ([_P, _I64, _I64, _I64, _P, _P, _P, _P], _I),
     "sp24_int8_quantize_act": ([_P, _I64, _I64, _I64, _P, _P, _P], _I),
     "sp24_int8_gemm": ([_P, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P, _I64, _P], _I),
+    "sp24_qk_norm_rope": ([_P, _I64, _I64, _I, _P, _P, _F, _P, _I64, _I, _I, _P, _P, _P, _I64, _P, _P], _I),
+    "sp24_attention_decode": ([_P, _I64, _I64, _I, _P, _P, _I64, _I64, _P, _F, _I, _I, _P, _I64, _P, _SZ, _P], _I),
+    "sp24_attention_decode_workspace_size": ([_I, _I, _I], _SZ),
+    "sp24_attention_prompt": ([_P, _I64, _I64, _I, _P, _I64, _P, _P, _I64, _I64, _P, _F, _I, _I, _P, _I64, _P], _I),
 }
 
 
@@ -438,6 +450,193 @@ def gemm_int8(xq, sx, values, meta, sw, bias=None, out=None, stream=None):
     return y
 
 
+# ------------------------------------------------------------------ attention
+class _KVCacheStruct(ctypes.Structure):
+    """sp24_kv_cache of the C header."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("num_pages", _I64), ("page_stride", _I64),
+                ("head_stride", _I64), ("token_stride", _I64), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class KVCache:
+    """A paged cache of keys and values: k and v [pages, heads, page size, head dim]
+    (the last dimension with unit stride, the others any, the same for both), as bf16,
+    or as uint8 e4m3 codes with k_scale and v_scale fp32 [heads].  It holds on to the
+    tensors and owns nothing else; their memory is read and written in place."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        e4m3 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
+        _dev_tensor(k, torch.uint8 if e4m3 else torch.bfloat16, "k")
+        _dev_tensor(v, k.dtype, "v", k.device)
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must be [pages, heads, page size, head dim] of one shape and one set of strides")
+        pages, heads, page_size, head_dim = k.shape
+        if pages < 1 or heads < 1 or head_dim not in (64, 128) or page_size not in (16, 32, 64, 128):
+            raise ValueError("a cache needs a page and a head, pages of 16, 32, 64 or 128 tokens and heads of 64 or "
+                             "128, got %s" % (tuple(k.shape),))
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale go with uint8 e4m3 codes, and only with them")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _dev_tensor(t, torch.float32, name, k.device)
+                _at_least(t, heads, name)
+        # An axis of one entry is never stepped along, and its stride may be anything.
+        token = k.stride(2)
+        head = k.stride(1) if heads > 1 else page_size * token
+        page = k.stride(0) if pages > 1 else max(heads * head, page_size * token)
+        if min(page, head, token) < head_dim or (page | head | token) * k.element_size() % 16 or \
+                (k.data_ptr() | v.data_ptr()) % 16:
+            raise ValueError("the cache's rows must not overlap, and start on 16-byte boundaries")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.page_size, self.head_dim, self.device = heads, page_size, head_dim, k.device
+        self._struct = _KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+                                      v_scale.data_ptr() if e4m3 else None, pages, page, head, token, heads,
+                                      page_size, head_dim, 1 if e4m3 else 0)
+        self._address = ctypes.addressof(self._struct)
+
+
+def _rows_of(t, rows, cols, device, name):
+    """A bf16 tensor of `rows` rows, [rows, cols] or [rows, heads, d] with contiguous
+    rows: its row stride."""
+    _dev_tensor(t, torch.bfloat16, name, device)
+    shape = t.shape
+    if t.dim() == 3:
+        ok = shape[1] * shape[2] == cols and (shape[1] == 1 or t.stride(1) == shape[2])
+    else:
+        ok = t.dim() == 2 and shape[1] == cols
+    if not ok or shape[0] != rows:
+        raise ValueError("%s must be [%d, %d] or [%d, heads, head dim] with contiguous rows, got %s"
+                         % (name, rows, cols, rows, tuple(shape)))
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _vector(t, dtype, n, device, name):
+    _dev_tensor(t, dtype, name, device)
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError("%s must be a vector of %d values, got %s" % (name, n, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _on(stream, device):
+    """What allocates for a kernel on `stream`: memory of that stream's own pool."""
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream)
+
+
+def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, interleaved: bool = False, out=None, stream=None):
+    """One pass over the QKV projection's rows: per-head RMS norm (with q_weight and
+    k_weight bf16 [head dim]; neither: no norm) and rotation of queries and keys, keys
+    and values appended to the cache.
+
+    qkv bf16 [T, (heads + 2 cache heads) * head dim]: query heads, key heads, value
+    heads.  positions int32 [T]: each token's row of cos_sin fp32 [max_pos, rot] (rot/2
+    cosines, then rot/2 sines); rot of the head dim's values are rotated, as pairs
+    (i, i + rot/2), or (2i, 2i + 1) if interleaved.  slots int64 [T]: page * page_size +
+    place of each token, negative for one that is not stored.  Returns the queries bf16
+    [T, heads, head dim] (in ``out`` if given)."""
+    lib = load()
+    dev_, d = cache.device, cache.head_dim
+    T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else -1
+    slots_p = _vector(slots, torch.int64, T, dev_, "slots")
+    pos_p = _vector(positions, torch.int32, T, dev_, "positions")
+    ldqkv = _rows_of(qkv, T, (heads + 2 * cache.heads) * d, dev_, "qkv")
+    _dev_tensor(cos_sin, torch.float32, "cos_sin", dev_)
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous [max_pos, rot]")
+    max_pos, rot = cos_sin.shape
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    qw = kw = None
+    if q_weight is not None:
+        qw, kw = _vector(q_weight, torch.bfloat16, d, dev_, "q_weight"), _vector(k_weight, torch.bfloat16, d, dev_,
+                                                                               "k_weight")
+    if out is None:
+        with _on(stream, dev_):
+            out = torch.empty((T, heads, d), dtype=torch.bfloat16, device=dev_)
+    ldq = _rows_of(out, T, heads * d, dev_, "out")
+    _check(lib.sp24_qk_norm_rope(qkv.data_ptr(), T, ldqkv, heads, qw, kw, eps, cos_sin.data_ptr() if rot else None,
+                                 max_pos, rot, bool(interleaved), pos_p, slots_p, out.data_ptr(), ldq,
+                                 cache._address, _stream(stream)), "sp24_qk_norm_rope")
+    return out
+
+
+def attention_decode_workspace_size(cache: KVCache, heads: int) -> int:
+    """Device scratch bytes attention_decode() needs for `heads` query heads."""
+    return int(load().sp24_attention_decode_workspace_size(heads, cache.heads, cache.head_dim))
+
+
+def _attention_args(q, cache, page_table, seq_lens, scale, out, stream):
+    """The checks and arguments that both attention calls have in common."""
+    dev_, d = cache.device, cache.head_dim
+    if not isinstance(q, torch.Tensor) or q.dim() not in (2, 3):
+        raise ValueError("q must be [rows, heads, head dim] or [rows, heads * head dim]")
+    rows = q.shape[0]
+    cols = q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1]
+    if cols % d or (q.dim() == 3 and q.shape[2] != d):
+        raise ValueError("q must have heads of %d values, as the cache" % d)
+    ldq = _rows_of(q, rows, cols, dev_, "q")
+    _dev_tensor(page_table, torch.int32, "page_table", dev_)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [sequences, pages]")
+    B, width = page_table.shape
+    lens_p = _vector(seq_lens, torch.int32, B, dev_, "seq_lens")
+    if out is None:
+        with _on(stream, dev_):
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev_)
+    ldy = _rows_of(out, rows, cols, dev_, "out")
+    if scale is None:
+        scale = d ** -0.5
+    ld_table = page_table.stride(0) if B > 1 else max(page_table.stride(0), width)
+    return rows, ldq, cols // d, B, width, ld_table, lens_p, scale, out, ldy
+
+
+def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = None, window: int = 0, sinks: int = 0,
+                     out=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over the cache, which already holds it:
+    q bf16 [B, heads, head dim], page_table int32 [B, pages], seq_lens int32 [B] (the new
+    token included) -> bf16 like q.  With a window only the latest `window` tokens and the
+    first `sinks` are seen.  scale defaults to head_dim ** -0.5.  `workspace` (uint8,
+    attention_decode_workspace_size() bytes, zeroed once) may be kept for all later calls
+    on one stream; without one, each call allocates a zeroed one."""
+    lib = load()
+    rows, ldq, heads, B, width, ld_table, lens_p, scale, out, ldy = _attention_args(
+        q, cache, page_table, seq_lens, scale, out, stream)
+    if rows != B:
+        raise ValueError("q has %d rows, page_table %d sequences" % (rows, B))
+    if workspace is None:
+        with _on(stream, cache.device):
+            workspace = torch.zeros(attention_decode_workspace_size(cache, heads), dtype=torch.uint8,
+                                    device=cache.device)
+    else:
+        _dev_tensor(workspace, torch.uint8, "workspace", cache.device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _check(lib.sp24_attention_decode(q.data_ptr(), B, ldq, heads, cache._address, page_table.data_ptr(), width,
+                                     ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
+                                     workspace.data_ptr(), workspace.numel(), _stream(stream)),
+           "sp24_attention_decode")
+    return out
+
+
+def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float = None, window: int = 0,
+                     sinks: int = 0, out=None, stream=None):
+    """Causal attention of a ragged batch of new tokens over the cache, which already
+    holds them: sequence b has the rows cu_q[b] .. cu_q[b + 1] - 1 of q bf16 [T, heads,
+    head dim], the last of the seq_lens[b] tokens that the cache holds for it.  cu_q int32
+    [B + 1]; the others as for attention_decode()."""
+    lib = load()
+    rows, ldq, heads, B, width, ld_table, lens_p, scale, out, ldy = _attention_args(
+        q, cache, page_table, seq_lens, scale, out, stream)
+    cu_p = _vector(cu_q, torch.int32, B + 1, cache.device, "cu_q")
+    _check(lib.sp24_attention_prompt(q.data_ptr(), rows, ldq, heads, cu_p, B, cache._address, page_table.data_ptr(),
+                                     width, ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
+                                     _stream(stream)), "sp24_attention_prompt")
+    return out
+
+
 def last_device_error(stream=None):
-    """Synchronise and raise if any library kernel gave up on a bounded wait."""
+    """Synchronise and raise if any library kernel gave up on a bounded wait, or met an
+    index out of range."""
     _check(load().sp24_last_device_error(_stream(stream)), "device")

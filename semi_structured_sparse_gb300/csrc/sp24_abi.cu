@@ -6,7 +6,8 @@
 namespace sp24 {
 
 // One word per device: kernels OR error bits into it when a bounded wait
-// gives up; sp24_last_device_error reads and clears it.
+// gives up or an index in device memory is out of range;
+// sp24_last_device_error reads and clears it.
 __device__ unsigned int g_device_error_word;
 
 namespace {
@@ -82,6 +83,23 @@ sp24_status make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType
   return r == CUDA_SUCCESS ? SP24_OK : SP24_ERR_CUDA;
 }
 
+sp24_status make_tmap_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int rank,
+                         const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                         CUtensorMapSwizzle swizzle) {
+  if (!g_encode || rank < 2 || rank > 5) return SP24_ERR_CUDA;
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], e[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i) s[i - 1] = strides_bytes[i - 1];
+  }
+  CUresult r = g_encode(map, dtype, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, e,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SP24_OK : SP24_ERR_CUDA;
+}
+
 }  // namespace sp24
 
 extern "C" {
@@ -96,6 +114,7 @@ const char* sp24_status_string(sp24_status s) {
     case SP24_ERR_ARCH: return "SP24_ERR_ARCH: device is not sm_103";
     case SP24_ERR_WORKSPACE: return "SP24_ERR_WORKSPACE: workspace missing or too small";
     case SP24_ERR_DEVICE_TIMEOUT: return "SP24_ERR_DEVICE_TIMEOUT: a kernel gave up on a bounded wait";
+    case SP24_ERR_DEVICE_INDEX: return "SP24_ERR_DEVICE_INDEX: a page, slot, position or length out of range";
   }
   return "SP24_ERR_UNKNOWN";
 }
@@ -116,7 +135,7 @@ sp24_status sp24_last_device_error(void* stream) {
   if (word != 0) {
     const unsigned int zero = 0;
     if (cudaMemcpy(dev->err_word, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess) return SP24_ERR_CUDA;
-    return SP24_ERR_DEVICE_TIMEOUT;
+    return (word & ~static_cast<unsigned int>(sp24::DEVERR_INDEX)) ? SP24_ERR_DEVICE_TIMEOUT : SP24_ERR_DEVICE_INDEX;
   }
   return SP24_OK;
 }

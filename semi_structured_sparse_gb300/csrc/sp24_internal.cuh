@@ -16,6 +16,7 @@ enum : unsigned int {
   DEVERR_TIMEOUT_PRODUCER = 1u,
   DEVERR_TIMEOUT_MMA = 2u,
   DEVERR_TIMEOUT_EPILOGUE = 4u,
+  DEVERR_INDEX = 8u,  // an index read from device memory was out of range
 };
 
 struct DeviceInfo {
@@ -39,6 +40,11 @@ sp24_status make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType
                          uint32_t box_rows, CUtensorMapSwizzle swizzle);
 sp24_status make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint64_t cols,
                          uint64_t rows, uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
+                         CUtensorMapSwizzle swizzle);
+
+// Any rank from 2 to 5, innermost dimension first; strides of dimensions 1 and up.
+sp24_status make_tmap_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int rank,
+                         const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
                          CUtensorMapSwizzle swizzle);
 
 // Launches `kern` with programmatic stream serialisation: it may begin while

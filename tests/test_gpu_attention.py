@@ -1,0 +1,435 @@
+"""The attention operators against their definitions in 64 bits (GPU)."""
+import pytest
+import torch
+
+from attention_util import E4M3, Setup, assert_attention, attend, sees
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- norm, rotation, append
+def rope_reference(x, weight, cos, sin, interleaved, eps):
+    """x [T, heads, d] in 64 bits -> (y, bound on the size of what was added up)."""
+    if weight is not None:
+        x = x / (x.pow(2).mean(-1, keepdim=True) + eps).sqrt() * weight.double()
+    rot = 2 * cos.shape[1]
+    i = torch.arange(rot // 2)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+    y, size = x.clone(), x.abs()
+    c, s = cos.double()[:, None], sin.double()[:, None]
+    y[..., a] = x[..., a] * c - x[..., b] * s
+    y[..., b] = x[..., b] * c + x[..., a] * s
+    size[..., a] = (x[..., a] * c).abs() + (x[..., b] * s).abs()
+    size[..., b] = (x[..., b] * c).abs() + (x[..., a] * s).abs()
+    return y, size
+
+
+# fp32 norm and rotation: a sum of d squares, a reciprocal root, and five products and sums, each within a few 2^-24
+# (2^-18 covers them with room); then one rounding, of half an ulp: 2^-8 of a bf16 value, 2^-4 of an e4m3 one or
+# half of its smallest step, 2^-10.
+def assert_rounded(got, y, size, e4m3, what):
+    got, fine = got.double(), 2.0 ** -18 * size
+    half = torch.maximum(2.0 ** -4 * y.abs(), torch.tensor(2.0 ** -10)) if e4m3 else 2.0 ** -8 * y.abs()
+    bad = ~((got - y).abs() <= half + fine * (1 + 2.0 ** -3) + 1e-38)
+    assert not bad.any(), "%s: %d of %d off, first %s" % (what, int(bad.sum()), bad.numel(), bad.nonzero()[0].tolist())
+
+
+@pytest.mark.parametrize("T,hq,hkv,d,page,e4m3,token_major,rot,interleaved,norm", [
+    (1, 32, 8, 128, 64, False, False, 128, False, True),
+    (1, 1, 1, 64, 16, True, True, 64, True, False),
+    (5, 3, 1, 64, 16, False, True, 16, False, True),      # an odd head count: half a warp idles
+    (7, 28, 4, 64, 32, False, True, 32, True, False),
+    (33, 14, 2, 128, 16, True, False, 96, False, True),   # partners 6 lanes away
+    (64, 32, 8, 128, 128, True, False, 128, False, True),
+    (65, 5, 5, 128, 32, False, True, 0, False, True),     # no rotation at all
+    (130, 8, 1, 64, 64, True, False, 48, True, True),
+    (700, 16, 4, 128, 64, False, False, 64, True, True),  # past the many-token rule
+    (1999, 7, 1, 64, 16, True, True, 64, False, False),
+])
+def test_qk_norm_rope(sp24, T, hq, hkv, d, page, e4m3, token_major, rot, interleaved, norm):
+    g = torch.Generator().manual_seed(T + d)
+    s = Setup(sp24, [T + page], hkv, d, page, e4m3, token_major, seed=T)
+    cache = s.upload()
+    before = {n: s.store[n].clone() for n in ("k", "v")}
+    width = (hq + 2 * hkv) * d
+    big = torch.randn(T, width + 24, generator=g).to(torch.bfloat16)
+    qkv = big[:, 8:8 + width]                                   # rows further apart than their length
+    pos = torch.randint(0, 500, (T,), generator=g, dtype=torch.int32)
+    angle = torch.rand(500, rot // 2, generator=g) * 6.28
+    table = torch.cat((angle.cos(), angle.sin()), 1)
+    slots = torch.randperm(before["k"].shape[0] * page, generator=g)[:T]
+    if T > 2:
+        slots[1] = -1                                           # a token that is not stored
+    qw = (1 + 0.3 * torch.randn(d, generator=g)).to(torch.bfloat16) if norm else None
+    kw = (1 + 0.3 * torch.randn(d, generator=g)).to(torch.bfloat16) if norm else None
+    up = lambda t: None if t is None else t.cuda()              # noqa: E731
+    q = sp24.qk_norm_rope(big.cuda()[:, 8:8 + width], hq, cache, pos.cuda(), slots.cuda(), table.cuda(), up(qw),
+                          up(kw), eps=1e-5, interleaved=interleaved)
+    sp24.last_device_error()
+    x = qkv.double().view(T, -1, d)
+    cos, sin = table[pos.long(), :rot // 2], table[pos.long(), rot // 2:]
+    y, size = rope_reference(x[:, :hq], qw, cos, sin, interleaved, 1e-5)
+    assert_rounded(q.cpu(), y, size, False, "q")
+    yk, sk = rope_reference(x[:, hq:hq + hkv], kw, cos, sin, interleaved, 1e-5)
+    for name, y, size in (("k", yk, sk), ("v", x[:, hq + hkv:], x[:, hq + hkv:].abs())):
+        got = (cache.k if name == "k" else cache.v).cpu()
+        want_untouched = torch.ones(got.shape[0], page, dtype=torch.bool)
+        ok = slots >= 0
+        want_untouched[slots[ok] // page, slots[ok] % page] = False
+        assert torch.equal(got.transpose(1, 2)[want_untouched].view(torch.uint8),
+                           before[name].transpose(1, 2)[want_untouched].view(torch.uint8)), name + ": other places"
+        mine = got.transpose(1, 2)[slots[ok] // page, slots[ok] % page]
+        y, size = y[ok], size[ok]
+        if e4m3:
+            sc = s.scale[name].double()[:, None]
+            y, size = (y / sc).clamp(-448, 448), size / sc
+            mine = mine.contiguous().view(E4M3)
+        assert_rounded(mine, y, size, e4m3, name)
+
+
+def test_qk_norm_rope_special_rows(sp24):
+    """A zero head stays zero, values beyond the largest code saturate, NaN stays NaN."""
+    s = Setup(sp24, [16], 1, 64, 16, True, False, seed=1)
+    s.scale = {"k": torch.tensor([0.5]), "v": torch.tensor([0.25])}
+    cache = s.upload()
+    qkv = torch.zeros(3, 3 * 64)
+    qkv[1] = 1000.0
+    qkv[2, 128:] = float("nan")
+    one = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.tensor([0, 5, 9], device="cuda")
+    q = sp24.qk_norm_rope(qkv.bfloat16().cuda(), 1, cache, torch.zeros(3, dtype=torch.int32, device="cuda"), slots,
+                          torch.zeros(1, 0, device="cuda"), one, one, eps=1e-6)
+    k, v = (t.cpu()[0, 0].view(E4M3).float() for t in (cache.k, cache.v))
+    assert (q[0] == 0).all() and (k[0] == 0).all() and (v[0] == 0).all()
+    assert (q[1] == 1).all() and (k[5] == 2).all() and (v[5] == 448).all()
+    assert v[9].isnan().all()
+
+
+def test_qk_norm_rope_index_errors(sp24):
+    """Positions and slots out of range touch nothing and are reported; negative slots are no error."""
+    s = Setup(sp24, [32], 1, 64, 16, False, False, seed=2)
+    cache = s.upload()
+    k0 = cache.k.clone()
+    qkv = torch.randn(2, 3 * 64, device="cuda").bfloat16()
+    table = torch.ones(4, 64, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    i64 = lambda *v: torch.tensor(v, device="cuda")                     # noqa: E731
+    most = k0.shape[0] * 16
+    for pos, slots in ((i32(4, -1), i64(0, 1)), (i32(0, 1), i64(most, 1 << 40))):
+        out = torch.full((2, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        sp24.qk_norm_rope(qkv, 1, cache, pos, slots, table, out=out)
+        with pytest.raises(sp24.Sp24Error) as e:
+            sp24.last_device_error()
+        assert e.value.status == 8
+        assert torch.equal(cache.k, k0)
+        assert (out == 7).all() == (int(pos[0]) == 4)
+    sp24.qk_norm_rope(qkv, 1, cache, i32(0, 1), i64(-1, -5), table)
+    sp24.last_device_error()
+    assert torch.equal(cache.k, k0)
+
+
+# ---------------------------------------------------------------- decode
+def run_decode(sp24, lens, hq, hkv, d, page, e4m3, token_major, window, sinks, seed, **kw):
+    s = Setup(sp24, lens, hkv, d, page, e4m3, token_major, seed)
+    see = [sees([n - 1], n, window, sinks) for n in lens]
+    s.poison([x[0] for x in see])
+    cache = s.upload()
+    g = torch.Generator().manual_seed(seed + 1)
+    q = (2 * torch.randn(len(lens), hq, d, generator=g)).to(torch.bfloat16)
+    y = sp24.attention_decode(q.cuda(), cache, s.table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                              window=window, sinks=sinks, **kw)
+    sp24.last_device_error()
+    ref, size = zip(*(attend(q[b:b + 1].double(), s.tokens("k", b), s.tokens("v", b), see[b], d ** -0.5)
+                      for b in range(len(lens))))
+    assert_attention(y, torch.cat(ref), torch.cat(size), "decode")
+    return s, q, y
+
+
+@pytest.mark.parametrize("e4m3,token_major", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("lens,hq,hkv,d,page,window,sinks", [
+    ([1], 1, 1, 64, 16, 0, 0),
+    ([0, 1, 2, 15, 16, 17], 8, 2, 128, 16, 0, 0),          # an empty sequence among short ones
+    ([63, 64, 65, 127, 128, 129, 500], 4, 4, 64, 64, 0, 0),
+    ([1000], 32, 8, 128, 64, 0, 0),
+    ([333, 0, 2049], 7, 1, 64, 32, 0, 0),                  # 7 heads share a kv head
+    ([700, 31], 16, 1, 128, 128, 0, 0),                    # 16 do
+    ([257, 90], 40, 1, 64, 16, 0, 0),                      # 40 do: more than one tile of heads
+    ([4000, 100, 3], 8, 1, 128, 16, 100, 4),               # window and sinks: most of the cache unseen
+    ([513, 600, 77], 6, 2, 64, 32, 1, 0),                  # a window of one
+    ([513, 600, 77], 6, 2, 128, 64, 64, 70),               # sinks longer than a page, than the window
+    ([130, 129, 128], 4, 2, 128, 16, 129, 1),              # sinks that meet the window
+])
+def test_decode(sp24, lens, hq, hkv, d, page, e4m3, token_major, window, sinks):
+    run_decode(sp24, lens, hq, hkv, d, page, e4m3, token_major, window, sinks, seed=len(lens) * 7 + hq)
+
+
+def test_decode_many_sequences(sp24):
+    """More sequences than threads in a block, most of them short."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 40, (700,), generator=g).tolist()
+    lens[350] = 5000
+    run_decode(sp24, lens, 2, 1, 64, 16, False, False, 0, 0, seed=5)
+
+
+def test_decode_one_workspace_for_all_shapes_and_graph_replay(sp24):
+    """A workspace kept over calls of other shapes, results that do not depend on the run, and a replayed graph."""
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    for lens, hq, hkv, d in (([5000, 17], 8, 1, 128), ([3], 4, 4, 64), ([900] * 40, 16, 2, 64), ([5000, 17], 8, 1, 128)):
+        s, q, y = run_decode(sp24, lens, hq, hkv, d, 32, False, False, 0, 0, seed=11, workspace=ws)
+    table, n = s.table.cuda(), torch.tensor(s.lens, dtype=torch.int32).cuda()
+    q, out = q.cuda(), torch.empty_like(y)
+    for _ in range(5):
+        sp24.attention_decode(q, s.cache, table, n, out=out, workspace=ws)
+        assert torch.equal(out, y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        sp24.attention_decode(q, s.cache, table, n, out=out, workspace=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            sp24.attention_decode(q, s.cache, table, n, out=out, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, y)
+
+
+def test_decode_strided_rows_and_another_stream(sp24):
+    """Queries read in place from wider rows, output rows further apart, scale given, a stream of its own."""
+    lens, hq, hkv, d = [100, 250], 4, 2, 64
+    s = Setup(sp24, lens, hkv, d, 16, False, False, seed=21)
+    cache = s.upload()
+    wide = torch.randn(2, 8 * d, device="cuda").bfloat16()
+    q = wide[:, 8:8 + hq * d]
+    out = torch.zeros(2, hq * d + 40, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(2, s.table.shape[1] + 5, dtype=torch.int32, device="cuda")
+    table[:, :s.table.shape[1]] = s.table.cuda()
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = sp24.attention_decode(q, cache, table[:, :s.table.shape[1]], n, scale=0.3, out=out[:, 16:16 + hq * d],
+                                stream=side)
+    alone = sp24.attention_decode(q, cache, table[:, :s.table.shape[1]], n, scale=0.3, stream=side)
+    side.synchronize()
+    assert (out[:, :16] == 0).all() and (out[:, 16 + hq * d:] == 0).all()
+    assert torch.equal(alone, got)
+    for b in range(2):
+        ref, size = attend(q[b:b + 1].double().cpu().view(1, hq, d), s.tokens("k", b), s.tokens("v", b),
+                           sees([lens[b] - 1], lens[b], 0, 0), 0.3)
+        assert_attention(got[b:b + 1], ref, size, "row %d" % b)
+
+
+def test_decode_large_scores_and_values(sp24):
+    """Scores of thousands (their maximum decides alone), and values near the type's ends."""
+    lens, hq, hkv, d = [300], 4, 1, 128
+    for e4m3 in (False, True):
+        s = Setup(sp24, lens, hkv, d, 16, e4m3, False, seed=31)
+        if not e4m3:
+            s.store["v"] *= 2.0 ** 60
+        cache = s.upload()
+        q = (2.0 ** torch.tensor([0.0, 8, 16, -20]))[:, None] * torch.randn(1, hq, d)
+        q = q.bfloat16()
+        y = sp24.attention_decode(q.cuda(), cache, s.table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+        ref, size = attend(q.double(), s.tokens("k", 0), s.tokens("v", 0), sees([299], 300, 0, 0), d ** -0.5)
+        # fp32 scores of size S are off by some 2^-22 S: heads 1 and 2 are exact only where one key decides
+        for h in (0, 3):
+            assert_attention(y[:, h], ref[:, h], size[:, h], "head %d" % h)
+        assert torch.isfinite(y).all()
+
+
+def test_decode_offsets_past_32_bits(sp24):
+    """Pages at the far end of a cache of more than 2^31 elements."""
+    hkv, d, page = 8, 128, 128
+    pages = (1 << 31) // (hkv * d * page) + 40
+    k = torch.empty((pages, hkv, page, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    n = 300
+    table = torch.tensor([[pages - 1, pages - 17, pages - 3]], dtype=torch.int32, device="cuda")
+    for t in (k, v):
+        t[table[0].long()] = torch.randn(3, hkv, page, d, device="cuda").bfloat16()
+    q = torch.randn(1, 16, d, device="cuda").bfloat16()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    cache = sp24.KVCache(k, v)
+    kk, vv = (t[table[0].long()].transpose(1, 2).reshape(-1, hkv, d)[:n].double().cpu() for t in (k, v))
+    ref, size = attend(q.double().cpu(), kk, vv, sees([n - 1], n, 0, 0), d ** -0.5)
+    assert_attention(sp24.attention_decode(q, cache, table, lens), ref, size, "decode")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    assert_attention(sp24.attention_prompt(q, cu, cache, table, lens), ref, size, "prompt")
+    slot = (pages - 2) * page + 5
+    qkv = torch.randn(1, 32 * d, device="cuda").bfloat16()
+    sp24.qk_norm_rope(qkv, 16, cache, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                      torch.tensor([slot], device="cuda"), torch.zeros(1, 0, device="cuda"))
+    assert torch.equal(k[pages - 2, :, 5].flatten(), qkv[0, 16 * d:24 * d])
+    assert torch.equal(v[pages - 2, :, 5].flatten(), qkv[0, 24 * d:])
+
+
+def test_attention_index_errors(sp24):
+    """Pages and lengths out of range are kept in bounds and reported."""
+    s = Setup(sp24, [40], 1, 64, 16, False, False, seed=41)
+    cache = s.upload()
+    q = torch.randn(1, 1, 64, device="cuda").bfloat16()
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    good = s.table.cuda()
+    i32 = lambda v: torch.tensor([v], dtype=torch.int32, device="cuda")  # noqa: E731
+    bad = good.clone()
+    bad[0, 1] = 1 << 20
+    zeroed = good.clone()
+    zeroed[0, 1] = 0
+    calls = (lambda t, n: sp24.attention_decode(q, cache, t, n), lambda t, n: sp24.attention_prompt(q, cu, cache, t, n))
+    for call in calls:
+        want = {"page": call(zeroed, i32(40)), "long": call(good, i32(48))}
+        sp24.last_device_error()
+        for got, w in ((call(bad, i32(40)), want["page"]), (call(good, i32(5000)), want["long"]),
+                       (call(good, i32(-3)), torch.zeros_like(want["page"]))):
+            assert torch.equal(got, w)
+        with pytest.raises(sp24.Sp24Error) as e:
+            sp24.last_device_error()
+        assert e.value.status == 8
+        sp24.last_device_error()
+
+
+# ---------------------------------------------------------------- prompt
+def run_prompt(sp24, new, prefix, hq, hkv, d, page, e4m3, token_major, window, sinks, seed, poison=True):
+    """new: query rows of each sequence; prefix: earlier tokens of each (negative: the cache is short of tokens)."""
+    lens = [max(0, a + b) for a, b in zip(new, prefix)]
+    s = Setup(sp24, lens, hkv, d, page, e4m3, token_major, seed)
+    see = [sees(torch.arange(n - m, n), n, window, sinks) for n, m in zip(lens, new)]
+    if poison:
+        s.poison([x.any(0) if x.shape[0] else torch.zeros(n, dtype=torch.bool) for x, n in zip(see, lens)])
+    cache = s.upload()
+    g = torch.Generator().manual_seed(seed + 1)
+    T = sum(new)
+    q = (2 * torch.randn(T, hq, d, generator=g)).to(torch.bfloat16)
+    cu = torch.tensor([0] + new).cumsum(0).to(torch.int32)
+    y = sp24.attention_prompt(q.cuda(), cu.cuda(), cache, s.table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                              window=window, sinks=sinks)
+    sp24.last_device_error()
+    for b, m in enumerate(new):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        ref, size = attend(q[rows].double(), s.tokens("k", b), s.tokens("v", b), see[b], d ** -0.5)
+        assert_attention(y[rows], ref, size, "sequence %d" % b)
+    return y
+
+
+@pytest.mark.parametrize("e4m3,token_major", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("new,prefix,hq,hkv,d,page,window,sinks", [
+    ([1], [0], 1, 1, 64, 16, 0, 0),
+    ([1, 0, 7, 0], [5, 3, 0, 0], 8, 2, 128, 16, 0, 0),       # sequences without new tokens
+    ([127, 128, 129], [0, 0, 0], 1, 1, 64, 64, 0, 0),
+    ([300], [0], 4, 1, 128, 128, 0, 0),
+    ([64, 63, 65, 1], [64, 200, 0, 511], 4, 1, 128, 16, 0, 0),  # one tile of 64 tokens, and one more
+    ([100, 33], [77, 1], 7, 1, 64, 32, 0, 0),                # 7 heads do not divide a tile
+    ([40, 5], [0, 300], 24, 2, 64, 64, 0, 0),
+    ([20], [130], 40, 1, 128, 16, 0, 0),                     # 3 tokens per tile
+    ([9], [20], 128, 1, 64, 16, 0, 0),                       # one token per tile
+    ([500], [0], 2, 1, 128, 32, 100, 4),                     # window and sinks
+    ([70, 200], [600, 300], 6, 2, 64, 16, 130, 1),
+    ([150], [400], 2, 2, 128, 64, 1, 0),                     # a window of one
+    ([150], [400], 2, 1, 64, 16, 64, 200),                   # sinks over several tiles
+    ([10, 200], [-4, -150], 4, 2, 128, 16, 0, 0),            # rows before the first token: nothing to see
+    ([6, 3], [-6, -3], 4, 2, 64, 16, 0, 0),                  # nothing in the cache at all
+])
+def test_prompt(sp24, new, prefix, hq, hkv, d, page, e4m3, token_major, window, sinks):
+    run_prompt(sp24, new, prefix, hq, hkv, d, page, e4m3, token_major, window, sinks, seed=sum(new) + hq)
+
+
+def test_prompt_many_sequences(sp24):
+    g = torch.Generator().manual_seed(9)
+    new = torch.randint(0, 9, (150,), generator=g).tolist()
+    prefix = torch.randint(0, 60, (150,), generator=g).tolist()
+    run_prompt(sp24, new, prefix, 4, 2, 64, 16, False, False, 0, 0, seed=9)
+
+
+def test_prompt_matches_decode_and_pieces(sp24):
+    """A prompt in one call, the same in pieces, and its last token as a decode step."""
+    n, hq, hkv, d = 421, 8, 2, 128
+    for e4m3 in (False, True):
+        s = Setup(sp24, [n], hkv, d, 16, e4m3, False, seed=51)
+        cache, table = s.upload(), s.table.cuda()
+        q = torch.randn(n, hq, d, device="cuda").bfloat16()
+        i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        whole = sp24.attention_prompt(q, i32(0, n), cache, table, i32(n), window=200, sinks=3)
+        ref, size = attend(q.double().cpu(), s.tokens("k", 0), s.tokens("v", 0), sees(torch.arange(n), n, 200, 3),
+                           d ** -0.5)
+        assert_attention(whole, ref, size, "whole")
+        for lo, hi in ((0, 100), (100, 357), (357, 420)):
+            y = sp24.attention_prompt(q[lo:hi], i32(0, hi - lo), cache, table, i32(hi), window=200, sinks=3)
+            assert_attention(y, ref[lo:hi], size[lo:hi], "piece")
+        y = sp24.attention_decode(q[n - 1:], cache, table, i32(n), window=200, sinks=3)
+        assert_attention(y, ref[n - 1:], size[n - 1:], "decode")
+
+
+def test_prompt_rows_of_no_sequence_stay(sp24):
+    s = Setup(sp24, [20], 1, 64, 16, False, False, seed=61)
+    cache = s.upload()
+    q = torch.randn(30, 2, 64, device="cuda").bfloat16()
+    out = torch.full((30, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    sp24.attention_prompt(q, torch.tensor([0, 20], dtype=torch.int32, device="cuda"), cache, s.table.cuda(),
+                          torch.tensor([20], dtype=torch.int32, device="cuda"), out=out)
+    assert (out[20:] == 5).all() and (out[:20] != 5).any()
+    ref, size = attend(q[:20].double().cpu(), s.tokens("k", 0), s.tokens("v", 0), sees(torch.arange(20), 20, 0, 0),
+                       64 ** -0.5)
+    assert_attention(out[:20], ref, size, "rows")
+
+
+# ---------------------------------------------------------------- refusals
+def test_binding_refusals(sp24):
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    codes = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, device="cuda")
+    scale = torch.ones(2, device="cuda")
+    for args in ((k, codes), (k, v[:3]), (codes, codes), (codes, codes, scale), (k, v, scale, scale),
+                 (codes, codes, scale, scale[:1]), (k[..., :32], v[..., :32]), (k[:, :, :8], v[:, :, :8]),
+                 (k.float(), v.float()), (k.cpu(), v.cpu()), (k.transpose(2, 3), v.transpose(2, 3)),
+                 (k.expand(4, 2, 16, 64)[:1].expand(4, 2, 16, 64),) * 2):
+        with pytest.raises(ValueError):
+            sp24.KVCache(*args)
+    cache = sp24.KVCache(k, v)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    lens = torch.ones(2, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    decode = lambda q=q, t=table, n=lens, **kw: sp24.attention_decode(q, cache, t, n, **kw)          # noqa: E731
+    prompt = lambda q=q, c=cu, t=table, n=lens, **kw: sp24.attention_prompt(q, c, cache, t, n, **kw)  # noqa: E731
+    for call in (decode, prompt):
+        call()
+        for kw in (dict(q=q.float()), dict(q=q[..., :32]), dict(q=q[:, :3]), dict(q=q.transpose(1, 2)),
+                   dict(t=table.long()), dict(t=table[0]), dict(n=lens.long()), dict(n=lens[:1]), dict(scale=0.0),
+                   dict(scale=float("nan")), dict(window=-1), dict(sinks=-1), dict(out=q[:1]), dict(out=q.float()),
+                   dict(q=q.cpu())):
+            with pytest.raises(ValueError):
+                call(**kw)
+    with pytest.raises(ValueError):
+        decode(q=q[:1])
+    with pytest.raises(ValueError):
+        prompt(c=cu[:2])
+    with pytest.raises(sp24.Sp24Error) as e:
+        decode(workspace=torch.zeros(0, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 6
+    qkv = torch.zeros(2, 8 * 64, dtype=torch.bfloat16, device="cuda")
+    pos, slots = lens, torch.arange(2, device="cuda")
+    turn, w = torch.zeros(4, 64, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    rope = lambda x=qkv, h=4, p=pos, s=slots, t=turn, **kw: sp24.qk_norm_rope(x, h, cache, p, s, t, **kw)  # noqa: E731
+    rope()
+    for kw in (dict(x=qkv.float()), dict(x=qkv[:, 1:]), dict(h=3), dict(p=pos.long()), dict(p=pos[:1]),
+               dict(s=slots.int()), dict(t=turn[:, :8]), dict(t=turn.double()), dict(t=turn[0]),
+               dict(t=torch.zeros(4, 80, device="cuda")), dict(q_weight=w), dict(q_weight=w, k_weight=w[:32]),
+               dict(q_weight=w, k_weight=w, eps=float("inf")), dict(out=q[:1])):
+        with pytest.raises(ValueError):
+            rope(**kw)
+    sp24.last_device_error()
+
+
+def test_empty_calls(sp24):
+    """No token, no sequence, no row: nothing to do, and no error."""
+    s = Setup(sp24, [20], 2, 64, 16, False, False, seed=71)
+    cache = s.upload()
+    z = lambda *n, t=torch.int32: torch.zeros(n, dtype=t, device="cuda")  # noqa: E731
+    bf = torch.bfloat16
+    assert sp24.qk_norm_rope(z(0, 8 * 64, t=bf), 4, cache, z(0), z(0, t=torch.int64), torch.ones(3, 64).cuda()).shape == (
+        0, 4, 64)
+    assert sp24.attention_decode(z(0, 4, 64, t=bf), cache, z(0, 3), z(0)).shape == (0, 4, 64)
+    assert sp24.attention_prompt(z(0, 4, 64, t=bf), z(1), cache, z(0, 3), z(0)).shape == (0, 4, 64)
+    assert sp24.attention_prompt(z(0, 4, 64, t=bf), z(3), cache, z(2, 3), z(2)).shape == (0, 4, 64)
+    sp24.last_device_error()
