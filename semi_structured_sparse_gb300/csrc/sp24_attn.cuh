@@ -64,7 +64,7 @@ inline sp24_status check_attention(const void* q, int64_t rows, int64_t ldq, int
     if (!q || !Y || !page_table || !seq_lens) return SP24_ERR_INVALID_ARG;
     if (ldq < width || ldy < width || ldq >= (int64_t(1) << 39) || ldy >= (int64_t(1) << 39))
       return SP24_ERR_INVALID_ARG;
-    if (table_width < 1 || ld_table < table_width || table_width > (INT32_MAX >> out->page_shift))
+    if (table_width < 1 || ld_table < table_width || table_width > (INT32_MAX / 2 >> out->page_shift))
       return SP24_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(Y) || ldq % 8 || ldy % 8) return SP24_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens)) & 3u)

@@ -1,5 +1,5 @@
-// sp24_attn_simple.cu -- sp24_attention_decode and sp24_attention_prompt, the
-// plain way: one warp per query row and head, one key at a time.
+// sp24_attn_simple.cu -- sp24_attention_prompt the plain
+// way: one warp per query row and head, one key at a time.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include "sp24_attn.cuh"
@@ -94,38 +94,6 @@ sp24_status run_simple(const SimpleParams& p, int rows, cudaStream_t s) {
 
 }  // namespace
 }  // namespace sp24
-
-extern "C" size_t sp24_attention_decode_workspace_size(int q_heads, int heads, int head_dim) {
-  if (q_heads < 1 || heads < 1 || q_heads % heads || q_heads / heads > 128 || (head_dim != 64 && head_dim != 128))
-    return 0;
-  const sp24::DeviceInfo* dev = nullptr;
-  if (sp24::current_device(&dev)) return 0;
-  return 16;
-}
-
-extern "C" sp24_status sp24_attention_decode(const void* q, int64_t B, int64_t ldq, int q_heads,
-                                             const sp24_kv_cache* cache, const int32_t* page_table,
-                                             int64_t table_width, int64_t ld_table, const int32_t* seq_lens,
-                                             float scale, int window, int sinks, void* Y, int64_t ldy,
-                                             void* workspace, size_t workspace_bytes, void* stream) {
-  using namespace sp24;
-  SimpleParams p = {};
-  if (sp24_status st = check_attention(q, B, ldq, q_heads, cache, page_table, table_width, ld_table, seq_lens, B, scale,
-                                       window, sinks, Y, ldy, &p.cache))
-    return st;
-  const DeviceInfo* dev = nullptr;
-  if (sp24_status st = current_device(&dev)) return st;
-  if (!workspace || workspace_bytes < sp24_attention_decode_workspace_size(q_heads, cache->heads, cache->head_dim))
-    return SP24_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return SP24_ERR_ALIGNMENT;
-  if (B == 0) return SP24_OK;
-  p.q = static_cast<const __nv_bfloat16*>(q), p.ldq = ldq, p.cu_q = nullptr, p.B = int(B), p.T = int(B);
-  p.page_table = page_table, p.table_width = int(table_width), p.ld_table = ld_table, p.seq_lens = seq_lens;
-  p.scale = scale, p.window = window, p.sinks = sinks, p.y = static_cast<__nv_bfloat16*>(Y), p.ldy = ldy;
-  p.q_heads = q_heads, p.group = q_heads / cache->heads, p.D = cache->head_dim, p.e4m3 = cache->dtype == SP24_E4M3;
-  p.err = dev->err_word;
-  return run_simple(p, int(B), static_cast<cudaStream_t>(stream));
-}
 
 extern "C" sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t ldq, int q_heads, const int32_t* cu_q,
                                              int64_t B, const sp24_kv_cache* cache, const int32_t* page_table,
