@@ -1,0 +1,676 @@
+// sp24_attn_prompt.cu -- sp24_attention_prompt: causal attention of a ragged
+// batch of new tokens over the paged cache, with an optional sliding window
+// and sinks.
+//
+//   S = Q K^T,  P = exp2(c S - m),  O = P V / sum(P),  c = scale log2(e)
+//   (times the cache's scale), m a row maximum that follows the true one
+//
+// Bound by the tensor core (4 D operations per visible key and query row) and,
+// close behind, by the exponentials.  A CTA takes 256 query rows of one kv
+// head as two tiles of 128: the rows of a tile are (token, head of the group)
+// pairs, so a short prompt fills tiles too and all heads of a group share the
+// keys' copies.  Keys and values come in tiles of 128 tokens, one TMA box per
+// page and 64 dims, through a ring of shared memory.  Per key tile and query
+// tile, S (128 x 128 fp32) and O (128 x D fp32) are in tensor memory, all 512
+// columns of it; P goes back into the columns of S as bf16 (f16 for an e4m3
+// cache) and is the A operand of P V straight from there.
+//
+// Two softmax warpgroups (a thread per query row: maxima and sums need no
+// shuffles) alternate with the tensor core: while one works on its tile, the
+// MMAs run on the other's.  P V of key tile i and Q K^T of tile i + 1 are issued
+// back to back for a query tile; the tensor core runs them in order, so S may
+// overwrite P.  A row's O is rescaled only when its maximum has grown by more
+// than 2^8 (P then stays below 256, which bf16 and fp32 sums hold as well as
+// 1); that is rare after the first tiles, so the softmax warps do it themselves.
+//
+// Places of a key tile that no row of the CTA sees are not loaded by whole
+// pages, and zeroed in V otherwise: 0 x NaN is not 0.  In S they are
+// overwritten with -inf.
+//
+// With an e4m3 cache a further warpgroup turns the tiles' codes into f16
+// (exactly) between the copy and the MMA; the softmax warps scale each query
+// row by a power of two, so that bf16 queries fit f16's range.
+#include <cuda_bf16.h>
+#include "sp24_attn.cuh"
+#include "sp24_ptx.cuh"
+
+namespace sp24 {
+namespace {
+
+constexpr int BM = 128;   // query rows per tile, two tiles per CTA
+constexpr int BN = 128;   // keys per tile
+
+struct PromptParams {
+  int T, B;
+  const int32_t* cu_q;
+  CacheView cache;
+  const int32_t* page_table;
+  int table_width;
+  int64_t ld_table;
+  const int32_t* seq_lens;
+  float scale;
+  int window, sinks;
+  __nv_bfloat16* y;
+  int64_t ldy;
+  int kv_heads, group, tile_tokens;  // tile_tokens = BM / group
+  unsigned int* err;
+};
+
+template <int D_, bool E4M3_>
+struct Cfg {
+  static constexpr int D = D_;
+  static constexpr bool E4M3 = E4M3_;
+  static constexpr int THREADS = E4M3 ? 512 : 384;
+  static constexpr int Q_TILE = BM * D * 2;
+  static constexpr int KV_TILE = BN * D * 2;              // as the MMA reads it
+  static constexpr int RAW_TILE = BN * D;                 // e4m3 codes
+  static constexpr int RAW = E4M3 ? (D == 128 ? 2 : 4) : 0;
+  static constexpr int SLOTS = D == 128 ? (E4M3 ? 4 : 5) : 8;
+  static constexpr int BARS = 2 + 2 + 2 + 2 + 2 + 1 + 2 * SLOTS + 2 * RAW;
+  static constexpr int SMEM = 1024 + 2 * Q_TILE + SLOTS * KV_TILE + RAW * RAW_TILE + BARS * 8;
+  // Registers after the split: the warpgroups' shares stay within the launch's
+  // (168 x 384 or 128 x 512).
+  static constexpr int REG_SOFTMAX = E4M3 ? 192 : 208;
+  static constexpr int REG_ISSUE = E4M3 ? 56 : 80;
+  static constexpr int REG_CONVERT = 72;
+};
+static_assert(2 * 128 * 208 + 128 * 80 <= 168 * 384, "register split, bf16");
+static_assert(2 * 128 * 192 + 128 * 56 + 128 * 72 <= 128 * 512, "register split, e4m3");
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {  // the low two bytes
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+// Tensor memory <-> registers: this warp's 32 lanes, 32 consecutive columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D (128 x N, fp32) (+)= A (tensor memory, 16-bit, 128 x 16) B (shared memory)
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+// kind::f16, fp32 accumulator; 16-bit type: 0 f16, 1 bf16; b_mn: B's rows (its N) are contiguous.
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, uint32_t type, bool b_mn) {
+  return (1u << 4) | (type << 7) | (type << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// What a CTA works on.
+struct Work {
+  int b;             // sequence, or -1: nothing
+  int row0, rows;    // its first query row (in q), and how many tokens from there on are the sequence's
+  int p0;            // position of that row's token
+  int p_hi;          // the last position (the last visible key) of the CTA's rows
+  int wlo, send;     // keys that some row sees: [0, send) and [wlo, p_hi]
+  int first, nst, nt;  // key tiles: 0 .. nst - 1 (sinks), then first, first + 1, ...; nt in all
+};
+
+__device__ __forceinline__ int tile_of(const Work& w, int i) { return i < w.nst ? i : w.first + i - w.nst; }
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    attention_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptParams p) {
+  constexpr int D = C::D, SLOTS = C::SLOTS, RAW = C::RAW;
+  constexpr bool E4M3 = C::E4M3;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Work s_work;
+  __shared__ uint32_t s_tmem;
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_s = smem;
+  uint8_t* kv_s = q_s + 2 * C::Q_TILE;
+  uint8_t* raw_s = kv_s + SLOTS * C::KV_TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raw_s + RAW * C::RAW_TILE);
+  uint64_t* q_full = bars;            // [2] the query tile has landed
+  uint64_t* q_ready = bars + 2;       // [2] ... and is f16 (e4m3 caches)
+  uint64_t* s_full = bars + 4;        // [2] S of the next key tile is there, and P V of the last one done
+  uint64_t* p_full = bars + 6;        // [2] P is there, and O at its scale
+  uint64_t* o_full = bars + 8;        // [2] O is complete
+  uint64_t* drain = bars + 10;
+  uint64_t* kv_full = bars + 11;      // [SLOTS]
+  uint64_t* kv_empty = kv_full + SLOTS;
+  uint64_t* raw_full = kv_empty + SLOTS;  // [RAW]
+  uint64_t* raw_empty = raw_full + RAW;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.x % p.kv_heads;
+
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+    if (lane == 0) {
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&q_full[x], 1);
+        mbar_init(&q_ready[x], 4);
+        mbar_init(&s_full[x], 1);
+        mbar_init(&p_full[x], 4);
+        mbar_init(&o_full[x], 1);
+      }
+      mbar_init(drain, 1);
+      for (int i = 0; i < SLOTS; ++i) {
+        mbar_init(&kv_full[i], E4M3 ? 4 : 1);
+        mbar_init(&kv_empty[i], 1);
+      }
+      for (int i = 0; i < RAW; ++i) {
+        mbar_init(&raw_full[i], 1);
+        mbar_init(&raw_empty[i], 4);
+      }
+      fence_mbar_init();
+    }
+  } else if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  pdl_wait();
+
+  if (warp == 0) {
+    // Blocks of 2 tile_tokens tokens, sequence by sequence; the last block of
+    // the last sequence is the first to start, since late blocks of a prompt
+    // see the most keys.
+    const int tok = 2 * p.tile_tokens;
+    auto bounds = [&](int b, int& lo, int& hi) {
+      const int a = __ldg(p.cu_q + b), z = __ldg(p.cu_q + b + 1);
+      lo = min(max(a, 0), p.T), hi = min(max(z, lo), p.T);
+      return lo != a || hi != z;
+    };
+    int total = 0;
+    bool bad = false;
+    for (int b = lane; b < p.B; b += 32) {
+      int lo, hi;
+      bad |= bounds(b, lo, hi);
+      total += (hi - lo + tok - 1) / tok;
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
+    if (bad && blockIdx.x == 0) atomicOr(p.err, DEVERR_INDEX);
+    const int want = total - 1 - static_cast<int>(blockIdx.x / p.kv_heads);
+    if (lane == 0) s_work.b = -1;
+    __syncwarp();
+    int seen = 0;
+    for (int b0 = 0; want >= 0 && b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int lo = 0, hi = 0;
+      if (b < p.B) bounds(b, lo, hi);
+      const int own = (hi - lo + tok - 1) / tok;
+      int incl = own;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+        if (lane >= m) incl += x;
+      }
+      incl += seen;
+      if (want < incl && want >= incl - own) {
+        Work w;
+        w.b = b;
+        const int i0 = (want - (incl - own)) * tok, m = hi - lo;
+        const int most = p.table_width << p.cache.page_shift;
+        int n = __ldg(p.seq_lens + b);
+        if (n < 0 || n > most) {
+          atomicOr(p.err, DEVERR_INDEX);
+          n = n < 0 ? 0 : most;
+        }
+        w.row0 = lo + i0;
+        w.rows = m - i0;
+        w.p0 = n - m + i0;
+        w.p_hi = w.p0 + min(tok, w.rows) - 1;
+        w.wlo = p.window > 0 ? max(0, w.p0 - p.window + 1) : 0;
+        w.send = min(p.sinks, w.wlo);
+        w.first = w.wlo / BN;
+        w.nst = min((w.send + BN - 1) / BN, w.first);
+        w.nt = w.p_hi < 0 ? 0 : w.nst + w.p_hi / BN + 1 - w.first;
+        s_work = w;
+      }
+      seen = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if (want < seen) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Work w = s_work;
+  const uint32_t tmem = s_tmem;
+  const int tiles = w.b < 0 ? 0 : w.rows > p.tile_tokens ? 2 : 1;  // query tiles with a token of the sequence
+  const int nt = w.b < 0 ? 0 : w.nt;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    setmaxnreg_inc<C::REG_SOFTMAX>();
+    const int x = warp >> 2, r = tid & 127;
+    const int token = r / p.group, head = r - token * p.group;
+    const int at = x * p.tile_tokens + token;            // token within the CTA's rows
+    const bool mine = token < p.tile_tokens && at < w.rows && x < tiles;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + x * BN, to = tmem + lanes + 2 * BN + x * D;
+    float l = 0.0f;
+    bool ok = true;
+    if (x < tiles && nt > 0) {
+      float c = p.scale * 1.4426950408889634f;
+      if (E4M3) {
+        ok = mbar_wait(&q_full[x], 0);
+        if (ok) {
+          // this row to f16, scaled by a power of two to at most 2
+          uint8_t* q = q_s + x * C::Q_TILE + r * 128;
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q + (i / 8) * (BM * 128) + (((i & 7) ^ (r & 7)) << 4));
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+          }
+          uint32_t e = __float_as_uint(top) >> 23;  // as in the decode kernel
+          e = e == 255 ? 127u : min(max(e, 64u), 253u);
+          const float down = __uint_as_float((254u - e) << 23);
+          c *= p.cache.k_scale[hk] * __uint_as_float(e << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            uint4* at16 = reinterpret_cast<uint4*>(q + (i / 8) * (BM * 128) + (((i & 7) ^ (r & 7)) << 4));
+            uint4 v = *at16;
+            uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              u[j] = f16x2_rn(__uint_as_float(u[j] << 16) * down, __uint_as_float(u[j] & 0xFFFF0000u) * down);
+            *at16 = v;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_ready[x]);
+        }
+      }
+      const int pos = mine ? w.p0 + at : -1;
+      const int p_min = w.p0 + x * p.tile_tokens, p_max = min(w.p_hi, p_min + p.tile_tokens - 1);
+      float m = -INFINITY;
+      for (int i = 0; i < nt && ok; ++i) {
+        ok = mbar_wait(&s_full[x], i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t su[BN];
+#pragma unroll
+        for (int j = 0; j < BN / 32; ++j) tmem_ld32(ts + 32 * j, su + 32 * j);
+        tmem_ld_wait();
+        float* s = reinterpret_cast<float*>(su);
+        const int base = tile_of(w, i) * BN, end = base + BN - 1;
+        const bool whole = end <= p_min && (p.window == 0 || base > p_max - p.window || end < p.sinks);
+        if (!whole) {
+          const int hi = pos - base, lo = p.window > 0 ? hi - p.window : -1, sk = p.sinks - base;
+#pragma unroll
+          for (int j = 0; j < BN; ++j)
+            if (!(j <= hi && (j > lo || j < sk))) s[j] = -INFINITY;
+        }
+        float top[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top[j] = s[j];
+#pragma unroll
+        for (int j = 4; j < BN; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
+        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+        const bool grow = now > m + 8.0f;  // also from -inf
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float to_m = grow ? now : m;
+          const float keep = m == to_m ? 1.0f : ex2(m - to_m);
+          m = to_m;
+          l *= keep;
+          if (i > 0) {
+#pragma unroll 1
+            for (int j = 0; j < D; j += 32) {
+              uint32_t o[32];
+              tmem_ld32(to + j, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+              tmem_st32(to + j, o);
+            }
+          }
+        }
+        const float use = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float a = ex2(fmaf(s[64 * h + 2 * j], c, -use)), b = ex2(fmaf(s[64 * h + 2 * j + 1], c, -use));
+            sum[2 * (j & 1)] += a;
+            sum[2 * (j & 1) + 1] += b;
+            pk[j] = E4M3 ? f16x2_rn(a, b) : bf16x2_rn(a, b);
+          }
+          tmem_st32(ts + 32 * h, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (ok) ok = mbar_wait(&o_full[x], 0);
+      if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
+      tc_fence_after();
+    }
+    if (x < tiles && ok) {
+      const float f = l == 0.0f ? 0.0f : (E4M3 ? p.cache.v_scale[hk] : 1.0f) / l;
+      __nv_bfloat16* y = p.y + static_cast<int64_t>(w.row0 + at) * p.ldy + static_cast<int64_t>(hk * p.group + head) * D;
+#pragma unroll 1
+      for (int j = 0; j < D; j += 32) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tmem_ld32(to + j, o);
+          tmem_ld_wait();
+        }
+        if (mine) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (nt > 0 && f != 0.0f) {
+              uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                u[e] = bf16x2_rn(__uint_as_float(o[k + 2 * e]) * f, __uint_as_float(o[k + 2 * e + 1]) * f);
+            }
+            *reinterpret_cast<uint4*>(y + j + k) = v;
+          }
+        }
+      }
+    }
+  } else if (warp < 12) {
+    setmaxnreg_dec<C::REG_ISSUE>();
+    if (warp == 8 && nt > 0) {
+      // ------------------------------------------------------------ MMA
+      bool ok = true;
+      const uint32_t id_qk = idesc_16(BM, BN, E4M3 ? 0 : 1, false), id_pv = idesc_16(BM, D, E4M3 ? 0 : 1, true);
+      const uint32_t q_a = smem_u32(q_s), kv_a = smem_u32(kv_s);
+      auto qk = [&](int x, int slot) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * (BM * 128) + (k % 4) * 32;
+          mma_bf16(tmem + x * BN, smem_desc(q_a + x * C::Q_TILE + off, 16, 1024, SWZ_128B),
+                   smem_desc(kv_a + slot * C::KV_TILE + off, 16, 1024, SWZ_128B), id_qk, k > 0);
+        }
+      };
+      auto pv = [&](int x, int slot, bool add) {
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_f16_ts(tmem + 2 * BN + x * D, tmem + x * BN + 8 * k,
+                     smem_desc(kv_a + slot * C::KV_TILE + k * 2048, BN * 128, 1024, SWZ_128B), id_pv, add || k > 0);
+      };
+      int c = 0;  // tiles of the ring so far: K 0, V 0, K 1, V 1, ...
+      auto wait_kv = [&](int n) { return mbar_wait(&kv_full[n % SLOTS], (n / SLOTS) & 1); };
+      ok = wait_kv(0);
+      for (int x = 0; x < tiles && ok; ++x) {
+        ok = mbar_wait(E4M3 ? &q_ready[x] : &q_full[x], 0);
+        tc_fence_after();
+        if (ok && lane == 0) {
+          qk(x, 0);
+          mma_commit(&s_full[x]);
+        }
+      }
+      if (ok && lane == 0) mma_commit(&kv_empty[0]);
+      c = 1;
+      for (int i = 0; i < nt && ok; ++i, c += 2) {
+        const bool more = i + 1 < nt;
+        const int sv = c % SLOTS, sk = (c + 1) % SLOTS;
+        ok = wait_kv(c);
+        if (!ok) break;
+        if (!E4M3) {
+          // Rows of V that no row of the CTA sees: zeros.
+          const int base = tile_of(w, i) * BN, end = base + BN - 1;
+          if (end > w.p_hi || (base < w.wlo && end >= w.send)) {
+            uint8_t* v = kv_s + sv * C::KV_TILE;
+            for (int r = 0; r < BN; ++r) {
+              const int j = base + r;
+              if (j > w.p_hi || (j < w.wlo && j >= w.send)) {
+                if (lane < D / 8)
+                  *reinterpret_cast<uint4*>(v + (lane / 8) * (BN * 128) + r * 128 + (lane & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        for (int x = 0; x < tiles && ok; ++x) {
+          ok = mbar_wait(&p_full[x], i & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            pv(x, sv, i > 0);
+            if (x == tiles - 1) mma_commit(&kv_empty[sv]);
+            if (!more) mma_commit(&o_full[x]);
+          }
+          if (more) {
+            if (x == 0) ok = wait_kv(c + 1);
+            if (!ok) break;
+            if (lane == 0) {
+              qk(x, sk);
+              mma_commit(&s_full[x]);
+              if (x == tiles - 1) mma_commit(&kv_empty[sk]);
+            }
+          }
+        }
+      }
+      if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_MMA);
+      if (lane == 0) mma_commit(drain);  // every MMA issued must finish before tensor memory is freed
+      __syncwarp();
+      mbar_wait(drain, 0);
+    } else if (warp == 9 && nt > 0) {
+      // ------------------------------------------------------------ copies
+      constexpr int BOX_D = E4M3 ? D : 64;                 // dims per box
+      constexpr int BOX_STRIDE = BN * 128;                 // between a tile's halves
+      constexpr int RING = E4M3 ? RAW : SLOTS;
+      uint64_t* full = E4M3 ? raw_full : kv_full;
+      uint64_t* empty = E4M3 ? raw_empty : kv_empty;
+      bool ok = true;
+      if (lane == 0) {
+        for (int x = 0; x < tiles; ++x) {
+          mbar_arrive_expect_tx(&q_full[x], p.tile_tokens * p.group * D * 2);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(q_s + x * C::Q_TILE + h * (BM * 128), &qmap, &q_full[x], 64 * h, hk * p.group,
+                        w.row0 + x * p.tile_tokens);
+        }
+      }
+      const int page_size = 1 << p.cache.page_shift, pages = BN >> p.cache.page_shift;
+      const int32_t* table = p.page_table + int64_t(w.b) * p.ld_table;
+      int c = 0;
+      for (int i = 0; i < nt && ok; ++i) {
+        // lane j < pages: page j of the tile, if some row sees a token of it
+        const int base = tile_of(w, i) * BN;
+        const int a = base + lane * page_size, z = a + page_size - 1;
+        const bool need = lane < pages && a <= w.p_hi && (z >= w.wlo || a < w.send);
+        int page = 0;
+        if (need) {
+          page = __ldg(table + (a >> p.cache.page_shift));
+          if (page < 0 || page >= p.cache.num_pages) {
+            atomicOr(p.err, DEVERR_INDEX);
+            page = 0;
+          }
+        }
+        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, need));
+        for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
+          const int slot = c % RING;
+          if (c >= RING) ok = mbar_wait(&empty[slot], (c / RING - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * page_size * D * (E4M3 ? 1 : 2));
+          __syncwarp();
+          if (need) {
+            uint8_t* dst = (E4M3 ? raw_s + slot * C::RAW_TILE : kv_s + slot * C::KV_TILE) +
+                           lane * page_size * (E4M3 ? D : 128);
+#pragma unroll
+            for (int h = 0; h < D / BOX_D; ++h)
+              tma_load_4d(dst + h * BOX_STRIDE, kv ? &vmap : &kmap, &full[slot], BOX_D * h, 0, hk, page);
+          }
+        }
+      }
+      if (!ok) {
+        if (lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
+        for (int n = max(0, c - RING); n < c; ++n) mbar_wait(&full[n % RING], (n / RING) & 1);  // copies in flight
+        for (int x = 0; x < tiles; ++x) mbar_wait(&q_full[x], 0);
+      }
+    }
+  } else if (E4M3) {
+    // -------------------------------------------------------------- e4m3 -> f16
+    setmaxnreg_dec<C::REG_CONVERT>();
+    const int r = tid & 127;  // this thread's token of each tile
+    bool ok = true;
+    for (int c = 0; c < 2 * nt && ok; ++c) {
+      const int from = c % (RAW ? RAW : 1), slot = c % SLOTS;
+      ok = mbar_wait(&raw_full[from], (c / (RAW ? RAW : 1)) & 1);
+      if (ok && c >= SLOTS) ok = mbar_wait(&kv_empty[slot], (c / SLOTS - 1) & 1);
+      if (!ok) break;
+      const int j = tile_of(w, c >> 1) * BN + r;
+      const bool seen = j <= w.p_hi && (j >= w.wlo || j < w.send);
+      const uint8_t* src = raw_s + from * C::RAW_TILE + r * D;
+      uint8_t* dst = kv_s + slot * C::KV_TILE + r * 128;
+      const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint4 v = *reinterpret_cast<const uint4*>(src + ((i ^ sw) << 4));
+        if (!seen) v = make_uint4(0, 0, 0, 0);
+        uint8_t* to = dst + (i / 4) * (BN * 128);
+        const int c0 = (2 * i) & 7;
+        *reinterpret_cast<uint4*>(to + ((c0 ^ (r & 7)) << 4)) =
+            make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16));
+        *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (r & 7)) << 4)) =
+            make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&raw_empty[from]);
+        mbar_arrive(&kv_full[slot]);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
+  }
+  tc_fence_before();
+  __syncthreads();
+  pdl_trigger();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool E4M3>
+sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_heads, const sp24_kv_cache& cache,
+                   cudaStream_t s) {
+  using C = Cfg<D, E4M3>;
+  CUtensorMap qmap, kmap, vmap;
+  {
+    const uint64_t dims[3] = {uint64_t(D), uint64_t(q_heads), uint64_t(p.T)};
+    const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(ldq) * 2};
+    const uint32_t box[3] = {64, uint32_t(p.group), uint32_t(p.tile_tokens)};
+    if (sp24_status st = make_tmap_nd(&qmap, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box,
+                                      CU_TENSOR_MAP_SWIZZLE_128B))
+      return st;
+  }
+  const uint64_t dims[4] = {uint64_t(D), uint64_t(cache.page_size), uint64_t(cache.heads), uint64_t(cache.num_pages)};
+  const uint64_t strides[3] = {uint64_t(p.cache.token_stride), uint64_t(p.cache.head_stride),
+                               uint64_t(p.cache.page_stride)};
+  const uint32_t box[4] = {uint32_t(E4M3 ? D : 64), uint32_t(cache.page_size), 1, 1};
+  const auto type = E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto swizzle = E4M3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (sp24_status st = make_tmap_nd(&kmap, cache.k, type, 4, dims, strides, box, swizzle)) return st;
+  if (sp24_status st = make_tmap_nd(&vmap, cache.v, type, 4, dims, strides, box, swizzle)) return st;
+  auto kern = attention_prompt_kernel<C>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return SP24_ERR_CUDA;
+  // Every sequence's last block may be partly filled.
+  const int64_t blocks = p.T / (2 * p.tile_tokens) + p.B;
+  if (blocks > INT32_MAX / p.kv_heads) return SP24_ERR_UNSUPPORTED;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks * p.kv_heads)), dim3(C::THREADS), C::SMEM, s, qmap, kmap,
+                    vmap, p) == cudaSuccess
+             ? SP24_OK
+             : SP24_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace sp24
+
+extern "C" sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t ldq, int q_heads, const int32_t* cu_q,
+                                             int64_t B, const sp24_kv_cache* cache, const int32_t* page_table,
+                                             int64_t table_width, int64_t ld_table, const int32_t* seq_lens,
+                                             float scale, int window, int sinks, void* Y, int64_t ldy, void* stream) {
+  using namespace sp24;
+  PromptParams p = {};
+  if (sp24_status st = check_attention(q, T, ldq, q_heads, cache, page_table, table_width, ld_table, seq_lens, B, scale,
+                                       window, sinks, Y, ldy, &p.cache))
+    return st;
+  if (T > 0 && B > 0 && !cu_q) return SP24_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(cu_q) & 3u) return SP24_ERR_ALIGNMENT;
+  const DeviceInfo* dev = nullptr;
+  if (sp24_status st = current_device(&dev)) return st;
+  if (T == 0 || B == 0) return SP24_OK;
+  p.T = static_cast<int>(T);
+  p.B = static_cast<int>(B);
+  p.cu_q = cu_q;
+  p.page_table = page_table;
+  p.table_width = static_cast<int>(table_width);
+  p.ld_table = ld_table;
+  p.seq_lens = seq_lens;
+  p.scale = scale;
+  p.window = window;
+  p.sinks = sinks;
+  p.y = static_cast<__nv_bfloat16*>(Y);
+  p.ldy = ldy;
+  p.kv_heads = cache->heads;
+  p.group = q_heads / cache->heads;
+  p.tile_tokens = BM / p.group;
+  p.err = dev->err_word;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->dtype == SP24_E4M3;
+  if (cache->head_dim == 128)
+    return e4m3 ? launch<128, true>(p, q, ldq, q_heads, *cache, s) : launch<128, false>(p, q, ldq, q_heads, *cache, s);
+  return e4m3 ? launch<64, true>(p, q, ldq, q_heads, *cache, s) : launch<64, false>(p, q, ldq, q_heads, *cache, s);
+}
