@@ -66,7 +66,7 @@ struct Cfg {
   static constexpr int RAW_TILE = BN * D;                 // e4m3 codes
   static constexpr int RAW = E4M3 ? (D == 128 ? 2 : 4) : 0;
   static constexpr int SLOTS = D == 128 ? (E4M3 ? 4 : 5) : 8;
-  static constexpr int BARS = 2 + 2 + 2 + 2 + 2 + 1 + 2 * SLOTS + 2 * RAW;
+  static constexpr int BARS = 2 + 2 + 2 + 2 + 2 + 2 + 2 * SLOTS + 2 * RAW;
   static constexpr int SMEM = 1024 + 2 * Q_TILE + SLOTS * KV_TILE + RAW * RAW_TILE + BARS * 8;
   // Registers after the split: the warpgroups' shares stay within the launch's
   // (168 x 384 or 128 x 512).
@@ -77,6 +77,12 @@ struct Cfg {
 static_assert(2 * 128 * 208 + 128 * 80 <= 168 * 384, "register split, bf16");
 static_assert(2 * 128 * 192 + 128 * 56 + 128 * 72 <= 128 * 512, "register split, e4m3");
 
+// One lane of the warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+  return x != 0;
+}
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -178,13 +184,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t* s_full = bars + 4;        // [2] S of the next key tile is there, and P V of the last one done
   uint64_t* p_full = bars + 6;        // [2] P is there, and O at its scale
   uint64_t* o_full = bars + 8;        // [2] O is complete
-  uint64_t* drain = bars + 10;
-  uint64_t* kv_full = bars + 11;      // [SLOTS]
+  uint64_t* drain = bars + 10;        // [2]
+  uint64_t* kv_full = bars + 12;      // [SLOTS]
   uint64_t* kv_empty = kv_full + SLOTS;
   uint64_t* raw_full = kv_empty + SLOTS;  // [RAW]
   uint64_t* raw_empty = raw_full + RAW;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be uniform
   const int hk = blockIdx.x % p.kv_heads;
 
   if (warp == 8) {
@@ -197,11 +204,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_init(&s_full[x], 1);
         mbar_init(&p_full[x], 4);
         mbar_init(&o_full[x], 1);
+        mbar_init(&drain[x], 1);
       }
-      mbar_init(drain, 1);
       for (int i = 0; i < SLOTS; ++i) {
         mbar_init(&kv_full[i], E4M3 ? 4 : 1);
-        mbar_init(&kv_empty[i], 1);
+        mbar_init(&kv_empty[i], 2);
       }
       for (int i = 0; i < RAW; ++i) {
         mbar_init(&raw_full[i], 1);
@@ -426,45 +433,53 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   } else if (warp < 12) {
     setmaxnreg_dec<C::REG_ISSUE>();
-    if (warp == 8 && nt > 0) {
+    if ((warp == 8 || warp == 10) && (warp - 8) / 2 < tiles && nt > 0) {
       // ------------------------------------------------------------ MMA
+      // Each query tile has a warp of its own: a commit holds its thread back
+      // until the MMAs that it tracks are done, and the other tile's MMAs fill
+      // that time.
+      const int x = (warp - 8) / 2;
       bool ok = true;
       const uint32_t id_qk = idesc_16(BM, BN, E4M3 ? 0 : 1, false), id_pv = idesc_16(BM, D, E4M3 ? 0 : 1, true);
-      const uint32_t q_a = smem_u32(q_s), kv_a = smem_u32(kv_s);
-      auto qk = [&](int x, int slot) {
+      const uint64_t q_d = smem_desc(smem_u32(q_s) + x * C::Q_TILE, 16, 1024, SWZ_128B);
+      const uint64_t k_d = smem_desc(smem_u32(kv_s), 16, 1024, SWZ_128B);
+      const uint64_t v_d = smem_desc(smem_u32(kv_s), BN * 128, 1024, SWZ_128B);
+      const uint32_t t_s = tmem + x * BN, t_o = tmem + 2 * BN + x * D;
+      auto qk = [&](int slot) {
+        const uint64_t kd = k_d + slot * (C::KV_TILE >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * (BM * 128) + (k % 4) * 32;
-          mma_bf16(tmem + x * BN, smem_desc(q_a + x * C::Q_TILE + off, 16, 1024, SWZ_128B),
-                   smem_desc(kv_a + slot * C::KV_TILE + off, 16, 1024, SWZ_128B), id_qk, k > 0);
+          const int off = ((k / 4) * (BM * 128) + (k % 4) * 32) >> 4;
+          mma_bf16(t_s, q_d + off, kd + off, id_qk, k > 0);
         }
       };
-      auto pv = [&](int x, int slot, bool add) {
+      auto pv = [&](int slot, bool add) {
+        const uint64_t vd = v_d + slot * (C::KV_TILE >> 4);
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          mma_f16_ts(tmem + 2 * BN + x * D, tmem + x * BN + 8 * k,
-                     smem_desc(kv_a + slot * C::KV_TILE + k * 2048, BN * 128, 1024, SWZ_128B), id_pv, add || k > 0);
+        for (int k = 0; k < BN / 16; ++k) mma_f16_ts(t_o, t_s + 8 * k, vd + k * (2048 >> 4), id_pv, add || k > 0);
       };
-      int c = 0;  // tiles of the ring so far: K 0, V 0, K 1, V 1, ...
+      // A slot is free when both tiles' MMAs have read it (a lone tile says so twice).
+      auto release = [&](int slot) {
+        mma_commit(&kv_empty[slot]);
+        if (tiles == 1) mma_commit(&kv_empty[slot]);
+      };
       auto wait_kv = [&](int n) { return mbar_wait(&kv_full[n % SLOTS], (n / SLOTS) & 1); };
-      ok = wait_kv(0);
-      for (int x = 0; x < tiles && ok; ++x) {
-        ok = mbar_wait(E4M3 ? &q_ready[x] : &q_full[x], 0);
-        tc_fence_after();
-        if (ok && lane == 0) {
-          qk(x, 0);
-          mma_commit(&s_full[x]);
-        }
+      ok = mbar_wait(E4M3 ? &q_ready[x] : &q_full[x], 0) && wait_kv(0);
+      tc_fence_after();
+      if (ok && elect_one()) {
+        qk(0);
+        mma_commit(&s_full[x]);
+        release(0);
       }
-      if (ok && lane == 0) mma_commit(&kv_empty[0]);
-      c = 1;
+      __syncwarp();
+      int c = 1;  // tiles of the ring so far: K 0, V 0, K 1, V 1, ...
       for (int i = 0; i < nt && ok; ++i, c += 2) {
         const bool more = i + 1 < nt;
         const int sv = c % SLOTS, sk = (c + 1) % SLOTS;
         ok = wait_kv(c);
         if (!ok) break;
         if (!E4M3) {
-          // Rows of V that no row of the CTA sees: zeros.
+          // Rows of V that no row of the CTA sees: zeros (from both tiles' warps, each before its own MMAs).
           const int base = tile_of(w, i) * BN, end = base + BN - 1;
           if (end > w.p_hi || (base < w.wlo && end >= w.send)) {
             uint8_t* v = kv_s + sv * C::KV_TILE;
@@ -480,30 +495,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             __syncwarp();
           }
         }
-        for (int x = 0; x < tiles && ok; ++x) {
-          ok = mbar_wait(&p_full[x], i & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            pv(x, sv, i > 0);
-            if (x == tiles - 1) mma_commit(&kv_empty[sv]);
-            if (!more) mma_commit(&o_full[x]);
-          }
+        ok = mbar_wait(&p_full[x], i & 1) && (!more || wait_kv(c + 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          pv(sv, i > 0);
           if (more) {
-            if (x == 0) ok = wait_kv(c + 1);
-            if (!ok) break;
-            if (lane == 0) {
-              qk(x, sk);
-              mma_commit(&s_full[x]);
-              if (x == tiles - 1) mma_commit(&kv_empty[sk]);
-            }
+            qk(sk);
+            mma_commit(&s_full[x]);
+            release(sv);
+            release(sk);
+          } else {
+            mma_commit(&o_full[x]);
           }
         }
+        __syncwarp();
       }
       if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_MMA);
-      if (lane == 0) mma_commit(drain);  // every MMA issued must finish before tensor memory is freed
+      if (elect_one()) mma_commit(&drain[x]);  // every MMA issued must finish before tensor memory is freed
       __syncwarp();
-      mbar_wait(drain, 0);
+      mbar_wait(&drain[x], 0);
     } else if (warp == 9 && nt > 0) {
       // ------------------------------------------------------------ copies
       constexpr int BOX_D = E4M3 ? D : 64;                 // dims per box
