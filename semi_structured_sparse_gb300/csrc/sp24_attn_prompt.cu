@@ -5,9 +5,9 @@
 //   S = Q K^T,  P = exp2(c S - m),  O = P V / sum(P),  c = scale log2(e)
 //   (times the cache's scale), m a row maximum that follows the true one
 //
-// Bound by the tensor core (4 D operations per visible key and query row) and,
-// close behind, by the exponentials.  A CTA takes 256 query rows of one kv
-// head as two tiles of 128: the rows of a tile are (token, head of the group)
+// Bound by the tensor core (4 D operations per visible key and query row) with
+// heads of 128, and as much by the exponentials with heads of 64.  A block is
+// 256 query rows of one kv head, as two tiles of 128: the rows of a tile are (token, head of the group)
 // pairs, so a short prompt fills tiles too and all heads of a group share the
 // keys' copies.  Keys and values come in tiles of 128 tokens, one TMA box per
 // page and 64 dims, through a ring of shared memory.  Per key tile and query
@@ -22,6 +22,22 @@
 // overwrite P.  A row's O is rescaled only when its maximum has grown by more
 // than 2^8 (P then stays below 256, which bf16 and fp32 sums hold as well as
 // 1); that is rare after the first tiles, so the softmax warps do it themselves.
+//
+// One CTA per SM works through blocks: the first is its own, the others it
+// takes from the part of the grid that no SM has begun (cluster launch
+// control), so that copies of the next block's queries and keys, and its first
+// Q K^T, overlap the end of this one, and SMs that are done early take more.
+// Blocks that see many keys come first.  (With a launch per block, setting up
+// and draining took 16,000 cycles of a block's 92,000 at 8192 tokens.)
+//
+// Measured (GB300, one call after the other): 8192 tokens, 32/8 heads of 128,
+// 350 us, 1570 TFLOP/s of visible products (80 % of the measured bf16 rate);
+// 16001 tokens under a window of 4096 and 4 sinks, 28/4 heads of 64, 484 us,
+// 850 TFLOP/s; pieces of 1839 and 1629 tokens over 14000 in an e4m3 cache
+// 555 us, 1520 TFLOP/s.  A query tile's chain (S read 52 cycles, maximum 250,
+// exponentials 690, P written and seen 270, P V and Q K^T 1024 plus what the
+// other tile's MMAs take) is 2700 cycles per key tile, against 2048 of MMAs
+// for both tiles: tensor memory has no room for a second S.
 //
 // Places of a key tile that no row of the CTA sees are not loaded by whole
 // pages, and zeroed in V otherwise: 0 x NaN is not 0.  In S they are
@@ -66,16 +82,20 @@ struct Cfg {
   static constexpr int RAW_TILE = BN * D;                 // e4m3 codes
   static constexpr int RAW = E4M3 ? (D == 128 ? 2 : 4) : 0;
   static constexpr int SLOTS = D == 128 ? (E4M3 ? 4 : 5) : 8;
-  static constexpr int BARS = 2 + 2 + 2 + 2 + 2 + 2 + 2 * SLOTS + 2 * RAW;
+  static constexpr int BARS = 21 + 2 * SLOTS + 2 * RAW;
   static constexpr int SMEM = 1024 + 2 * Q_TILE + SLOTS * KV_TILE + RAW * RAW_TILE + BARS * 8;
   // Registers after the split: the warpgroups' shares stay within the launch's
   // (168 x 384 or 128 x 512).
-  static constexpr int REG_SOFTMAX = E4M3 ? 192 : 208;
-  static constexpr int REG_ISSUE = E4M3 ? 56 : 80;
-  static constexpr int REG_CONVERT = 72;
+  static constexpr int REG_SOFTMAX = E4M3 ? 208 : 216;
+  static constexpr int REG_ISSUE = E4M3 ? 48 : 64;
+  static constexpr int REG_CONVERT = 48;
+  // Whether P V begins when half of P is there.  It shortens the chain S -> P -> O -> next S of a query tile (8192
+  // tokens: 350 us against 354; with a window, heads of 64: 484 against 496), but not beside the e4m3 conversion
+  // (576 us against 555).
+  static constexpr bool EARLY = !E4M3;
 };
-static_assert(2 * 128 * 208 + 128 * 80 <= 168 * 384, "register split, bf16");
-static_assert(2 * 128 * 192 + 128 * 56 + 128 * 72 <= 128 * 512, "register split, e4m3");
+static_assert(2 * 128 * 216 + 128 * 64 <= 168 * 384, "register split, bf16");
+static_assert(2 * 128 * 208 + 128 * 48 + 128 * 48 <= 128 * 512, "register split, e4m3");
 
 // One lane of the warp, the same every time.
 __device__ __forceinline__ bool elect_one() {
@@ -94,6 +114,11 @@ __device__ __forceinline__ void setmaxnreg_dec() {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
@@ -118,14 +143,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -152,9 +175,35 @@ __host__ __device__ constexpr uint32_t idesc_16(int M, int N, uint32_t type, boo
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The next block of the grid that no SM has begun, if any, to this CTA: its
+// index arrives in `response` (16 bytes of shared memory) and completes 16
+// bytes on `bar`.
+__device__ __forceinline__ void steal_block(void* response, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(response)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// Its index along x, or -1.
+__device__ __forceinline__ int stolen_block(const void* response) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  return ok ? static_cast<int>(x) : -1;
+}
+
 // What a CTA works on.
 struct Work {
   int b;             // sequence, or -1: nothing
+  int hk;            // kv head
   int row0, rows;    // its first query row (in q), and how many tokens from there on are the sequence's
   int p0;            // position of that row's token
   int p_hi;          // the last position (the last visible key) of the CTA's rows
@@ -164,6 +213,59 @@ struct Work {
 
 __device__ __forceinline__ int tile_of(const Work& w, int i) { return i < w.nst ? i : w.first + i - w.nst; }
 
+// Block `block` of the grid, as the warp sees it; `total`: blocks of 2
+// tile_tokens tokens in all sequences.  The last block of the last sequence
+// comes first, since late blocks of a prompt see the most keys; all kv heads of
+// a block come together.
+__device__ __forceinline__ void find_work(const PromptParams& p, int block, int total, int lane, Work* out) {
+  const int tok = 2 * p.tile_tokens;
+  const int want = block < 0 ? -1 : total - 1 - block / p.kv_heads;
+  if (lane == 0) out->b = -1;
+  __syncwarp();
+  int seen = 0;
+  for (int b0 = 0; want >= 0 && b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int lo = 0, hi = 0, n = 0;
+    if (b < p.B) {
+      lo = min(max(__ldg(p.cu_q + b), 0), p.T);
+      hi = min(max(__ldg(p.cu_q + b + 1), lo), p.T);
+      n = __ldg(p.seq_lens + b);
+    }
+    const int own = (hi - lo + tok - 1) / tok;
+    int incl = own;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+      if (lane >= m) incl += x;
+    }
+    incl += seen;
+    if (want < incl && want >= incl - own) {
+      Work w;
+      w.b = b;
+      w.hk = block % p.kv_heads;
+      const int i0 = (want - (incl - own)) * tok, m = hi - lo;
+      const int most = p.table_width << p.cache.page_shift;
+      if (n < 0 || n > most) {
+        atomicOr(p.err, DEVERR_INDEX);
+        n = n < 0 ? 0 : most;
+      }
+      w.row0 = lo + i0;
+      w.rows = m - i0;
+      w.p0 = n - m + i0;
+      w.p_hi = w.p0 + min(tok, w.rows) - 1;
+      w.wlo = p.window > 0 ? max(0, w.p0 - p.window + 1) : 0;
+      w.send = min(p.sinks, w.wlo);
+      w.first = w.wlo / BN;
+      w.nst = min((w.send + BN - 1) / BN, w.first);
+      w.nt = w.p_hi < 0 ? 0 : w.nst + w.p_hi / BN + 1 - w.first;
+      *out = w;
+    }
+    seen = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    if (want < seen) break;
+  }
+  __syncwarp();
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     attention_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -171,7 +273,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   constexpr int D = C::D, SLOTS = C::SLOTS, RAW = C::RAW;
   constexpr bool E4M3 = C::E4M3;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Work s_work;
+  __shared__ Work s_work[2];
+  __shared__ __align__(16) uint4 s_response;
   __shared__ uint32_t s_tmem;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -181,133 +284,90 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(raw_s + RAW * C::RAW_TILE);
   uint64_t* q_full = bars;            // [2] the query tile has landed
   uint64_t* q_ready = bars + 2;       // [2] ... and is f16 (e4m3 caches)
-  uint64_t* s_full = bars + 4;        // [2] S of the next key tile is there, and P V of the last one done
-  uint64_t* p_full = bars + 6;        // [2] P is there, and O at its scale
-  uint64_t* o_full = bars + 8;        // [2] O is complete
-  uint64_t* drain = bars + 10;        // [2]
-  uint64_t* kv_full = bars + 12;      // [SLOTS]
+  uint64_t* q_empty = bars + 4;       // [2] its last Q K^T is done
+  uint64_t* s_full = bars + 6;        // [2] S of the next key tile is there, and P V of the last one done
+  uint64_t* p_half = bars + 8;        // [2] P of the first 64 keys is there, and O at its scale
+  uint64_t* p_full = bars + 10;       // [2] P is there
+  uint64_t* o_full = bars + 12;       // [2] O is complete
+  uint64_t* drain = bars + 14;        // [2]
+  uint64_t* work_full = bars + 16;    // [2]
+  uint64_t* work_empty = bars + 18;   // [2]
+  uint64_t* stolen = bars + 20;
+  uint64_t* kv_full = bars + 21;      // [SLOTS]
   uint64_t* kv_empty = kv_full + SLOTS;
   uint64_t* raw_full = kv_empty + SLOTS;  // [RAW]
   uint64_t* raw_empty = raw_full + RAW;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be uniform
-  const int hk = blockIdx.x % p.kv_heads;
 
   if (warp == 8) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
-    if (lane == 0) {
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(&q_full[x], 1);
-        mbar_init(&q_ready[x], 4);
-        mbar_init(&s_full[x], 1);
-        mbar_init(&p_full[x], 4);
-        mbar_init(&o_full[x], 1);
-        mbar_init(&drain[x], 1);
-      }
-      for (int i = 0; i < SLOTS; ++i) {
-        mbar_init(&kv_full[i], E4M3 ? 4 : 1);
-        mbar_init(&kv_empty[i], 2);
-      }
-      for (int i = 0; i < RAW; ++i) {
-        mbar_init(&raw_full[i], 1);
-        mbar_init(&raw_empty[i], 4);
-      }
-      fence_mbar_init();
+  } else if (warp == 10 && lane == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_ready[x], 4);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_half[x], 4);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&drain[x], 1);
+      mbar_init(&work_full[x], 1);
+      mbar_init(&work_empty[x], E4M3 ? 15 : 11);  // the warps that read the work
     }
+    mbar_init(stolen, 1);
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&kv_full[i], E4M3 ? 4 : 1);
+      mbar_init(&kv_empty[i], 2);
+    }
+    for (int i = 0; i < RAW; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    fence_mbar_init();
   } else if (warp == 9 && lane == 0) {
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
   pdl_wait();
-
-  if (warp == 0) {
-    // Blocks of 2 tile_tokens tokens, sequence by sequence; the last block of
-    // the last sequence is the first to start, since late blocks of a prompt
-    // see the most keys.
-    const int tok = 2 * p.tile_tokens;
-    auto bounds = [&](int b, int& lo, int& hi) {
-      const int a = __ldg(p.cu_q + b), z = __ldg(p.cu_q + b + 1);
-      lo = min(max(a, 0), p.T), hi = min(max(z, lo), p.T);
-      return lo != a || hi != z;
-    };
-    int total = 0;
-    bool bad = false;
-    for (int b = lane; b < p.B; b += 32) {
-      int lo, hi;
-      bad |= bounds(b, lo, hi);
-      total += (hi - lo + tok - 1) / tok;
-    }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
-    if (bad && blockIdx.x == 0) atomicOr(p.err, DEVERR_INDEX);
-    const int want = total - 1 - static_cast<int>(blockIdx.x / p.kv_heads);
-    if (lane == 0) s_work.b = -1;
-    __syncwarp();
-    int seen = 0;
-    for (int b0 = 0; want >= 0 && b0 < p.B; b0 += 32) {
-      const int b = b0 + lane;
-      int lo = 0, hi = 0;
-      if (b < p.B) bounds(b, lo, hi);
-      const int own = (hi - lo + tok - 1) / tok;
-      int incl = own;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-        if (lane >= m) incl += x;
-      }
-      incl += seen;
-      if (want < incl && want >= incl - own) {
-        Work w;
-        w.b = b;
-        const int i0 = (want - (incl - own)) * tok, m = hi - lo;
-        const int most = p.table_width << p.cache.page_shift;
-        int n = __ldg(p.seq_lens + b);
-        if (n < 0 || n > most) {
-          atomicOr(p.err, DEVERR_INDEX);
-          n = n < 0 ? 0 : most;
-        }
-        w.row0 = lo + i0;
-        w.rows = m - i0;
-        w.p0 = n - m + i0;
-        w.p_hi = w.p0 + min(tok, w.rows) - 1;
-        w.wlo = p.window > 0 ? max(0, w.p0 - p.window + 1) : 0;
-        w.send = min(p.sinks, w.wlo);
-        w.first = w.wlo / BN;
-        w.nst = min((w.send + BN - 1) / BN, w.first);
-        w.nt = w.p_hi < 0 ? 0 : w.nst + w.p_hi / BN + 1 - w.first;
-        s_work = w;
-      }
-      seen = __shfl_sync(0xFFFFFFFFu, incl, 31);
-      if (want < seen) break;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Work w = s_work;
   const uint32_t tmem = s_tmem;
-  const int tiles = w.b < 0 ? 0 : w.rows > p.tile_tokens ? 2 : 1;  // query tiles with a token of the sequence
-  const int nt = w.b < 0 ? 0 : w.nt;
+  // The work of this CTA's next block, for every role but the one that finds
+  // it; done_with says that this warp will not read it again.
+  auto wait_work = [&](int item) { return mbar_wait(&work_full[item & 1], (item >> 1) & 1); };
+  auto done_with = [&](int item) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&work_empty[item & 1]);
+  };
+  auto tiles_of = [&](const Work& w) { return w.rows > p.tile_tokens ? 2 : 1; };
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
     setmaxnreg_inc<C::REG_SOFTMAX>();
     const int x = warp >> 2, r = tid & 127;
-    const int token = r / p.group, head = r - token * p.group;
-    const int at = x * p.tile_tokens + token;            // token within the CTA's rows
-    const bool mine = token < p.tile_tokens && at < w.rows && x < tiles;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + x * BN, to = tmem + lanes + 2 * BN + x * D;
-    float l = 0.0f;
+    uint32_t sn = 0, on = 0;  // key tiles and blocks so far, for the barriers' parities
     bool ok = true;
-    if (x < tiles && nt > 0) {
-      float c = p.scale * 1.4426950408889634f;
-      if (E4M3) {
-        ok = mbar_wait(&q_full[x], 0);
-        if (ok) {
+    for (int item = 0; ok; ++item) {
+      ok = wait_work(item);
+      const Work& w = s_work[item & 1];
+      if (!ok || w.b < 0) break;
+      if (x >= tiles_of(w)) {
+        done_with(item);
+        continue;
+      }
+      float l = 0.0f;
+      if (w.nt > 0) {
+        float c = p.scale * 1.4426950408889634f;
+        if (E4M3) {
+          ok = mbar_wait(&q_full[x], on & 1);
+          if (!ok) break;
           // this row to f16, scaled by a power of two to at most 2
           uint8_t* q = q_s + x * C::Q_TILE + r * 128;
           float top = 0.0f;
@@ -322,7 +382,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           uint32_t e = __float_as_uint(top) >> 23;  // as in the decode kernel
           e = e == 255 ? 127u : min(max(e, 64u), 253u);
           const float down = __uint_as_float((254u - e) << 23);
-          c *= p.cache.k_scale[hk] * __uint_as_float(e << 23);
+          c *= p.cache.k_scale[w.hk] * __uint_as_float(e << 23);
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
             uint4* at16 = reinterpret_cast<uint4*>(q + (i / 8) * (BM * 128) + (((i & 7) ^ (r & 7)) << 4));
@@ -337,109 +397,151 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_ready[x]);
         }
-      }
-      const int pos = mine ? w.p0 + at : -1;
-      const int p_min = w.p0 + x * p.tile_tokens, p_max = min(w.p_hi, p_min + p.tile_tokens - 1);
-      float m = -INFINITY;
-      for (int i = 0; i < nt && ok; ++i) {
-        ok = mbar_wait(&s_full[x], i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t su[BN];
+        // What the loop needs of the block, in registers: shared memory is busy with the MMAs' operands, and a read
+        // would take some hundred cycles.
+        const int nt = w.nt, nst = w.nst, first = w.first * BN;
+        const int p_min = w.p0 + x * p.tile_tokens, p_max = min(w.p_hi, p_min + p.tile_tokens - 1);
+        int base = nst > 0 ? 0 : first;
+        float m = -INFINITY;
+        for (int i = 0; i < nt; ++i, ++sn, base = i == nst ? first : base + BN) {
+          ok = mbar_wait(&s_full[x], sn & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const int end = base + BN - 1;
+          // Columns that this row does not see: past its own position, or before its window and after the sinks.
+          const bool cut_hi = end > p_min, cut_lo = p.window > 0 && base <= p_max - p.window && end >= p.sinks;
+          uint32_t su[BN];
 #pragma unroll
-        for (int j = 0; j < BN / 32; ++j) tmem_ld32(ts + 32 * j, su + 32 * j);
-        tmem_ld_wait();
-        float* s = reinterpret_cast<float*>(su);
-        const int base = tile_of(w, i) * BN, end = base + BN - 1;
-        const bool whole = end <= p_min && (p.window == 0 || base > p_max - p.window || end < p.sinks);
-        if (!whole) {
-          const int hi = pos - base, lo = p.window > 0 ? hi - p.window : -1, sk = p.sinks - base;
+          for (int j = 0; j < BN / 32; ++j) tmem_ld32(ts + 32 * j, su + 32 * j);
+          tmem_ld_wait();
+          float* s = reinterpret_cast<float*>(su);
+          if (cut_hi || cut_lo) {
+            // (The position is worked out here, once or twice per block, to leave the registers to S.)
+            int rr = r;
+            asm volatile("" : "+r"(rr));  // here, not ahead of the loop
+            const int token = rr / p.group;
+            const int hi = token < p.tile_tokens ? p_min + token - base : -1, lo = hi - p.window, sk = p.sinks - base;
+            if (cut_lo) {
 #pragma unroll
-          for (int j = 0; j < BN; ++j)
-            if (!(j <= hi && (j > lo || j < sk))) s[j] = -INFINITY;
-        }
-        float top[4];
+              for (int j = 0; j < BN; ++j)
+                if (!(j > lo || j < sk)) s[j] = -INFINITY;
+            }
+            if (cut_hi) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top[j] = s[j];
-#pragma unroll
-        for (int j = 4; j < BN; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
-        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-        const bool grow = now > m + 8.0f;  // also from -inf
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float to_m = grow ? now : m;
-          const float keep = m == to_m ? 1.0f : ex2(m - to_m);
-          m = to_m;
-          l *= keep;
-          if (i > 0) {
-#pragma unroll 1
-            for (int j = 0; j < D; j += 32) {
-              uint32_t o[32];
-              tmem_ld32(to + j, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-              tmem_st32(to + j, o);
+              for (int j = 0; j < BN; ++j)
+                if (j > hi) s[j] = -INFINITY;
             }
           }
-        }
-        const float use = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          float top[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
+          for (int j = 0; j < 4; ++j) top[j] = max3(s[3 * j], s[3 * j + 1], s[3 * j + 2]);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float a = ex2(fmaf(s[64 * h + 2 * j], c, -use)), b = ex2(fmaf(s[64 * h + 2 * j + 1], c, -use));
-            sum[2 * (j & 1)] += a;
-            sum[2 * (j & 1) + 1] += b;
-            pk[j] = E4M3 ? f16x2_rn(a, b) : bf16x2_rn(a, b);
+          for (int j = 12; j < BN; j += 2) top[(j >> 1) & 3] = max3(top[(j >> 1) & 3], s[j], s[j + 1]);
+          const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+          const bool grow = now > m + 8.0f;  // also from -inf
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            const float to_m = grow ? now : m;
+            const float keep = m == to_m ? 1.0f : ex2(m - to_m);
+            m = to_m;
+            l *= keep;
+            if (i > 0) {
+#pragma unroll 1
+              for (int j = 0; j < D; j += 16) {  // 16 columns at a time: S takes 128 registers
+                uint32_t o[16];
+                tmem_ld16(to + j, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                tmem_st16(to + j, o);
+              }
+            }
           }
-          tmem_st32(ts + 32 * h, pk);
+          const float less = m == -INFINITY ? 0.0f : -m;
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int h = 0; h < BN / 32; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float2 e = __ffma2_rn(make_float2(s[32 * h + 2 * j], s[32 * h + 2 * j + 1]), make_float2(c, c),
+                                    make_float2(less, less));
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+              pk[j] = E4M3 ? f16x2_rn(e.x, e.y) : bf16x2_rn(e.x, e.y);
+            }
+            tmem_st16(ts + 16 * h, pk);
+            if (C::EARLY && h == 1) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_half[x]);
+            }
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (ok) ok = mbar_wait(&o_full[x], on & 1);
+        if (!ok) break;
+        ++on;
+        tc_fence_after();
       }
-      if (ok) ok = mbar_wait(&o_full[x], 0);
-      if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
-      tc_fence_after();
-    }
-    if (x < tiles && ok) {
-      const float f = l == 0.0f ? 0.0f : (E4M3 ? p.cache.v_scale[hk] : 1.0f) / l;
-      __nv_bfloat16* y = p.y + static_cast<int64_t>(w.row0 + at) * p.ldy + static_cast<int64_t>(hk * p.group + head) * D;
+      // O / l to bf16, 32 dims at a time: a lane's 64 bytes of its row change places with those of its three neighbours,
+      // so that four lanes write 64 bytes of one row together.
+      const float f = l == 0.0f ? 0.0f : (E4M3 ? p.cache.v_scale[w.hk] : 1.0f) / l;
+      __nv_bfloat16* rows[4];
+      int rr = r;
+      asm volatile("" : "+r"(rr));  // worked out here, not ahead of the loop: S takes the registers there
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rk = (rr & ~3) + k, tk = rk / p.group, ak = x * p.tile_tokens + tk;
+        rows[k] = tk < p.tile_tokens && ak < w.rows
+                      ? p.y + static_cast<int64_t>(w.row0 + ak) * p.ldy +
+                            static_cast<int64_t>(w.hk * p.group + rk - tk * p.group) * D + (lane & 3) * 8
+                      : nullptr;
+      }
 #pragma unroll 1
       for (int j = 0; j < D; j += 32) {
         uint32_t o[32];
-        if (nt > 0) {
+        if (w.nt > 0) {
           tmem_ld32(to + j, o);
           tmem_ld_wait();
         }
-        if (mine) {
+        uint32_t v[4][4];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (nt > 0 && f != 0.0f) {
-              uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+        for (int k = 0; k < 16; ++k)
+          v[k >> 2][k & 3] = f == 0.0f ? 0u : bf16x2_rn(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                u[e] = bf16x2_rn(__uint_as_float(o[k + 2 * e]) * f, __uint_as_float(o[k + 2 * e + 1]) * f);
+        for (int bit = 1; bit < 4; bit <<= 1)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k & bit) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool upper = lane & bit;
+              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? v[k][e] : v[k | bit][e], bit);
+              (upper ? v[k][e] : v[k | bit][e]) = got;
             }
-            *reinterpret_cast<uint4*>(y + j + k) = v;
           }
-        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (rows[k]) *reinterpret_cast<uint4*>(rows[k] + j) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
       }
+      tc_fence_before();  // O is read before this warp lets the next block's P V begin
+      done_with(item);
     }
+    if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
   } else if (warp < 12) {
     setmaxnreg_dec<C::REG_ISSUE>();
-    if ((warp == 8 || warp == 10) && (warp - 8) / 2 < tiles && nt > 0) {
+    if (warp == 8 || warp == 10) {
       // ------------------------------------------------------------ MMA
       // Each query tile has a warp of its own: a commit holds its thread back
       // until the MMAs that it tracks are done, and the other tile's MMAs fill
       // that time.
       const int x = (warp - 8) / 2;
-      bool ok = true;
       const uint32_t id_qk = idesc_16(BM, BN, E4M3 ? 0 : 1, false), id_pv = idesc_16(BM, D, E4M3 ? 0 : 1, true);
       const uint64_t q_d = smem_desc(smem_u32(q_s) + x * C::Q_TILE, 16, 1024, SWZ_128B);
       const uint64_t k_d = smem_desc(smem_u32(kv_s), 16, 1024, SWZ_128B);
@@ -453,105 +555,179 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           mma_bf16(t_s, q_d + off, kd + off, id_qk, k > 0);
         }
       };
-      auto pv = [&](int slot, bool add) {
+      auto pv = [&](int slot, int half, bool add) {
         const uint64_t vd = v_d + slot * (C::KV_TILE >> 4);
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k) mma_f16_ts(t_o, t_s + 8 * k, vd + k * (2048 >> 4), id_pv, add || k > 0);
-      };
-      // A slot is free when both tiles' MMAs have read it (a lone tile says so twice).
-      auto release = [&](int slot) {
-        mma_commit(&kv_empty[slot]);
-        if (tiles == 1) mma_commit(&kv_empty[slot]);
-      };
-      auto wait_kv = [&](int n) { return mbar_wait(&kv_full[n % SLOTS], (n / SLOTS) & 1); };
-      ok = mbar_wait(E4M3 ? &q_ready[x] : &q_full[x], 0) && wait_kv(0);
-      tc_fence_after();
-      if (ok && elect_one()) {
-        qk(0);
-        mma_commit(&s_full[x]);
-        release(0);
-      }
-      __syncwarp();
-      int c = 1;  // tiles of the ring so far: K 0, V 0, K 1, V 1, ...
-      for (int i = 0; i < nt && ok; ++i, c += 2) {
-        const bool more = i + 1 < nt;
-        const int sv = c % SLOTS, sk = (c + 1) % SLOTS;
-        ok = wait_kv(c);
-        if (!ok) break;
-        if (!E4M3) {
-          // Rows of V that no row of the CTA sees: zeros (from both tiles' warps, each before its own MMAs).
-          const int base = tile_of(w, i) * BN, end = base + BN - 1;
-          if (end > w.p_hi || (base < w.wlo && end >= w.send)) {
-            uint8_t* v = kv_s + sv * C::KV_TILE;
-            for (int r = 0; r < BN; ++r) {
-              const int j = base + r;
-              if (j > w.p_hi || (j < w.wlo && j >= w.send)) {
-                if (lane < D / 8)
-                  *reinterpret_cast<uint4*>(v + (lane / 8) * (BN * 128) + r * 128 + (lane & 7) * 16) =
-                      make_uint4(0, 0, 0, 0);
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+        for (int j = 0; j < BN / 32; ++j) {
+          const int k = half * (BN / 32) + j;
+          mma_f16_ts(t_o, t_s + 8 * k, vd + k * (2048 >> 4), id_pv, add || j > 0);
         }
-        ok = mbar_wait(&p_full[x], i & 1) && (!more || wait_kv(c + 1));
-        if (!ok) break;
+      };
+      bool ok = true;
+      int ring = 0;               // tiles of the ring so far: K, V, K, V, ...
+      uint32_t pn = 0, qn = 0;    // key tiles and blocks so far
+      auto wait_kv = [&](int n) { return mbar_wait(&kv_full[n % SLOTS], (n / SLOTS) & 1); };
+      for (int item = 0; ok; ++item) {
+        ok = wait_work(item);
+        const Work w = s_work[item & 1];
+        if (!ok || w.b < 0) break;
+        const int tiles = tiles_of(w), nt = w.nt;
+        if (nt == 0 || x >= tiles) {
+          ring += 2 * nt;
+          done_with(item);
+          continue;
+        }
+        // A slot is free when both tiles' MMAs have read it (a lone tile says so twice).
+        auto release = [&](int n) {
+          mma_commit(&kv_empty[n % SLOTS]);
+          if (tiles == 1) mma_commit(&kv_empty[n % SLOTS]);
+        };
+        ok = mbar_wait(E4M3 ? &q_ready[x] : &q_full[x], qn & 1) && wait_kv(ring);
+        ++qn;
         tc_fence_after();
-        if (elect_one()) {
-          pv(sv, i > 0);
-          if (more) {
-            qk(sk);
-            mma_commit(&s_full[x]);
-            release(sv);
-            release(sk);
-          } else {
-            mma_commit(&o_full[x]);
-          }
+        if (ok && elect_one()) {
+          qk(ring % SLOTS);
+          mma_commit(&s_full[x]);
+          release(ring);
+          if (nt == 1) mma_commit(&q_empty[x]);
         }
         __syncwarp();
+        for (int i = 0; i < nt && ok; ++i, ++pn) {
+          const bool more = i + 1 < nt;
+          const int vn = ring + 1, kn = ring + 2;
+          ring += 2;
+          ok = wait_kv(vn);
+          if (!ok) break;
+          if (!E4M3) {
+            // Rows of V that no row of the CTA sees: zeros (from both tiles' warps, each before its own MMAs).
+            const int base = tile_of(w, i) * BN;
+            auto clear = [&](int lo, int hi) {
+              uint8_t* v = kv_s + (vn % SLOTS) * C::KV_TILE;
+              for (int j = lo * (D / 8) + lane; j < hi * (D / 8); j += 32) {
+                const int r = j / (D / 8), ch = j % (D / 8);
+                *reinterpret_cast<uint4*>(v + (ch / 8) * (BN * 128) + r * 128 + (ch & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+            };
+            if (base + BN - 1 > w.p_hi || (base < w.wlo && base + BN > w.send)) {
+              clear(max(0, w.send - base), min(BN, w.wlo - base));
+              clear(max(0, w.p_hi + 1 - base), BN);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          if (C::EARLY) {
+            ok = mbar_wait(&p_half[x], pn & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) pv(vn % SLOTS, 0, i > 0);
+            __syncwarp();
+          }
+          ok = (!more || wait_kv(kn)) && mbar_wait(&p_full[x], pn & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (!C::EARLY) pv(vn % SLOTS, 0, i > 0);
+            pv(vn % SLOTS, 1, true);
+            if (more) {
+              qk(kn % SLOTS);
+              mma_commit(&s_full[x]);
+              release(vn);
+              release(kn);
+              if (i + 2 == nt) mma_commit(&q_empty[x]);
+            } else {
+              mma_commit(&o_full[x]);
+              release(vn);
+            }
+          }
+          __syncwarp();
+        }
+        done_with(item);
       }
       if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_MMA);
       if (elect_one()) mma_commit(&drain[x]);  // every MMA issued must finish before tensor memory is freed
       __syncwarp();
       mbar_wait(&drain[x], 0);
-    } else if (warp == 9 && nt > 0) {
+    } else {
       // ------------------------------------------------------------ copies
+      // Warp 9 finds the CTA's work and copies K; warp 11 copies Q and V.
+      const bool keys = warp == 9;
       constexpr int BOX_D = E4M3 ? D : 64;                 // dims per box
       constexpr int BOX_STRIDE = BN * 128;                 // between a tile's halves
       constexpr int RING = E4M3 ? RAW : SLOTS;
       uint64_t* full = E4M3 ? raw_full : kv_full;
       uint64_t* empty = E4M3 ? raw_empty : kv_empty;
-      bool ok = true;
-      if (lane == 0) {
-        for (int x = 0; x < tiles; ++x) {
-          mbar_arrive_expect_tx(&q_full[x], p.tile_tokens * p.group * D * 2);
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(q_s + x * C::Q_TILE + h * (BM * 128), &qmap, &q_full[x], 64 * h, hk * p.group,
-                        w.row0 + x * p.tile_tokens);
-        }
-      }
       const int page_size = 1 << p.cache.page_shift, pages = BN >> p.cache.page_shift;
-      const int32_t* table = p.page_table + int64_t(w.b) * p.ld_table;
-      int c = 0;
-      for (int i = 0; i < nt && ok; ++i) {
-        // lane j < pages: page j of the tile, if some row sees a token of it
-        const int base = tile_of(w, i) * BN;
-        const int a = base + lane * page_size, z = a + page_size - 1;
-        const bool need = lane < pages && a <= w.p_hi && (z >= w.wlo || a < w.send);
-        int page = 0;
-        if (need) {
-          page = __ldg(table + (a >> p.cache.page_shift));
-          if (page < 0 || page >= p.cache.num_pages) {
-            atomicOr(p.err, DEVERR_INDEX);
-            page = 0;
+      bool ok = true, asked = false;
+      int ring = 0, last = -1, block = blockIdx.x, total = 0;
+      uint32_t qn[2] = {0, 0};
+      if (keys) {
+        bool bad = false;
+        for (int b = lane; b < p.B; b += 32) {
+          const int a = __ldg(p.cu_q + b), z = __ldg(p.cu_q + b + 1);
+          const int lo = min(max(a, 0), p.T), hi = min(max(z, lo), p.T);
+          bad |= lo != a || hi != z;
+          total += (hi - lo + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+        }
+        if (bad && blockIdx.x == 0) atomicOr(p.err, DEVERR_INDEX);
+#pragma unroll
+        for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
+      }
+      int item = 0;
+      for (; ok; ++item) {
+        Work w;
+        if (keys) {
+          if (item >= 2) ok = mbar_wait(&work_empty[item & 1], ((item >> 1) - 1) & 1);
+          if (!ok) break;
+          find_work(p, block, total, lane, &s_work[item & 1]);
+          w = s_work[item & 1];
+          if (lane == 0) mbar_arrive(&work_full[item & 1]);
+          if (w.b < 0) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(stolen, 16);
+            steal_block(&s_response, stolen);
+          }
+          asked = true;
+        } else {
+          ok = wait_work(item);
+          if (!ok) break;
+          w = s_work[item & 1];
+          done_with(item);
+          if (w.b < 0) break;
+          if (w.nt > 0) {
+            for (int x = 0; x < tiles_of(w) && ok; ++x) {
+              if (qn[x] > 0) ok = mbar_wait(&q_empty[x], (qn[x] - 1) & 1);
+              if (!ok) break;
+              ++qn[x];
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full[x], p.tile_tokens * p.group * D * 2);
+                for (int h = 0; h < D / 64; ++h)
+                  tma_load_3d(q_s + x * C::Q_TILE + h * (BM * 128), &qmap, &q_full[x], 64 * h, w.hk * p.group,
+                              w.row0 + x * p.tile_tokens);
+              }
+              __syncwarp();
+            }
           }
         }
-        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, need));
-        for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
-          const int slot = c % RING;
+        const int32_t* table = p.page_table + int64_t(w.b) * p.ld_table;
+        const CUtensorMap* map = keys ? &kmap : &vmap;
+        for (int i = 0; i < w.nt && ok; ++i) {
+          // lane j < pages: page j of the tile, if some row sees a token of it
+          const int a = tile_of(w, i) * BN + lane * page_size, z = a + page_size - 1;
+          const bool need = lane < pages && a <= w.p_hi && (z >= w.wlo || a < w.send);
+          int page = 0;
+          if (need) {
+            page = __ldg(table + (a >> p.cache.page_shift));
+            if (page < 0 || page >= p.cache.num_pages) {
+              atomicOr(p.err, DEVERR_INDEX);
+              page = 0;
+            }
+          }
+          const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, need));
+          const int c = ring + 2 * i + (keys ? 0 : 1), slot = c % RING;
           if (c >= RING) ok = mbar_wait(&empty[slot], (c / RING - 1) & 1);
           if (!ok) break;
+          last = c;
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * page_size * D * (E4M3 ? 1 : 2));
           __syncwarp();
           if (need) {
@@ -559,48 +735,70 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                            lane * page_size * (E4M3 ? D : 128);
 #pragma unroll
             for (int h = 0; h < D / BOX_D; ++h)
-              tma_load_4d(dst + h * BOX_STRIDE, kv ? &vmap : &kmap, &full[slot], BOX_D * h, 0, hk, page);
+              tma_load_4d(dst + h * BOX_STRIDE, map, &full[slot], BOX_D * h, 0, w.hk, page);
           }
+          __syncwarp();
+        }
+        ring += 2 * w.nt;
+        if (keys && ok) {
+          ok = mbar_wait(stolen, item & 1);
+          if (!ok) break;
+          asked = false;
+          block = stolen_block(&s_response);
+          fence_proxy_async_smem();  // read before the next answer is written
+          __syncwarp();
         }
       }
       if (!ok) {
+        // What is in flight has to land before this CTA's shared memory goes.
         if (lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
-        for (int n = max(0, c - RING); n < c; ++n) mbar_wait(&full[n % RING], (n / RING) & 1);  // copies in flight
-        for (int x = 0; x < tiles; ++x) mbar_wait(&q_full[x], 0);
+        for (int c = last; c >= 0 && c > last - RING; c -= 2) mbar_wait(&full[c % RING], (c / RING) & 1);
+        if (!keys)
+          for (int x = 0; x < 2; ++x)
+            if (qn[x] > 0) mbar_wait(&q_full[x], (qn[x] - 1) & 1);
+        if (asked) mbar_wait(stolen, item & 1);
       }
     }
   } else if (E4M3) {
     // -------------------------------------------------------------- e4m3 -> f16
     setmaxnreg_dec<C::REG_CONVERT>();
+    constexpr int R = RAW ? RAW : 1;
     const int r = tid & 127;  // this thread's token of each tile
     bool ok = true;
-    for (int c = 0; c < 2 * nt && ok; ++c) {
-      const int from = c % (RAW ? RAW : 1), slot = c % SLOTS;
-      ok = mbar_wait(&raw_full[from], (c / (RAW ? RAW : 1)) & 1);
-      if (ok && c >= SLOTS) ok = mbar_wait(&kv_empty[slot], (c / SLOTS - 1) & 1);
-      if (!ok) break;
-      const int j = tile_of(w, c >> 1) * BN + r;
-      const bool seen = j <= w.p_hi && (j >= w.wlo || j < w.send);
-      const uint8_t* src = raw_s + from * C::RAW_TILE + r * D;
-      uint8_t* dst = kv_s + slot * C::KV_TILE + r * 128;
-      const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+    int ring = 0;
+    for (int item = 0; ok; ++item) {
+      ok = wait_work(item);
+      const Work w = s_work[item & 1];
+      if (!ok || w.b < 0) break;
+      for (int i = 0; i < 2 * w.nt && ok; ++i, ++ring) {
+        const int from = ring % R, slot = ring % SLOTS;
+        ok = mbar_wait(&raw_full[from], (ring / R) & 1);
+        if (ok && ring >= SLOTS) ok = mbar_wait(&kv_empty[slot], (ring / SLOTS - 1) & 1);
+        if (!ok) break;
+        const int j = tile_of(w, i >> 1) * BN + r;
+        const bool seen = j <= w.p_hi && (j >= w.wlo || j < w.send);
+        const uint8_t* src = raw_s + from * C::RAW_TILE + r * D;
+        uint8_t* dst = kv_s + slot * C::KV_TILE + r * 128;
+        const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint4 v = *reinterpret_cast<const uint4*>(src + ((i ^ sw) << 4));
-        if (!seen) v = make_uint4(0, 0, 0, 0);
-        uint8_t* to = dst + (i / 4) * (BN * 128);
-        const int c0 = (2 * i) & 7;
-        *reinterpret_cast<uint4*>(to + ((c0 ^ (r & 7)) << 4)) =
-            make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16));
-        *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (r & 7)) << 4)) =
-            make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16));
+        for (int i = 0; i < D / 16; ++i) {
+          uint4 v = *reinterpret_cast<const uint4*>(src + ((i ^ sw) << 4));
+          if (!seen) v = make_uint4(0, 0, 0, 0);
+          uint8_t* to = dst + (i / 4) * (BN * 128);
+          const int c0 = (2 * i) & 7;
+          *reinterpret_cast<uint4*>(to + ((c0 ^ (r & 7)) << 4)) =
+              make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16));
+          *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (r & 7)) << 4)) =
+              make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[from]);
+          mbar_arrive(&kv_full[slot]);
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&raw_empty[from]);
-        mbar_arrive(&kv_full[slot]);
-      }
+      done_with(item);
     }
     if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
   }
