@@ -489,39 +489,64 @@ class KVCache:
             raise ValueError("the cache's rows must not overlap, and start on 16-byte boundaries")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.heads, self.page_size, self.head_dim, self.device = heads, page_size, head_dim, k.device
+        self._index = k.get_device()
         self._struct = _KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
                                       v_scale.data_ptr() if e4m3 else None, pages, page, head, token, heads,
                                       page_size, head_dim, 1 if e4m3 else 0)
         self._address = ctypes.addressof(self._struct)
 
 
-def _rows_of(t, rows, cols, device, name):
+# The checks below run on every call of a decode step, where a call's time on the
+# host is several times its kernel's: they ask each tensor as few questions as
+# they can.
+def _refuse(t, dtype, device, name, what):
+    """The error for a tensor that one of the checks below did not take."""
+    _dev_tensor(t, dtype, name, device)
+    raise ValueError("%s must be %s, got %s with strides %s" % (name, what, tuple(t.shape), t.stride()))
+
+
+def _rows_of(t, rows, cols, cache, name):
     """A bf16 tensor of `rows` rows, [rows, cols] or [rows, heads, d] with contiguous
     rows: its row stride."""
-    _dev_tensor(t, torch.bfloat16, name, device)
-    shape = t.shape
-    if t.dim() == 3:
-        ok = shape[1] * shape[2] == cols and (shape[1] == 1 or t.stride(1) == shape[2])
-    else:
-        ok = t.dim() == 2 and shape[1] == cols
-    if not ok or shape[0] != rows:
-        raise ValueError("%s must be [%d, %d] or [%d, heads, head dim] with contiguous rows, got %s"
-                         % (name, rows, cols, rows, tuple(shape)))
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == cache._index:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 3:
+            ok = shape[1] * shape[2] == cols and stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
+        else:
+            ok = len(shape) == 2 and shape[1] == cols and stride[1] == 1
+        if ok and shape[0] == rows:
+            return stride[0] if rows > 1 else max(stride[0], cols)
+    _refuse(t, torch.bfloat16, cache.device, name, "[%d, %d] or [%d, heads, head dim] with contiguous rows"
+            % (rows, cols, rows))
 
 
-def _vector(t, dtype, n, device, name):
-    _dev_tensor(t, dtype, name, device)
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError("%s must be a vector of %d values, got %s" % (name, n, tuple(t.shape)))
-    return t.data_ptr()
+def _vector(t, dtype, n, cache, name):
+    """The address of a contiguous vector of n values."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == cache._index and t.shape == (n,) and \
+            t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, cache.device, name, "a contiguous vector of %d values" % n)
 
 
-def _on(stream, device):
-    """What allocates for a kernel on `stream`: memory of that stream's own pool."""
-    if stream is None or stream == torch.cuda.current_stream(device):
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream)
+# The current stream's handle without a Stream object around it, where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, cache):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(cache._index)
+    return torch.cuda.current_stream(cache.device).cuda_stream
+
+
+def _new(shape, dtype, stream, cache, zero=False):
+    """Memory for a kernel on `stream`, from that stream's own pool."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=cache.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=cache.device)
 
 
 def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_weight=None, k_weight=None,
@@ -536,29 +561,32 @@ def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_w
     (i, i + rot/2), or (2i, 2i + 1) if interleaved.  slots int64 [T]: page * page_size +
     place of each token, negative for one that is not stored.  Returns the queries bf16
     [T, heads, head dim] (in ``out`` if given)."""
-    lib = load()
-    dev_, d = cache.device, cache.head_dim
+    lib = _lib or load()
+    d = cache.head_dim
     T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else -1
-    slots_p = _vector(slots, torch.int64, T, dev_, "slots")
-    pos_p = _vector(positions, torch.int32, T, dev_, "positions")
-    ldqkv = _rows_of(qkv, T, (heads + 2 * cache.heads) * d, dev_, "qkv")
-    _dev_tensor(cos_sin, torch.float32, "cos_sin", dev_)
-    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous [max_pos, rot]")
+    slots_p = _vector(slots, torch.int64, T, cache, "slots")
+    pos_p = _vector(positions, torch.int32, T, cache, "positions")
+    ldqkv = _rows_of(qkv, T, (heads + 2 * cache.heads) * d, cache, "qkv")
+    if not (isinstance(cos_sin, torch.Tensor) and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and
+            cos_sin.get_device() == cache._index and cos_sin.is_contiguous()):
+        _refuse(cos_sin, torch.float32, cache.device, "cos_sin", "a contiguous [max_pos, rot]")
     max_pos, rot = cos_sin.shape
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     qw = kw = None
     if q_weight is not None:
-        qw, kw = _vector(q_weight, torch.bfloat16, d, dev_, "q_weight"), _vector(k_weight, torch.bfloat16, d, dev_,
-                                                                               "k_weight")
+        qw = _vector(q_weight, torch.bfloat16, d, cache, "q_weight")
+        kw = _vector(k_weight, torch.bfloat16, d, cache, "k_weight")
     if out is None:
-        with _on(stream, dev_):
-            out = torch.empty((T, heads, d), dtype=torch.bfloat16, device=dev_)
-    ldq = _rows_of(out, T, heads * d, dev_, "out")
-    _check(lib.sp24_qk_norm_rope(qkv.data_ptr(), T, ldqkv, heads, qw, kw, eps, cos_sin.data_ptr() if rot else None,
-                                 max_pos, rot, bool(interleaved), pos_p, slots_p, out.data_ptr(), ldq,
-                                 cache._address, _stream(stream)), "sp24_qk_norm_rope")
+        out = _new((T, heads, d), torch.bfloat16, stream, cache)
+        ldq = heads * d
+    else:
+        ldq = _rows_of(out, T, heads * d, cache, "out")
+    st = lib.sp24_qk_norm_rope(qkv.data_ptr(), T, ldqkv, heads, qw, kw, eps, cos_sin.data_ptr() if rot else None,
+                               max_pos, rot, bool(interleaved), pos_p, slots_p, out.data_ptr(), ldq, cache._address,
+                               _stream_of(stream, cache))
+    if st:
+        _check(st, "sp24_qk_norm_rope")
     return out
 
 
@@ -569,27 +597,28 @@ def attention_decode_workspace_size(cache: KVCache, heads: int) -> int:
 
 def _attention_args(q, cache, page_table, seq_lens, scale, out, stream):
     """The checks and arguments that both attention calls have in common."""
-    dev_, d = cache.device, cache.head_dim
-    if not isinstance(q, torch.Tensor) or q.dim() not in (2, 3):
-        raise ValueError("q must be [rows, heads, head dim] or [rows, heads * head dim]")
-    rows = q.shape[0]
-    cols = q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1]
-    if cols % d or (q.dim() == 3 and q.shape[2] != d):
-        raise ValueError("q must have heads of %d values, as the cache" % d)
-    ldq = _rows_of(q, rows, cols, dev_, "q")
-    _dev_tensor(page_table, torch.int32, "page_table", dev_)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [sequences, pages]")
+    d = cache.head_dim
+    shape = q.shape if isinstance(q, torch.Tensor) else ()
+    if len(shape) == 3 and shape[2] == d:
+        cols = shape[1] * d
+    elif len(shape) == 2 and shape[1] % d == 0:
+        cols = shape[1]
+    else:
+        raise ValueError("q must be [rows, heads, %d] or [rows, heads * %d], got %s" % (d, d, tuple(shape)))
+    rows = shape[0]
+    ldq = _rows_of(q, rows, cols, cache, "q")
+    if not (isinstance(page_table, torch.Tensor) and page_table.dtype is torch.int32 and page_table.dim() == 2 and
+            page_table.get_device() == cache._index and page_table.stride(1) == 1):
+        _refuse(page_table, torch.int32, cache.device, "page_table", "[sequences, pages]")
     B, width = page_table.shape
-    lens_p = _vector(seq_lens, torch.int32, B, dev_, "seq_lens")
+    lens_p = _vector(seq_lens, torch.int32, B, cache, "seq_lens")
     if out is None:
-        with _on(stream, dev_):
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev_)
-    ldy = _rows_of(out, rows, cols, dev_, "out")
-    if scale is None:
-        scale = d ** -0.5
-    ld_table = page_table.stride(0) if B > 1 else max(page_table.stride(0), width)
-    return rows, ldq, cols // d, B, width, ld_table, lens_p, scale, out, ldy
+        out = _new(shape, torch.bfloat16, stream, cache)
+        ldy = cols
+    else:
+        ldy = _rows_of(out, rows, cols, cache, "out")
+    ld_table = page_table.stride(0) if B > 1 else width
+    return rows, ldq, cols // d, B, width, ld_table, lens_p, d ** -0.5 if scale is None else scale, out, ldy
 
 
 def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = None, window: int = 0, sinks: int = 0,
@@ -600,23 +629,21 @@ def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = Non
     first `sinks` are seen.  scale defaults to head_dim ** -0.5.  `workspace` (uint8,
     attention_decode_workspace_size() bytes, zeroed once) may be kept for all later calls
     on one stream; without one, each call allocates a zeroed one."""
-    lib = load()
+    lib = _lib or load()
     rows, ldq, heads, B, width, ld_table, lens_p, scale, out, ldy = _attention_args(
         q, cache, page_table, seq_lens, scale, out, stream)
     if rows != B:
         raise ValueError("q has %d rows, page_table %d sequences" % (rows, B))
     if workspace is None:
-        with _on(stream, cache.device):
-            workspace = torch.zeros(attention_decode_workspace_size(cache, heads), dtype=torch.uint8,
-                                    device=cache.device)
-    else:
-        _dev_tensor(workspace, torch.uint8, "workspace", cache.device)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    _check(lib.sp24_attention_decode(q.data_ptr(), B, ldq, heads, cache._address, page_table.data_ptr(), width,
-                                     ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
-                                     workspace.data_ptr(), workspace.numel(), _stream(stream)),
-           "sp24_attention_decode")
+        workspace = _new(attention_decode_workspace_size(cache, heads), torch.uint8, stream, cache, zero=True)
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and
+              workspace.get_device() == cache._index and workspace.is_contiguous()):
+        _refuse(workspace, torch.uint8, cache.device, "workspace", "contiguous")
+    st = lib.sp24_attention_decode(q.data_ptr(), B, ldq, heads, cache._address, page_table.data_ptr(), width,
+                                   ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
+                                   workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache))
+    if st:
+        _check(st, "sp24_attention_decode")
     return out
 
 
@@ -626,13 +653,15 @@ def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float
     holds them: sequence b has the rows cu_q[b] .. cu_q[b + 1] - 1 of q bf16 [T, heads,
     head dim], the last of the seq_lens[b] tokens that the cache holds for it.  cu_q int32
     [B + 1]; the others as for attention_decode()."""
-    lib = load()
+    lib = _lib or load()
     rows, ldq, heads, B, width, ld_table, lens_p, scale, out, ldy = _attention_args(
         q, cache, page_table, seq_lens, scale, out, stream)
-    cu_p = _vector(cu_q, torch.int32, B + 1, cache.device, "cu_q")
-    _check(lib.sp24_attention_prompt(q.data_ptr(), rows, ldq, heads, cu_p, B, cache._address, page_table.data_ptr(),
-                                     width, ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
-                                     _stream(stream)), "sp24_attention_prompt")
+    cu_p = _vector(cu_q, torch.int32, B + 1, cache, "cu_q")
+    st = lib.sp24_attention_prompt(q.data_ptr(), rows, ldq, heads, cu_p, B, cache._address, page_table.data_ptr(),
+                                   width, ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
+                                   _stream_of(stream, cache))
+    if st:
+        _check(st, "sp24_attention_prompt")
     return out
 
 
