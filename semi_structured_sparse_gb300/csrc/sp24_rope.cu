@@ -6,11 +6,14 @@
 //
 // Bound by memory: 2 bytes read and 2 (1 in an e4m3 cache) written per
 // element.  A row's heads are independent, and the cosines and sines of its
-// position are the same for all of them, so a warp stays with one token: lane
-// l holds the cosines and sines of its 8 elements in registers and walks the
-// token's heads, 32 / (D / 8) of them at a time, one 16-byte load and store
-// per lane and head.  A rotated pair's other half comes from another lane by
-// shuffle (half-split pairs) or sits in the same lane (neighbouring pairs).
+// position are the same for all of them, so a warp stays with one token and
+// walks its heads, 32 / (D / 8) of them at a time.  Of each head a lane has 4
+// values and, for half-split pairs, the 4 values that they are rotated with: a
+// rotation needs no other lane, and 4 cosines and 4 sines per lane do for all
+// heads.  (One 16-byte piece per lane, with the partners fetched by shuffles,
+// took 155 instructions per step and 70 registers; this takes about half, and
+// 8192 tokens went from 49.7 to 40.8 us, 5.0 TB/s.)  All of a warp's loads are issued
+// before the position is known.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include "sp24_attn.cuh"
@@ -20,6 +23,7 @@ namespace sp24 {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kMany = 3;  // head groups whose loads a warp issues together in long calls
 
 struct RopeParams {
   const __nv_bfloat16* qkv;
@@ -40,16 +44,13 @@ struct RopeParams {
   unsigned int* err;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+// Four bf16 values as two pairs of fp32.
+__device__ __forceinline__ void unpack4(const uint2& v, float2 (&x)[2]) {
+  x[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+  x[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]), bf16x2_rn(x[4], x[5]), bf16x2_rn(x[6], x[7]));
+__device__ __forceinline__ uint2 pack4(const float2 (&x)[2]) {
+  return make_uint2(bf16x2_rn(x[0].x, x[0].y), bf16x2_rn(x[1].x, x[1].y));
 }
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -57,127 +58,133 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// U head groups per step: their loads are issued together.
+// U head groups at a time: their loads are issued together.
 template <int D, bool E4M3, bool INTERLEAVED, int U>
 __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPH = D / 8;           // lanes per head
   constexpr int HPW = 32 / LPH;        // heads per warp and step
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x;
-  const int e0 = (lane % LPH) * 8;     // this lane's first element within a head
-  const int heads = p.q_heads + 2 * p.kv_heads;
+  const int heads = p.q_heads + 2 * p.kv_heads, turned = p.q_heads + p.kv_heads;  // queries and keys
   const int groups = (heads + HPW - 1) / HPW;
   const int gstep = kWarps * gridDim.y;
-  const __nv_bfloat16* row = p.qkv + t * p.ldqkv + e0;
+  // This lane's elements of a head: four from ea, four from eb.  Half-split
+  // pairs: (ea + i, eb + i), for the first rot / 8 lanes; neighbours otherwise.
+  const int l = lane % LPH, pairs = INTERLEAVED ? 0 : p.rot / 8;
+  const int ea = l < pairs ? 4 * l : 8 * l, eb = l < pairs ? p.rot / 2 + 4 * l : 8 * l + 4;
+  const bool rotates = INTERLEAVED ? ea < p.rot : l < pairs;
+  const __nv_bfloat16* row = p.qkv + t * p.ldqkv;
   pdl_wait();
 
+  uint2 ra[U], rb[U];
+  auto load = [&](int g0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = (g0 + u * gstep) * HPW + lane / LPH;
+      ra[u] = rb[u] = make_uint2(0, 0);
+      if (h < heads) {
+        ra[u] = *reinterpret_cast<const uint2*>(row + h * D + ea);
+        rb[u] = *reinterpret_cast<const uint2*>(row + h * D + eb);
+      }
+    }
+  };
+  int g0 = blockIdx.y * kWarps + warp;
+  load(g0);
+
+  uint2 wq[2], wk[2];
+  const bool norm = p.q_weight != nullptr;
+  if (norm) {
+    wq[0] = *reinterpret_cast<const uint2*>(p.q_weight + ea), wq[1] = *reinterpret_cast<const uint2*>(p.q_weight + eb);
+    wk[0] = *reinterpret_cast<const uint2*>(p.k_weight + ea), wk[1] = *reinterpret_cast<const uint2*>(p.k_weight + eb);
+  }
   const int64_t slot = p.slots[t];
-  if (slot >= p.num_slots && lane == 0) atomicOr(p.err, DEVERR_INDEX);
+  const int64_t pos = p.rot > 0 ? p.positions[t] : 0;
+  if (slot >= p.num_slots && threadIdx.x == 0) atomicOr(p.err, DEVERR_INDEX);
   const bool store = slot >= 0 && slot < p.num_slots;
-  const int64_t page = slot >> p.cache.page_shift;
-  const int64_t place = slot & ((1 << p.cache.page_shift) - 1);
-  const int64_t at = page * p.cache.page_stride + place * p.cache.token_stride + e0 * (E4M3 ? 1 : 2);
-
-  // This lane's cosines and sines.  Elements past rot keep (1, 0).  half-split:
-  // element i < rot/2 has the partner i + rot/2 and a sine of -sin, the others
-  // the partner i - rot/2 and +sin.  Neighbouring: c[j], s[j] for pair j.
-  float c[8], s[8];
-  int partner = lane;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.0f;
-    s[i] = 0.0f;
+  const int64_t at = (slot >> p.cache.page_shift) * p.cache.page_stride +
+                     (slot & ((1 << p.cache.page_shift) - 1)) * p.cache.token_stride;
+  if (p.rot > 0 && (pos < 0 || pos >= p.max_pos)) {  // the whole CTA works on this token
+    if (threadIdx.x == 0) atomicOr(p.err, DEVERR_INDEX);
+    pdl_trigger();
+    return;
   }
-  if (p.rot > 0) {
-    const int64_t pos = p.positions[t];
-    if (pos < 0 || pos >= p.max_pos) {  // the whole CTA works on this token
-      if (lane == 0) atomicOr(p.err, DEVERR_INDEX);
-      pdl_trigger();
-      return;
-    }
-    const float* table = p.cos_sin + pos * p.rot;
-    const int half = p.rot / 2;
-    if (e0 < p.rot) {
-      if (INTERLEAVED) {
-        const float4 cv = *reinterpret_cast<const float4*>(table + e0 / 2);
-        const float4 sv = *reinterpret_cast<const float4*>(table + half + e0 / 2);
-        c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-        s[0] = sv.x, s[1] = sv.y, s[2] = sv.z, s[3] = sv.w;
-      } else {
-        const bool first = e0 < half;
-        const int i0 = first ? e0 : e0 - half;
-        partner = first ? lane + half / 8 : lane - half / 8;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 cv = *reinterpret_cast<const float4*>(table + i0 + i);
-          const float4 sv = *reinterpret_cast<const float4*>(table + half + i0 + i);
-          c[i] = cv.x, c[i + 1] = cv.y, c[i + 2] = cv.z, c[i + 3] = cv.w;
-          s[i] = first ? -sv.x : sv.x, s[i + 1] = first ? -sv.y : sv.y;
-          s[i + 2] = first ? -sv.z : sv.z, s[i + 3] = first ? -sv.w : sv.w;
-        }
-      }
-    }
+  // Half-split: pair i turns by (c[i], s[i]), i < 4.  Neighbours: the pairs of
+  // ea turn by (c0.x, s0.x) and (c0.y, s0.y), those of eb by (c1, s1).
+  float2 c[2], s[2];
+  c[0] = c[1] = make_float2(1.0f, 1.0f);
+  s[0] = s[1] = make_float2(0.0f, 0.0f);
+  if (rotates) {
+    const float* table = p.cos_sin + pos * p.rot + (INTERLEAVED ? ea / 2 : ea);
+    const float4 cv = *reinterpret_cast<const float4*>(table);
+    const float4 sv = *reinterpret_cast<const float4*>(table + p.rot / 2);
+    c[0] = make_float2(cv.x, cv.y), c[1] = make_float2(cv.z, cv.w);
+    s[0] = make_float2(sv.x, sv.y), s[1] = make_float2(sv.z, sv.w);
   }
 
-  for (int g0 = blockIdx.y * kWarps + warp; g0 < groups; g0 += gstep * U) {
-    uint4 raw[U];
+  for (; g0 < groups; g0 += gstep * U) {
+    if (g0 != blockIdx.y * kWarps + warp) load(g0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = (g0 + u * gstep) * HPW + lane / LPH;
-      raw[u] = h < heads ? *reinterpret_cast<const uint4*>(row + int64_t(h) * D) : make_uint4(0, 0, 0, 0);
-    }
+      const int hfirst = (g0 + u * gstep) * HPW;  // uniform over the warp
+      if (hfirst >= heads) break;
+      const int h = hfirst + lane / LPH;
+      const bool query = h < p.q_heads;
+      const bool key = h < turned;  // or a query
+      float2 a[2], b[2];
+      unpack4(ra[u], a);
+      unpack4(rb[u], b);
+      if (hfirst < turned) {
+        if (norm) {
+          float2 q = __fmul2_rn(a[0], a[0]);
+          q = __ffma2_rn(a[1], a[1], q);
+          q = __ffma2_rn(b[0], b[0], q);
+          q = __ffma2_rn(b[1], b[1], q);
+          float ss = q.x + q.y;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if ((g0 + u * gstep) * HPW >= heads) break;  // uniform over the warp
-      const int h = (g0 + u * gstep) * HPW + lane / LPH;
-      float x[8];
-      unpack8(raw[u], x);
-      const bool turned = h < p.q_heads + p.kv_heads;  // queries and keys
-      if (p.q_weight != nullptr) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
-        if (turned) {
-          const float r = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
-          float w[8];
-          unpack8(*reinterpret_cast<const uint4*>((h < p.q_heads ? p.q_weight : p.k_weight) + e0), w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-        }
-      }
-      if (INTERLEAVED) {
-        if (turned && e0 < p.rot) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * c[i] - b * s[i];
-            x[2 * i + 1] = b * c[i] + a * s[i];
+          for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
+          if (key) {
+            const float r = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
+            const float2 rr = make_float2(r, r);
+            float2 w[2];
+            unpack4(query ? wq[0] : wk[0], w);
+            a[0] = __fmul2_rn(__fmul2_rn(a[0], rr), w[0]), a[1] = __fmul2_rn(__fmul2_rn(a[1], rr), w[1]);
+            unpack4(query ? wq[1] : wk[1], w);
+            b[0] = __fmul2_rn(__fmul2_rn(b[0], rr), w[0]), b[1] = __fmul2_rn(__fmul2_rn(b[1], rr), w[1]);
           }
         }
-      } else if (p.rot > 0) {
-        float y[8];
+        if (rotates && key) {
+          if (INTERLEAVED) {
+            auto turn = [](float2 x, float cc, float ss) {
+              return make_float2(x.x * cc - x.y * ss, x.y * cc + x.x * ss);
+            };
+            a[0] = turn(a[0], c[0].x, s[0].x), a[1] = turn(a[1], c[0].y, s[0].y);
+            b[0] = turn(b[0], c[1].x, s[1].x), b[1] = turn(b[1], c[1].y, s[1].y);
+          } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xFFFFFFFFu, x[i], partner);
-        if (turned && e0 < p.rot) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + y[i] * s[i];
+            for (int i = 0; i < 2; ++i) {
+              const float2 x = a[i], y = b[i], n = make_float2(-s[i].x, -s[i].y);
+              a[i] = __ffma2_rn(y, n, __fmul2_rn(x, c[i]));
+              b[i] = __ffma2_rn(x, s[i], __fmul2_rn(y, c[i]));
+            }
+          }
         }
       }
-      if (h < p.q_heads) {
-        *reinterpret_cast<uint4*>(p.q_out + t * p.ldq + int64_t(h) * D + e0) = pack8(x);
+      if (query) {
+        __nv_bfloat16* dst = p.q_out + t * p.ldq + h * D;
+        *reinterpret_cast<uint2*>(dst + ea) = pack4(a);
+        *reinterpret_cast<uint2*>(dst + eb) = pack4(b);
       } else if (h < heads && store) {
-        const bool key = h < p.q_heads + p.kv_heads;
-        const int hk = h - p.q_heads - (key ? 0 : p.kv_heads);
+        const int hk = h - (key ? p.q_heads : turned);
         uint8_t* dst = const_cast<uint8_t*>(key ? p.cache.k : p.cache.v) + at + hk * p.cache.head_stride;
         if (E4M3) {
           const float d = (key ? p.cache.k_scale : p.cache.v_scale)[hk];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], d);
-          *reinterpret_cast<uint2*>(dst) = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+          *reinterpret_cast<uint32_t*>(dst + ea) = e4m3x4(__fdiv_rn(a[0].x, d), __fdiv_rn(a[0].y, d),
+                                                          __fdiv_rn(a[1].x, d), __fdiv_rn(a[1].y, d));
+          *reinterpret_cast<uint32_t*>(dst + eb) = e4m3x4(__fdiv_rn(b[0].x, d), __fdiv_rn(b[0].y, d),
+                                                          __fdiv_rn(b[1].x, d), __fdiv_rn(b[1].y, d));
         } else {
-          *reinterpret_cast<uint4*>(dst) = pack8(x);
+          *reinterpret_cast<uint2*>(dst + 2 * ea) = pack4(a);
+          *reinterpret_cast<uint2*>(dst + 2 * eb) = pack4(b);
         }
       }
     }
@@ -189,11 +196,15 @@ template <int D, bool E4M3, bool INTERLEAVED>
 cudaError_t launch(const RopeParams& p, int64_t T, const DeviceInfo& dev, cudaStream_t s) {
   const int groups = (p.q_heads + 2 * p.kv_heads + 32 / (D / 8) - 1) / (32 / (D / 8));
   // Few tokens: a warp per head group, so that one row's latency is one load's.
-  // Many: a CTA per token, whose warps load 3 groups at a time.
+  // Many: a CTA per token, whose warps have up to kMany groups' loads in flight
+  // (6: 41.6 us for 8192 tokens and 9.7 for 3000 of the 64-wide heads, against
+  // 40.8 and 7.8; warps that walk over tokens and prefetch the next one's values
+  // need too many registers: 40 to 55 us).  3000 tokens of the 64-wide heads:
+  // 7.8 us; one token: 1.5 us.
   const bool few = T < 4 * dev.sm_count;
   const dim3 grid(static_cast<unsigned>(T), few ? static_cast<unsigned>((groups + kWarps - 1) / kWarps) : 1u);
   if (few) return launch_pdl(qk_norm_rope_kernel<D, E4M3, INTERLEAVED, 1>, grid, dim3(kWarps * 32), 0, s, p);
-  return launch_pdl(qk_norm_rope_kernel<D, E4M3, INTERLEAVED, 3>, grid, dim3(kWarps * 32), 0, s, p);
+  return launch_pdl(qk_norm_rope_kernel<D, E4M3, INTERLEAVED, kMany>, grid, dim3(kWarps * 32), 0, s, p);
 }
 
 }  // namespace
