@@ -13,7 +13,8 @@
 //   workspace, in the order of the keys: the result does not depend on timing.
 // - Within a CTA every warp streams its own chunks of a tile through its own
 //   ring of shared memory (cp.async, no barrier in the loop), with a running
-//   maximum and sum of its own; the warps are joined at the end of a pair.
+//   maximum and sum of its own; the warps are joined at the end of a pair, while
+//   the next pair's first keys are on their way.
 //   Keys outside [lo, hi) of a chunk are not read: zeros take their place, so
 //   whatever the cache holds there (NaN too) cannot reach a sum.
 // - The few query heads of a pair are the narrow side of the products: S^T =
@@ -24,6 +25,13 @@
 // - e4m3 codes become f16 in registers (exactly), so the products of an e4m3
 //   cache are f16 ones; each query head is scaled by a power of two, which
 //   keeps bf16 queries within f16's range.
+//
+// Measured (GB300, 32/8 heads of 128 but for the last): one sequence of 131071
+// tokens 87 us, 6.2 TB/s (91 % of the measured copy rate); 64 of 1 to 16000
+// in an e4m3 cache 171 us, 6.2 TB/s (92 %); one of 1000 tokens 7.1 us, of
+// which the keys take 1: launch, lengths, pages, keys and the join of 16 pieces
+// are a chain of seven memory latencies; 128 of up to 9000 tokens under a
+// window of 2000 with 4 sinks, 28/4 heads of 64, 45.3 us, 5.2 TB/s (76 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "sp24_attn.cuh"
@@ -32,13 +40,13 @@
 namespace sp24 {
 namespace {
 
-constexpr int kWarps = 4;           // per CTA
+constexpr int kWarps = 4;           // per CTA (2, and twice the CTAs: 131071 tokens 95 us against 88; 8, and half: e4m3 178
+                                    // us against 170)
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 3;          // of a warp's ring
 constexpr int kHalf = 4096;         // bytes of keys (and of values) per chunk and stage
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kRing = kStages * kStageBytes;
+constexpr int kPieces = 16;         // of a pair, that a thread joins in one round of loads
 
 struct DecodeParams {
   const __nv_bfloat16* q;
@@ -115,21 +123,21 @@ __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
   return r;
 }
 
-// A tile's tokens are kWarps chunks of CT; a pair's tiles are those of its
-// sinks (from token 0), then those of its window (from `from`, a multiple of 16,
-// so that 16 tokens in a row never cross a page).
+// A sequence's visible keys are those of its sinks, [0, sinks), and those of
+// its window, [lo, n).  In chunks of CT: the sinks' from token 0, then the
+// window's from `from`, a multiple of 16 (so that 16 tokens in a row never
+// cross a page).  A tile is kWarps chunks in a row.
 struct Span {
   int n;             // tokens
-  int lo, sinks;     // visible: [0, sinks) and [lo, n)
-  int from;          // where the window's tiles begin
-  int sink_tiles, tiles;
+  int lo, sinks;
+  int from;          // where the window's chunks begin
+  int sink_chunks, tiles;
 };
 
-template <int TT>
-__device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool report) {
+template <int CT>
+__device__ __forceinline__ Span span_of(const DecodeParams& p, int n, bool report) {
   Span s;
   const int most = p.table_width << p.cache.page_shift;
-  int n = __ldg(p.seq_lens + b);
   if (n < 0 || n > most) {
     if (report) atomicOr(p.err, DEVERR_INDEX);
     n = n < 0 ? 0 : most;
@@ -139,162 +147,210 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool repor
   s.sinks = min(p.sinks, s.lo);
   if (s.sinks == s.lo) s.lo = s.sinks = 0;
   s.from = s.lo & ~15;
-  s.sink_tiles = (s.sinks + TT - 1) / TT;
-  s.tiles = max(1, s.sink_tiles + (n - s.from + TT - 1) / TT);  // an empty sequence has one, without keys
+  s.sink_chunks = (s.sinks + CT - 1) / CT;
+  const int chunks = s.sink_chunks + (n - s.from + CT - 1) / CT;
+  s.tiles = max(1, (chunks + kWarps - 1) / kWarps);  // an empty sequence has one, without keys
   return s;
 }
+
+// Stages of a warp's ring.  e4m3: 3 (64 ragged sequences 169.6 us, 172.2 with
+// 2), but 2 where 16 heads' exchange buffer takes the room.  bf16: 2 (131071
+// tokens 86.6 us against 87.5, 128 windowed sequences 45.7 against 47.2).
+template <bool E4M3, int NH>
+constexpr int kStages = E4M3 && NH == 1 ? 3 : 2;
+template <int D, bool E4M3, int NH>
+constexpr int kSmem = kWarps * (kStages<E4M3, NH> * kStageBytes + 8 * NH * (D + 4) * 4);
+
+// What a CTA does in one go: tiles t0 .. t1 - 1 of a sequence, for one kv head
+// and up to 8 NH of its query heads.
+struct Item {
+  int b, hh, t0, t1;
+  Span sp;
+};
 
 template <int D, bool E4M3, int NH>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int ROWB = D * (E4M3 ? 1 : 2);   // bytes of a token's key
   constexpr int CT = kHalf / ROWB;           // tokens per chunk: 16, 32 or 64
-  constexpr int TT = CT * kWarps;            // tokens per tile
   constexpr int MT = CT / 16;
   constexpr int PIECES = ROWB / 16;          // 16-byte pieces of a row
   constexpr int RPI = 32 / PIECES;           // rows that a warp's 32 pieces cover: 2, 4 or 8
   constexpr int LOADS = CT / RPI;            // loads per lane and chunk half: 8
   constexpr int HEADS = 8 * NH;
   constexpr int PAD = D + 4;                 // row of the exchange buffer, in floats
-  static_assert(LOADS == 8 && HEADS * PAD * 4 <= kRing, "");
+  constexpr int S = kStages<E4M3, NH>, RING = S * kStageBytes;
+  static_assert(LOADS == 8, "");
 
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_red[kWarps];
+  __shared__ int s_sum[2][kWarps];
   __shared__ int s_found[2];
   __shared__ float s_m[kWarps][HEADS], s_l[kWarps][HEADS];
   __shared__ unsigned int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * kRing;
-  const uint32_t ring_a = smem_u32(ring);
+  const uint32_t ring_a = smem_u32(smem + warp * RING);
+  float* const exchange = reinterpret_cast<float*>(smem + kWarps * RING);  // [kWarps][HEADS][PAD]
   pdl_wait();
 
   // ---- this CTA's range of tiles
   const int HH = p.kv_heads * p.head_blocks;
-  int mine = 0;
-  for (int b = tid; b < p.B; b += kThreads) mine += span_of<TT>(p, b, blockIdx.x == 0).tiles;
+  // Tiles of the sequences: a sum over all, and a running sum over the first kThreads.
+  auto tiles_of = [&](int x, bool report) {
+    return x < p.B ? span_of<CT>(p, __ldg(p.seq_lens + x), report).tiles : 0;
+  };
+  auto scan = [&](int x) {  // inclusive, over the warp
 #pragma unroll
-  for (int m = 16; m; m >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, m);
-  if (lane == 0) s_red[warp] = mine;
+    for (int m = 1; m < 32; m <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, m);
+      if (lane >= m) x += y;
+    }
+    return x;
+  };
+  int own = tiles_of(tid, blockIdx.x == 0), rest = 0;
+  for (int x = tid + kThreads; x < p.B; x += kThreads) rest += tiles_of(x, blockIdx.x == 0);
+  int incl = scan(own);
+  if (p.B > kThreads) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, m);
+  }
+  if (lane == 31) s_sum[0][warp] = incl, s_sum[1][warp] = rest;
   __syncthreads();
   unsigned int total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += s_red[w];
+  for (int w = 0; w < kWarps; ++w) total += s_sum[0][w] + s_sum[1][w];
   total *= HH;
   const unsigned int ctas = min(gridDim.x, total), cta = blockIdx.x;
   if (cta >= ctas) return;  // uniform
-  const unsigned int per = total / ctas, more = total % ctas;  // the first `more` CTAs take a tile more
-  unsigned int u = cta * per + min(cta, more);
-  const unsigned int u_end = u + per + (cta < more ? 1u : 0u);
-  auto cta_of = [&](unsigned int x) { return x < more * (per + 1) ? x / (per + 1) : more + (x - more * (per + 1)) / per; };
-  // the sequence that tile u belongs to
-  int b = 0, before = 0;  // before: tiles (of one head) of the sequences before b
+  const unsigned int per = total / ctas, extra = total % ctas;  // the first `extra` CTAs take a tile more
+  unsigned int u = cta * per + min(cta, extra);
+  const unsigned int u_end = u + per + (cta < extra ? 1u : 0u);
+  auto cta_of = [&](unsigned int x) {
+    return x < extra * (per + 1) ? x / (per + 1) : extra + (x - extra * (per + 1)) / per;
+  };
+  // The sequence that tile u belongs to, and the tiles (of one head) of those before it.
+  int b = 0, before = 0;
   {
     const int want = static_cast<int>(u / HH);
-    int seen = 0;
-    for (int b0 = 0;; b0 += kThreads) {
-      const int mb = b0 + tid;
-      const int own = mb < p.B ? span_of<TT>(p, mb, false).tiles : 0;
-      int incl = own;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-        if (lane >= m) incl += x;
-      }
-      __syncthreads();  // s_red and s_found are free
-      if (lane == 31) s_red[warp] = incl;
-      if (tid == 0) s_found[0] = -1;
-      __syncthreads();
+    for (int b0 = 0, seen = 0;; b0 += kThreads) {
       int base = seen, all = seen;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) base += s_red[w];
-        all += s_red[w];
+        if (w < warp) base += s_sum[0][w];
+        all += s_sum[0][w];
       }
       incl += base;
       if (want < incl && want >= incl - own) {
-        s_found[0] = mb;
+        s_found[0] = b0 + tid;
         s_found[1] = incl - own;
       }
       __syncthreads();
-      if (s_found[0] >= 0 || b0 + kThreads >= p.B) break;
+      if (want < all || b0 + kThreads >= p.B) break;  // uniform
       seen = all;
+      own = tiles_of(b0 + kThreads + tid, false);
+      incl = scan(own);
+      if (lane == 31) s_sum[0][warp] = incl;
+      __syncthreads();
     }
-    b = max(s_found[0], 0);
+    b = s_found[0];
     before = s_found[1];
   }
 
-  Span sp = span_of<TT>(p, b, false);
-  while (u < u_end) {
+  Item it;
+  it.b = b;
+  it.sp = span_of<CT>(p, __ldg(p.seq_lens + b), false);
+  // The item that tile u of the launch begins.
+  auto place = [&](Item& x) {
     const unsigned int local = u - static_cast<unsigned int>(before) * HH;
-    const int hh = local / sp.tiles, t0 = local % sp.tiles;
-    const int t1 = min(sp.tiles, t0 + static_cast<int>(u_end - u));
-    const int hk = hh / p.head_blocks, hb = hh % p.head_blocks;
+    x.hh = local / x.sp.tiles;
+    x.t0 = local % x.sp.tiles;
+    x.t1 = min(x.sp.tiles, x.t0 + static_cast<int>(u_end - u));
+  };
+  place(it);
+
+  // ---- loads of chunks into stages
+  const int row0 = lane / PIECES;
+  auto chunk_at = [&](const Item& x, int ti, int& tok, int& lo, int& hi) {
+    const int q = ti * kWarps + warp;
+    if (q < x.sp.sink_chunks) {
+      tok = q * CT;
+      lo = 0, hi = x.sp.sinks;
+    } else {
+      tok = x.sp.from + (q - x.sp.sink_chunks) * CT;
+      lo = x.sp.lo, hi = x.sp.n;
+    }
+  };
+  // Page of each 16 tokens of the chunks ahead: lane i holds chunk (batch + i)'s.
+  int page_now[MT], page_next[MT], page_then[MT];
+  auto fetch_pages = [&](const Item& x, int ti, int (&out)[MT]) {
+    const int32_t* table = p.page_table + int64_t(x.b) * p.ld_table;
+    int tok = 0, lo = 0, hi = 0;
+    if (ti < x.t1) chunk_at(x, ti, tok, lo, hi);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int j = tok + 16 * i;
+      out[i] = 0;
+      if (ti < x.t1 && j < hi && j + 16 > lo) {
+        int id = __ldg(table + (j >> p.cache.page_shift));
+        if (id < 0 || id >= p.cache.num_pages) {
+          atomicOr(p.err, DEVERR_INDEX);
+          id = 0;
+        }
+        out[i] = id;
+      }
+    }
+  };
+  auto issue = [&](const Item& x, int ti, int stage) {
+    if (ti < x.t1) {
+      int tok, lo, hi;
+      chunk_at(x, ti, tok, lo, hi);
+      const bool whole = tok >= lo && tok + CT <= hi;
+      if (whole || (tok < hi && tok + CT > lo)) {
+        const int64_t head = (x.hh / p.head_blocks) * p.cache.head_stride + (lane % PIECES) * 16;
+        const uint32_t dst = ring_a + stage * kStageBytes;
+        const int in_page = tok & ((1 << p.cache.page_shift) - 1);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          const int sub = i * RPI / 16, row = i * RPI + row0;
+          const int page = __shfl_sync(0xFFFFFFFFu, page_now[sub], (ti - x.t0) & 31);
+          const int64_t at = page * p.cache.page_stride + head +
+                             (((in_page + sub * 16) & ((1 << p.cache.page_shift) - 1)) + (row & 15)) *
+                                 p.cache.token_stride;
+          const int sw = ROWB >= 128 ? (row & 7) : ((row >> 1) & 3);
+          const uint32_t to = dst + row * ROWB + (((lane % PIECES) ^ sw) << 4);
+          const bool ok = whole || (tok + row >= lo && tok + row < hi);
+          cp_async_16(to, p.cache.k + (ok ? at : 0), ok ? 16u : 0u);
+          cp_async_16(to + kHalf, p.cache.v + (ok ? at : 0), ok ? 16u : 0u);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  fetch_pages(it, it.t0 + lane, page_now);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(it, it.t0 + i, i);
+  int stage = 0;
+
+  while (true) {
+    fetch_pages(it, it.t0 + 32 + lane, page_next);
+    // The item after this one, and the pages of its first chunks: their copies are issued as soon as this one's keys
+    // are done, before the warps are joined.
+    const int tile0 = before * HH + it.hh * it.sp.tiles;  // the pair's first tile in the launch
+    u += it.t1 - it.t0;
+    const bool more = u < u_end;
+    Item nx = it;
+    if (more) {
+      if (it.hh == HH - 1) {
+        before += it.sp.tiles;
+        nx.b = it.b + 1;
+        nx.sp = span_of<CT>(p, __ldg(p.seq_lens + nx.b), false);
+      }
+      place(nx);
+      fetch_pages(nx, nx.t0 + lane, page_then);
+    }
+    const int b = it.b, hk = it.hh / p.head_blocks, hb = it.hh % p.head_blocks;
     const int h0 = hk * p.group + hb * HEADS;                // first query head
     const int heads = min(HEADS, p.group - hb * HEADS);
-
-    // ---- loads of one chunk into a stage
-    const uint8_t* kbase = p.cache.k + hk * p.cache.head_stride + (lane % PIECES) * 16;
-    const uint8_t* vbase = p.cache.v + hk * p.cache.head_stride + (lane % PIECES) * 16;
-    const int32_t* table = p.page_table + int64_t(b) * p.ld_table;
-    const int row0 = lane / PIECES;
-    auto chunk_at = [&](int ti, int& tok, int& lo, int& hi) {
-      if (ti < sp.sink_tiles) {
-        tok = ti * TT + warp * CT;
-        lo = 0, hi = sp.sinks;
-      } else {
-        tok = sp.from + (ti - sp.sink_tiles) * TT + warp * CT;
-        lo = sp.lo, hi = sp.n;
-      }
-    };
-    // Page of each 16 tokens of the chunks ahead: lane i holds chunk (batch + i)'s.
-    int page_now[MT], page_next[MT];
-    auto fetch_pages = [&](int ti, int (&out)[MT]) {
-      int tok = 0, lo = 0, hi = 0;
-      if (ti < t1) chunk_at(ti, tok, lo, hi);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int j = tok + 16 * i;
-        out[i] = 0;
-        if (ti < t1 && j < hi && j + 16 > lo) {
-          int id = __ldg(table + (j >> p.cache.page_shift));
-          if (id < 0 || id >= p.cache.num_pages) {
-            atomicOr(p.err, DEVERR_INDEX);
-            id = 0;
-          }
-          out[i] = id;
-        }
-      }
-    };
-    auto issue = [&](int ti, int stage) {
-      if (ti < t1) {
-        int tok, lo, hi;
-        chunk_at(ti, tok, lo, hi);
-        const bool whole = tok >= lo && tok + CT <= hi;
-        if (whole || (tok < hi && tok + CT > lo)) {
-          const uint32_t dst = ring_a + stage * kStageBytes;
-          const int in_page = tok & ((1 << p.cache.page_shift) - 1);
-#pragma unroll
-          for (int i = 0; i < LOADS; ++i) {
-            const int sub = i * RPI / 16, row = i * RPI + row0;
-            const int page = __shfl_sync(0xFFFFFFFFu, page_now[sub], (ti - t0) & 31);
-            const int64_t at = page * p.cache.page_stride +
-                               (((in_page + sub * 16) & ((1 << p.cache.page_shift) - 1)) + (row & 15)) *
-                                   p.cache.token_stride;
-            const int sw = ROWB >= 128 ? (row & 7) : ((row >> 1) & 3);
-            const uint32_t to = dst + row * ROWB + (((lane % PIECES) ^ sw) << 4);
-            const bool ok = whole || (tok + row >= lo && tok + row < hi);
-            cp_async_16(to, ok ? kbase + at : p.cache.k, ok ? 16u : 0u);
-            cp_async_16(to + kHalf, ok ? vbase + at : p.cache.v, ok ? 16u : 0u);
-          }
-        }
-      }
-      cp_async_commit();
-    };
-    fetch_pages(t0 + lane, page_now);
-    fetch_pages(t0 + 32 + lane, page_next);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(t0 + i, i);
 
     // ---- the queries, as the B operand of S^T = K Q^T (column g: head h0 + 8 n + g)
     uint32_t qf[NH][D / 16][2];
@@ -353,24 +409,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     }
 
     // ---- this warp's chunk of each tile
-    int stage = 0;
-    for (int ti = t0; ti < t1; ++ti) {
-      cp_async_wait<kStages - 2>();
+    for (int ti = it.t0; ti < it.t1; ++ti) {
+      cp_async_wait<S - 2>();
       __syncwarp();
       {
-        const int ahead = ti + kStages - 1;
-        if (((ahead - t0) & 31) == 0) {
+        const int ahead = ti + S - 1;
+        if (((ahead - it.t0) & 31) == 0) {
 #pragma unroll
           for (int i = 0; i < MT; ++i) page_now[i] = page_next[i];
-          fetch_pages(ahead + 32 + lane, page_next);
+          fetch_pages(it, ahead + 32 + lane, page_next);
         }
-        const int to = stage == 0 ? kStages - 1 : stage - 1;
-        issue(ahead, to);
+        issue(it, ahead, stage == 0 ? S - 1 : stage - 1);
       }
       int tok, lo, hi;
-      chunk_at(ti, tok, lo, hi);
+      chunk_at(it, ti, tok, lo, hi);
       const uint32_t ks = ring_a + stage * kStageBytes, vs = ks + kHalf;
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      stage = stage + 1 == S ? 0 : stage + 1;
       if (tok >= hi || tok + CT <= lo) continue;  // nothing visible: uniform over the warp
 
       float s[MT][NH][4];
@@ -496,10 +550,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
       }
     }
 
-    // ---- join the warps: O^T of each through its own ring (idle now)
-    cp_async_wait<0>();
-    __syncwarp();
-    float* ex = reinterpret_cast<float*>(ring);
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) page_now[i] = page_then[i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < S - 1; ++i) issue(nx, nx.t0 + i, (stage + i) % S);
+    }
+
+    // ---- join the warps
+    float* ex = exchange + warp * (HEADS * PAD);
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
 #pragma unroll
@@ -521,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     }
     __syncthreads();
 
-    const bool cut = t0 > 0 || t1 < sp.tiles;
-    const int slot = 2 * cta + (t0 == 0 ? 1 : 0);
+    const bool cut = it.t0 > 0 || it.t1 < it.sp.tiles;
+    const int slot = 2 * cta + (it.t0 == 0 ? 1 : 0);
     float* part = p.partials + int64_t(slot) * (HEADS * D);
     float* part_ml = p.partials + int64_t(2) * gridDim.x * (HEADS * D) + int64_t(slot) * (HEADS * 2);
     const float vscale = E4M3 ? p.cache.v_scale[hk] : 1.0f;
@@ -536,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(s_m[w][h] - use);
-        const float4 v = *reinterpret_cast<const float4*>(smem + w * kRing + (h * PAD + d) * 4);
+        const float4 v = *reinterpret_cast<const float4*>(exchange + (w * HEADS + h) * PAD + d);
         sum = fmaf(s_l[w][h], f, sum);
         acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
         acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
@@ -550,13 +610,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
             make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
       }
     }
-    __syncthreads();  // the rings are free again; the partial is written
+    __syncthreads();  // the exchange buffer is free again; the partial is written
 
     if (cut) {
       // The pair's pieces are those of CTAs first .. last: the first in its second
       // slot, the others in their first.
-      const unsigned int u0 = static_cast<unsigned int>(before) * HH + static_cast<unsigned int>(hh) * sp.tiles;
-      const unsigned int first = cta_of(u0), last = cta_of(u0 + sp.tiles - 1);
+      const unsigned int first = cta_of(tile0), last = cta_of(tile0 + it.sp.tiles - 1);
       const int pieces = static_cast<int>(last - first + 1);
       if (tid == 0) {
         __threadfence();
@@ -568,82 +627,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
       }
       __syncthreads();
       if (s_last) {
-        // weight of each piece and head: exp2(its maximum - the maximum of all)
-        float* weight = reinterpret_cast<float*>(smem);                        // [pieces][heads]
-        float* sums = reinterpret_cast<float*>(smem) + pieces * HEADS;         // [pieces][heads]
+        // Each thread by itself, kPieces pieces at a time: their maxima, sums and values in one round of loads.
         const float* ml = p.partials + int64_t(2) * gridDim.x * (HEADS * D);
-        auto slot_of = [&](int i) { return int64_t(2) * (first + i) + (i == 0 ? 1 : 0); };
-        for (int i = tid; i < pieces * heads; i += kThreads) {
-          const int pc = i / heads, h = i % heads;
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(ml + slot_of(pc) * (HEADS * 2) + 2 * h));
-          weight[pc * HEADS + h] = v.x;
-          sums[pc * HEADS + h] = v.y;
-        }
-        __syncthreads();
-        for (int h = warp; h < heads; h += kWarps) {
-          float top = -INFINITY, sum = 0.0f;
-          for (int i = lane; i < pieces; i += 32) top = fmaxf(top, weight[i * HEADS + h]);
-#pragma unroll
-          for (int mask = 16; mask; mask >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, mask));
-          const float use = top == -INFINITY ? 0.0f : top;
-          for (int i = lane; i < pieces; i += 32) {
-            const float f = ex2(weight[i * HEADS + h] - use);
-            weight[i * HEADS + h] = f;
-            sum = fmaf(sums[i * HEADS + h], f, sum);
-          }
-#pragma unroll
-          for (int mask = 16; mask; mask >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, mask);
-          if (lane == 0) s_l[0][h] = sum == 0.0f ? 0.0f : vscale / sum;
-        }
-        __syncthreads();
-        // Warp w adds pieces w, w + kWarps, ...; the warps' sums meet in shared memory.
-        float* sum_ex = reinterpret_cast<float*>(smem) + 2 * pieces * HEADS;   // [kWarps][HEADS * D]
-        for (int v0 = 0; v0 < heads * (D / 4); v0 += 32 * 4) {
-          float4 acc[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = make_float4(0, 0, 0, 0);
-#pragma unroll 2
-          for (int pc = warp; pc < pieces; pc += kWarps) {
-            const float4* src = reinterpret_cast<const float4*>(p.partials + slot_of(pc) * (HEADS * D));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int vec = v0 + i * 32 + lane;
-              if (vec < heads * (D / 4)) {
-                const float4 x = __ldcg(src + vec);
-                const float f = weight[pc * HEADS + vec / (D / 4)];
-                acc[i].x = fmaf(x.x, f, acc[i].x), acc[i].y = fmaf(x.y, f, acc[i].y);
-                acc[i].z = fmaf(x.z, f, acc[i].z), acc[i].w = fmaf(x.w, f, acc[i].w);
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int vec = v0 + i * 32 + lane;
-            if (vec < heads * (D / 4)) reinterpret_cast<float4*>(sum_ex + warp * (HEADS * D))[vec] = acc[i];
-          }
-        }
-        __syncthreads();
         for (int vec = tid; vec < heads * (D / 4); vec += kThreads) {
           const int h = vec / (D / 4), d = (vec % (D / 4)) * 4;
+          float top = -INFINITY, sum = 0.0f;
           float4 acc = make_float4(0, 0, 0, 0);
+          for (int i0 = 0; i0 < pieces; i0 += kPieces) {
+            float4 v[kPieces];
+            float2 w[kPieces];
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float4 x = reinterpret_cast<const float4*>(sum_ex + w * (HEADS * D))[vec];
-            acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+            for (int i = 0; i < kPieces; ++i) {
+              v[i] = make_float4(0, 0, 0, 0);
+              w[i] = make_float2(-INFINITY, 0.0f);
+              if (i0 + i < pieces) {
+                const int64_t sl = int64_t(2) * (first + i0 + i) + (i0 + i == 0 ? 1 : 0);
+                w[i] = __ldcg(reinterpret_cast<const float2*>(ml + sl * (HEADS * 2) + 2 * h));
+                v[i] = __ldcg(reinterpret_cast<const float4*>(p.partials + sl * (HEADS * D)) + vec);
+              }
+            }
+            float now = top;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) now = fmaxf(now, w[i].x);
+            const float use = now == -INFINITY ? 0.0f : now, keep = ex2(top - use);
+            top = now;
+            sum *= keep;
+            acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              const float f = ex2(w[i].x - use);
+              sum = fmaf(w[i].y, f, sum);
+              acc.x = fmaf(v[i].x, f, acc.x), acc.y = fmaf(v[i].y, f, acc.y);
+              acc.z = fmaf(v[i].z, f, acc.z), acc.w = fmaf(v[i].w, f, acc.w);
+            }
           }
-          const float f = s_l[0][h];
+          const float f = sum == 0.0f ? 0.0f : vscale / sum;
           *reinterpret_cast<uint2*>(p.y + b * p.ldy + int64_t(h0 + h) * D + d) =
               make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
         }
-        __syncthreads();  // shared memory is free again
       }
     }
 
-    u += t1 - t0;
-    if (hh == HH - 1 && t1 == sp.tiles && u < u_end) {
-      before += sp.tiles;
-      sp = span_of<TT>(p, ++b, false);
-    }
+    if (!more) break;
+    it = nx;
   }
   pdl_trigger();
 }
@@ -661,9 +687,7 @@ sp24_status launch(const DecodeParams& p, int ctas, cudaStream_t s) {
   // Tile numbers are 32-bit: the host refuses what could pass them.
   const int64_t most = (int64_t(p.table_width) << p.cache.page_shift) / TT + 3;
   if (most * p.B > INT32_MAX / (int64_t(p.kv_heads) * p.head_blocks)) return SP24_ERR_UNSUPPORTED;
-  const int smem = kWarps * kRing;
-  // join of a pair cut into one piece per CTA
-  if (2 * ctas * 8 * NH * 4 + kWarps * 8 * NH * D * 4 > smem) return SP24_ERR_UNSUPPORTED;
+  const int smem = kSmem<D, E4M3, NH>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SP24_ERR_CUDA;
   return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, p) == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;

@@ -219,7 +219,7 @@ extern "C" sp24_status sp24_qk_norm_rope(const void* qkv, int64_t T, int64_t ldq
   if (T < 0 || T > INT32_MAX) return SP24_ERR_INVALID_ARG;
   if (sp24_status st = check_cache(cache, &p.cache)) return st;
   const int D = cache->head_dim;
-  if (q_heads < 1 || q_heads > (1 << 20) || cache->heads > (1 << 20)) return SP24_ERR_INVALID_ARG;
+  if (q_heads < 1 || q_heads > (1 << 16) || cache->heads > (1 << 16)) return SP24_ERR_INVALID_ARG;
   if (rot < 0 || rot > D) return SP24_ERR_INVALID_ARG;
   if (rot % 16 != 0) return SP24_ERR_UNSUPPORTED;
   if ((q_weight != nullptr) != (k_weight != nullptr)) return SP24_ERR_INVALID_ARG;
