@@ -82,7 +82,7 @@ struct Cfg {
   static constexpr int RAW_TILE = BN * D;                 // e4m3 codes
   static constexpr int RAW = E4M3 ? (D == 128 ? 2 : 4) : 0;
   static constexpr int SLOTS = D == 128 ? (E4M3 ? 4 : 5) : 8;
-  static constexpr int BARS = 21 + 2 * SLOTS + 2 * RAW;
+  static constexpr int BARS = 23 + 2 * SLOTS + 2 * RAW;
   static constexpr int SMEM = 1024 + 2 * Q_TILE + SLOTS * KV_TILE + RAW * RAW_TILE + BARS * 8;
   // Registers after the split: the warpgroups' shares stay within the launch's
   // (168 x 384 or 128 x 512).
@@ -92,7 +92,13 @@ struct Cfg {
   // Whether P V begins when half of P is there.  It shortens the chain S -> P -> O -> next S of a query tile (8192
   // tokens: 350 us against 354; with a window, heads of 64: 484 against 496), but not beside the e4m3 conversion
   // (576 us against 555).
-  static constexpr bool EARLY = !E4M3;
+  static constexpr bool EARLY = !E4M3 && D == 128;
+  // Whether P has columns of its own in tensor memory (heads of 64 leave room
+  // for it).  Then Q K^T of the next key tile runs while the softmax warps are
+  // busy with this one, as soon as they have read S.
+  static constexpr bool APART = D == 64;
+  static constexpr uint32_t P_COL = APART ? 2 * BN : 0, P_STEP = APART ? BN / 2 : BN;  // P of query tile x
+  static constexpr uint32_t O_COL = APART ? 3 * BN : 2 * BN;                           // O of query tile x: + x D
 };
 static_assert(2 * 128 * 216 + 128 * 64 <= 168 * 384, "register split, bf16");
 static_assert(2 * 128 * 208 + 128 * 48 + 128 * 48 <= 128 * 512, "register split, e4m3");
@@ -288,12 +294,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t* s_full = bars + 6;        // [2] S of the next key tile is there, and P V of the last one done
   uint64_t* p_half = bars + 8;        // [2] P of the first 64 keys is there, and O at its scale
   uint64_t* p_full = bars + 10;       // [2] P is there
-  uint64_t* o_full = bars + 12;       // [2] O is complete
+  uint64_t* o_full = bars + 12;       // [2] O is complete (APART: O of this key tile)
   uint64_t* drain = bars + 14;        // [2]
   uint64_t* work_full = bars + 16;    // [2]
   uint64_t* work_empty = bars + 18;   // [2]
   uint64_t* stolen = bars + 20;
-  uint64_t* kv_full = bars + 21;      // [SLOTS]
+  uint64_t* s_read = bars + 21;       // [2] S is in the softmax warps' registers (APART)
+  uint64_t* kv_full = bars + 23;      // [SLOTS]
   uint64_t* kv_empty = kv_full + SLOTS;
   uint64_t* raw_full = kv_empty + SLOTS;  // [RAW]
   uint64_t* raw_empty = raw_full + RAW;
@@ -310,6 +317,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&q_ready[x], 4);
       mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
+      mbar_init(&s_read[x], 4);
       mbar_init(&p_half[x], 4);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
@@ -351,7 +359,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     setmaxnreg_inc<C::REG_SOFTMAX>();
     const int x = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + x * BN, to = tmem + lanes + 2 * BN + x * D;
+    const uint32_t ts = tmem + lanes + x * BN, tp = tmem + lanes + C::P_COL + x * C::P_STEP;
+    const uint32_t to = tmem + lanes + C::O_COL + x * D;
     uint32_t sn = 0, on = 0;  // key tiles and blocks so far, for the barriers' parities
     bool ok = true;
     for (int item = 0; ok; ++item) {
@@ -414,22 +423,39 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < BN / 32; ++j) tmem_ld32(ts + 32 * j, su + 32 * j);
           tmem_ld_wait();
+          if (C::APART) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_read[x]);
+          }
           float* s = reinterpret_cast<float*>(su);
           if (cut_hi || cut_lo) {
             // (The position is worked out here, once or twice per block, to leave the registers to S.)
             int rr = r;
             asm volatile("" : "+r"(rr));  // here, not ahead of the loop
             const int token = rr / p.group;
-            const int hi = token < p.tile_tokens ? p_min + token - base : -1, lo = hi - p.window, sk = p.sinks - base;
+            // (rows past the tile's tokens are no one's)
+            const int hi = token < p.tile_tokens ? p_min + token - base : BN, lo = hi - p.window, sk = p.sinks - base;
+            // Each 32 columns only where some row of the warp does not see them all.
             if (cut_lo) {
+              const int last = __reduce_max_sync(0xFFFFFFFFu, lo);
 #pragma unroll
-              for (int j = 0; j < BN; ++j)
-                if (!(j > lo || j < sk)) s[j] = -INFINITY;
+              for (int j0 = 0; j0 < BN; j0 += 32) {
+                if (last < j0 || j0 + 31 < sk) continue;
+#pragma unroll
+                for (int j = j0; j < j0 + 32; ++j)
+                  if (!(j > lo || j < sk)) s[j] = -INFINITY;
+              }
             }
             if (cut_hi) {
+              const int least = __reduce_min_sync(0xFFFFFFFFu, hi);
 #pragma unroll
-              for (int j = 0; j < BN; ++j)
-                if (j > hi) s[j] = -INFINITY;
+              for (int j0 = 0; j0 < BN; j0 += 32) {
+                if (least >= j0 + 31) continue;
+#pragma unroll
+                for (int j = j0; j < j0 + 32; ++j)
+                  if (j > hi) s[j] = -INFINITY;
+              }
             }
           }
           float top[4];
@@ -439,6 +465,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int j = 12; j < BN; j += 2) top[(j >> 1) & 3] = max3(top[(j >> 1) & 3], s[j], s[j + 1]);
           const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
           const bool grow = now > m + 8.0f;  // also from -inf
+          if (C::APART && i > 0) {  // P V of the last key tile is done with P and O
+            ok = mbar_wait(&o_full[x], (sn - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
           if (__any_sync(0xFFFFFFFFu, grow)) {
             const float to_m = grow ? now : m;
             const float keep = m == to_m ? 1.0f : ex2(m - to_m);
@@ -470,7 +501,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               sum[j & 1] = __fadd2_rn(sum[j & 1], e);
               pk[j] = E4M3 ? f16x2_rn(e.x, e.y) : bf16x2_rn(e.x, e.y);
             }
-            tmem_st16(ts + 16 * h, pk);
+            tmem_st16(tp + 16 * h, pk);
             if (C::EARLY && h == 1) {
               tmem_st_wait();
               tc_fence_before();
@@ -484,7 +515,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[x]);
         }
-        if (ok) ok = mbar_wait(&o_full[x], on & 1);
+        if (ok) ok = mbar_wait(&o_full[x], (C::APART ? sn - 1 : on) & 1);
         if (!ok) break;
         ++on;
         tc_fence_after();
@@ -546,7 +577,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const uint64_t q_d = smem_desc(smem_u32(q_s) + x * C::Q_TILE, 16, 1024, SWZ_128B);
       const uint64_t k_d = smem_desc(smem_u32(kv_s), 16, 1024, SWZ_128B);
       const uint64_t v_d = smem_desc(smem_u32(kv_s), BN * 128, 1024, SWZ_128B);
-      const uint32_t t_s = tmem + x * BN, t_o = tmem + 2 * BN + x * D;
+      const uint32_t t_s = tmem + x * BN, t_p = tmem + C::P_COL + x * C::P_STEP, t_o = tmem + C::O_COL + x * D;
       auto qk = [&](int slot) {
         const uint64_t kd = k_d + slot * (C::KV_TILE >> 4);
 #pragma unroll
@@ -560,7 +591,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < BN / 32; ++j) {
           const int k = half * (BN / 32) + j;
-          mma_f16_ts(t_o, t_s + 8 * k, vd + k * (2048 >> 4), id_pv, add || j > 0);
+          mma_f16_ts(t_o, t_p + 8 * k, vd + k * (2048 >> 4), id_pv, add || j > 0);
         }
       };
       bool ok = true;
@@ -596,6 +627,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const bool more = i + 1 < nt;
           const int vn = ring + 1, kn = ring + 2;
           ring += 2;
+          if (C::APART && more) {
+            ok = wait_kv(kn) && mbar_wait(&s_read[x], pn & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              qk(kn % SLOTS);
+              mma_commit(&s_full[x]);
+              release(kn);
+              if (i + 2 == w.nt) mma_commit(&q_empty[x]);
+            }
+            __syncwarp();
+          }
           ok = wait_kv(vn);
           if (!ok) break;
           if (!E4M3) {
@@ -623,13 +666,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (elect_one()) pv(vn % SLOTS, 0, i > 0);
             __syncwarp();
           }
-          ok = (!more || wait_kv(kn)) && mbar_wait(&p_full[x], pn & 1);
+          ok = (C::APART || !more || wait_kv(kn)) && mbar_wait(&p_full[x], pn & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             if (!C::EARLY) pv(vn % SLOTS, 0, i > 0);
             pv(vn % SLOTS, 1, true);
-            if (more) {
+            if (C::APART) {
+              mma_commit(&o_full[x]);
+              release(vn);
+            } else if (more) {
               qk(kn % SLOTS);
               mma_commit(&s_full[x]);
               release(vn);
