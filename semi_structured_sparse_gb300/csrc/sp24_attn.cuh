@@ -49,12 +49,18 @@ inline sp24_status check_cache(const sp24_kv_cache* c, CacheView* out) {
   return SP24_OK;
 }
 
+// Tokens of a sequence, and rows of a call, at most: positions, and their
+// differences, stay within 32 bits.
+constexpr int kMostTokens = (1 << 30) - 1;
+// A window that no sequence fills is none.
+inline int effective_window(int window) { return window > kMostTokens ? 0 : window; }
+
 // What decode and prompt calls have in common.
 inline sp24_status check_attention(const void* q, int64_t rows, int64_t ldq, int q_heads, const sp24_kv_cache* c,
                                    const int32_t* page_table, int64_t table_width, int64_t ld_table,
                                    const int32_t* seq_lens, int64_t B, float scale, int window, int sinks,
                                    const void* Y, int64_t ldy, CacheView* out) {
-  if (rows < 0 || rows > INT32_MAX || B < 0 || B > INT32_MAX / 2) return SP24_ERR_INVALID_ARG;
+  if (rows < 0 || rows > kMostTokens || B < 0 || B > kMostTokens) return SP24_ERR_INVALID_ARG;
   if (sp24_status st = check_cache(c, out)) return st;
   if (q_heads < 1 || q_heads % c->heads != 0) return SP24_ERR_INVALID_ARG;
   if (q_heads / c->heads > 128) return SP24_ERR_UNSUPPORTED;
@@ -64,7 +70,7 @@ inline sp24_status check_attention(const void* q, int64_t rows, int64_t ldq, int
     if (!q || !Y || !page_table || !seq_lens) return SP24_ERR_INVALID_ARG;
     if (ldq < width || ldy < width || ldq >= (int64_t(1) << 39) || ldy >= (int64_t(1) << 39))
       return SP24_ERR_INVALID_ARG;
-    if (table_width < 1 || ld_table < table_width || table_width > (INT32_MAX / 2 >> out->page_shift))
+    if (table_width < 1 || ld_table < table_width || table_width > (kMostTokens >> out->page_shift))
       return SP24_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(Y) || ldq % 8 || ldy % 8) return SP24_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens)) & 3u)

@@ -915,7 +915,7 @@ extern "C" sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t l
   p.ld_table = ld_table;
   p.seq_lens = seq_lens;
   p.scale = scale;
-  p.window = window;
+  p.window = effective_window(window);
   p.sinks = sinks;
   p.y = static_cast<__nv_bfloat16*>(Y);
   p.ldy = ldy;

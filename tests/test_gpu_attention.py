@@ -341,6 +341,21 @@ def test_prompt_many_sequences(sp24):
     run_prompt(sp24, new, prefix, 4, 2, 64, 16, False, False, 0, 0, seed=9)
 
 
+def test_window_and_sinks_past_every_length(sp24):
+    """The largest window and sinks that fit the argument are no limit at all."""
+    most = 2 ** 31 - 1
+    n = 300
+    s = Setup(sp24, [n], 1, 64, 16, False, False, seed=81)
+    cache, table = s.upload(), s.table.cuda()
+    q = torch.randn(n, 2, 64, device="cuda").bfloat16()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    want = sp24.attention_prompt(q, i32(0, n), cache, table, i32(n))
+    last = sp24.attention_decode(q[n - 1:], cache, table, i32(n))
+    for window, sinks in ((most, 0), (most, most), (5, most), (n, 0)):
+        assert torch.equal(sp24.attention_prompt(q, i32(0, n), cache, table, i32(n), window=window, sinks=sinks), want)
+        assert torch.equal(sp24.attention_decode(q[n - 1:], cache, table, i32(n), window=window, sinks=sinks), last)
+
+
 def test_prompt_matches_decode_and_pieces(sp24):
     """A prompt in one call, the same in pieces, and its last token as a decode step."""
     n, hq, hkv, d = 421, 8, 2, 128
