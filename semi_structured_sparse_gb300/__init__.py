@@ -490,42 +490,50 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.heads, self.page_size, self.head_dim, self.device = heads, page_size, head_dim, k.device
         self._index = k.get_device()
+        self._scale = head_dim ** -0.5
         self._struct = _KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
                                       v_scale.data_ptr() if e4m3 else None, pages, page, head, token, heads,
                                       page_size, head_dim, 1 if e4m3 else 0)
         self._address = ctypes.addressof(self._struct)
 
 
-# The checks below run on every call of a decode step, where a call's time on the
-# host is several times its kernel's: they ask each tensor as few questions as
-# they can.
-def _refuse(t, dtype, device, name, what):
-    """The error for a tensor that one of the checks below did not take."""
-    _dev_tensor(t, dtype, name, device)
-    raise ValueError("%s must be %s, got %s with strides %s" % (name, what, tuple(t.shape), t.stride()))
+# The calls below run on every step of a decode loop, where a call's time on the
+# host is several times its kernel's.  So each first asks its tensors, in one
+# expression, whether all is as it should be, and only a call that is not goes
+# through the checks that say what is wrong.
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 def _rows_of(t, rows, cols, cache, name):
-    """A bf16 tensor of `rows` rows, [rows, cols] or [rows, heads, d] with contiguous
-    rows: its row stride."""
-    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == cache._index:
-        shape, stride = t.shape, t.stride()
-        if len(shape) == 3:
-            ok = shape[1] * shape[2] == cols and stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
-        else:
-            ok = len(shape) == 2 and shape[1] == cols and stride[1] == 1
-        if ok and shape[0] == rows:
-            return stride[0] if rows > 1 else max(stride[0], cols)
-    _refuse(t, torch.bfloat16, cache.device, name, "[%d, %d] or [%d, heads, head dim] with contiguous rows"
-            % (rows, cols, rows))
+    """Checks a bf16 tensor of `rows` rows, [rows, cols] or [rows, heads, d] with contiguous rows."""
+    _dev_tensor(t, torch.bfloat16, name, cache.device)
+    shape = tuple(t.shape)
+    if not (_row_stride(t, cols) and shape[0] == rows):
+        raise ValueError("%s must be [%d, %d] or [%d, heads, head dim] with contiguous rows, got %s with strides %s"
+                         % (name, rows, cols, rows, shape, t.stride()))
+
+
+def _row_stride(t, cols):
+    """The row stride of a tensor whose rows are `cols` contiguous values (0: they are not)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        if shape[1] * shape[2] != cols or stride[2] != 1 or (stride[1] != shape[2] and shape[1] != 1):
+            return 0
+    elif len(shape) != 2 or shape[1] != cols or stride[1] != 1:
+        return 0
+    return stride[0] if shape[0] > 1 else max(stride[0], cols)
 
 
 def _vector(t, dtype, n, cache, name):
-    """The address of a contiguous vector of n values."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == cache._index and t.shape == (n,) and \
-            t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, dtype, cache.device, name, "a contiguous vector of %d values" % n)
+    _dev_tensor(t, dtype, name, cache.device)
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous vector of %d values, got %s" % (name, n, tuple(t.shape)))
+
+
+def _matrix_of(t, dtype, cache, name, what):
+    _dev_tensor(t, dtype, name, cache.device)
+    if t.dim() != 2:
+        raise ValueError("%s must be %s, got %s" % (name, what, tuple(t.shape)))
 
 
 # The current stream's handle without a Stream object around it, where torch has that.
@@ -562,29 +570,47 @@ def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_w
     place of each token, negative for one that is not stored.  Returns the queries bf16
     [T, heads, head dim] (in ``out`` if given)."""
     lib = _lib or load()
-    d = cache.head_dim
-    T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else -1
-    slots_p = _vector(slots, torch.int64, T, cache, "slots")
-    pos_p = _vector(positions, torch.int32, T, cache, "positions")
-    ldqkv = _rows_of(qkv, T, (heads + 2 * cache.heads) * d, cache, "qkv")
-    if not (isinstance(cos_sin, torch.Tensor) and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and
-            cos_sin.get_device() == cache._index and cos_sin.is_contiguous()):
-        _refuse(cos_sin, torch.float32, cache.device, "cos_sin", "a contiguous [max_pos, rot]")
-    max_pos, rot = cos_sin.shape
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight go together")
-    qw = kw = None
-    if q_weight is not None:
-        qw = _vector(q_weight, torch.bfloat16, d, cache, "q_weight")
-        kw = _vector(k_weight, torch.bfloat16, d, cache, "k_weight")
-    if out is None:
-        out = _new((T, heads, d), torch.bfloat16, stream, cache)
-        ldq = heads * d
-    else:
-        ldq = _rows_of(out, T, heads * d, cache, "out")
+    d, at = cache.head_dim, cache._index
+    ok = False
+    try:
+        T = slots.shape[0]
+        ldqkv = _row_stride(qkv, (heads + 2 * cache.heads) * d)
+        max_pos, rot = cos_sin.shape
+        if out is None:
+            out, ldq = _new((T, heads, d), _BF16, stream, cache), heads * d
+        else:
+            ldq = _row_stride(out, heads * d)
+        qw = kw = None
+        ok = (slots.dtype is _I64 and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == at and
+              positions.dtype is _I32 and positions.shape == slots.shape and positions.is_contiguous() and
+              positions.get_device() == at and qkv.dtype is _BF16 and ldqkv and qkv.shape[0] == T and
+              qkv.get_device() == at and out.dtype is _BF16 and ldq and out.shape[0] == T and
+              out.get_device() == at and cos_sin.dtype is _F32 and cos_sin.is_contiguous() and
+              cos_sin.get_device() == at)
+        if q_weight is not None or k_weight is not None:
+            ok = (ok and q_weight.dtype is _BF16 and q_weight.shape == (d,) and q_weight.is_contiguous() and
+                  q_weight.get_device() == at and k_weight.dtype is _BF16 and k_weight.shape == (d,) and
+                  k_weight.is_contiguous() and k_weight.get_device() == at)
+            qw, kw = q_weight.data_ptr(), k_weight.data_ptr()
+    except (AttributeError, IndexError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        _vector(slots, _I64, slots.numel() if isinstance(slots, torch.Tensor) else 0, cache, "slots")
+        T = slots.shape[0]
+        _vector(positions, _I32, T, cache, "positions")
+        _rows_of(qkv, T, (heads + 2 * cache.heads) * d, cache, "qkv")
+        if out is not None:
+            _rows_of(out, T, heads * d, cache, "out")
+        _matrix_of(cos_sin, _F32, cache, "cos_sin", "[max_pos, rot]")
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("q_weight and k_weight go together")
+        if q_weight is not None:
+            _vector(q_weight, _BF16, d, cache, "q_weight")
+            _vector(k_weight, _BF16, d, cache, "k_weight")
+        raise ValueError("cos_sin must be contiguous")
     st = lib.sp24_qk_norm_rope(qkv.data_ptr(), T, ldqkv, heads, qw, kw, eps, cos_sin.data_ptr() if rot else None,
-                               max_pos, rot, bool(interleaved), pos_p, slots_p, out.data_ptr(), ldq, cache._address,
-                               _stream_of(stream, cache))
+                               max_pos, rot, 1 if interleaved else 0, positions.data_ptr(), slots.data_ptr(),
+                               out.data_ptr(), ldq, cache._address, _stream_of(stream, cache))
     if st:
         _check(st, "sp24_qk_norm_rope")
     return out
@@ -597,28 +623,37 @@ def attention_decode_workspace_size(cache: KVCache, heads: int) -> int:
 
 def _attention_args(q, cache, page_table, seq_lens, scale, out, stream):
     """The checks and arguments that both attention calls have in common."""
-    d = cache.head_dim
-    shape = q.shape if isinstance(q, torch.Tensor) else ()
-    if len(shape) == 3 and shape[2] == d:
-        cols = shape[1] * d
-    elif len(shape) == 2 and shape[1] % d == 0:
-        cols = shape[1]
-    else:
-        raise ValueError("q must be [rows, heads, %d] or [rows, heads * %d], got %s" % (d, d, tuple(shape)))
-    rows = shape[0]
-    ldq = _rows_of(q, rows, cols, cache, "q")
-    if not (isinstance(page_table, torch.Tensor) and page_table.dtype is torch.int32 and page_table.dim() == 2 and
-            page_table.get_device() == cache._index and page_table.stride(1) == 1):
-        _refuse(page_table, torch.int32, cache.device, "page_table", "[sequences, pages]")
-    B, width = page_table.shape
-    lens_p = _vector(seq_lens, torch.int32, B, cache, "seq_lens")
-    if out is None:
-        out = _new(shape, torch.bfloat16, stream, cache)
-        ldy = cols
-    else:
-        ldy = _rows_of(out, rows, cols, cache, "out")
+    d, at = cache.head_dim, cache._index
+    ok = False
+    try:
+        shape = q.shape
+        cols = shape[1] * shape[2] if len(shape) == 3 else shape[1]
+        rows, heads = shape[0], cols // d
+        ldq = _row_stride(q, cols)
+        B, width = page_table.shape
+        if out is None:
+            out, ldy = _new(shape, _BF16, stream, cache), cols
+        else:
+            ldy = _row_stride(out, cols)
+        ok = (q.dtype is _BF16 and ldq and q.get_device() == at and shape[-1] % d == 0 and
+              (len(shape) == 2 or shape[2] == d) and out.dtype is _BF16 and ldy and out.shape[0] == rows and
+              out.get_device() == at and page_table.dtype is _I32 and page_table.stride(1) == 1 and
+              page_table.get_device() == at and seq_lens.dtype is _I32 and seq_lens.shape == (B,) and
+              seq_lens.is_contiguous() and seq_lens.get_device() == at)
+    except (AttributeError, IndexError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        if not isinstance(q, torch.Tensor) or q.dim() not in (2, 3) or q.shape[-1] % d or (
+                q.dim() == 3 and q.shape[2] != d):
+            raise ValueError("q must be [rows, heads, %d] or [rows, heads * %d]" % (d, d))
+        cols = q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1]
+        _rows_of(q, q.shape[0], cols, cache, "q")
+        _matrix_of(page_table, _I32, cache, "page_table", "[sequences, pages]")
+        _vector(seq_lens, _I32, page_table.shape[0], cache, "seq_lens")
+        _rows_of(out, q.shape[0], cols, cache, "out")
+        raise ValueError("the arguments' layouts are not ones that the library takes")
     ld_table = page_table.stride(0) if B > 1 else width
-    return rows, ldq, cols // d, B, width, ld_table, lens_p, d ** -0.5 if scale is None else scale, out, ldy
+    return rows, ldq, heads, B, width, ld_table, seq_lens.data_ptr(), cache._scale if scale is None else scale, out, ldy
 
 
 def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = None, window: int = 0, sinks: int = 0,
@@ -636,9 +671,10 @@ def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = Non
         raise ValueError("q has %d rows, page_table %d sequences" % (rows, B))
     if workspace is None:
         workspace = _new(attention_decode_workspace_size(cache, heads), torch.uint8, stream, cache, zero=True)
-    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and
               workspace.get_device() == cache._index and workspace.is_contiguous()):
-        _refuse(workspace, torch.uint8, cache.device, "workspace", "contiguous")
+        _dev_tensor(workspace, _U8, "workspace", cache.device)
+        raise ValueError("workspace must be contiguous")
     st = lib.sp24_attention_decode(q.data_ptr(), B, ldq, heads, cache._address, page_table.data_ptr(), width,
                                    ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
                                    workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache))
@@ -656,8 +692,10 @@ def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float
     lib = _lib or load()
     rows, ldq, heads, B, width, ld_table, lens_p, scale, out, ldy = _attention_args(
         q, cache, page_table, seq_lens, scale, out, stream)
-    cu_p = _vector(cu_q, torch.int32, B + 1, cache, "cu_q")
-    st = lib.sp24_attention_prompt(q.data_ptr(), rows, ldq, heads, cu_p, B, cache._address, page_table.data_ptr(),
+    if not (isinstance(cu_q, torch.Tensor) and cu_q.dtype is _I32 and cu_q.shape == (B + 1,) and cu_q.is_contiguous() and
+            cu_q.get_device() == cache._index):
+        _vector(cu_q, _I32, B + 1, cache, "cu_q")
+    st = lib.sp24_attention_prompt(q.data_ptr(), rows, ldq, heads, cu_q.data_ptr(), B, cache._address, page_table.data_ptr(),
                                    width, ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
                                    _stream_of(stream, cache))
     if st:
