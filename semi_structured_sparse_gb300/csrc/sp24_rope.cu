@@ -10,10 +10,15 @@
 // walks its heads, 32 / (D / 8) of them at a time.  Of each head a lane has 4
 // values and, for half-split pairs, the 4 values that they are rotated with: a
 // rotation needs no other lane, and 4 cosines and 4 sines per lane do for all
-// heads.  (One 16-byte piece per lane, with the partners fetched by shuffles,
-// took 155 instructions per step and 70 registers; this takes about half, and
-// 8192 tokens went from 49.7 to 40.8 us, 5.0 TB/s.)  All of a warp's loads are issued
-// before the position is known.
+// heads.  All of a warp's loads are issued before the position is known.
+//
+// Measured (GB300): 8192 tokens of 32 + 8 + 8 heads of 128 33.7 us, 6.1 TB/s
+// (90 % of the measured copy rate); 3000 of 28 + 4 + 4 of 64 7.6 us; one token
+// 1.6 us.  What it took at 8192 tokens: one 16-byte piece per lane with the
+// partners fetched by shuffles, 49.7 us, 155 instructions per step; rotated
+// pairs within a lane and packed fp32 arithmetic, 40.8; a warp's heads all of
+// one kind and at fixed distances (no selects, no address arithmetic), 35.5; two
+// warps with 6 groups' loads each instead of four with 3, 33.7.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include "sp24_attn.cuh"
@@ -22,8 +27,8 @@
 namespace sp24 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kMany = 3;  // head groups whose loads a warp issues together in long calls
+constexpr int kWarps = 2;
+constexpr int kMany = 6;  // head groups whose loads a warp issues together in long calls
 
 struct RopeParams {
   const __nv_bfloat16* qkv;
@@ -58,44 +63,50 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// U head groups at a time: their loads are issued together.
-template <int D, bool E4M3, bool INTERLEAVED, int U>
+// U head groups at a time: their loads are issued together.  FEW: the token's
+// groups are spread over gridDim.y CTAs, one per warp.  EVEN: no group holds heads
+// of two kinds (queries, keys, values), so that a warp's lanes all do the same.
+template <int D, bool E4M3, bool INTERLEAVED, int U, bool FEW, bool EVEN>
 __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPH = D / 8;           // lanes per head
-  constexpr int HPW = 32 / LPH;        // heads per warp and step
+  constexpr int HPW = 32 / LPH;        // heads per group
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x;
   const int heads = p.q_heads + 2 * p.kv_heads, turned = p.q_heads + p.kv_heads;  // queries and keys
-  const int groups = (heads + HPW - 1) / HPW;
-  const int gstep = kWarps * gridDim.y;
   // This lane's elements of a head: four from ea, four from eb.  Half-split
   // pairs: (ea + i, eb + i), for the first rot / 8 lanes; neighbours otherwise.
   const int l = lane % LPH, pairs = INTERLEAVED ? 0 : p.rot / 8;
   const int ea = l < pairs ? 4 * l : 8 * l, eb = l < pairs ? p.rot / 2 + 4 * l : 8 * l + 4;
   const bool rotates = INTERLEAVED ? ea < p.rot : l < pairs;
-  const __nv_bfloat16* row = p.qkv + t * p.ldqkv;
+  const int sub = lane / LPH;
   pdl_wait();
 
+  // Loads of the groups at g0, g0 + kWarps, ...; a lane past the last head reads that head.
+  int hfirst = (FEW ? static_cast<int>(blockIdx.y) * kWarps + warp : warp) * HPW;  // uniform over the warp
+  const __nv_bfloat16* row = p.qkv + t * p.ldqkv;
   uint2 ra[U], rb[U];
-  auto load = [&](int g0) {
+  auto load = [&]() {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = (g0 + u * gstep) * HPW + lane / LPH;
-      ra[u] = rb[u] = make_uint2(0, 0);
-      if (h < heads) {
-        ra[u] = *reinterpret_cast<const uint2*>(row + h * D + ea);
-        rb[u] = *reinterpret_cast<const uint2*>(row + h * D + eb);
-      }
+      const int h = min(hfirst + u * (kWarps * HPW) + sub, heads - 1);
+      ra[u] = *reinterpret_cast<const uint2*>(row + h * D + ea);
+      rb[u] = *reinterpret_cast<const uint2*>(row + h * D + eb);
     }
   };
-  int g0 = blockIdx.y * kWarps + warp;
-  load(g0);
+  load();
 
-  uint2 wq[2], wk[2];
   const bool norm = p.q_weight != nullptr;
+  float2 wq[4], wk[4];
   if (norm) {
-    wq[0] = *reinterpret_cast<const uint2*>(p.q_weight + ea), wq[1] = *reinterpret_cast<const uint2*>(p.q_weight + eb);
-    wk[0] = *reinterpret_cast<const uint2*>(p.k_weight + ea), wk[1] = *reinterpret_cast<const uint2*>(p.k_weight + eb);
+    auto weights = [&](const __nv_bfloat16* w, float2 (&x)[4]) {
+      float2 y[2];
+      unpack4(*reinterpret_cast<const uint2*>(w + ea), y);
+      x[0] = y[0], x[1] = y[1];
+      unpack4(*reinterpret_cast<const uint2*>(w + eb), y);
+      x[2] = y[0], x[3] = y[1];
+    };
+    weights(p.q_weight, wq);
+    weights(p.k_weight, wk);
   }
   const int64_t slot = p.slots[t];
   const int64_t pos = p.rot > 0 ? p.positions[t] : 0;
@@ -110,7 +121,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const __grid_
   }
   // Half-split: pair i turns by (c[i], s[i]), i < 4.  Neighbours: the pairs of
   // ea turn by (c0.x, s0.x) and (c0.y, s0.y), those of eb by (c1, s1).
-  float2 c[2], s[2];
+  float2 c[2], s[2], ns[2];
   c[0] = c[1] = make_float2(1.0f, 1.0f);
   s[0] = s[1] = make_float2(0.0f, 0.0f);
   if (rotates) {
@@ -120,74 +131,96 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const __grid_
     c[0] = make_float2(cv.x, cv.y), c[1] = make_float2(cv.z, cv.w);
     s[0] = make_float2(sv.x, sv.y), s[1] = make_float2(sv.z, sv.w);
   }
+  ns[0] = make_float2(-s[0].x, -s[0].y), ns[1] = make_float2(-s[1].x, -s[1].y);
+  __nv_bfloat16* const q_row = p.q_out + t * p.ldq;
 
-  for (; g0 < groups; g0 += gstep * U) {
-    if (g0 != blockIdx.y * kWarps + warp) load(g0);
+  // Norm (weights w) and rotation of one head's values.
+  auto turn = [&](float2 (&a)[2], float2 (&b)[2], const float2 (&w)[4]) {
+    if (norm) {
+      float2 q = __fmul2_rn(a[0], a[0]);
+      q = __ffma2_rn(a[1], a[1], q);
+      q = __ffma2_rn(b[0], b[0], q);
+      q = __ffma2_rn(b[1], b[1], q);
+      float ss = q.x + q.y;
+#pragma unroll
+      for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
+      const float r = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
+      const float2 rr = make_float2(r, r);
+      a[0] = __fmul2_rn(a[0], __fmul2_rn(w[0], rr)), a[1] = __fmul2_rn(a[1], __fmul2_rn(w[1], rr));
+      b[0] = __fmul2_rn(b[0], __fmul2_rn(w[2], rr)), b[1] = __fmul2_rn(b[1], __fmul2_rn(w[3], rr));
+    }
+    if (!rotates) return;
+    if (INTERLEAVED) {
+      auto pair = [](float2 x, float cc, float ss) {
+        return make_float2(x.x * cc - x.y * ss, x.y * cc + x.x * ss);
+      };
+      a[0] = pair(a[0], c[0].x, s[0].x), a[1] = pair(a[1], c[0].y, s[0].y);
+      b[0] = pair(b[0], c[1].x, s[1].x), b[1] = pair(b[1], c[1].y, s[1].y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = a[i], y = b[i];
+        a[i] = __ffma2_rn(y, ns[i], __fmul2_rn(x, c[i]));
+        b[i] = __ffma2_rn(x, s[i], __fmul2_rn(y, c[i]));
+      }
+    }
+  };
+  auto put_query = [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+    *reinterpret_cast<uint2*>(q_row + h * D + ea) = pack4(a);
+    *reinterpret_cast<uint2*>(q_row + h * D + eb) = pack4(b);
+  };
+  auto put_cache = [&](const uint8_t* base, const float* scale, int hk, const float2 (&a)[2], const float2 (&b)[2]) {
+    if (!store) return;
+    uint8_t* dst = const_cast<uint8_t*>(base) + at + hk * p.cache.head_stride;
+    if (E4M3) {
+      const float d = scale[hk];
+      *reinterpret_cast<uint32_t*>(dst + ea) =
+          e4m3x4(__fdiv_rn(a[0].x, d), __fdiv_rn(a[0].y, d), __fdiv_rn(a[1].x, d), __fdiv_rn(a[1].y, d));
+      *reinterpret_cast<uint32_t*>(dst + eb) =
+          e4m3x4(__fdiv_rn(b[0].x, d), __fdiv_rn(b[0].y, d), __fdiv_rn(b[1].x, d), __fdiv_rn(b[1].y, d));
+    } else {
+      *reinterpret_cast<uint2*>(dst + 2 * ea) = pack4(a);
+      *reinterpret_cast<uint2*>(dst + 2 * eb) = pack4(b);
+    }
+  };
+
+  while (true) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int hfirst = (g0 + u * gstep) * HPW;  // uniform over the warp
-      if (hfirst >= heads) break;
-      const int h = hfirst + lane / LPH;
-      const bool query = h < p.q_heads;
-      const bool key = h < turned;  // or a query
+      const int hu = hfirst + u * (kWarps * HPW), h = hu + sub;
+      if (hu >= heads) break;  // uniform
       float2 a[2], b[2];
       unpack4(ra[u], a);
       unpack4(rb[u], b);
-      if (hfirst < turned) {
-        if (norm) {
-          float2 q = __fmul2_rn(a[0], a[0]);
-          q = __ffma2_rn(a[1], a[1], q);
-          q = __ffma2_rn(b[0], b[0], q);
-          q = __ffma2_rn(b[1], b[1], q);
-          float ss = q.x + q.y;
-#pragma unroll
-          for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
-          if (key) {
-            const float r = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
-            const float2 rr = make_float2(r, r);
-            float2 w[2];
-            unpack4(query ? wq[0] : wk[0], w);
-            a[0] = __fmul2_rn(__fmul2_rn(a[0], rr), w[0]), a[1] = __fmul2_rn(__fmul2_rn(a[1], rr), w[1]);
-            unpack4(query ? wq[1] : wk[1], w);
-            b[0] = __fmul2_rn(__fmul2_rn(b[0], rr), w[0]), b[1] = __fmul2_rn(__fmul2_rn(b[1], rr), w[1]);
-          }
-        }
-        if (rotates && key) {
-          if (INTERLEAVED) {
-            auto turn = [](float2 x, float cc, float ss) {
-              return make_float2(x.x * cc - x.y * ss, x.y * cc + x.x * ss);
-            };
-            a[0] = turn(a[0], c[0].x, s[0].x), a[1] = turn(a[1], c[0].y, s[0].y);
-            b[0] = turn(b[0], c[1].x, s[1].x), b[1] = turn(b[1], c[1].y, s[1].y);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float2 x = a[i], y = b[i], n = make_float2(-s[i].x, -s[i].y);
-              a[i] = __ffma2_rn(y, n, __fmul2_rn(x, c[i]));
-              b[i] = __ffma2_rn(x, s[i], __fmul2_rn(y, c[i]));
-            }
-          }
-        }
-      }
-      if (query) {
-        __nv_bfloat16* dst = p.q_out + t * p.ldq + h * D;
-        *reinterpret_cast<uint2*>(dst + ea) = pack4(a);
-        *reinterpret_cast<uint2*>(dst + eb) = pack4(b);
-      } else if (h < heads && store) {
-        const int hk = h - (key ? p.q_heads : turned);
-        uint8_t* dst = const_cast<uint8_t*>(key ? p.cache.k : p.cache.v) + at + hk * p.cache.head_stride;
-        if (E4M3) {
-          const float d = (key ? p.cache.k_scale : p.cache.v_scale)[hk];
-          *reinterpret_cast<uint32_t*>(dst + ea) = e4m3x4(__fdiv_rn(a[0].x, d), __fdiv_rn(a[0].y, d),
-                                                          __fdiv_rn(a[1].x, d), __fdiv_rn(a[1].y, d));
-          *reinterpret_cast<uint32_t*>(dst + eb) = e4m3x4(__fdiv_rn(b[0].x, d), __fdiv_rn(b[0].y, d),
-                                                          __fdiv_rn(b[1].x, d), __fdiv_rn(b[1].y, d));
+      if (EVEN) {
+        if (hu < p.q_heads) {
+          turn(a, b, wq);
+          put_query(h, a, b);
+        } else if (hu < turned) {
+          turn(a, b, wk);
+          put_cache(p.cache.k, p.cache.k_scale, h - p.q_heads, a, b);
         } else {
-          *reinterpret_cast<uint2*>(dst + 2 * ea) = pack4(a);
-          *reinterpret_cast<uint2*>(dst + 2 * eb) = pack4(b);
+          put_cache(p.cache.v, p.cache.v_scale, h - turned, a, b);
         }
+      } else {
+        const bool query = h < p.q_heads, key = !query && h < turned;
+        const float2 va[2] = {a[0], a[1]}, vb[2] = {b[0], b[1]};
+        float2 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = query ? wq[i] : wk[i];
+        turn(a, b, w);
+        if (query)
+          put_query(h, a, b);
+        else if (key)
+          put_cache(p.cache.k, p.cache.k_scale, h - p.q_heads, a, b);
+        else if (h < heads)
+          put_cache(p.cache.v, p.cache.v_scale, h - turned, va, vb);
       }
     }
+    if (FEW) break;
+    hfirst += U * kWarps * HPW;
+    if (hfirst >= heads) break;  // uniform
+    load();
   }
   pdl_trigger();
 }
@@ -195,16 +228,16 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const __grid_
 template <int D, bool E4M3, bool INTERLEAVED>
 cudaError_t launch(const RopeParams& p, int64_t T, const DeviceInfo& dev, cudaStream_t s) {
   const int groups = (p.q_heads + 2 * p.kv_heads + 32 / (D / 8) - 1) / (32 / (D / 8));
-  // Few tokens: a warp per head group, so that one row's latency is one load's.
-  // Many: a CTA per token, whose warps have up to kMany groups' loads in flight
-  // (6: 41.6 us for 8192 tokens and 9.7 for 3000 of the 64-wide heads, against
-  // 40.8 and 7.8; warps that walk over tokens and prefetch the next one's values
-  // need too many registers: 40 to 55 us).  3000 tokens of the 64-wide heads:
-  // 7.8 us; one token: 1.5 us.
-  const bool few = T < 4 * dev.sm_count;
+  // Few tokens: a warp per head group, so that a call takes one load's latency.
+  // Many: a CTA per token (with 8192 tokens, a warp per group would read the
+  // table and the weights 24 times per token).
+  const bool few = T < 4 * dev.sm_count, even = p.q_heads % (32 / (D / 8)) == 0 && p.kv_heads % (32 / (D / 8)) == 0;
   const dim3 grid(static_cast<unsigned>(T), few ? static_cast<unsigned>((groups + kWarps - 1) / kWarps) : 1u);
-  if (few) return launch_pdl(qk_norm_rope_kernel<D, E4M3, INTERLEAVED, 1>, grid, dim3(kWarps * 32), 0, s, p);
-  return launch_pdl(qk_norm_rope_kernel<D, E4M3, INTERLEAVED, kMany>, grid, dim3(kWarps * 32), 0, s, p);
+  auto kern = few ? (even ? qk_norm_rope_kernel<D, E4M3, INTERLEAVED, 1, true, true>
+                          : qk_norm_rope_kernel<D, E4M3, INTERLEAVED, 1, true, false>)
+                  : (even ? qk_norm_rope_kernel<D, E4M3, INTERLEAVED, kMany, false, true>
+                          : qk_norm_rope_kernel<D, E4M3, INTERLEAVED, kMany, false, false>);
+  return launch_pdl(kern, grid, dim3(kWarps * 32), 0, s, p);
 }
 
 }  // namespace
