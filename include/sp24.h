@@ -4,7 +4,8 @@
  *
  *   Y[M,N] (bf16) = X[M,K] . W[N,K]^T  with W pruned 2:4 along K,
  *   both operands e4m3 with group-wise fp32 scales, plus an optional bf16
- *   side term X2[M,r] . W2[N,r]^T added into the same output.
+ *   side term X2[M,r] . W2[N,r]^T added into the same output; and, at the
+ * end, the attention operators that stand between such layers.
  *
  * General conventions
  *   - Pointers marked (device) are CUDA device pointers owned by the caller;
