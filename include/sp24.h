@@ -494,6 +494,13 @@ SP24_API size_t sp24_attention_decode_workspace_size(int q_heads, int heads, int
  *   q       (device) bf16 [T][q_heads * D], row stride ldq.
  *   cu_q    (device) int32 [B + 1], ascending from 0 to T.  Rows of Y that
  *           belong to no sequence are not written.
+ *   workspace, workspace_bytes: device scratch of at least
+ *           sp24_attention_prompt_workspace_size bytes, 16-byte aligned, of
+ *           any contents (may be NULL when that size is 0).  A call whose
+ *           rows leave SMs idle while the cache may be long cuts the keys of
+ *           its rows into parts, whose sums meet there and are added up in
+ *           order by a second launch.  With less than that size the keys are
+ *           not cut.  Calls that overlap on the GPU must not share it.
  *   Others as for sp24_attention_decode.
  * Values of a sequence's own tokens are finite: a weight of zero times an
  * infinite value is not a number.  (Places of the cache that no query of the
@@ -502,7 +509,13 @@ SP24_API size_t sp24_attention_decode_workspace_size(int q_heads, int heads, int
 SP24_API sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t ldq, int q_heads, const int32_t* cu_q,
                                            int64_t B, const sp24_kv_cache* cache, const int32_t* page_table,
                                            int64_t table_width, int64_t ld_table, const int32_t* seq_lens,
-                                           float scale, int window, int sinks, void* Y, int64_t ldy, void* stream);
+                                           float scale, int window, int sinks, void* Y, int64_t ldy, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* Device scratch bytes sp24_attention_prompt would use for a call of this
+ * shape on the current device (0: none). */
+SP24_API size_t sp24_attention_prompt_workspace_size(int64_t T, int64_t B, int q_heads, const sp24_kv_cache* cache,
+                                                     int64_t table_width, int window, int sinks);
 
 #ifdef __cplusplus
 }

@@ -58,7 +58,9 @@ SIGNATURES = {
     "sp24_qk_norm_rope": ([_P, _I64, _I64, _I, _P, _P, _F, _P, _I64, _I, _I, _P, _P, _P, _I64, _P, _P], _I),
     "sp24_attention_decode": ([_P, _I64, _I64, _I, _P, _P, _I64, _I64, _P, _F, _I, _I, _P, _I64, _P, _SZ, _P], _I),
     "sp24_attention_decode_workspace_size": ([_I, _I, _I], _SZ),
-    "sp24_attention_prompt": ([_P, _I64, _I64, _I, _P, _I64, _P, _P, _I64, _I64, _P, _F, _I, _I, _P, _I64, _P], _I),
+    "sp24_attention_prompt": ([_P, _I64, _I64, _I, _P, _I64, _P, _P, _I64, _I64, _P, _F, _I, _I, _P, _I64, _P, _SZ, _P],
+                              _I),
+    "sp24_attention_prompt_workspace_size": ([_I64, _I64, _I, _P, _I64, _I, _I], _SZ),
 }
 
 
@@ -683,21 +685,39 @@ def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = Non
     return out
 
 
+def attention_prompt_workspace_size(cache: KVCache, heads: int, rows: int, sequences: int, pages: int, window: int = 0,
+                                    sinks: int = 0) -> int:
+    """Device scratch bytes attention_prompt() would use for `rows` query rows of `heads`
+    heads in `sequences` sequences with page tables of `pages` entries (0: none)."""
+    return int(load().sp24_attention_prompt_workspace_size(rows, sequences, heads, cache._address, pages, window, sinks))
+
+
 def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float = None, window: int = 0,
-                     sinks: int = 0, out=None, stream=None):
+                     sinks: int = 0, out=None, workspace=None, stream=None):
     """Causal attention of a ragged batch of new tokens over the cache, which already
     holds them: sequence b has the rows cu_q[b] .. cu_q[b + 1] - 1 of q bf16 [T, heads,
     head dim], the last of the seq_lens[b] tokens that the cache holds for it.  cu_q int32
-    [B + 1]; the others as for attention_decode()."""
+    [B + 1]; the others as for attention_decode().  `workspace` (uint8, of any contents, at
+    least attention_prompt_workspace_size() bytes) is what few rows over a long cache are
+    split through; without one, a call that would use it allocates it."""
     lib = _lib or load()
     rows, ldq, heads, B, width, ld_table, lens_p, scale, out, ldy = _attention_args(
         q, cache, page_table, seq_lens, scale, out, stream)
     if not (isinstance(cu_q, torch.Tensor) and cu_q.dtype is _I32 and cu_q.shape == (B + 1,) and cu_q.is_contiguous() and
             cu_q.get_device() == cache._index):
         _vector(cu_q, _I32, B + 1, cache, "cu_q")
+    if workspace is None:
+        need = lib.sp24_attention_prompt_workspace_size(rows, B, heads, cache._address, width, window, sinks)
+        if need:
+            workspace = _new(need, _U8, stream, cache)
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and
+              workspace.get_device() == cache._index and workspace.is_contiguous()):
+        _dev_tensor(workspace, _U8, "workspace", cache.device)
+        raise ValueError("workspace must be contiguous")
     st = lib.sp24_attention_prompt(q.data_ptr(), rows, ldq, heads, cu_q.data_ptr(), B, cache._address, page_table.data_ptr(),
                                    width, ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
-                                   _stream_of(stream, cache))
+                                   None if workspace is None else workspace.data_ptr(),
+                                   0 if workspace is None else workspace.numel(), _stream_of(stream, cache))
     if st:
         _check(st, "sp24_attention_prompt")
     return out

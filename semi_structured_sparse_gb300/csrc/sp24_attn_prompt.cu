@@ -31,13 +31,18 @@
 // and draining took 16,000 cycles of a block's 92,000 at 8192 tokens.)
 //
 // Measured (GB300, one call after the other): 8192 tokens, 32/8 heads of 128,
-// 350 us, 1570 TFLOP/s of visible products (80 % of the measured bf16 rate);
-// 16001 tokens under a window of 4096 and 4 sinks, 28/4 heads of 64, 484 us,
-// 850 TFLOP/s; pieces of 1839 and 1629 tokens over 14000 in an e4m3 cache
-// 555 us, 1520 TFLOP/s.  A query tile's chain (S read 52 cycles, maximum 250,
-// exponentials 690, P written and seen 270, P V and Q K^T 1024 plus what the
-// other tile's MMAs take) is 2700 cycles per key tile, against 2048 of MMAs
-// for both tiles: tensor memory has no room for a second S.
+// 329 us, 1670 TFLOP/s of visible products (85 % of the measured bf16 rate);
+// 16001 tokens under a window of 4096 and 4 sinks, 28/4 heads of 64, 456 us,
+// 897 TFLOP/s; pieces of 1839 and 1629 tokens over 14000 in an e4m3 cache
+// 555 us, 1520 TFLOP/s.  With heads of 128 a query tile's chain (S read 52
+// cycles, the first half's exponentials beside the search for the maximum 450,
+// the second half's 350, P written and seen 200, the rest of P V and Q K^T 768
+// plus what the other tile's MMAs take) is 2600 cycles per key tile, against
+// 2048 of MMAs for both tiles: tensor memory has no room for a second S.
+//
+// Where a call's blocks leave SMs idle and its page tables are long, a block's
+// key tiles are cut into parts, each a block of the grid; a second, small launch
+// adds their O up.
 //
 // Places of a key tile that no row of the CTA sees are not loaded by whole
 // pages, and zeroed in V otherwise: 0 x NaN is not 0.  In S they are
@@ -46,6 +51,7 @@
 // With an e4m3 cache a further warpgroup turns the tiles' codes into f16
 // (exactly) between the copy and the MMA; the softmax warps scale each query
 // row by a power of two, so that bf16 queries fit f16's range.
+#include <algorithm>
 #include <cuda_bf16.h>
 #include "sp24_attn.cuh"
 #include "sp24_ptx.cuh"
@@ -55,6 +61,7 @@ namespace {
 
 constexpr int BM = 128;   // query rows per tile, two tiles per CTA
 constexpr int BN = 128;   // keys per tile
+constexpr int kLeastTiles = 4;  // key tiles of a part, at least, where a block's keys are cut
 
 struct PromptParams {
   int T, B;
@@ -69,6 +76,9 @@ struct PromptParams {
   __nv_bfloat16* y;
   int64_t ldy;
   int kv_heads, group, tile_tokens;  // tile_tokens = BM / group
+  int splits;      // parts that a block's key tiles are cut into
+  float* part;     // splits > 1: of each part, O [2 BM][D], and then of all parts, maxima and sums [2 BM][2]
+  int parts;       // how many `part` holds
   unsigned int* err;
 };
 
@@ -220,18 +230,23 @@ struct Work {
   int p0;            // position of that row's token
   int p_hi;          // the last position (the last visible key) of the CTA's rows
   int wlo, send;     // keys that some row sees: [0, send) and [wlo, p_hi]
-  int first, nst, nt;  // key tiles: 0 .. nst - 1 (sinks), then first, first + 1, ...; nt in all
+  int first, nst;    // key tiles: 0 .. nst - 1 (sinks), then first, first + 1, ...
+  int t0, nt;        // which of them: nt from number t0 on
+  int part;          // where this part's sums go (splits > 1)
 };
 
-__device__ __forceinline__ int tile_of(const Work& w, int i) { return i < w.nst ? i : w.first + i - w.nst; }
+__device__ __forceinline__ int tile_of(const Work& w, int i) {
+  return w.t0 + i < w.nst ? w.t0 + i : w.first + w.t0 + i - w.nst;
+}
 
 // Block `block` of the grid, as the warp sees it; `total`: blocks of 2
 // tile_tokens tokens in all sequences.  The last block of the last sequence
-// comes first, since late blocks of a prompt see the most keys; all kv heads of
-// a block come together.
+// comes first, since late blocks of a prompt see the most keys; all parts and kv
+// heads of a block come together.
 __device__ __forceinline__ void find_work(const PromptParams& p, int block, int total, int lane, Work* out) {
   const int tok = 2 * p.tile_tokens;
-  const int want = block < 0 ? -1 : total - 1 - block / p.kv_heads;
+  const int rank = block / p.kv_heads / p.splits, split = block / p.kv_heads % p.splits;
+  const int want = block < 0 ? -1 : total - 1 - rank;
   if (lane == 0) out->b = -1;
   __syncwarp();
   int seen = 0;
@@ -269,7 +284,10 @@ __device__ __forceinline__ void find_work(const PromptParams& p, int block, int 
       w.send = min(p.sinks, w.wlo);
       w.first = w.wlo / BN;
       w.nst = min((w.send + BN - 1) / BN, w.first);
-      w.nt = w.p_hi < 0 ? 0 : w.nst + w.p_hi / BN + 1 - w.first;
+      const int tiles = w.p_hi < 0 ? 0 : w.nst + w.p_hi / BN + 1 - w.first;
+      w.t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
+      w.nt = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits) - w.t0;
+      w.part = (rank * p.kv_heads + w.hk) * p.splits + split;
       *out = w;
     }
     seen = __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -377,7 +395,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         done_with(item);
         continue;
       }
-      float l = 0.0f;
+      float l = 0.0f, m = -INFINITY;
       if (w.nt > 0) {
         float c = p.scale * 1.4426950408889634f;
         if (E4M3) {
@@ -414,11 +432,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         // What the loop needs of the block, in registers: shared memory is busy with the MMAs' operands, and a read
         // would take some hundred cycles.
-        const int nt = w.nt, nst = w.nst, first = w.first * BN;
+        const int nt = w.nt, nst = w.nst - w.t0, first = w.first * BN;  // nst: sink tiles from here on
         const int p_min = w.p0 + x * p.tile_tokens, p_max = min(w.p_hi, p_min + p.tile_tokens - 1);
-        int base = nst > 0 ? 0 : first;
-        float m = -INFINITY;
-        for (int i = 0; i < nt; ++i, ++sn, base = i == nst ? first : base + BN) {
+        int base = tile_of(w, 0) * BN;
+        for (int i = 0; i < nt; ++i, ++sn, base = i == nst && nst > 0 ? first : base + BN) {
           ok = mbar_wait(&s_full[x], sn & 1);
           if (!ok) break;
           tc_fence_after();
@@ -540,31 +557,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ++on;
         tc_fence_after();
       }
-      // O / l to bf16, 32 dims at a time: a lane's 64 bytes of its row change places with those of its three neighbours,
-      // so that four lanes write 64 bytes of one row together.
-      const float f = l == 0.0f ? 0.0f : (E4M3 ? p.cache.v_scale[w.hk] : 1.0f) / l;
-      __nv_bfloat16* rows[4];
-      int rr = r;
-      asm volatile("" : "+r"(rr));  // worked out here, not ahead of the loop: S takes the registers there
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int rk = (rr & ~3) + k, tk = rk / p.group, ak = x * p.tile_tokens + tk;
-        rows[k] = tk < p.tile_tokens && ak < w.rows
-                      ? p.y + static_cast<int64_t>(w.row0 + ak) * p.ldy +
-                            static_cast<int64_t>(w.hk * p.group + rk - tk * p.group) * D + (lane & 3) * 8
-                      : nullptr;
-      }
-#pragma unroll 1
-      for (int j = 0; j < D; j += 32) {
-        uint32_t o[32];
-        if (w.nt > 0) {
-          tmem_ld32(to + j, o);
-          tmem_ld_wait();
-        }
-        uint32_t v[4][4];
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          v[k >> 2][k & 3] = f == 0.0f ? 0u : bf16x2_rn(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
+      // Out, a few dims at a time: a lane's 64 bytes of its row change places with those of its three neighbours, so that
+      // four lanes write 64 bytes of one row together.
+      auto exchange = [&](uint32_t (&v)[4][4]) {
 #pragma unroll
         for (int bit = 1; bit < 4; bit <<= 1)
 #pragma unroll
@@ -577,9 +572,53 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               (upper ? v[k][e] : v[k | bit][e]) = got;
             }
           }
+      };
+      int rr = r;
+      asm volatile("" : "+r"(rr));  // worked out here, not ahead of the loop: S takes the registers there
+      if (p.splits > 1) {
+        // This part's O as it is, and its maximum and sum; attention_join_kernel adds the parts up.
+        float* const o_part = p.part + static_cast<int64_t>(w.part) * (2 * BM * D) + x * (BM * D);
+        float* const ml = p.part + static_cast<int64_t>(p.parts) * (2 * BM * D) + w.part * (2 * BM * 2) + x * (BM * 2);
+        *reinterpret_cast<float2*>(ml + 2 * rr) = make_float2(m, l);
+#pragma unroll 1
+        for (int j = 0; j < D && w.nt > 0; j += 16) {
+          uint32_t v[4][4];
+          tmem_ld16(to + j, reinterpret_cast<uint32_t(&)[16]>(v));
+          tmem_ld_wait();
+          exchange(v);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (rows[k]) *reinterpret_cast<uint4*>(rows[k] + j) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(o_part + ((rr & ~3) + k) * D + j + (lane & 3) * 4) =
+                make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        }
+      } else {
+        const float f = l == 0.0f ? 0.0f : (E4M3 ? p.cache.v_scale[w.hk] : 1.0f) / l;
+        __nv_bfloat16* rows[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rk = (rr & ~3) + k, tk = rk / p.group, ak = x * p.tile_tokens + tk;
+          rows[k] = tk < p.tile_tokens && ak < w.rows
+                        ? p.y + static_cast<int64_t>(w.row0 + ak) * p.ldy +
+                              static_cast<int64_t>(w.hk * p.group + rk - tk * p.group) * D + (lane & 3) * 8
+                        : nullptr;
+        }
+#pragma unroll 1
+        for (int j = 0; j < D; j += 32) {
+          uint32_t o[32];
+          if (w.nt > 0) {
+            tmem_ld32(to + j, o);
+            tmem_ld_wait();
+          }
+          uint32_t v[4][4];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            v[k >> 2][k & 3] =
+                f == 0.0f ? 0u : bf16x2_rn(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
+          exchange(v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (rows[k]) *reinterpret_cast<uint4*>(rows[k] + j) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        }
       }
       tc_fence_before();  // O is read before this warp lets the next block's P V begin
       done_with(item);
@@ -877,9 +916,111 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
 }
 
+// Adds up the parts of the blocks' rows (splits > 1): a warp per row (two rows
+// with heads of 64), whose lanes first look at a part's maximum and sum each.
+// Always in the same order: the result does not depend on timing.
+constexpr int kJoinWarps = 4;
+constexpr int kMostSplits = 32;
+template <int D>
+constexpr int kJoinRows = kJoinWarps * (128 / D);  // rows per CTA
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ PromptParams p) {
+  __shared__ Work s_work;
+  constexpr int LPR = D / 4, RPW = 32 / LPR, CHUNKS = BM / kJoinRows<D>;  // lanes per row, rows per warp
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item = blockIdx.x / (2 * CHUNKS);  // rank * kv_heads + kv head
+  const int x = blockIdx.x / CHUNKS % 2, r = blockIdx.x % CHUNKS * kJoinRows<D> + warp * RPW + lane / LPR;
+  pdl_wait();
+  if (warp == 0) {
+    int total = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      const int lo = min(max(__ldg(p.cu_q + b), 0), p.T), hi = min(max(__ldg(p.cu_q + b + 1), lo), p.T);
+      total += (hi - lo + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
+    find_work(p, (item / p.kv_heads) * p.splits * p.kv_heads + item % p.kv_heads, total, lane, &s_work);
+  }
+  __syncthreads();
+  const Work w = s_work;
+  const int token = r / p.group, at = x * p.tile_tokens + token;
+  const bool mine = w.b >= 0 && token < p.tile_tokens && at < w.rows;
+  if (__any_sync(0xFFFFFFFFu, mine)) {
+    // (Rows of another token's, or of no one's, go along: their parts are there, too, or not a number.)
+    const int64_t row = static_cast<int64_t>(w.part) * (2 * BM) + x * BM + r;
+    const float* ml = p.part + static_cast<int64_t>(p.parts) * (2 * BM * D) + 2 * row;
+    const float* o = p.part + row * D + lane % LPR * 4;
+    float2 v[kMostSplits / LPR];  // parts lane % LPR and, with heads of 64, 16 more
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMostSplits / LPR; ++k) {
+      const int s = k * LPR + lane % LPR;
+      v[k] = s < p.splits ? __ldcg(reinterpret_cast<const float2*>(ml + s * (2 * BM * 2))) : make_float2(-INFINITY, 0.0f);
+      top = fmaxf(top, v[k].x);
+    }
+#pragma unroll
+    for (int m = LPR / 2; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+    const float use = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int k = 0; k < kMostSplits / LPR; ++k) {
+      v[k].x = ex2(v[k].x - use);
+      sum = fmaf(v[k].y, v[k].x, sum);
+    }
+#pragma unroll
+    for (int m = LPR / 2; m; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+    float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < kMostSplits / LPR; ++k) {
+#pragma unroll 8
+      for (int i = 0; i < LPR; ++i) {
+        const int s = k * LPR + i;
+        if (s >= p.splits) break;  // uniform
+        const float f = __shfl_sync(0xFFFFFFFFu, v[k].x, (lane & ~(LPR - 1)) + i);
+        if (f != 0.0f) {  // (a part without keys has written no O)
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(o + static_cast<int64_t>(s) * (2 * BM * D)));
+          acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
+          acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
+        }
+      }
+    }
+    if (mine) {
+      const float f = sum == 0.0f ? 0.0f : (p.cache.v_scale ? p.cache.v_scale[w.hk] : 1.0f) / sum;
+      __nv_bfloat16* y = p.y + static_cast<int64_t>(w.row0 + at) * p.ldy +
+                         static_cast<int64_t>(w.hk * p.group + r - token * p.group) * D + (lane % LPR) * 4;
+      *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
+    }
+  }
+  pdl_trigger();
+}
+
+// Blocks of query rows of a call, at most (every sequence's last may be partly
+// filled), and into how many parts each is cut: where the blocks leave SMs idle
+// and the cache may be long, one part per SM, of at least kLeastTiles key tiles.
+// (32/8 heads of 128, cut against whole: 16 rows over 100000 keys 74 us and
+// 900, 200 over 10000 41 and 121, 64 over 4000 19 and 48, 64 over 1000 19 and
+// 21.  With 6 tiles per part 64 over 4000 takes 22 us, with 8 23.)
+struct Shape {
+  int64_t blocks;
+  int splits;
+};
+inline Shape shape_of(int64_t T, int64_t B, int q_heads, const sp24_kv_cache& c, int64_t table_width, int window,
+                      int sinks, int sms) {
+  const int64_t tokens = 2 * (BM / (q_heads / c.heads));
+  Shape s = {T / tokens + B, 1};
+  int64_t keys = table_width * c.page_size;
+  if (window > 0) keys = std::min(keys, int64_t(window) + tokens + std::min(sinks, kMostTokens) + 2 * BN);
+  const int64_t idle = sms / std::max<int64_t>(1, s.blocks * c.heads);
+  const int64_t most = std::min<int64_t>({idle, keys / (kLeastTiles * BN), kMostSplits});
+  if (most > 1) s.splits = static_cast<int>(most);
+  return s;
+}
+inline size_t part_bytes(const Shape& s, int heads, int D) {
+  return s.splits > 1 ? static_cast<size_t>(s.blocks) * heads * s.splits * (2 * BM) * (D + 2) * 4 : 0;
+}
+
 template <int D, bool E4M3>
 sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_heads, const sp24_kv_cache& cache,
-                   cudaStream_t s) {
+                   int64_t blocks, cudaStream_t s) {
   using C = Cfg<D, E4M3>;
   CUtensorMap qmap, kmap, vmap;
   {
@@ -901,22 +1042,37 @@ sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_head
   auto kern = attention_prompt_kernel<C>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SP24_ERR_CUDA;
-  // Every sequence's last block may be partly filled.
-  const int64_t blocks = p.T / (2 * p.tile_tokens) + p.B;
-  if (blocks > INT32_MAX / p.kv_heads) return SP24_ERR_UNSUPPORTED;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks * p.kv_heads)), dim3(C::THREADS), C::SMEM, s, qmap, kmap,
-                    vmap, p) == cudaSuccess
-             ? SP24_OK
-             : SP24_ERR_CUDA;
+  if (launch_pdl(kern, dim3(static_cast<unsigned>(blocks * p.splits * p.kv_heads)), dim3(C::THREADS), C::SMEM, s, qmap,
+                 kmap, vmap, p) != cudaSuccess)
+    return SP24_ERR_CUDA;
+  if (p.splits > 1 &&
+      launch_pdl(attention_join_kernel<D>, dim3(static_cast<unsigned>(blocks * p.kv_heads * 2 * (BM / kJoinRows<D>))),
+                 dim3(kJoinWarps * 32), 0, s, p) != cudaSuccess)
+    return SP24_ERR_CUDA;
+  return SP24_OK;
 }
 
 }  // namespace
 }  // namespace sp24
 
+extern "C" size_t sp24_attention_prompt_workspace_size(int64_t T, int64_t B, int q_heads, const sp24_kv_cache* cache,
+                                                       int64_t table_width, int window, int sinks) {
+  using namespace sp24;
+  CacheView view;
+  const DeviceInfo* dev = nullptr;
+  if (check_cache(cache, &view) || T <= 0 || T > kMostTokens || B <= 0 || B > kMostTokens || q_heads < 1 ||
+      q_heads % cache->heads || q_heads / cache->heads > BM || table_width < 1 ||
+      table_width > (kMostTokens >> view.page_shift) || window < 0 || sinks < 0 || current_device(&dev))
+    return 0;
+  return part_bytes(shape_of(T, B, q_heads, *cache, table_width, effective_window(window), sinks, dev->sm_count),
+                    cache->heads, cache->head_dim);
+}
+
 extern "C" sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t ldq, int q_heads, const int32_t* cu_q,
                                              int64_t B, const sp24_kv_cache* cache, const int32_t* page_table,
                                              int64_t table_width, int64_t ld_table, const int32_t* seq_lens,
-                                             float scale, int window, int sinks, void* Y, int64_t ldy, void* stream) {
+                                             float scale, int window, int sinks, void* Y, int64_t ldy,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
   using namespace sp24;
   PromptParams p = {};
   if (sp24_status st = check_attention(q, T, ldq, q_heads, cache, page_table, table_width, ld_table, seq_lens, B, scale,
@@ -943,9 +1099,17 @@ extern "C" sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t l
   p.group = q_heads / cache->heads;
   p.tile_tokens = BM / p.group;
   p.err = dev->err_word;
+  Shape shape = shape_of(T, B, q_heads, *cache, table_width, p.window, sinks, dev->sm_count);
+  if (!aligned16(workspace)) return SP24_ERR_ALIGNMENT;
+  if (shape.splits > 1 && (!workspace || workspace_bytes < part_bytes(shape, cache->heads, cache->head_dim)))
+    shape.splits = 1;
+  if (shape.blocks * shape.splits > INT32_MAX / 2 / p.kv_heads) return SP24_ERR_UNSUPPORTED;
+  p.splits = shape.splits;
+  p.parts = static_cast<int>(shape.blocks * p.kv_heads * shape.splits);
+  p.part = static_cast<float*>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->dtype == SP24_E4M3;
   if (cache->head_dim == 128)
-    return e4m3 ? launch<128, true>(p, q, ldq, q_heads, *cache, s) : launch<128, false>(p, q, ldq, q_heads, *cache, s);
-  return e4m3 ? launch<64, true>(p, q, ldq, q_heads, *cache, s) : launch<64, false>(p, q, ldq, q_heads, *cache, s);
+    return e4m3 ? launch<128, true>(p, q, ldq, q_heads, *cache, shape.blocks, s) : launch<128, false>(p, q, ldq, q_heads, *cache, shape.blocks, s);
+  return e4m3 ? launch<64, true>(p, q, ldq, q_heads, *cache, shape.blocks, s) : launch<64, false>(p, q, ldq, q_heads, *cache, shape.blocks, s);
 }

@@ -38,7 +38,8 @@ def test_caches(lib, kw, status):
     a = ctypes.addressof(keep)
     assert lib.sp24_qk_norm_rope(P, 1, 512, 4, None, None, 1e-6, P, 9, 64, 0, P, P, P, 256, a, None) == status
     assert lib.sp24_attention_decode(P, 1, 256, 4, a, P, 3, 3, P, 1.0, 0, 0, P, 256, P, 1 << 30, None) == status
-    assert lib.sp24_attention_prompt(P, 1, 256, 4, P, 1, a, P, 3, 3, P, 1.0, 0, 0, P, 256, None) == status
+    assert lib.sp24_attention_prompt(P, 1, 256, 4, P, 1, a, P, 3, 3, P, 1.0, 0, 0, P, 256, None, 0, None) == status
+    assert lib.sp24_attention_prompt_workspace_size(1, 1, 4, a, 3, 0, 0) == 0
 
 
 def test_rope_arguments(lib):
@@ -73,7 +74,7 @@ def test_attention_arguments(lib):
         a = dict(q=P, T=2, ldq=256, hq=4, cu=P, B=2, c=ctypes.addressof(keep), t=P, w=3, ldt=3, n=P, scale=1.0, window=0,
                  sinks=0, y=P, ldy=256)
         a.update(kw)
-        return lib.sp24_attention_prompt(*a.values(), None)
+        return lib.sp24_attention_prompt(*a.values(), None, 0, None)
 
     for call in (decode, prompt):
         for kw in (dict(q=None), dict(y=None), dict(t=None), dict(n=None), dict(c=None), dict(B=-1), dict(hq=0),

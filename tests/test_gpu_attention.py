@@ -341,6 +341,43 @@ def test_prompt_many_sequences(sp24):
     run_prompt(sp24, new, prefix, 4, 2, 64, 16, False, False, 0, 0, seed=9)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new,prefix,hq,hkv,d,page,window,sinks", [
+    ([1], [5000], 4, 1, 128, 64, 0, 0),
+    ([70, 3], [4000, 10], 8, 2, 64, 16, 0, 0),             # the second sequence has less than one tile per part
+    ([5, 0, 2], [3000, 2000, -1], 7, 1, 64, 32, 0, 0),     # no new token; a row before the first
+    ([129], [2500], 1, 1, 128, 128, 0, 0),                 # two query tiles, the second with one row
+    ([40, 33], [4500, 300], 40, 1, 64, 16, 0, 0),
+    ([20], [6000], 2, 2, 128, 64, 2500, 700),              # sinks and window, over several parts
+    ([6], [-6], 4, 1, 64, 16, 0, 0),                       # nothing in the cache
+])
+def test_prompt_split_over_the_cache(sp24, new, prefix, hq, hkv, d, page, window, sinks, e4m3):
+    """Few rows over a long cache: the keys are cut into parts, and the parts' sums joined."""
+    lens = [max(0, a + b) for a, b in zip(new, prefix)]
+    s = Setup(sp24, lens, hkv, d, page, e4m3, False, seed=sum(new), extra_pages=5000 // page)
+    see = [sees(torch.arange(n - m, n), n, window, sinks) for n, m in zip(lens, new)]
+    cache, T = s.upload(), sum(new)
+    table = torch.zeros(len(new), max(s.table.shape[1], 5000 // page), dtype=torch.int32)  # room for more tokens
+    table[:, :s.table.shape[1]] = s.table
+    q = (2 * torch.randn(T, hq, d, generator=torch.Generator().manual_seed(T))).to(torch.bfloat16)
+    cu = torch.tensor([0] + new).cumsum(0).to(torch.int32)
+    need = sp24.attention_prompt_workspace_size(cache, hq, T, len(new), table.shape[1], window, sinks)
+    assert need > 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")  # any contents: NaN read as fp32
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    call = lambda **kw: sp24.attention_prompt(q.cuda(), cu.cuda(), cache, table.cuda(), n, window=window,  # noqa: E731
+                                              sinks=sinks, **kw)
+    y = call(workspace=ws)
+    assert torch.equal(call(workspace=ws), y) and torch.equal(call(), y)      # the same from run to run
+    whole = call(workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))  # not cut
+    sp24.last_device_error()
+    for b, m in enumerate(new):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        ref, size = attend(q[rows].double(), s.tokens("k", b), s.tokens("v", b), see[b], d ** -0.5)
+        assert_attention(y[rows], ref, size, "sequence %d" % b)
+        assert_attention(whole[rows], ref, size, "sequence %d, not cut" % b)
+
+
 def test_window_and_sinks_past_every_length(sp24):
     """The largest window and sinks that fit the argument are no limit at all."""
     most = 2 ** 31 - 1
