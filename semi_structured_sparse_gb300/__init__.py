@@ -707,7 +707,9 @@ def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float
             cu_q.get_device() == cache._index):
         _vector(cu_q, _I32, B + 1, cache, "cu_q")
     if workspace is None:
-        need = lib.sp24_attention_prompt_workspace_size(rows, B, heads, cache._address, width, window, sinks)
+        # (Page tables of fewer tokens are never cut: the library asks for 512 keys per part.)
+        need = width * cache.page_size >= 1024 and lib.sp24_attention_prompt_workspace_size(
+            rows, B, heads, cache._address, width, window, sinks)
         if need:
             workspace = _new(need, _U8, stream, cache)
     elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and

@@ -681,16 +681,14 @@ size_t workspace_bytes_for(int ctas, int heads, int D) {
 }
 
 template <int D, bool E4M3, int NH>
-sp24_status launch(const DecodeParams& p, int ctas, cudaStream_t s) {
-  auto kern = attention_decode_kernel<D, E4M3, NH>;
+sp24_status launch(const DecodeParams& p, const DeviceInfo& dev, int ctas, cudaStream_t s) {
   constexpr int TT = kHalf / (D * (E4M3 ? 1 : 2)) * kWarps;
   // Tile numbers are 32-bit: the host refuses what could pass them.
   const int64_t most = (int64_t(p.table_width) << p.cache.page_shift) / TT + 3;
   if (most * p.B > INT32_MAX / (int64_t(p.kv_heads) * p.head_blocks)) return SP24_ERR_UNSUPPORTED;
   const int smem = kSmem<D, E4M3, NH>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return SP24_ERR_CUDA;
-  return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, p) == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
+  const cudaError_t r = launch_pdl_smem<attention_decode_kernel<D, E4M3, NH>>(dev, dim3(ctas), dim3(kThreads), smem, s, p);
+  return r == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
 }
 
 }  // namespace
@@ -743,9 +741,9 @@ extern "C" sp24_status sp24_attention_decode(const void* q, int64_t B, int64_t l
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->dtype == SP24_E4M3;
   if (D == 128) {
-    if (hpc == 8) return e4m3 ? launch<128, true, 1>(p, ctas, s) : launch<128, false, 1>(p, ctas, s);
-    return e4m3 ? launch<128, true, 2>(p, ctas, s) : launch<128, false, 2>(p, ctas, s);
+    if (hpc == 8) return e4m3 ? launch<128, true, 1>(p, *dev, ctas, s) : launch<128, false, 1>(p, *dev, ctas, s);
+    return e4m3 ? launch<128, true, 2>(p, *dev, ctas, s) : launch<128, false, 2>(p, *dev, ctas, s);
   }
-  if (hpc == 8) return e4m3 ? launch<64, true, 1>(p, ctas, s) : launch<64, false, 1>(p, ctas, s);
-  return e4m3 ? launch<64, true, 2>(p, ctas, s) : launch<64, false, 2>(p, ctas, s);
+  if (hpc == 8) return e4m3 ? launch<64, true, 1>(p, *dev, ctas, s) : launch<64, false, 1>(p, *dev, ctas, s);
+  return e4m3 ? launch<64, true, 2>(p, *dev, ctas, s) : launch<64, false, 2>(p, *dev, ctas, s);
 }

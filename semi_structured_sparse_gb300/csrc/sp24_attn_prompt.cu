@@ -1020,7 +1020,7 @@ inline size_t part_bytes(const Shape& s, int heads, int D) {
 
 template <int D, bool E4M3>
 sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_heads, const sp24_kv_cache& cache,
-                   int64_t blocks, cudaStream_t s) {
+                   const DeviceInfo& dev, int64_t blocks, cudaStream_t s) {
   using C = Cfg<D, E4M3>;
   CUtensorMap qmap, kmap, vmap;
   {
@@ -1039,11 +1039,8 @@ sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_head
   const auto swizzle = E4M3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   if (sp24_status st = make_tmap_nd(&kmap, cache.k, type, 4, dims, strides, box, swizzle)) return st;
   if (sp24_status st = make_tmap_nd(&vmap, cache.v, type, 4, dims, strides, box, swizzle)) return st;
-  auto kern = attention_prompt_kernel<C>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return SP24_ERR_CUDA;
-  if (launch_pdl(kern, dim3(static_cast<unsigned>(blocks * p.splits * p.kv_heads)), dim3(C::THREADS), C::SMEM, s, qmap,
-                 kmap, vmap, p) != cudaSuccess)
+  if (launch_pdl_smem<attention_prompt_kernel<C>>(dev, dim3(static_cast<unsigned>(blocks * p.splits * p.kv_heads)),
+                                                  dim3(C::THREADS), C::SMEM, s, qmap, kmap, vmap, p) != cudaSuccess)
     return SP24_ERR_CUDA;
   if (p.splits > 1 &&
       launch_pdl(attention_join_kernel<D>, dim3(static_cast<unsigned>(blocks * p.kv_heads * 2 * (BM / kJoinRows<D>))),
@@ -1110,6 +1107,6 @@ extern "C" sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t l
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->dtype == SP24_E4M3;
   if (cache->head_dim == 128)
-    return e4m3 ? launch<128, true>(p, q, ldq, q_heads, *cache, shape.blocks, s) : launch<128, false>(p, q, ldq, q_heads, *cache, shape.blocks, s);
-  return e4m3 ? launch<64, true>(p, q, ldq, q_heads, *cache, shape.blocks, s) : launch<64, false>(p, q, ldq, q_heads, *cache, shape.blocks, s);
+    return e4m3 ? launch<128, true>(p, q, ldq, q_heads, *cache, *dev, shape.blocks, s) : launch<128, false>(p, q, ldq, q_heads, *cache, *dev, shape.blocks, s);
+  return e4m3 ? launch<64, true>(p, q, ldq, q_heads, *cache, *dev, shape.blocks, s) : launch<64, false>(p, q, ldq, q_heads, *cache, *dev, shape.blocks, s);
 }

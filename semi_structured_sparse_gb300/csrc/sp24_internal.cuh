@@ -5,6 +5,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 #include <cstddef>
 #include "../../include/sp24.h"
@@ -64,6 +65,33 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
+// The same for a kernel that needs more shared memory than a kernel has by
+// default: asks for it on each device's first launch (each time would cost a
+// fifth of a microsecond), and again if a launch fails for its sake, as after a reset of
+// the device's context.
+template <auto Kern, typename... Args>
+inline cudaError_t launch_pdl_smem(const DeviceInfo& dev, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                   const Args&... args) {
+  static std::atomic<uint64_t> asked{0};  // a bit per device
+  const uint64_t bit = uint64_t(1) << (dev.ordinal & 63);
+  auto ask = [&] {
+    return cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  };
+  const bool before = asked.load(std::memory_order_relaxed) & bit;
+  if (!before) {
+    const cudaError_t r = ask();
+    if (r != cudaSuccess) return r;
+    asked.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaError_t r = launch_pdl(Kern, grid, block, smem, stream, args...);
+  if (r == cudaErrorInvalidValue && before) {
+    (void)cudaGetLastError();
+    r = ask();
+    if (r == cudaSuccess) r = launch_pdl(Kern, grid, block, smem, stream, args...);
+  }
+  return r;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
