@@ -31,9 +31,9 @@
 // and draining took 16,000 cycles of a block's 92,000 at 8192 tokens.)
 //
 // Measured (GB300, one call after the other): 8192 tokens, 32/8 heads of 128,
-// 329 us, 1670 TFLOP/s of visible products (85 % of the measured bf16 rate);
-// 16001 tokens under a window of 4096 and 4 sinks, 28/4 heads of 64, 456 us,
-// 897 TFLOP/s; pieces of 1839 and 1629 tokens over 14000 in an e4m3 cache
+// 325 us, 1690 TFLOP/s of visible products (86 % of the measured bf16 rate);
+// 16001 tokens under a window of 4096 and 4 sinks, 28/4 heads of 64, 452 us,
+// 907 TFLOP/s; pieces of 1839 and 1629 tokens over 14000 in an e4m3 cache
 // 555 us, 1520 TFLOP/s.  With heads of 128 a query tile's chain (S read 52
 // cycles, the first half's exponentials beside the search for the maximum 450,
 // the second half's 350, P written and seen 200, the rest of P V and Q K^T 768
@@ -76,6 +76,7 @@ struct PromptParams {
   __nv_bfloat16* y;
   int64_t ldy;
   int kv_heads, group, tile_tokens;  // tile_tokens = BM / group
+  unsigned int inv_group;            // ceil(2^16 / group)
   int splits;      // parts that a block's key tiles are cut into
   float* part;     // splits > 1: of each part, O [2 BM][D], and then of all parts, maxima and sums [2 BM][2]
   int parts;       // how many `part` holds
@@ -222,6 +223,12 @@ __device__ __forceinline__ int stolen_block(const void* response) {
   return ok ? static_cast<int>(x) : -1;
 }
 
+// Token of a tile's row r < BM: r / group.  r (inv_group - 2^16 / group) is below 128, so the quotient is off by less
+// than 128 / 2^16 < 1 / group.
+__device__ __forceinline__ int token_of(const PromptParams& p, int r) {
+  return static_cast<int>(static_cast<unsigned int>(r) * p.inv_group >> 16);
+}
+
 // What a CTA works on.
 struct Work {
   int b;             // sequence, or -1: nothing
@@ -239,26 +246,55 @@ __device__ __forceinline__ int tile_of(const Work& w, int i) {
   return w.t0 + i < w.nst ? w.t0 + i : w.first + w.t0 + i - w.nst;
 }
 
+// Rows [lo, hi) of q of a sequence, and the tokens in its cache.
+struct Rows {
+  int lo, hi, n;
+};
+__device__ __forceinline__ Rows rows_of(const PromptParams& p, int b, bool report) {
+  Rows s = {0, 0, 0};
+  if (b < p.B) {
+    const int a = __ldg(p.cu_q + b), z = __ldg(p.cu_q + b + 1);
+    s.n = __ldg(p.seq_lens + b);
+    s.lo = min(max(a, 0), p.T), s.hi = min(max(z, s.lo), p.T);
+    const int most = p.table_width << p.cache.page_shift;
+    const bool bad = s.n < 0 || s.n > most;
+    if (bad) s.n = s.n < 0 ? 0 : most;
+    if (report && (bad || s.lo != a || s.hi != z)) atomicOr(p.err, DEVERR_INDEX);
+  }
+  return s;
+}
+// Blocks of all sequences, over the warp; `mine`: sequence `lane`'s rows.
+__device__ __forceinline__ int count_blocks(const PromptParams& p, int lane, bool report, Rows& mine) {
+  const int tok = 2 * p.tile_tokens;
+  mine = rows_of(p, lane, report);
+  int total = (mine.hi - mine.lo + tok - 1) / tok;
+  for (int b = lane + 32; b < p.B; b += 32) {
+    const Rows s = rows_of(p, b, report);
+    total += (s.hi - s.lo + tok - 1) / tok;
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
+  return total;
+}
+
 // Block `block` of the grid, as the warp sees it; `total`: blocks of 2
-// tile_tokens tokens in all sequences.  The last block of the last sequence
+// tile_tokens tokens in all sequences; `mine`: sequence `lane`'s rows, where
+// they are at hand.  The last block of the last sequence
 // comes first, since late blocks of a prompt see the most keys; all parts and kv
 // heads of a block come together.
-__device__ __forceinline__ void find_work(const PromptParams& p, int block, int total, int lane, Work* out) {
+__device__ __forceinline__ void find_work(const PromptParams& p, int block, int total, const Rows* mine, int lane,
+                                          Work* out) {
   const int tok = 2 * p.tile_tokens;
-  const int rank = block / p.kv_heads / p.splits, split = block / p.kv_heads % p.splits;
+  const int group = block / p.kv_heads;  // of blocks that differ in the kv head alone
+  const int rank = p.splits > 1 ? group / p.splits : group, split = group - rank * p.splits;
   const int want = block < 0 ? -1 : total - 1 - rank;
   if (lane == 0) out->b = -1;
   __syncwarp();
   int seen = 0;
   for (int b0 = 0; want >= 0 && b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int lo = 0, hi = 0, n = 0;
-    if (b < p.B) {
-      lo = min(max(__ldg(p.cu_q + b), 0), p.T);
-      hi = min(max(__ldg(p.cu_q + b + 1), lo), p.T);
-      n = __ldg(p.seq_lens + b);
-    }
-    const int own = (hi - lo + tok - 1) / tok;
+    const Rows s = b0 == 0 && mine ? *mine : rows_of(p, b, false);
+    const int own = (s.hi - s.lo + tok - 1) / tok;
     int incl = own;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -269,24 +305,22 @@ __device__ __forceinline__ void find_work(const PromptParams& p, int block, int 
     if (want < incl && want >= incl - own) {
       Work w;
       w.b = b;
-      w.hk = block % p.kv_heads;
-      const int i0 = (want - (incl - own)) * tok, m = hi - lo;
-      const int most = p.table_width << p.cache.page_shift;
-      if (n < 0 || n > most) {
-        atomicOr(p.err, DEVERR_INDEX);
-        n = n < 0 ? 0 : most;
-      }
-      w.row0 = lo + i0;
+      w.hk = block - group * p.kv_heads;
+      const int i0 = (want - (incl - own)) * tok, m = s.hi - s.lo;
+      w.row0 = s.lo + i0;
       w.rows = m - i0;
-      w.p0 = n - m + i0;
+      w.p0 = s.n - m + i0;
       w.p_hi = w.p0 + min(tok, w.rows) - 1;
       w.wlo = p.window > 0 ? max(0, w.p0 - p.window + 1) : 0;
       w.send = min(p.sinks, w.wlo);
       w.first = w.wlo / BN;
       w.nst = min((w.send + BN - 1) / BN, w.first);
       const int tiles = w.p_hi < 0 ? 0 : w.nst + w.p_hi / BN + 1 - w.first;
-      w.t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
-      w.nt = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits) - w.t0;
+      w.t0 = 0, w.nt = tiles;
+      if (p.splits > 1) {  // (tiles: below 2^24; splits: at most 32)
+        w.t0 = tiles * split / p.splits;
+        w.nt = tiles * (split + 1) / p.splits - w.t0;
+      }
       w.part = (rank * p.kv_heads + w.hk) * p.splits + split;
       *out = w;
     }
@@ -456,7 +490,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // (The position is worked out here, once or twice per block, to leave the registers to S.)
             int rr = r;
             asm volatile("" : "+r"(rr));  // here, not ahead of the loop
-            const int token = rr / p.group;
+            const int token = token_of(p, rr);
             // (rows past the tile's tokens are no one's)
             const int hi = token < p.tile_tokens ? p_min + token - base : BN, lo = hi - p.window, sk = p.sinks - base;
             // Each 32 columns only where some row of the warp does not see them all.
@@ -596,7 +630,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __nv_bfloat16* rows[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int rk = (rr & ~3) + k, tk = rk / p.group, ak = x * p.tile_tokens + tk;
+          const int rk = (rr & ~3) + k, tk = token_of(p, rk), ak = x * p.tile_tokens + tk;
           rows[k] = tk < p.tile_tokens && ak < w.rows
                         ? p.y + static_cast<int64_t>(w.row0 + ak) * p.ldy +
                               static_cast<int64_t>(w.hk * p.group + rk - tk * p.group) * D + (lane & 3) * 8
@@ -766,25 +800,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       bool ok = true, asked = false;
       int ring = 0, last = -1, block = blockIdx.x, total = 0;
       uint32_t qn[2] = {0, 0};
-      if (keys) {
-        bool bad = false;
-        for (int b = lane; b < p.B; b += 32) {
-          const int a = __ldg(p.cu_q + b), z = __ldg(p.cu_q + b + 1);
-          const int lo = min(max(a, 0), p.T), hi = min(max(z, lo), p.T);
-          bad |= lo != a || hi != z;
-          total += (hi - lo + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-        }
-        if (bad && blockIdx.x == 0) atomicOr(p.err, DEVERR_INDEX);
-#pragma unroll
-        for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
-      }
+      Rows mine = {0, 0, 0};
+      if (keys) total = count_blocks(p, lane, blockIdx.x == 0, mine);
       int item = 0;
       for (; ok; ++item) {
         Work w;
         if (keys) {
           if (item >= 2) ok = mbar_wait(&work_empty[item & 1], ((item >> 1) - 1) & 1);
           if (!ok) break;
-          find_work(p, block, total, lane, &s_work[item & 1]);
+          find_work(p, block, total, item == 0 ? &mine : nullptr, lane, &s_work[item & 1]);
           w = s_work[item & 1];
           if (lane == 0) mbar_arrive(&work_full[item & 1]);
           if (w.b < 0) break;
@@ -932,18 +956,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
   const int x = blockIdx.x / CHUNKS % 2, r = blockIdx.x % CHUNKS * kJoinRows<D> + warp * RPW + lane / LPR;
   pdl_wait();
   if (warp == 0) {
-    int total = 0;
-    for (int b = lane; b < p.B; b += 32) {
-      const int lo = min(max(__ldg(p.cu_q + b), 0), p.T), hi = min(max(__ldg(p.cu_q + b + 1), lo), p.T);
-      total += (hi - lo + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-    }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
-    find_work(p, (item / p.kv_heads) * p.splits * p.kv_heads + item % p.kv_heads, total, lane, &s_work);
+    Rows mine;
+    const int total = count_blocks(p, lane, false, mine);
+    find_work(p, (item / p.kv_heads) * p.splits * p.kv_heads + item % p.kv_heads, total, &mine, lane,
+              &s_work);
   }
   __syncthreads();
   const Work w = s_work;
-  const int token = r / p.group, at = x * p.tile_tokens + token;
+  const int token = token_of(p, r), at = x * p.tile_tokens + token;
   const bool mine = w.b >= 0 && token < p.tile_tokens && at < w.rows;
   if (__any_sync(0xFFFFFFFFu, mine)) {
     // (Rows of another token's, or of no one's, go along: their parts are there, too, or not a number.)
@@ -1095,6 +1115,7 @@ extern "C" sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t l
   p.kv_heads = cache->heads;
   p.group = q_heads / cache->heads;
   p.tile_tokens = BM / p.group;
+  p.inv_group = (65536u + p.group - 1) / p.group;
   p.err = dev->err_word;
   Shape shape = shape_of(T, B, q_heads, *cache, table_width, p.window, sinks, dev->sm_count);
   if (!aligned16(workspace)) return SP24_ERR_ALIGNMENT;
