@@ -28,10 +28,10 @@
 //
 // Measured (GB300, 32/8 heads of 128 but for the last): one sequence of 131071
 // tokens 87 us, 6.2 TB/s (91 % of the measured copy rate); 64 of 1 to 16000
-// in an e4m3 cache 171 us, 6.2 TB/s (92 %); one of 1000 tokens 7.1 us, of
+// in an e4m3 cache 170 us, 6.3 TB/s (93 %); one of 1000 tokens 7.3 us, of
 // which the keys take 1: launch, lengths, pages, keys and the join of 16 pieces
 // are a chain of seven memory latencies; 128 of up to 9000 tokens under a
-// window of 2000 with 4 sinks, 28/4 heads of 64, 45.3 us, 5.2 TB/s (76 %).
+// window of 2000 with 4 sinks, 28/4 heads of 64, 45.1 us, 5.2 TB/s (76 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "sp24_attn.cuh"
