@@ -6,14 +6,15 @@
 //   (times the cache's scale), m a row maximum that follows the true one
 //
 // Bound by the tensor core (4 D operations per visible key and query row) with
-// heads of 128, and as much by the exponentials with heads of 64.  A block is
-// 256 query rows of one kv head, as two tiles of 128: the rows of a tile are (token, head of the group)
-// pairs, so a short prompt fills tiles too and all heads of a group share the
-// keys' copies.  Keys and values come in tiles of 128 tokens, one TMA box per
+// heads of 128, by the softmax warps with heads of 64.  A block is 256 query
+// rows of one kv head, as two tiles of 128: the rows of a tile are (token, head
+// of the group) pairs, so a short prompt fills tiles too and all heads of a
+// group share the keys' copies.  Keys and values come in tiles of 128 tokens, one TMA box per
 // page and 64 dims, through a ring of shared memory.  Per key tile and query
 // tile, S (128 x 128 fp32) and O (128 x D fp32) are in tensor memory, all 512
-// columns of it; P goes back into the columns of S as bf16 (f16 for an e4m3
-// cache) and is the A operand of P V straight from there.
+// columns of it; P goes back into the columns of S (into columns of its own with
+// heads of 64) as bf16 (f16 for an e4m3 cache) and is the A operand of P V
+// straight from there.
 //
 // Two softmax warpgroups (a thread per query row: maxima and sums need no
 // shuffles) alternate with the tensor core: while one works on its tile, the
@@ -100,9 +101,10 @@ struct Cfg {
   static constexpr int REG_SOFTMAX = E4M3 ? 208 : 216;
   static constexpr int REG_ISSUE = E4M3 ? 48 : 64;
   static constexpr int REG_CONVERT = 48;
-  // Whether P V begins when half of P is there.  It shortens the chain S -> P -> O -> next S of a query tile (8192
-  // tokens: 350 us against 354; with a window, heads of 64: 484 against 496), but not beside the e4m3 conversion
-  // (576 us against 555).
+  // Whether P V begins when half of P is there.  It shortens the chain S -> P ->
+  // O -> next S of a query tile (8192 tokens: 350 us against 354, when it was
+  // added), but costs beside the e4m3 conversion (576 us against 555) and with P
+  // apart (460 against 454).
   static constexpr bool EARLY = !E4M3 && D == 128;
   // Whether P has columns of its own in tensor memory (heads of 64 leave room
   // for it).  Then Q K^T of the next key tile runs while the softmax warps are
@@ -279,9 +281,9 @@ __device__ __forceinline__ int count_blocks(const PromptParams& p, int lane, boo
 
 // Block `block` of the grid, as the warp sees it; `total`: blocks of 2
 // tile_tokens tokens in all sequences; `mine`: sequence `lane`'s rows, where
-// they are at hand.  The last block of the last sequence
-// comes first, since late blocks of a prompt see the most keys; all parts and kv
-// heads of a block come together.
+// they are at hand.  The last block of the last sequence comes first, since late
+// blocks of a prompt see the most keys; all parts and kv heads of a block come
+// together.
 __device__ __forceinline__ void find_work(const PromptParams& p, int block, int total, const Rows* mine, int lane,
                                           Work* out) {
   const int tok = 2 * p.tile_tokens;
@@ -735,7 +737,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ok = wait_kv(vn);
           if (!ok) break;
           if (!E4M3) {
-            // Rows of V that no row of the CTA sees: zeros (from both tiles' warps, each before its own MMAs).
+            // Rows of V that no row of the CTA sees: zeros, from both tiles' warps, each before its own MMAs (where the
+            // other's MMAs already read the same zeros).
             const int base = tile_of(w, i) * BN;
             auto clear = [&](int lo, int hi) {
               uint8_t* v = kv_s + (vn % SLOTS) * C::KV_TILE;
