@@ -550,6 +550,14 @@ def _stream_of(stream, cache):
     return torch.cuda.current_stream(cache.device).cuda_stream
 
 
+_MOST = 2 ** 31 - 1
+
+
+def _int32(n):
+    """A count of tokens that may pass 32 bits: above them it is all there are, and below zero stays below."""
+    return min(max(n, -1), _MOST)  # (ctypes would keep the low 32 bits)
+
+
 def _new(shape, dtype, stream, cache, zero=False):
     """Memory for a kernel on `stream`, from that stream's own pool."""
     make = torch.zeros if zero else torch.empty
@@ -671,6 +679,8 @@ def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = Non
         q, cache, page_table, seq_lens, scale, out, stream)
     if rows != B:
         raise ValueError("q has %d rows, page_table %d sequences" % (rows, B))
+    if not (0 <= window <= _MOST and 0 <= sinks <= _MOST):
+        window, sinks = _int32(window), _int32(sinks)
     if workspace is None:
         workspace = _new(attention_decode_workspace_size(cache, heads), torch.uint8, stream, cache, zero=True)
     elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and
@@ -689,7 +699,8 @@ def attention_prompt_workspace_size(cache: KVCache, heads: int, rows: int, seque
                                     sinks: int = 0) -> int:
     """Device scratch bytes attention_prompt() would use for `rows` query rows of `heads`
     heads in `sequences` sequences with page tables of `pages` entries (0: none)."""
-    return int(load().sp24_attention_prompt_workspace_size(rows, sequences, heads, cache._address, pages, window, sinks))
+    return int(load().sp24_attention_prompt_workspace_size(rows, sequences, heads, cache._address, pages, _int32(window),
+                                                           _int32(sinks)))
 
 
 def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float = None, window: int = 0,
@@ -706,6 +717,8 @@ def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float
     if not (isinstance(cu_q, torch.Tensor) and cu_q.dtype is _I32 and cu_q.shape == (B + 1,) and cu_q.is_contiguous() and
             cu_q.get_device() == cache._index):
         _vector(cu_q, _I32, B + 1, cache, "cu_q")
+    if not (0 <= window <= _MOST and 0 <= sinks <= _MOST):
+        window, sinks = _int32(window), _int32(sinks)
     if workspace is None:
         # (Page tables of fewer tokens are never cut: the library asks for 512 keys per part.)
         need = width * cache.page_size >= 1024 and lib.sp24_attention_prompt_workspace_size(

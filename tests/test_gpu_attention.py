@@ -485,3 +485,26 @@ def test_empty_calls(sp24):
     assert sp24.attention_prompt(z(0, 4, 64, t=bf), z(1), cache, z(0, 3), z(0)).shape == (0, 4, 64)
     assert sp24.attention_prompt(z(0, 4, 64, t=bf), z(3), cache, z(2, 3), z(2)).shape == (0, 4, 64)
     sp24.last_device_error()
+
+
+# ---------------------------------------------------------------- odd but valid arguments
+@pytest.mark.parametrize("window,sinks", [(2 ** 31, 0), (2 ** 63 - 1, 0), (2 ** 32 + 5, 0), (5, 2 ** 32), (5, 2 ** 63 - 1)])
+def test_counts_past_32_bits_see_everything(sp24, window, sinks):
+    """A window, or sinks, beyond any length: all keys are seen, as without a window."""
+    s = Setup(sp24, [70, 33], 2, 64, 16, False, False, seed=73)
+    cache, table = s.upload(), s.table.cuda()
+    lens = torch.tensor(s.lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(74)).to(torch.bfloat16).cuda()
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    assert torch.equal(sp24.attention_decode(q, cache, table, lens, window=window, sinks=sinks),
+                       sp24.attention_decode(q, cache, table, lens))
+    assert torch.equal(sp24.attention_prompt(q, cu, cache, table, lens, window=window, sinks=sinks),
+                       sp24.attention_prompt(q, cu, cache, table, lens))
+    assert sp24.attention_prompt_workspace_size(cache, 4, 2, 2, 5000, window, sinks) == \
+        sp24.attention_prompt_workspace_size(cache, 4, 2, 2, 5000)
+    for kw in (dict(window=-2 ** 32), dict(window=-2 ** 32 + 5), dict(window=5, sinks=-2 ** 32)):
+        with pytest.raises(ValueError):
+            sp24.attention_decode(q, cache, table, lens, **kw)
+        with pytest.raises(ValueError):
+            sp24.attention_prompt(q, cu, cache, table, lens, **kw)
+
