@@ -523,7 +523,7 @@ def _row_stride(t, cols):
             return 0
     elif len(shape) != 2 or shape[1] != cols or stride[1] != 1:
         return 0
-    return stride[0] if shape[0] > 1 else max(stride[0], cols)
+    return stride[0] if shape[0] > 1 else cols  # a lone row's stride is never stepped along
 
 
 def _vector(t, dtype, n, cache, name):

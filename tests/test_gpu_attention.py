@@ -508,3 +508,27 @@ def test_counts_past_32_bits_see_everything(sp24, window, sinks):
         with pytest.raises(ValueError):
             sp24.attention_prompt(q, cu, cache, table, lens, **kw)
 
+
+def test_a_lone_row_of_any_stride(sp24):
+    """With one token the row strides are not stepped along, so they need not be multiples of anything."""
+    s = Setup(sp24, [40], 2, 64, 16, False, False, seed=75)
+    cache, table = s.upload(), s.table.cuda()
+    lens = torch.tensor([40], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(76)
+
+    def lone(cols):
+        return torch.randn(3, cols + 3, generator=g).to(torch.bfloat16).cuda()[:1, :cols]  # rows cols + 3 apart
+
+    q, out = lone(256), lone(256)
+    assert q.stride(0) == 259
+    want = sp24.attention_decode(q.contiguous(), cache, table, lens)
+    assert torch.equal(sp24.attention_decode(q, cache, table, lens, out=out), want)
+    want = sp24.attention_prompt(q.contiguous(), cu, cache, table, lens)
+    assert torch.equal(sp24.attention_prompt(q, cu, cache, table, lens, out=out), want)
+    x = lone(8 * 64)
+    args = (4, cache, torch.tensor([2], dtype=torch.int32, device="cuda"), torch.tensor([-1], device="cuda"),
+            torch.randn(3, 64, generator=g).cuda())
+    want = sp24.qk_norm_rope(x.contiguous(), *args)
+    assert torch.equal(sp24.qk_norm_rope(x, *args, out=out).reshape(want.shape), want)
+    sp24.last_device_error()
