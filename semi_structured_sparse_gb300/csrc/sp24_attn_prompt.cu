@@ -698,15 +698,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const Work w = s_work[item & 1];
         if (!ok || w.b < 0) break;
         const int tiles = tiles_of(w), nt = w.nt;
+        // A slot is free when both warps have said so: each when its tile's MMAs have read it, or, for a tile without
+        // rows, when the copy has landed.  That warp must not leave positions out: a parity tells a phase from the one
+        // before it only, and copies may land in any order, so its wait in the next block could take a copy that is
+        // still on its way for one that has landed.  With an e4m3 cache it may, and the other warp speaks for both: the
+        // converting warps fill the ring in order, so a position that is filled says that all before it are.  (Going
+        // along there too makes the compiler spill: pieces in an e4m3 cache 583 us against 554.)
         if (nt == 0 || x >= tiles) {
-          ring += 2 * nt;
+          if (E4M3) {
+            ring += 2 * nt;
+          } else {
+            for (const int end = ring + 2 * nt; ring < end && ok; ++ring) {
+              ok = wait_kv(ring);
+              __syncwarp();  // the slot's next copy may land as soon as lane 0 has arrived
+              if (ok && lane == 0) mbar_arrive(&kv_empty[ring % SLOTS]);
+            }
+          }
           done_with(item);
           continue;
         }
-        // A slot is free when both tiles' MMAs have read it (a lone tile says so twice).
         auto release = [&](int n) {
           mma_commit(&kv_empty[n % SLOTS]);
-          if (tiles == 1) mma_commit(&kv_empty[n % SLOTS]);
+          if (E4M3 && tiles == 1) mma_commit(&kv_empty[n % SLOTS]);
         };
         ok = mbar_wait(E4M3 ? &q_ready[x] : &q_full[x], qn & 1) && wait_kv(ring);
         ++qn;
