@@ -448,8 +448,10 @@ SP24_API sp24_status sp24_qk_norm_rope(const void* qkv, int64_t T, int64_t ldqkv
  * and (window = 0, or j > p - window, or j < sinks).  Head h reads the
  * cache's head h / (q_heads / heads).  A sequence without a key gives zero.
  * Scores, their running maximum and sum, and the weighted sum of values are
- * fp32; the weights enter the tensor core rounded to bf16 (f16 for e4m3
- * caches), and Y is rounded once to bf16.
+ * fp32; the weights enter the tensor core rounded to bf16, or, for e4m3
+ * caches, to f16 (scaled up, so that f16's smallest step moves a weight by
+ * 2^-40 of the row's largest at most, 2^-32 in sp24_attention_prompt); and Y is
+ * rounded once to bf16.
  *
  *   q       (device) bf16 [B][q_heads * D], row stride ldq.
  *   page_table (device) int32 [B][table_width], row stride ld_table: the

@@ -153,6 +153,13 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int n, bool repor
   return s;
 }
 
+// With an e4m3 cache weights, and their sums, are 2^kUp times p_j: the largest is
+// 2^15, near f16's end, so that those down to 2^-29 of it keep all 11 bits, and
+// one is off by 2^-40 of the largest at most.  (With the largest at 1 f16's
+// smallest step is 2^-24 of it: of 131071 keys some 17 nats below one other, half
+// a percent of the sum, each would be rounded by up to a half.)
+constexpr float kUp = 15.0f;
+
 // Stages of a warp's ring.  e4m3: 3 (64 ragged sequences 169.6 us, 172.2 with
 // 2), but 2 where 16 heads' exchange buffer takes the room.  bf16: 2 (131071
 // tokens 86.6 us against 87.5, 128 windowed sequences 45.7 against 47.2).
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
       uint32_t pf[MT][NH][2];
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
-        float top[2] = {-INFINITY, -INFINITY}, use[2];
+        float top[2] = {-INFINITY, -INFINITY}, less[2];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           top[0] = fmaxf(top[0], fmaxf(s[i][n][0], s[i][n][2]));
@@ -486,8 +493,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
 #pragma unroll
           for (int mask = 4; mask < 32; mask <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], mask));
           const float now = fmaxf(m[n][x], top[x] * c[n][x]);
-          use[x] = now == -INFINITY ? 0.0f : now;
-          keep[x] = ex2(m[n][x] - use[x]);
+          const float use = now == -INFINITY ? 0.0f : now;
+          less[x] = E4M3 ? kUp - use : -use;
+          keep[x] = ex2(m[n][x] - use);
           moved |= now > m[n][x];
           m[n][x] = now;
         }
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
           float e[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            e[x] = ex2(fmaf(s[i][n][x], c[n][x & 1], -use[x & 1]));
+            e[x] = ex2(fmaf(s[i][n][x], c[n][x & 1], less[x & 1]));
             l[n][x & 1] += e[x];
           }
           // P^T with keys along k: [key g][heads 2t, 2t + 1] -> [head g][keys 2t, 2t + 1]

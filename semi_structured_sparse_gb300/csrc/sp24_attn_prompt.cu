@@ -21,8 +21,9 @@
 // MMAs run on the other's.  P V of key tile i and Q K^T of tile i + 1 are issued
 // back to back for a query tile; the tensor core runs them in order, so S may
 // overwrite P.  A row's O is rescaled only when its maximum has grown by more
-// than 2^8 (P then stays below 256, which bf16 and fp32 sums hold as well as
-// 1); that is rare after the first tiles, so the softmax warps do it themselves.
+// than 2^8 (P then stays below 256, which bf16 and fp32 sums hold as well as 1;
+// f16 has its own room for it, Cfg::UP); that is rare after the first tiles, so
+// the softmax warps do it themselves.
 //
 // One CTA per SM works through blocks: the first is its own, the others it
 // takes from the part of the grid that no SM has begun (cluster launch
@@ -116,6 +117,11 @@ struct Cfg {
   // cache (579 us against 555: the registers do not reach), nor with P apart
   // (P V of the last key tile is still reading P then).
   static constexpr bool AHEAD = D == 128 && !E4M3;
+  // With an e4m3 cache P, and its sums, are 2^UP times exp2(c S - m): up to 2^8
+  // times that where the maximum has grown by less, so up to 2^15, near f16's end.
+  // The row's largest weight is 2^7 at least; f16's smallest step, 2^-24, rounds
+  // the smallest weights by 2^-32 of it at most.
+  static constexpr float UP = 7.0f;
   static constexpr uint32_t P_COL = APART ? 2 * BN : 0, P_STEP = APART ? BN / 2 : BN;  // P of query tile x
   static constexpr uint32_t O_COL = APART ? 3 * BN : 2 * BN;                           // O of query tile x: + x D
 };
@@ -568,7 +574,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               }
             }
           }
-          const float less = m == -INFINITY ? 0.0f : -m;
+          const float less = m == -INFINITY ? 0.0f : E4M3 ? C::UP - m : -m;
           if (!ahead || any) {
             sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
