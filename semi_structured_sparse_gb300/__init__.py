@@ -538,12 +538,26 @@ def _matrix_of(t, dtype, cache, name, what):
         raise ValueError("%s must be %s, got %s" % (name, what, tuple(t.shape)))
 
 
+# The library launches on the calling thread's current GPU, which need not be the operands'.
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on(index, fn, *args):
+    """fn(*args) with the GPU `index` as the current one."""
+    if _current_gpu() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
 # The current stream's handle without a Stream object around it, where torch has that.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_of(stream, cache):
     if stream is not None:
+        if stream.device_index != cache._index:
+            raise ValueError("the stream is one of GPU %d, the cache is on GPU %d" % (stream.device_index, cache._index))
         return stream.cuda_stream
     if _raw_stream is not None:
         return _raw_stream(cache._index)
@@ -618,9 +632,9 @@ def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_w
             _vector(q_weight, _BF16, d, cache, "q_weight")
             _vector(k_weight, _BF16, d, cache, "k_weight")
         raise ValueError("cos_sin must be contiguous")
-    st = lib.sp24_qk_norm_rope(qkv.data_ptr(), T, ldqkv, heads, qw, kw, eps, cos_sin.data_ptr() if rot else None,
-                               max_pos, rot, 1 if interleaved else 0, positions.data_ptr(), slots.data_ptr(),
-                               out.data_ptr(), ldq, cache._address, _stream_of(stream, cache))
+    st = _on(at, lib.sp24_qk_norm_rope, qkv.data_ptr(), T, ldqkv, heads, qw, kw, eps, cos_sin.data_ptr() if rot else None,
+             max_pos, rot, 1 if interleaved else 0, positions.data_ptr(), slots.data_ptr(), out.data_ptr(), ldq,
+             cache._address, _stream_of(stream, cache))
     if st:
         _check(st, "sp24_qk_norm_rope")
     return out
@@ -628,7 +642,7 @@ def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_w
 
 def attention_decode_workspace_size(cache: KVCache, heads: int) -> int:
     """Device scratch bytes attention_decode() needs for `heads` query heads."""
-    return int(load().sp24_attention_decode_workspace_size(heads, cache.heads, cache.head_dim))
+    return int(_on(cache._index, load().sp24_attention_decode_workspace_size, heads, cache.heads, cache.head_dim))
 
 
 def _attention_args(q, cache, page_table, seq_lens, scale, out, stream):
@@ -687,9 +701,9 @@ def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = Non
               workspace.get_device() == cache._index and workspace.is_contiguous()):
         _dev_tensor(workspace, _U8, "workspace", cache.device)
         raise ValueError("workspace must be contiguous")
-    st = lib.sp24_attention_decode(q.data_ptr(), B, ldq, heads, cache._address, page_table.data_ptr(), width,
-                                   ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
-                                   workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache))
+    st = _on(cache._index, lib.sp24_attention_decode, q.data_ptr(), B, ldq, heads, cache._address, page_table.data_ptr(),
+             width, ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy, workspace.data_ptr(), workspace.numel(),
+             _stream_of(stream, cache))
     if st:
         _check(st, "sp24_attention_decode")
     return out
@@ -699,8 +713,8 @@ def attention_prompt_workspace_size(cache: KVCache, heads: int, rows: int, seque
                                     sinks: int = 0) -> int:
     """Device scratch bytes attention_prompt() would use for `rows` query rows of `heads`
     heads in `sequences` sequences with page tables of `pages` entries (0: none)."""
-    return int(load().sp24_attention_prompt_workspace_size(rows, sequences, heads, cache._address, pages, _int32(window),
-                                                           _int32(sinks)))
+    return int(_on(cache._index, load().sp24_attention_prompt_workspace_size, rows, sequences, heads, cache._address, pages,
+                   _int32(window), _int32(sinks)))
 
 
 def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float = None, window: int = 0,
@@ -721,18 +735,18 @@ def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float
         window, sinks = _int32(window), _int32(sinks)
     if workspace is None:
         # (Page tables of fewer tokens are never cut: the library asks for 512 keys per part.)
-        need = width * cache.page_size >= 1024 and lib.sp24_attention_prompt_workspace_size(
-            rows, B, heads, cache._address, width, window, sinks)
+        need = width * cache.page_size >= 1024 and _on(
+            cache._index, lib.sp24_attention_prompt_workspace_size, rows, B, heads, cache._address, width, window, sinks)
         if need:
             workspace = _new(need, _U8, stream, cache)
     elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and
               workspace.get_device() == cache._index and workspace.is_contiguous()):
         _dev_tensor(workspace, _U8, "workspace", cache.device)
         raise ValueError("workspace must be contiguous")
-    st = lib.sp24_attention_prompt(q.data_ptr(), rows, ldq, heads, cu_q.data_ptr(), B, cache._address, page_table.data_ptr(),
-                                   width, ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
-                                   None if workspace is None else workspace.data_ptr(),
-                                   0 if workspace is None else workspace.numel(), _stream_of(stream, cache))
+    st = _on(cache._index, lib.sp24_attention_prompt, q.data_ptr(), rows, ldq, heads, cu_q.data_ptr(), B, cache._address,
+             page_table.data_ptr(), width, ld_table, lens_p, scale, window, sinks, out.data_ptr(), ldy,
+             None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+             _stream_of(stream, cache))
     if st:
         _check(st, "sp24_attention_prompt")
     return out
@@ -740,5 +754,6 @@ def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float
 
 def last_device_error(stream=None):
     """Synchronise and raise if any library kernel gave up on a bounded wait, or met an
-    index out of range."""
-    _check(load().sp24_last_device_error(_stream(stream)), "device")
+    index out of range, on the stream's GPU (without a stream: on the current one)."""
+    index = _current_gpu() if stream is None else stream.device_index
+    _check(_on(index, load().sp24_last_device_error, _stream(stream)), "device")

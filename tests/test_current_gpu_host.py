@@ -1,0 +1,96 @@
+"""Calls work on the operands' GPU, whichever one is current (host logic: tensors of the CPU, whose index is -1, and a
+library that records which GPU was current when it was called)."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+import semi_structured_sparse_gb300 as s
+
+CPU = torch.device("cpu")
+
+
+class Library:
+    """Stands in for libsp24.so: every call succeeds, or gives a size of 64."""
+
+    def __init__(self, gpu):
+        self.gpu, self.calls = gpu, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, self.gpu.current))
+            return 64 if name.endswith("_workspace_size") else 0
+        return call
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    g = types.SimpleNamespace(current=0)
+
+    @contextlib.contextmanager
+    def device(index):
+        index = getattr(index, "index", index)
+        before, g.current = g.current, -1 if index is None else index
+        yield
+        g.current = before
+
+    g.lib = Library(g)
+    monkeypatch.setattr(s, "_lib", g.lib)
+    monkeypatch.setattr(s, "_current_gpu", lambda: g.current, raising=False)
+    monkeypatch.setattr(s, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    return g
+
+
+def cache():
+    c = s.KVCache.__new__(s.KVCache)
+    c.heads, c.page_size, c.head_dim, c.device, c._index, c._scale, c._address = 2, 16, 64, CPU, -1, 0.125, 0
+    return c
+
+
+def attention_calls(c):
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(2, 100, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32)
+    qkv = torch.zeros(2, 8 * 64, dtype=torch.bfloat16)
+    slots, turn = torch.zeros(2, dtype=torch.int64), torch.zeros(4, 64)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    return {
+        "sp24_qk_norm_rope": lambda **kw: s.qk_norm_rope(qkv, 4, c, lens, slots, turn, **kw),
+        "sp24_attention_decode": lambda **kw: s.attention_decode(q, c, table, lens, workspace=ws, **kw),
+        "sp24_attention_prompt": lambda **kw: s.attention_prompt(q, cu, c, table, lens, workspace=ws, **kw),
+    }
+
+
+@pytest.mark.parametrize("current", [0, -1])
+def test_attention_calls_work_on_the_caches_gpu(gpu, current):
+    gpu.current = current
+    c = cache()
+    for name, call in attention_calls(c).items():
+        call()
+        assert gpu.lib.calls[-1] == (name, -1)
+    assert s.attention_decode_workspace_size(c, 4) == 64
+    assert s.attention_prompt_workspace_size(c, 4, 2, 2, 100) == 64
+    # a prompt that asks for its workspace itself
+    s.attention_prompt(torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.tensor([0, 1, 2], dtype=torch.int32), c,
+                       torch.zeros(2, 100, dtype=torch.int32), torch.ones(2, dtype=torch.int32))
+    assert len(gpu.lib.calls) == 7 and {at for _, at in gpu.lib.calls} == {-1}
+    assert gpu.current == current
+
+
+def test_attention_calls_refuse_a_stream_of_another_gpu(gpu):
+    out = torch.zeros(2, 256, dtype=torch.bfloat16)
+    for call in attention_calls(cache()).values():
+        call(out=out, stream=types.SimpleNamespace(cuda_stream=7, device_index=-1))
+        done = len(gpu.lib.calls)
+        with pytest.raises(ValueError):
+            call(out=out, stream=types.SimpleNamespace(cuda_stream=7, device_index=0))
+        assert len(gpu.lib.calls) == done
+
+
+def test_device_errors_are_those_of_the_streams_gpu(gpu):
+    s.last_device_error(types.SimpleNamespace(cuda_stream=7, device_index=-1))
+    gpu.current = 3
+    s.last_device_error(types.SimpleNamespace(cuda_stream=7, device_index=3))
+    assert gpu.lib.calls == [("sp24_last_device_error", -1), ("sp24_last_device_error", 3)]
