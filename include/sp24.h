@@ -13,8 +13,7 @@
  *     (host) are ordinary host memory.
  *   - Calls work on the calling thread's current device: device pointers and
  *     `stream` are that device's (the C ABI cannot see whose they are; the
- *     Python binding makes the operands' device current for each attention
- *     call).
+ *     Python binding makes the operands' device current for each call).
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Every call is stream-ordered and asynchronous; none
  *     synchronises except sp24_last_device_error().

@@ -104,9 +104,25 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+# The library launches on the calling thread's current GPU, which need not be the operands'.
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on(index, fn, *args):
+    """fn(*args) with the GPU `index` as the current one."""
+    if _current_gpu() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
+def _stream(stream=None, index=None):
+    """The handle of `stream`, or of GPU `index`'s current stream; None: the current GPU's."""
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    elif index is not None and stream.device_index != index:
+        raise ValueError("the stream is one of GPU %d, the operands are on GPU %d" % (stream.device_index, index))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _dev_tensor(t, dtype, name, device=None):
@@ -209,8 +225,8 @@ def compress(w: torch.Tensor, gN: int = 1, gK: int = None, out=None, stream=None
         _at_least(values, N * (K // 2), "values")
         _at_least(meta, N * (K // 8), "meta")
         _at_least(scales, _scale_count(K, gK, N, gN), "scales")
-    _check(lib.sp24_fp8_compress(_ptr(w), N, K, w.stride(0), gN, gK, _ptr(values), _ptr(meta), _ptr(scales),
-                                 _stream(stream)), "sp24_fp8_compress")
+    _check(_on(w.get_device(), lib.sp24_fp8_compress, _ptr(w), N, K, w.stride(0), gN, gK, _ptr(values), _ptr(meta),
+               _ptr(scales), _stream(stream, w.get_device())), "sp24_fp8_compress")
     return values, meta, scales
 
 
@@ -233,8 +249,8 @@ def decompress(values, meta, scales, gN: int = 1, gK: int = None, out=None, stre
     else:
         W = _dev_tensor(out, torch.bfloat16, "out", values.device)
         _matrix(W, N, K, "out")
-    _check(lib.sp24_fp8_decompress(_ptr(values), _ptr(meta), _ptr(scales), N, K, gN, gK, _ptr(W), W.stride(0),
-                                   _stream(stream)), "sp24_fp8_decompress")
+    _check(_on(values.get_device(), lib.sp24_fp8_decompress, _ptr(values), _ptr(meta), _ptr(scales), N, K, gN, gK, _ptr(W),
+               W.stride(0), _stream(stream, values.get_device())), "sp24_fp8_decompress")
     return W
 
 
@@ -259,7 +275,7 @@ def quantize_act(x: torch.Tensor, gK: int = None, out=None, stream=None):
         _at_least(sx, _scale_count(K, gK, M, 1), "sx")
     f, name = ((lib.sp24_fp8_quantize_act_bf16, "sp24_fp8_quantize_act_bf16") if bf16
                else (lib.sp24_fp8_quantize_act, "sp24_fp8_quantize_act"))
-    _check(f(_ptr(x), M, K, x.stride(0), gK, _ptr(xq), _ptr(sx), _stream(stream)), name)
+    _check(_on(x.get_device(), f, _ptr(x), M, K, x.stride(0), gK, _ptr(xq), _ptr(sx), _stream(stream, x.get_device())), name)
     return xq, sx
 
 
@@ -306,17 +322,17 @@ def gemm(xq, sx, values, meta, sw, gM: int = 1, gN: int = 1, gK: int = None, x2=
     else:
         y = _dev_tensor(out, torch.bfloat16, "out", dev_)
         _matrix(y, M, N, "out")
-    ws_bytes = int(lib.sp24_fp8_gemm_workspace_size(M, N, K, r))
+    ws_bytes = int(_on(xq.get_device(), lib.sp24_fp8_gemm_workspace_size, M, N, K, r))
     if ws_bytes and workspace is None:
         workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=dev_)
     elif workspace is not None:
         _dev_tensor(workspace, torch.uint8, "workspace", dev_)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    _check(lib.sp24_fp8_gemm(_ptr(xq), _ptr(sx), M, K, xq.stride(0), gM, _ptr(values), _ptr(meta), _ptr(sw), N,
-                             gN, gK, _ptr(x2), _ptr(w2), r, _ptr(bias), _ptr(y), y.stride(0), _ptr(workspace),
-                             0 if workspace is None else workspace.numel() * workspace.element_size(),
-                             _stream(stream)), "sp24_fp8_gemm")
+    _check(_on(xq.get_device(), lib.sp24_fp8_gemm, _ptr(xq), _ptr(sx), M, K, xq.stride(0), gM, _ptr(values), _ptr(meta),
+               _ptr(sw), N, gN, gK, _ptr(x2), _ptr(w2), r, _ptr(bias), _ptr(y), y.stride(0), _ptr(workspace),
+               0 if workspace is None else workspace.numel() * workspace.element_size(),
+               _stream(stream, xq.get_device())), "sp24_fp8_gemm")
     return y
 
 
@@ -352,19 +368,19 @@ def gemm_batched(xq, sx, values, meta, sw, gM: int = 1, gN: int = 1, gK: int = N
         y = _dev_tensor(out, torch.bfloat16, "out", dev_)
         if y.dim() != 3 or tuple(y.shape) != (L, M, N) or y.stride(1) < N:
             raise ValueError("out must be [L, M, N]")
-    ws_bytes = L * int(lib.sp24_fp8_gemm_workspace_size(M, N, K, 0))
+    ws_bytes = L * int(_on(xq.get_device(), lib.sp24_fp8_gemm_workspace_size, M, N, K, 0))
     if ws_bytes and workspace is None:
         workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=dev_)
     elif workspace is not None:
         _dev_tensor(workspace, torch.uint8, "workspace", dev_)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    _check(lib.sp24_fp8_gemm_batched(
-        _ptr(xq), _ptr(sx), M, K, xq.stride(1), gM, _ptr(values), _ptr(meta), _ptr(sw), N, gN, gK, _ptr(bias),
+    _check(_on(
+        xq.get_device(), lib.sp24_fp8_gemm_batched, _ptr(xq), _ptr(sx), M, K, xq.stride(1), gM, _ptr(values), _ptr(meta), _ptr(sw), N, gN, gK, _ptr(bias),
         _ptr(y), y.stride(1), L, xq.stride(0), sx.stride(0), values.stride(0), meta.stride(0), sw.stride(0),
         0 if bias is None else bias.stride(0), y.stride(0), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
-        "sp24_fp8_gemm_batched")
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream, xq.get_device())), "sp24_fp8_gemm_batched")
     return y
 
 
@@ -390,8 +406,8 @@ def compress_int8(w: torch.Tensor, out=None, stream=None):
         _at_least(values, N * (K // 2), "values")
         _at_least(meta, N * (K // 8), "meta")
         _at_least(scales, N, "scales")
-    _check(lib.sp24_int8_compress(_ptr(w), N, K, w.stride(0), _ptr(values), _ptr(meta), _ptr(scales),
-                                  _stream(stream)), "sp24_int8_compress")
+    _check(_on(w.get_device(), lib.sp24_int8_compress, _ptr(w), N, K, w.stride(0), _ptr(values), _ptr(meta), _ptr(scales),
+               _stream(stream, w.get_device())), "sp24_int8_compress")
     return values, meta, scales
 
 
@@ -413,8 +429,8 @@ def quantize_act_int8(x: torch.Tensor, out=None, stream=None):
         if not xq.is_contiguous():
             raise ValueError("xq must be contiguous")
         _at_least(sx, M, "sx")
-    _check(lib.sp24_int8_quantize_act(_ptr(x), M, K, x.stride(0), _ptr(xq), _ptr(sx), _stream(stream)),
-           "sp24_int8_quantize_act")
+    _check(_on(x.get_device(), lib.sp24_int8_quantize_act, _ptr(x), M, K, x.stride(0), _ptr(xq), _ptr(sx),
+               _stream(stream, x.get_device())), "sp24_int8_quantize_act")
     return xq, sx
 
 
@@ -447,8 +463,8 @@ def gemm_int8(xq, sx, values, meta, sw, bias=None, out=None, stream=None):
     else:
         y = _dev_tensor(out, torch.bfloat16, "out", dev_)
         _matrix(y, M, N, "out")
-    _check(lib.sp24_int8_gemm(_ptr(xq), _ptr(sx), M, K, xq.stride(0), _ptr(values), _ptr(meta), _ptr(sw), N,
-                              _ptr(bias), _ptr(y), y.stride(0), _stream(stream)), "sp24_int8_gemm")
+    _check(_on(xq.get_device(), lib.sp24_int8_gemm, _ptr(xq), _ptr(sx), M, K, xq.stride(0), _ptr(values), _ptr(meta),
+               _ptr(sw), N, _ptr(bias), _ptr(y), y.stride(0), _stream(stream, xq.get_device())), "sp24_int8_gemm")
     return y
 
 
@@ -536,18 +552,6 @@ def _matrix_of(t, dtype, cache, name, what):
     _dev_tensor(t, dtype, name, cache.device)
     if t.dim() != 2:
         raise ValueError("%s must be %s, got %s" % (name, what, tuple(t.shape)))
-
-
-# The library launches on the calling thread's current GPU, which need not be the operands'.
-_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-def _on(index, fn, *args):
-    """fn(*args) with the GPU `index` as the current one."""
-    if _current_gpu() == index:
-        return fn(*args)
-    with torch.cuda.device(index):
-        return fn(*args)
 
 
 # The current stream's handle without a Stream object around it, where torch has that.

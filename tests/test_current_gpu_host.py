@@ -94,3 +94,38 @@ def test_device_errors_are_those_of_the_streams_gpu(gpu):
     gpu.current = 3
     s.last_device_error(types.SimpleNamespace(cuda_stream=7, device_index=3))
     assert gpu.lib.calls == [("sp24_last_device_error", -1), ("sp24_last_device_error", 3)]
+
+
+def linear_calls():
+    u8, f32, bf16, i8 = torch.uint8, torch.float32, torch.bfloat16, torch.int8
+    z = lambda *shape, t=u8: torch.zeros(shape, dtype=t)  # noqa: E731
+    sx, sw, values, meta = z(1, 4, t=f32), z(1, 256, t=f32), z(256, 64), z(256, 16)
+    return {
+        "sp24_fp8_compress": lambda **kw: s.compress(z(256, 128, t=bf16), **kw),
+        "sp24_fp8_decompress": lambda **kw: s.decompress(values, meta, sw, **kw),
+        "sp24_fp8_quantize_act": lambda **kw: s.quantize_act(z(4, 128, t=f32), **kw),
+        "sp24_fp8_quantize_act_bf16": lambda **kw: s.quantize_act(z(4, 128, t=bf16), **kw),
+        "sp24_fp8_gemm": lambda **kw: s.gemm(z(4, 128), sx, values, meta, sw, **kw),
+        "sp24_fp8_gemm_batched": lambda **kw: s.gemm_batched(z(1, 4, 128), sx[None], values[None], meta[None], sw[None], **kw),
+        "sp24_int8_compress": lambda **kw: s.compress_int8(z(256, 128, t=bf16), **kw),
+        "sp24_int8_quantize_act": lambda **kw: s.quantize_act_int8(z(4, 128, t=f32), **kw),
+        "sp24_int8_gemm": lambda **kw: s.gemm_int8(z(4, 128, t=i8), sx, values.to(i8), meta, sw, **kw),
+    }
+
+
+@pytest.mark.parametrize("current", [0, -1])
+def test_linear_calls_work_on_the_operands_gpu(gpu, monkeypatch, current):
+    gpu.current = current
+    asked = []
+    monkeypatch.setattr(s, "_dev_tensor", lambda t, *_: t)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda index=None: asked.append(index) or types.SimpleNamespace(cuda_stream=7, device_index=index))
+    for name, call in linear_calls().items():
+        call()
+        assert gpu.lib.calls[-1] == (name, -1) and asked.pop() == -1
+        done = len(gpu.lib.calls)
+        with pytest.raises(ValueError):
+            call(stream=types.SimpleNamespace(cuda_stream=7, device_index=0))
+        assert name not in [n for n, _ in gpu.lib.calls[done:]]
+    assert {at for _, at in gpu.lib.calls} == {-1} and len(gpu.lib.calls) == 13  # two calls of each GEMM ask for a size
+    assert gpu.current == current
