@@ -665,7 +665,7 @@ def _attention_args(q, cache, page_table, seq_lens, scale, out, stream):
             ldy = _row_stride(out, cols)
         ok = (q.dtype is _BF16 and ldq and q.get_device() == at and shape[-1] % d == 0 and
               (len(shape) == 2 or shape[2] == d) and out.dtype is _BF16 and ldy and out.shape[0] == rows and
-              out.get_device() == at and page_table.dtype is _I32 and page_table.stride(1) == 1 and
+              out.get_device() == at and page_table.dtype is _I32 and (page_table.stride(1) == 1 or width == 1) and
               page_table.get_device() == at and seq_lens.dtype is _I32 and seq_lens.shape == (B,) and
               seq_lens.is_contiguous() and seq_lens.get_device() == at)
     except (AttributeError, IndexError, ValueError, TypeError):
