@@ -486,7 +486,8 @@ class KVCache:
         e4m3 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
         _dev_tensor(k, torch.uint8 if e4m3 else torch.bfloat16, "k")
         _dev_tensor(v, k.dtype, "v", k.device)
-        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+        if k.dim() != 4 or k.shape != v.shape or any(
+                a != b for n, a, b in zip(k.shape, k.stride(), v.stride()) if n > 1):
             raise ValueError("k and v must be [pages, heads, page size, head dim] of one shape and one set of strides")
         pages, heads, page_size, head_dim = k.shape
         if pages < 1 or heads < 1 or head_dim not in (64, 128) or page_size not in (16, 32, 64, 128):

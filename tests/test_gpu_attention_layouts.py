@@ -26,3 +26,23 @@ def test_a_page_table_of_one_column(sp24):
         with pytest.raises(ValueError):
             call()
     sp24.last_device_error()
+
+
+def test_keys_and_values_that_differ_in_a_lone_axis_stride(sp24):
+    """With one kv head, pages of tokens and pages of heads are the same memory: k may be one and v the other."""
+    s = Setup(sp24, [40, 7], 1, 64, 16, False, False, seed=93)
+    cache, table = s.upload(), s.table.cuda()
+    lens = torch.tensor(s.lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(94)).to(torch.bfloat16).cuda()
+    want = sp24.attention_decode(q, cache, table, lens)
+    k = cache.k.transpose(1, 2).clone(memory_format=torch.contiguous_format).transpose(1, 2)
+    assert k.stride(1) != cache.v.stride(1)
+    assert torch.equal(sp24.attention_decode(q, sp24.KVCache(k, cache.v), table, lens), want)
+    one = sp24.KVCache(k[:1].as_strided((1, 1, 16, 64), (5, 7, 64, 1)), cache.v[:1])
+    first = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    assert torch.equal(sp24.attention_decode(q[:1], one, first, lens[1:]),
+                       sp24.attention_decode(q[:1], cache, first, lens[1:]))
+    two = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")  # a stride that is stepped along does count
+    with pytest.raises(ValueError):
+        sp24.KVCache(two, two.transpose(1, 2).contiguous().transpose(1, 2))
+    sp24.last_device_error()
