@@ -520,7 +520,7 @@ class KVCache:
 # host is several times its kernel's.  So each first asks its tensors, in one
 # expression, whether all is as it should be, and only a call that is not goes
 # through the checks that say what is wrong.
-_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+_BF16, _F32, _I32, _INT64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 def _rows_of(t, rows, cols, cache, name):
@@ -610,7 +610,7 @@ def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_w
         else:
             ldq = _row_stride(out, heads * d)
         qw = kw = None
-        ok = (slots.dtype is _I64 and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == at and
+        ok = (slots.dtype is _INT64 and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == at and
               positions.dtype is _I32 and positions.shape == slots.shape and positions.is_contiguous() and
               positions.get_device() == at and qkv.dtype is _BF16 and ldqkv and qkv.shape[0] == T and
               qkv.get_device() == at and out.dtype is _BF16 and ldq and out.shape[0] == T and
@@ -624,7 +624,7 @@ def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_w
     except (AttributeError, IndexError, ValueError, TypeError):
         ok = False
     if not ok:
-        _vector(slots, _I64, slots.numel() if isinstance(slots, torch.Tensor) else 0, cache, "slots")
+        _vector(slots, _INT64, slots.numel() if isinstance(slots, torch.Tensor) else 0, cache, "slots")
         T = slots.shape[0]
         _vector(positions, _I32, T, cache, "positions")
         _rows_of(qkv, T, (heads + 2 * cache.heads) * d, cache, "qkv")
