@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __shared__ Work s_work[2];
   __shared__ __align__(16) uint4 s_response;
   __shared__ uint32_t s_tmem;
+  __shared__ int s_last[2];  // position in the ring of the last copy of keys, and of values
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;
@@ -876,6 +877,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, need));
           const int c = ring + 2 * i + (keys ? 0 : 1), slot = c % RING;
+#ifdef SP24_FAULT_WITHHOLD_FIRST_STAGE
+          if (c == 0) continue;  // the fault-test build: each CTA's first keys never come
+#endif
           if (c >= RING) ok = mbar_wait(&empty[slot], (c / RING - 1) & 1);
           if (!ok) break;
           last = c;
@@ -900,15 +904,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           __syncwarp();
         }
       }
-      if (!ok) {
-        // What is in flight has to land before this CTA's shared memory goes.
-        if (lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
-        for (int c = last; c >= 0 && c > last - RING; c -= 2) mbar_wait(&full[c % RING], (c / RING) & 1);
-        if (!keys)
-          for (int x = 0; x < 2; ++x)
-            if (qn[x] > 0) mbar_wait(&q_full[x], (qn[x] - 1) & 1);
-        if (asked) mbar_wait(stolen, item & 1);
+      if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
+      // Copies in flight have to land before this CTA's shared memory goes, also where only other warps gave up on them:
+      // of each slot the last copy, whichever warp's it is (a parity cannot tell a copy that has been overtaken from one
+      // that has not landed, so both warps have to be done first).
+      if (lane == 0) s_last[keys ? 0 : 1] = last;
+      __syncwarp();
+      asm volatile("bar.sync 1, 64;" ::: "memory");  // the two copying warps
+      if (keys) {
+        const int top = max(s_last[0], s_last[1]);
+#pragma unroll 1
+        for (int n = top; n > top - RING; --n) {
+          const int c = n <= s_last[n & 1] ? n : n - RING;
+          if (c >= 0) mbar_wait(&full[c % RING], (c / RING) & 1);
+        }
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x)
+          if (qn[x] > 0) mbar_wait(&q_full[x], (qn[x] - 1) & 1);
       }
+      if (asked) mbar_wait(stolen, item & 1);
     }
   } else if (E4M3) {
     // -------------------------------------------------------------- e4m3 -> f16
