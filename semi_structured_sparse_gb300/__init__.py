@@ -125,6 +125,15 @@ def _stream(stream=None, index=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(shape, dtype, stream, device, zero=False):
+    """Memory for a kernel on `stream`, from that stream's own pool."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _dev_tensor(t, dtype, name, device=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
@@ -214,9 +223,9 @@ def compress(w: torch.Tensor, gN: int = 1, gK: int = None, out=None, stream=None
     N, K = w.shape
     gK = K if gK is None else gK
     if out is None:
-        values = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-        meta = torch.empty((N, K // 8), dtype=torch.uint8, device=w.device)
-        scales = torch.empty((K // gK, (N + gN - 1) // gN), dtype=torch.float32, device=w.device)
+        values = _new((N, K // 2), torch.uint8, stream, w.device)
+        meta = _new((N, K // 8), torch.uint8, stream, w.device)
+        scales = _new((K // gK, (N + gN - 1) // gN), torch.float32, stream, w.device)
     else:
         values, meta, scales = out
         _dev_tensor(values, torch.uint8, "values", w.device)
@@ -245,7 +254,7 @@ def decompress(values, meta, scales, gN: int = 1, gK: int = None, out=None, stre
     _at_least(meta, N * (K // 8), "meta")
     _at_least(scales, _scale_count(K, gK, N, gN), "scales")
     if out is None:
-        W = torch.empty((N, K), dtype=torch.bfloat16, device=values.device)
+        W = _new((N, K), torch.bfloat16, stream, values.device)
     else:
         W = _dev_tensor(out, torch.bfloat16, "out", values.device)
         _matrix(W, N, K, "out")
@@ -265,8 +274,8 @@ def quantize_act(x: torch.Tensor, gK: int = None, out=None, stream=None):
     M, K = x.shape
     gK = K if gK is None else gK
     if out is None:
-        xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-        sx = torch.empty((K // gK, M), dtype=torch.float32, device=x.device)
+        xq = _new((M, K), torch.uint8, stream, x.device)
+        sx = _new((K // gK, M), torch.float32, stream, x.device)
     else:
         xq, sx = out
         _dev_tensor(xq, torch.uint8, "xq", x.device)
@@ -318,13 +327,13 @@ def gemm(xq, sx, values, meta, sw, gM: int = 1, gN: int = 1, gK: int = None, x2=
         if not bias.is_contiguous() or bias.numel() != N:
             raise ValueError("bias must be a contiguous bf16 vector of N values")
     if out is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev_)
+        y = _new((M, N), torch.bfloat16, stream, dev_)
     else:
         y = _dev_tensor(out, torch.bfloat16, "out", dev_)
         _matrix(y, M, N, "out")
     ws_bytes = int(_on(xq.get_device(), lib.sp24_fp8_gemm_workspace_size, M, N, K, r))
     if ws_bytes and workspace is None:
-        workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=dev_)
+        workspace = _new(ws_bytes, torch.uint8, stream, dev_, zero=True)
     elif workspace is not None:
         _dev_tensor(workspace, torch.uint8, "workspace", dev_)
         if not workspace.is_contiguous():
@@ -363,14 +372,14 @@ def gemm_batched(xq, sx, values, meta, sw, gM: int = 1, gN: int = 1, gK: int = N
         if bias.shape != (L, N):
             raise ValueError("bias must be [L, N]")
     if out is None:
-        y = torch.empty((L, M, N), dtype=torch.bfloat16, device=dev_)
+        y = _new((L, M, N), torch.bfloat16, stream, dev_)
     else:
         y = _dev_tensor(out, torch.bfloat16, "out", dev_)
         if y.dim() != 3 or tuple(y.shape) != (L, M, N) or y.stride(1) < N:
             raise ValueError("out must be [L, M, N]")
     ws_bytes = L * int(_on(xq.get_device(), lib.sp24_fp8_gemm_workspace_size, M, N, K, 0))
     if ws_bytes and workspace is None:
-        workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=dev_)
+        workspace = _new(ws_bytes, torch.uint8, stream, dev_, zero=True)
     elif workspace is not None:
         _dev_tensor(workspace, torch.uint8, "workspace", dev_)
         if not workspace.is_contiguous():
@@ -395,9 +404,9 @@ def compress_int8(w: torch.Tensor, out=None, stream=None):
         raise ValueError("w must be [N, K]")
     N, K = w.shape
     if out is None:
-        values = torch.empty((N, K // 2), dtype=torch.int8, device=w.device)
-        meta = torch.empty((N, K // 8), dtype=torch.uint8, device=w.device)
-        scales = torch.empty(N, dtype=torch.float32, device=w.device)
+        values = _new((N, K // 2), torch.int8, stream, w.device)
+        meta = _new((N, K // 8), torch.uint8, stream, w.device)
+        scales = _new(N, torch.float32, stream, w.device)
     else:
         values, meta, scales = out
         _dev_tensor(values, torch.int8, "values", w.device)
@@ -419,8 +428,8 @@ def quantize_act_int8(x: torch.Tensor, out=None, stream=None):
         raise ValueError("x must be [M, K]")
     M, K = x.shape
     if out is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
-        sx = torch.empty(M, dtype=torch.float32, device=x.device)
+        xq = _new((M, K), torch.int8, stream, x.device)
+        sx = _new(M, torch.float32, stream, x.device)
     else:
         xq, sx = out
         _dev_tensor(xq, torch.int8, "xq", x.device)
@@ -459,7 +468,7 @@ def gemm_int8(xq, sx, values, meta, sw, bias=None, out=None, stream=None):
         if not bias.is_contiguous() or bias.numel() != N:
             raise ValueError("bias must be a contiguous bf16 vector of N values")
     if out is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev_)
+        y = _new((M, N), torch.bfloat16, stream, dev_)
     else:
         y = _dev_tensor(out, torch.bfloat16, "out", dev_)
         _matrix(y, M, N, "out")
@@ -577,15 +586,6 @@ def _int32(n):
     return min(max(n, -1), _MOST)  # (ctypes would keep the low 32 bits)
 
 
-def _new(shape, dtype, stream, cache, zero=False):
-    """Memory for a kernel on `stream`, from that stream's own pool."""
-    make = torch.zeros if zero else torch.empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=cache.device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=cache.device)
-
-
 def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_weight=None, k_weight=None,
                  eps: float = 1e-6, interleaved: bool = False, out=None, stream=None):
     """One pass over the QKV projection's rows: per-head RMS norm (with q_weight and
@@ -606,7 +606,7 @@ def qk_norm_rope(qkv, heads: int, cache: KVCache, positions, slots, cos_sin, q_w
         ldqkv = _row_stride(qkv, (heads + 2 * cache.heads) * d)
         max_pos, rot = cos_sin.shape
         if out is None:
-            out, ldq = _new((T, heads, d), _BF16, stream, cache), heads * d
+            out, ldq = _new((T, heads, d), _BF16, stream, cache.device), heads * d
         else:
             ldq = _row_stride(out, heads * d)
         qw = kw = None
@@ -661,7 +661,7 @@ def _attention_args(q, cache, page_table, seq_lens, scale, out, stream):
         ldq = _row_stride(q, cols)
         B, width = page_table.shape
         if out is None:
-            out, ldy = _new(shape, _BF16, stream, cache), cols
+            out, ldy = _new(shape, _BF16, stream, cache.device), cols
         else:
             ldy = _row_stride(out, cols)
         ok = (q.dtype is _BF16 and ldq and q.get_device() == at and shape[-1] % d == 0 and
@@ -701,7 +701,7 @@ def attention_decode(q, cache: KVCache, page_table, seq_lens, scale: float = Non
     if not (0 <= window <= _MOST and 0 <= sinks <= _MOST):
         window, sinks = _int32(window), _int32(sinks)
     if workspace is None:
-        workspace = _new(attention_decode_workspace_size(cache, heads), torch.uint8, stream, cache, zero=True)
+        workspace = _new(attention_decode_workspace_size(cache, heads), torch.uint8, stream, cache.device, zero=True)
     elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and
               workspace.get_device() == cache._index and workspace.is_contiguous()):
         _dev_tensor(workspace, _U8, "workspace", cache.device)
@@ -743,7 +743,7 @@ def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float
         need = width * cache.page_size >= 1024 and _on(
             cache._index, lib.sp24_attention_prompt_workspace_size, rows, B, heads, cache._address, width, window, sinks)
         if need:
-            workspace = _new(need, _U8, stream, cache)
+            workspace = _new(need, _U8, stream, cache.device)
     elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and
               workspace.get_device() == cache._index and workspace.is_contiguous()):
         _dev_tensor(workspace, _U8, "workspace", cache.device)

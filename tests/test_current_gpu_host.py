@@ -40,6 +40,7 @@ def gpu(monkeypatch):
     monkeypatch.setattr(s, "_current_gpu", lambda: g.current, raising=False)
     monkeypatch.setattr(s, "_raw_stream", lambda index: 100 + index)
     monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "stream", contextlib.nullcontext)
     return g
 
 
@@ -129,3 +130,30 @@ def test_linear_calls_work_on_the_operands_gpu(gpu, monkeypatch, current):
         assert name not in [n for n, _ in gpu.lib.calls[done:]]
     assert {at for _, at in gpu.lib.calls} == {-1} and len(gpu.lib.calls) == 13  # two calls of each GEMM ask for a size
     assert gpu.current == current
+
+
+def test_memory_for_a_call_on_another_stream_is_that_streams(gpu, monkeypatch):
+    """Outputs and zeroed workspaces of a call with `stream` are allocated (and zeroed) on it, not on the current one."""
+    now, made = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, now[0] = now[0], stream
+        yield
+        now[0] = before
+
+    def recorded(make):
+        return lambda *a, **kw: made.append(now[0]) or make(*a, **kw)
+
+    calls = {**linear_calls(), **attention_calls(cache())}
+    monkeypatch.setattr(s, "_dev_tensor", lambda t, *_: t)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    side = types.SimpleNamespace(cuda_stream=7, device_index=-1)
+    empty, zeros = torch.empty, torch.zeros
+    monkeypatch.setattr(torch, "empty", recorded(empty))
+    # (the calls' own inputs here are made with torch.zeros, too, but without a device)
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: (recorded(zeros) if "device" in kw else zeros)(*a, **kw))
+    for name, call in calls.items():
+        call(stream=side)
+        assert made and all(x is side for x in made), name
+        made.clear()
