@@ -22,16 +22,19 @@
 //   mma.sync m16n8k16 and 8 heads on the other, so 8 heads waste nothing (with
 //   heads on the 16-row side, half the products and half the registers of O
 //   would be padding).  tcgen05 would want 128 rows.
+// - The weights enter the tensor core as bf16 (f16 with an e4m3 cache), which
+//   moves a result by 2^-8 of the weighted mean of |v| at most and in the mean far
+//   less; their sum is of the fp32 values.
 // - e4m3 codes become f16 in registers (exactly), so the products of an e4m3
 //   cache are f16 ones; each query head is scaled by a power of two, which
-//   keeps bf16 queries within f16's range.
+//   keeps bf16 queries within f16's range, and each weight by 2^15 (kUp).
 //
 // Measured (GB300, 32/8 heads of 128 but for the last): one sequence of 131071
-// tokens 87 us, 6.2 TB/s (91 % of the measured copy rate); 64 of 1 to 16000
-// in an e4m3 cache 170 us, 6.3 TB/s (93 %); one of 1000 tokens 7.3 us, of
+// tokens 88 us, 6.1 TB/s (90 % of the measured copy rate); 64 of 1 to 16000
+// in an e4m3 cache 171 us, 6.2 TB/s (92 %); one of 1000 tokens 7.3 us, of
 // which the keys take 1: launch, lengths, pages, keys and the join of 16 pieces
 // are a chain of seven memory latencies; 128 of up to 9000 tokens under a
-// window of 2000 with 4 sinks, 28/4 heads of 64, 45.1 us, 5.2 TB/s (76 %).
+// window of 2000 with 4 sinks, 28/4 heads of 64, 45.8 us, 5.1 TB/s (75 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "sp24_attn.cuh"

@@ -32,11 +32,12 @@
 // Blocks that see many keys come first.  (With a launch per block, setting up
 // and draining took 16,000 cycles of a block's 92,000 at 8192 tokens.)
 //
-// Measured (GB300, one call after the other): 8192 tokens, 32/8 heads of 128,
-// 325 us, 1690 TFLOP/s of visible products (86 % of the measured bf16 rate);
-// 16001 tokens under a window of 4096 and 4 sinks, 28/4 heads of 64, 452 us,
-// 907 TFLOP/s; pieces of 1839 and 1629 tokens over 14000 in an e4m3 cache
-// 555 us, 1520 TFLOP/s.  With heads of 128 a query tile's chain (S read 52
+// Measured (GB300, in a CUDA graph of a few calls): 8192 tokens, 32/8 heads of
+// 128, 325 us, 1690 TFLOP/s of visible products (86 % of the measured bf16
+// rate); 16001 tokens under a window of 4096 and 4 sinks, 28/4 heads of 64, 450
+// us, 911 TFLOP/s; pieces of 1839 and 1629 tokens over 14000 in an e4m3 cache
+// 554 us, 1525 TFLOP/s.  Calls back to back for 0.15 s, where the clock falls:
+// 352 us, 448 and 570.  With heads of 128 a query tile's chain (S read 52
 // cycles, the first half's exponentials beside the search for the maximum 450,
 // the second half's 350, P written and seen 200, the rest of P V and Q K^T 768
 // plus what the other tile's MMAs take) is 2600 cycles per key tile, against

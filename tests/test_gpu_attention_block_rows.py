@@ -8,8 +8,8 @@ import torch
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
-# Both ways round the softmax weights and the result to bf16, errors of 2^-9 / sqrt(3) of each weight and of the result
-# that have no preferred sign: 0.16 % of a row's norm each way, 0.23 % between them.  (The QKV rows are the same but for a
+# Both ways round the softmax weights and the result to bf16, errors of up to 2^-9 to 2^-8 of each weight and of the result
+# that have no preferred sign: some 2^-8.5 / sqrt(3) each, 0.23 % of a row's norm each way, 0.33 % between them.  (The QKV rows are the same but for a
 # bf16 rounding here and there, where the linear sums in another order for another number of tokens.)  One of the 62 keys
 # that a row sees is 1/62 of the weight in the mean, about 1/62 |v| beside a row of 1.6 / sqrt(62) |v| (weights exp of
 # scores with a deviation of 1): 8 % of the norm.

@@ -19,14 +19,14 @@ def setup(sp24, n, strong, d, page, e4m3):
     return sp24.KVCache(k, v, scale, scale), torch.arange(pages, dtype=torch.int32, device="cuda")[None]
 
 
-# A weight enters the tensor core rounded by 2^-9 of itself (bf16: 8 bits; f16 has 11), and f16's smallest step rounds it
-# by 2^-25 besides.  The largest weight is 2^15 in a decode step (a step of 2^-40 of it) and at least 2^7 in a prompt
+# A weight enters the tensor core rounded by up to 2^-8 of itself (bf16: 8 bits), or 2^-11 (f16), whose smallest step rounds
+# it by up to 2^-25 besides.  The largest weight is 2^15 in a decode step (a step of 2^-40 of it) and at least 2^7 in a prompt
 # (2^-32).  fp32 scores of 30 are off by 30 x 2^-23 at most, so exponentials by less than 2^-16; the result is rounded by
 # 2^-8 of it.
 def assert_tail(y, others, gap, e4m3, step, what):
     tail = others.double() * math.exp(-gap)
     want = (tail / (1 + tail)).view(-1, 1, 1)
-    bound = (2.0 ** -8 * 1.02 + 2.0 ** -9 + 2.0 ** -15) * want
+    bound = (2.0 ** -8 * 1.02 + (2.0 ** -11 if e4m3 else 2.0 ** -8) + 2.0 ** -15) * want
     if e4m3:
         bound = bound + (others.double() * step).view(-1, 1, 1)
     off = ((y.double().cpu() - want).abs() / bound).max()
