@@ -522,6 +522,99 @@ SP24_API sp24_status sp24_attention_prompt(const void* q, int64_t T, int64_t ldq
 SP24_API size_t sp24_attention_prompt_workspace_size(int64_t T, int64_t B, int q_heads, const sp24_kv_cache* cache,
                                                      int64_t table_width, int window, int sinks);
 
+/*
+ * sp24_attention_decode_shared -- sp24_attention_decode for a batch in which
+ * groups of sequences have their first tokens in common (one instruction
+ * before many requests): those keys and values are read once for the group, not
+ * once per sequence.  The result is the same.
+ *
+ *   cu_shared (device) int32 [G + 1], ascending within [0, B]: group g is the
+ *           sequences cu_shared[g] .. cu_shared[g + 1] - 1.  Sequences before the
+ *           first group and after the last have nothing in common.
+ *   shared_lens (device) int32 [G]: the first shared_lens[g] tokens of the
+ *           group's sequences are the same, and are read through the pages of
+ *           its first sequence.  (Any number of tokens: where it is no multiple
+ *           of the page size, each sequence has the page in which they end as a
+ *           copy of its own, sp24_cache_copy.)  A sequence that does not see all
+ *           of them, because it is shorter or its window begins later, is
+ *           attended by itself, through its own pages, as in
+ *           sp24_attention_decode.
+ *   workspace: device scratch of sp24_attention_decode_shared_workspace_size
+ *           bytes, 16-byte aligned, zeroed once before its first use and then
+ *           consistent from call to call, whatever their shapes; calls that
+ *           overlap on the GPU must not share it.
+ *   Others as for sp24_attention_decode.
+ * cu_shared out of order or out of [0, B] is brought into it, shared_lens out of
+ * [0, table_width * page_size] as well; sp24_last_device_error then reports
+ * SP24_ERR_DEVICE_INDEX.
+ * Values of the shared tokens are finite: a weight of zero times an infinite
+ * value is not a number.
+ * Preconditions: G >= 0; cu_shared given (shared_lens may be NULL with G = 0).
+ */
+SP24_API sp24_status sp24_attention_decode_shared(const void* q, int64_t B, int64_t ldq, int q_heads,
+                                                  const sp24_kv_cache* cache, const int32_t* page_table,
+                                                  int64_t table_width, int64_t ld_table, const int32_t* seq_lens,
+                                                  const int32_t* cu_shared, const int32_t* shared_lens, int64_t G,
+                                                  float scale, int window, int sinks, void* Y, int64_t ldy,
+                                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device scratch bytes sp24_attention_decode_shared needs for at most B
+ * sequences in at most G groups on the current device (0 for an invalid layout
+ * or without a usable device). */
+SP24_API size_t sp24_attention_decode_shared_workspace_size(int64_t B, int64_t G, int q_heads, int heads,
+                                                            int head_dim);
+
+/*
+ * sp24_cache_copy -- keys and values of T tokens, all heads, from places of one
+ * cache to places of another, or of the same: a prefix quantised for those that
+ * will read it, e4m3 tokens read back, the page in which shared tokens end copied
+ * for a sequence.  The caches may differ in type, page size and strides.
+ *
+ *   x   = the source's value: bf16, or fp32 code * scale[head]
+ *   dst = bf16 rounded from x (the same bits from a bf16 cache), or
+ *         e4m3_rn_satfinite(x / scale[head]), the destination's scale, with a
+ *         correctly rounded division.
+ *
+ *   src_slots, dst_slots (device) int64 [T]: page * page_size + place in the
+ *           source and in the destination; a token with a negative number in
+ *           either is left out.  A slot out of range leaves its token out and is
+ *           reported by sp24_last_device_error (SP24_ERR_DEVICE_INDEX).  Places
+ *           that a call both reads and writes, or writes twice, hold a mixture
+ *           afterwards.
+ * Preconditions: T >= 0; the caches have the same heads (at most 65536) and
+ * head_dim.
+ */
+SP24_API sp24_status sp24_cache_copy(const sp24_kv_cache* src, const int64_t* src_slots, const sp24_kv_cache* dst,
+                                     const int64_t* dst_slots, int64_t T, void* stream);
+
+/*
+ * ---------------------------------------------------------------- adapters
+ * sp24_add_adapters -- low-rank adapters of many requests beside one shared
+ * projection: to each row of its output the product of the two narrow matrices
+ * that the row's request has (sp24_fp8_gemm's side term has one for all rows):
+ *
+ *   out[t] = bf16( y[t] + scales[i] * B_i (A_i x[t]) ),  i = ids[t]
+ *
+ * Sums are fp32.  A row with a negative id has no adapter: out[t] = y[t].  An id
+ * of `count` or more counts as negative and is reported by
+ * sp24_last_device_error (SP24_ERR_DEVICE_INDEX).
+ *
+ *   Y    (device) bf16 [T][N], row stride ldy; X (device) bf16 [T][K], ldx.
+ *   A    (device) bf16 [count][r][K], stride_a elements between adapters;
+ *   B    (device) bf16 [count][N][r], stride_b.  An adapter of a smaller rank has
+ *        zeros in the rest.
+ *   ids  (device) int32 [T], in any order (rows of one adapter in a row read it
+ *        least often); scales (device) fp32 [count], or NULL for 1.
+ *   out  (device, out) bf16 [T][N], row stride ldo; may be Y (with ldo = ldy).
+ * Preconditions: T >= 0; K, N and r positive multiples of 8, r at most 128
+ * (SP24_ERR_UNSUPPORTED), K and N at most 2^24; matrices 16-byte aligned, strides
+ * multiples of 8 and no shorter than what they step over.
+ */
+SP24_API sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void* X, int64_t ldx, int64_t T, int64_t K,
+                                       int64_t N, const void* A, int64_t stride_a, const void* B, int64_t stride_b,
+                                       int64_t r, int64_t count, const int32_t* ids, const float* scales, void* out,
+                                       int64_t ldo, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,6 +15,12 @@ Between a layer's QKV and output projections (attention over a paged cache):
     q     = qk_norm_rope(qkv, heads, cache, positions, slots, cos_sin)
     y     = attention_decode(q, cache, page_table, seq_lens)   # one new token per sequence
     y     = attention_prompt(q, cu_q, cache, page_table, seq_lens)
+
+For a batch of many requests that have their first tokens, or a projection, in common:
+
+    y     = attention_decode_shared(q, cache, page_table, seq_lens, cu_shared, shared_lens)
+    cache_copy(cache, slots, other_cache, other_slots)         # quantised or read back on the way
+    y     = add_adapters(y, x, a, b, ids)                      # each row's own low-rank adapter
 """
 import contextlib
 import ctypes
@@ -61,6 +67,12 @@ SIGNATURES = {
     "sp24_attention_prompt": ([_P, _I64, _I64, _I, _P, _I64, _P, _P, _I64, _I64, _P, _F, _I, _I, _P, _I64, _P, _SZ, _P],
                               _I),
     "sp24_attention_prompt_workspace_size": ([_I64, _I64, _I, _P, _I64, _I, _I], _SZ),
+    "sp24_attention_decode_shared": ([_P, _I64, _I64, _I, _P, _P, _I64, _I64, _P, _P, _P, _I64, _F, _I, _I, _P, _I64,
+                                      _P, _SZ, _P], _I),
+    "sp24_attention_decode_shared_workspace_size": ([_I64, _I64, _I, _I, _I], _SZ),
+    "sp24_cache_copy": ([_P, _P, _P, _P, _I64, _P], _I),
+    "sp24_add_adapters": ([_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64,
+                           _P], _I),
 }
 
 
@@ -754,6 +766,149 @@ def attention_prompt(q, cu_q, cache: KVCache, page_table, seq_lens, scale: float
              _stream_of(stream, cache))
     if st:
         _check(st, "sp24_attention_prompt")
+    return out
+
+
+def attention_decode_shared_workspace_size(cache: KVCache, heads: int, sequences: int, groups: int) -> int:
+    """Device scratch bytes attention_decode_shared() needs for `heads` query heads and at
+    most `sequences` sequences in at most `groups` groups."""
+    return int(_on(cache._index, load().sp24_attention_decode_shared_workspace_size, sequences, groups, heads, cache.heads,
+                   cache.head_dim))
+
+
+def attention_decode_shared(q, cache: KVCache, page_table, seq_lens, cu_shared, shared_lens, scale: float = None,
+                            window: int = 0, sinks: int = 0, out=None, workspace=None, stream=None):
+    """attention_decode() for a batch in which groups of sequences have their first tokens
+    in common, which are read once for the group: sequences cu_shared[g] .. cu_shared[g + 1]
+    - 1 are group g (cu_shared int32 [G + 1]; those before the first and after the last are
+    in none), and their first shared_lens[g] tokens (int32 [G]) are those in the pages of the
+    group's first sequence.  A sequence that does not see all of them (shorter, or under a
+    window that begins later) is attended by itself.  The others as for attention_decode();
+    `workspace` (uint8, attention_decode_shared_workspace_size() bytes, zeroed once) may be
+    kept for all later calls on one stream; without one, each call allocates a zeroed one."""
+    lib = _lib or load()
+    rows, ldq, heads, B, width, ld_table, lens_p, scale, out, ldy = _attention_args(
+        q, cache, page_table, seq_lens, scale, out, stream)
+    if rows != B:
+        raise ValueError("q has %d rows, page_table %d sequences" % (rows, B))
+    at = cache._index
+    if not (isinstance(shared_lens, torch.Tensor) and isinstance(cu_shared, torch.Tensor) and
+            shared_lens.dtype is _I32 and shared_lens.dim() == 1 and shared_lens.is_contiguous() and
+            shared_lens.get_device() == at and cu_shared.dtype is _I32 and
+            cu_shared.shape == (shared_lens.shape[0] + 1,) and cu_shared.is_contiguous() and cu_shared.get_device() == at):
+        groups = shared_lens.numel() if isinstance(shared_lens, torch.Tensor) else 0
+        _vector(shared_lens, _I32, groups, cache, "shared_lens")
+        _vector(cu_shared, _I32, groups + 1, cache, "cu_shared")
+    G = shared_lens.shape[0]
+    if not (0 <= window <= _MOST and 0 <= sinks <= _MOST):
+        window, sinks = _int32(window), _int32(sinks)
+    if workspace is None:
+        workspace = _new(attention_decode_shared_workspace_size(cache, heads, B, G), _U8, stream, cache.device, zero=True)
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and
+              workspace.get_device() == at and workspace.is_contiguous()):
+        _dev_tensor(workspace, _U8, "workspace", cache.device)
+        raise ValueError("workspace must be contiguous")
+    st = _on(at, lib.sp24_attention_decode_shared, q.data_ptr(), B, ldq, heads, cache._address, page_table.data_ptr(),
+             width, ld_table, lens_p, cu_shared.data_ptr(), shared_lens.data_ptr(), G, scale, window, sinks,
+             out.data_ptr(), ldy, workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache))
+    if st:
+        _check(st, "sp24_attention_decode_shared")
+    return out
+
+
+def cache_copy(src: KVCache, src_slots, dst: KVCache, dst_slots, stream=None):
+    """Keys and values of tokens, all heads, from slots of one cache to slots of another
+    (or of the same): src_slots and dst_slots int64 [T], page * page_size + place, negative
+    for a token to leave out.  The caches may differ in type, page size and strides: bf16
+    tokens are quantised with the destination's scales, e4m3 ones read back."""
+    lib = _lib or load()
+    at = src._index
+    if dst._index != at:
+        raise ValueError("the source cache is on %s, the destination on %s" % (src.device, dst.device))
+    if src.heads != dst.heads or src.head_dim != dst.head_dim:
+        raise ValueError("the caches must have the same heads, got %d of %d and %d of %d" % (
+            src.heads, src.head_dim, dst.heads, dst.head_dim))
+    if not (isinstance(src_slots, torch.Tensor) and isinstance(dst_slots, torch.Tensor) and
+            src_slots.dtype is _INT64 and src_slots.dim() == 1 and src_slots.is_contiguous() and
+            src_slots.get_device() == at and dst_slots.dtype is _INT64 and dst_slots.shape == src_slots.shape and
+            dst_slots.is_contiguous() and dst_slots.get_device() == at):
+        T = src_slots.numel() if isinstance(src_slots, torch.Tensor) else 0
+        _vector(src_slots, _INT64, T, src, "src_slots")
+        _vector(dst_slots, _INT64, T, src, "dst_slots")
+    st = _on(at, lib.sp24_cache_copy, src._address, src_slots.data_ptr(), dst._address, dst_slots.data_ptr(),
+             src_slots.shape[0], _stream_of(stream, src))
+    if st:
+        _check(st, "sp24_cache_copy")
+
+
+# ------------------------------------------------------------------- adapters
+def _adapter_stack(t, shape, name, what, device):
+    """Adapters [count, rows, columns], each contiguous: their distance."""
+    _dev_tensor(t, _BF16, name, device)
+    if t.dim() != 3 or tuple(t.shape) != shape or (shape[1] > 1 and t.stride(1) != shape[2]) or (
+            shape[0] > 1 and t.stride(0) < shape[1] * shape[2]):
+        raise ValueError("%s must be %s = %s with contiguous matrices, got %s with strides %s" % (
+            name, what, list(shape), tuple(t.shape), t.stride()))
+
+
+def add_adapters(y, x, a, b, ids, scales=None, out=None, stream=None):
+    """Low-rank adapters of many requests beside one projection: to row t of its output y
+    bf16 [T, N] the product of the adapter i = ids[t] (int32 [T], in any order; negative:
+    none), scales[i] * b[i] (a[i] x[t]), for the projection's input x bf16 [T, K].  a bf16
+    [count, r, K] and b bf16 [count, N, r], r a multiple of 8 up to 128; scales fp32 [count],
+    or None for 1.  Returns bf16 [T, N] (in ``out`` if given, which may be y)."""
+    lib = _lib or load()
+    ok = False
+    try:
+        at = y.get_device()
+        T, N = y.shape
+        count, r, K = a.shape
+        ldy, ldx = _row_stride(y, N), _row_stride(x, K)
+        if out is None:
+            out, ldo = _new((T, N), _BF16, stream, y.device), N
+        else:
+            ldo = _row_stride(out, N)
+        stride_a, stride_b = (a.stride(0), b.stride(0)) if count > 1 else (r * K, N * r)
+        ok = (y.dtype is _BF16 and y.is_cuda and ldy and x.dtype is _BF16 and ldx and x.shape == (T, K) and
+              x.get_device() == at and out.dtype is _BF16 and ldo and out.shape == (T, N) and out.get_device() == at and
+              a.dtype is _BF16 and a.get_device() == at and a.stride(2) == 1 and a.stride(1) == K and stride_a >= r * K and
+              b.dtype is _BF16 and b.get_device() == at and b.shape == (count, N, r) and b.stride(2) == 1 and
+              b.stride(1) == r and stride_b >= N * r and ids.dtype is _I32 and ids.shape == (T,) and
+              ids.is_contiguous() and ids.get_device() == at)
+        if scales is not None:
+            ok = (ok and scales.dtype is _F32 and scales.shape == (count,) and scales.is_contiguous() and
+                  scales.get_device() == at)
+    except (AttributeError, IndexError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        _dev_tensor(y, _BF16, "y")
+        if y.dim() != 2:
+            raise ValueError("y must be [T, N], got %s" % (tuple(y.shape),))
+        T, N = y.shape
+        _matrix(y, T, N, "y")
+        _dev_tensor(x, _BF16, "x", y.device)
+        _matrix(x, T, x.shape[-1], "x")
+        _dev_tensor(a, _BF16, "a", y.device)
+        if a.dim() != 3:
+            raise ValueError("a must be [count, r, K], got %s" % (tuple(a.shape),))
+        count, r, K = a.shape
+        _adapter_stack(a, (count, r, x.shape[1]), "a", "[count, r, K]", y.device)
+        _adapter_stack(b, (count, N, r), "b", "[count, N, r]", y.device)
+        if out is not None:
+            _dev_tensor(out, _BF16, "out", y.device)
+            _matrix(out, T, N, "out")
+        for t, dtype, n, name in ((ids, _I32, T, "ids"), (scales, _F32, count, "scales")):
+            if t is None and name == "scales":
+                continue
+            _dev_tensor(t, dtype, name, y.device)
+            if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous vector of %d values, got %s" % (name, n, tuple(t.shape)))
+        raise ValueError("the arguments' layouts are not ones that the library takes")
+    s = _raw_stream(at) if stream is None and _raw_stream is not None else _stream(stream, at)
+    st = _on(at, lib.sp24_add_adapters, y.data_ptr(), ldy, x.data_ptr(), ldx, T, K, N, a.data_ptr(), stride_a, b.data_ptr(),
+             stride_b, r, count, ids.data_ptr(), None if scales is None else scales.data_ptr(), out.data_ptr(), ldo, s)
+    if st:
+        _check(st, "sp24_add_adapters")
     return out
 
 

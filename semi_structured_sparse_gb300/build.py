@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsp24.so")
 SOURCES = ["sp24_abi.cu", "sp24_compress.cu", "sp24_gemm.cu", "sp24_gemm_pair.cu", "sp24_int8.cu",
-           "sp24_rope.cu", "sp24_attn_decode.cu", "sp24_attn_prompt.cu"]
+           "sp24_rope.cu", "sp24_attn_decode.cu", "sp24_attn_prompt.cu", "sp24_attn_shared.cu", "sp24_cache_copy.cu",
+           "sp24_adapters.cu"]
 HEADERS = ["sp24_internal.cuh", "sp24_ptx.cuh", "sp24_gemm_common.cuh", "sp24_attn.cuh"]
 ROOT = os.path.dirname(HERE)
 

@@ -1,0 +1,182 @@
+"""Low-rank adapters of many requests against their definition in 64 bits (GPU)."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def inputs(T, K, N, r, count, seed, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g).bfloat16()  # noqa: E731
+    x, y = n(T, K + pad)[:, :K], n(T, N + pad)[:, :N]
+    a = (torch.randn(count, r, K, generator=g) * K ** -0.5).bfloat16()
+    b = (torch.randn(count, N, r, generator=g) * r ** -0.5).bfloat16()
+    return y, x, a, b, torch.rand(count, generator=g) + 0.5
+
+
+def reference(y, x, a, b, ids, scales):
+    """(out, sum of the magnitudes that were added up) in 64 bits."""
+    out, size = y.double(), torch.zeros(y.shape, dtype=torch.float64)
+    for i in set(ids.tolist()):
+        if i < 0 or i >= a.shape[0]:
+            continue
+        rows = ids == i
+        h, hs = x[rows].double() @ a[i].double().T, x[rows].double().abs() @ a[i].double().abs().T
+        s = 1.0 if scales is None else float(scales[i])
+        out[rows] += s * (h @ b[i].double().T)
+        size[rows] += abs(s) * (hs @ b[i].double().abs().T)
+    return out, size
+
+
+# bf16's half an ulp is at most 2^-8 of the result.  Within, as a share of the sum of magnitudes: fp32 sums in chains of
+# at most 128 additions, each off by 2^-23 of the sum so far at most (a tensor core may cut off instead of rounding),
+# 2^-16; A x in two bf16 parts, each within 2^-8 of what it stands for, 2^-16; the second product's 17 additions, 2^-18.
+def assert_adapted(got, out, size, what):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), what + ": not finite"
+    bound = 2.0 ** -8 * out.abs() * (1 + 2.0 ** -7) + (2.0 ** -15 + 2.0 ** -18) * size + 1e-30
+    err = (got - out).abs()
+    bad = err > bound
+    assert not bad.any(), "%s: %d of %d outside the bound, worst %.3g of it at %s" % (
+        what, int(bad.sum()), bad.numel(), float((err / bound).max()), bad.nonzero()[0].tolist())
+
+
+def ids_of(T, count, kind, seed):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "any":
+        return torch.randint(-1, count, (T,), generator=g, dtype=torch.int32)
+    if kind == "runs":
+        out = torch.empty(0, dtype=torch.int64)
+        while len(out) < T:
+            out = torch.cat((out, torch.randint(-1, count, (1,), generator=g).repeat(int(torch.randint(1, 90, (1,), generator=g)))))
+        return out[:T].to(torch.int32)
+    if kind == "none":
+        return torch.full((T,), -3, dtype=torch.int32)
+    return torch.full((T,), count - 1, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("T,K,N,r,count,kind", [
+    (1, 8, 8, 8, 1, "one"),
+    (1, 4096, 4096, 16, 3, "one"),
+    (1, 128, 256, 128, 1, "none"),
+    (2, 136, 72, 24, 2, "any"),
+    (7, 1000, 520, 8, 4, "any"),          # no multiple of 16 anywhere
+    (8, 264, 8, 40, 8, "any"),
+    (9, 8, 1032, 16, 3, "any"),
+    (17, 4096, 1024, 64, 20, "any"),
+    (33, 520, 2056, 72, 5, "runs"),
+    (64, 2048, 3080, 16, 64, "any"),
+    (65, 14336, 256, 32, 6, "any"),
+    (100, 1024, 1024, 128, 7, "runs"),
+    (257, 512, 776, 56, 9, "any"),
+    (300, 2048, 512, 64, 1, "one"),
+    (700, 1032, 1032, 16, 6, "runs"),     # the many-row form
+    (1030, 256, 2048, 104, 40, "any"),
+    (1500, 3000, 640, 8, 3, "runs"),
+    (2049, 640, 1000, 128, 5, "runs"),
+    (600, 64, 64, 32, 2, "none"),
+])
+@pytest.mark.parametrize("scaled", [True, False])
+def test_add_adapters(sp24, T, K, N, r, count, kind, scaled):
+    y, x, a, b, scales = inputs(T, K, N, r, count, seed=T + K)
+    ids = ids_of(T, count, kind, T)
+    s = scales if scaled else None
+    got = sp24.add_adapters(y.cuda(), x.cuda(), a.cuda(), b.cuda(), ids.cuda(), None if s is None else s.cuda())
+    sp24.last_device_error()
+    assert got.shape == (T, N) and got.dtype == torch.bfloat16
+    out, size = reference(y, x, a, b, ids, s)
+    assert_adapted(got, out, size, "adapters")
+    bare = ids < 0
+    assert torch.equal(got.cpu()[bare], y[bare])        # rows without an adapter keep every bit
+
+
+@pytest.mark.parametrize("T", [5, 40, 900])
+def test_strides_in_place_and_bounds(sp24, T):
+    """Rows and adapters further apart than their length; the result in place; nothing else is written, and NaN in what
+    belongs to no row's adapter, or lies between, reaches no result."""
+    K, N, r, count = 520, 264, 24, 6
+    y, x, a, b, scales = inputs(T, K, N, r, count, seed=T)
+    ids = ids_of(T, count, "runs" if T > 100 else "any", T)
+    ids[ids == 4] = 2                                   # nobody's
+    nan = float("nan")
+    xb, yb = torch.full((T + 2, K + 40), nan), torch.full((T + 2, N + 16), nan)
+    xb[1:T + 1, 16:16 + K], yb[1:T + 1, 8:8 + N] = x.float(), y.float()
+    ab, bb = torch.full((count, r * K + 64), nan), torch.full((count, N * r + 8), nan)
+    ab[:, :r * K], bb[:, :N * r] = a.float().flatten(1), b.float().flatten(1)
+    ab[4], bb[4] = nan, nan
+    xd, yd, ad, bd = (t.bfloat16().cuda() for t in (xb, yb, ab, bb))
+    av = torch.as_strided(ad, (count, r, K), (r * K + 64, K, 1))
+    bv = torch.as_strided(bd, (count, N, r), (N * r + 8, r, 1))
+    yv = yd[1:T + 1, 8:8 + N]
+    sc = scales.cuda()
+    sc[4] = nan
+    got = sp24.add_adapters(yv, xd[1:T + 1, 16:16 + K], av, bv, ids.cuda(), sc, out=yv)
+    sp24.last_device_error()
+    assert got is yv
+    out, size = reference(y, x, a, b, ids, scales)
+    assert_adapted(got, out, size, "in place")
+    rest = yd.clone()
+    rest[1:T + 1, 8:8 + N] = nan
+    assert rest.isnan().all()
+
+
+def test_a_row_that_is_not_finite_keeps_to_itself(sp24):
+    for T in (20, 800):
+        y, x, a, b, scales = inputs(T, 256, 136, 16, 2, seed=T)
+        ids = torch.zeros(T, dtype=torch.int32)
+        ids[1::3] = 1
+        clean = sp24.add_adapters(y.cuda(), x.cuda(), a.cuda(), b.cuda(), ids.cuda())
+        x[7, 3] = float("inf")
+        y[9, 5] = float("nan")
+        got = sp24.add_adapters(y.cuda(), x.cuda(), a.cuda(), b.cuda(), ids.cuda())
+        sp24.last_device_error()
+        assert not torch.isfinite(got[7].float()).any() and got[9, 5].isnan()
+        keep = torch.ones(T, 136, dtype=torch.bool)
+        keep[7], keep[9, 5] = False, False
+        assert torch.equal(got.cpu()[keep], clean.cpu()[keep])
+
+
+@pytest.mark.parametrize("T", [1, 48, 700])
+def test_the_same_every_time_streams_and_graphs(sp24, T):
+    y, x, a, b, scales = inputs(T, 1024, 520, 32, 5, seed=T)
+    ids = ids_of(T, 5, "any", 1)
+    yd, xd, ad, bd, sd, idd = (t.cuda() for t in (y, x, a, b, scales, ids))
+    first = sp24.add_adapters(yd, xd, ad, bd, idd, sd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    on_side = sp24.add_adapters(yd, xd, ad, bd, idd, sd, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(first, on_side)
+    out = torch.empty_like(yd)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sp24.add_adapters(yd, xd, ad, bd, idd, sd, out=out)
+    graph.replay()
+    assert torch.equal(first, out)
+    other = ids_of(T, 5, "any", 2)
+    idd.copy_(other)
+    graph.replay()
+    sp24.last_device_error()
+    want, size = reference(y, x, a, b, other, scales)
+    assert_adapted(out, want, size, "replayed with other adapters")
+
+
+def test_ids_out_of_range(sp24):
+    for T in (6, 600):
+        y, x, a, b, _ = inputs(T, 64, 72, 8, 2, seed=T)
+        ids = torch.zeros(T, dtype=torch.int32)
+        ids[3], ids[4] = 2, 2 ** 31 - 1
+        got = sp24.add_adapters(y.cuda(), x.cuda(), a.cuda(), b.cuda(), ids.cuda())
+        with pytest.raises(sp24.Sp24Error) as e:
+            sp24.last_device_error()
+        assert e.value.status == 8
+        out, size = reference(y, x, a, b, ids, None)
+        assert_adapted(got, out, size, "bad ids")
+        assert torch.equal(got.cpu()[3:5], y[3:5])
+
+
+def test_no_rows(sp24):
+    y, x, a, b, _ = inputs(3, 64, 72, 8, 2, seed=1)
+    got = sp24.add_adapters(y.cuda()[:0], x.cuda()[:0], a.cuda(), b.cuda(), torch.zeros(0, dtype=torch.int32, device="cuda"))
+    sp24.last_device_error()
+    assert got.shape == (0, 72)
