@@ -79,4 +79,49 @@ inline sp24_status check_attention(const void* q, int64_t rows, int64_t ldq, int
   return SP24_OK;
 }
 
+// ---------------------------------------------------------- shared first tokens
+// sp24_attention_decode_shared in two launches: the prompt kernel attends the
+// shared tokens of each group for all of its sequences' queries at once and
+// leaves sums in the workspace; the decode kernel attends each sequence's own tokens and
+// adds those sums.  What both know of the groups:
+struct SharedGroups {
+  const int32_t* cu;    // [G + 1]
+  const int32_t* lens;  // [G]
+  int G;
+  int2* where;          // [sequences] {pair of its block of rows with kv head 0, row in the block}
+  int2* pieces;         // [pairs] {first piece, how many}: what the pair's keys were cut into
+  float* part;          // [parts][2 kTileRows][D] sums of values, then [parts][2 kTileRows][2] maxima and sums
+  int pairs, parts;     // how many there is room for
+};
+constexpr int kTileRows = 128;          // query rows of a tile of the prompt kernel; two tiles are a block
+constexpr float kPromptUp = 7.0f;       // weights of an e4m3 cache are 2^this times exp2(c S - m) there
+
+// The tokens that a group [lo, hi) of sequences reads together: none if it is
+// one sequence, and no more than the sequence has whose pages they are read through.
+__device__ __forceinline__ int shared_tokens(int lo, int hi, int shared, const int32_t* seq_lens, int most) {
+  return hi - lo < 2 ? 0 : max(0, min(min(shared, most), __ldg(seq_lens + lo)));
+}
+
+// A call, as the entry point hands it to both launches.
+struct SharedCall {
+  const void* q;
+  int64_t ldq;
+  int B, q_heads;
+  const sp24_kv_cache* cache;
+  CacheView view;
+  const int32_t* page_table;
+  int table_width;
+  int64_t ld_table;
+  const int32_t* seq_lens;
+  float scale;
+  int window, sinks;
+  void* y;
+  int64_t ldy;
+  SharedGroups groups;
+  void* decode_workspace;
+};
+sp24_status launch_shared_tokens(const SharedCall& c, const DeviceInfo& dev, cudaStream_t s);  // sp24_attn_prompt.cu
+sp24_status launch_own_tokens(const SharedCall& c, const DeviceInfo& dev, cudaStream_t s);     // sp24_attn_decode.cu
+size_t decode_workspace_bytes(const DeviceInfo& dev, int q_heads, int heads, int head_dim);    // sp24_attn_decode.cu
+
 }  // namespace sp24

@@ -68,6 +68,7 @@ struct DecodeParams {
   float* partials;                   // [2 slots per CTA][8 NH][D], then [2 slots][8 NH][2] maxima and sums
   unsigned int* counters;            // [CTAs] pieces that arrived, by the pair's first CTA
   unsigned int* err;
+  SharedGroups sh;
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
@@ -119,11 +120,24 @@ struct Span {
   int lo, sinks;
   int from;          // where the window's chunks begin
   int sink_chunks, tiles;
+  bool shared;       // the keys before lo are in the workspace already
 };
 
-template <int CT>
-__device__ __forceinline__ Span span_of(const DecodeParams& p, int n, bool report) {
+// How many first tokens sequence b reads together with its group.
+__device__ __forceinline__ int shared_of(const DecodeParams& p, int b) {
+  int g = 0, end = p.sh.G;
+  while (end - g > 1) {  // the last group that begins at b or before
+    const int mid = (g + end) / 2;
+    if (__ldg(p.sh.cu + mid) <= b) g = mid; else end = mid;
+  }
+  const int lo = max(__ldg(p.sh.cu + g), 0), hi = min(__ldg(p.sh.cu + g + 1), p.B);
+  return b < lo || b >= hi ? 0 : shared_tokens(lo, hi, __ldg(p.sh.lens + g), p.seq_lens, p.table_width << p.cache.page_shift);
+}
+
+template <int CT, bool SHARED>
+__device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool report) {
   Span s;
+  int n = __ldg(p.seq_lens + b);
   const int most = p.table_width << p.cache.page_shift;
   if (n < 0 || n > most) {
     if (report) atomicOr(p.err, DEVERR_INDEX);
@@ -133,6 +147,11 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int n, bool repor
   s.lo = p.window > 0 && n > p.window ? n - p.window : 0;
   s.sinks = min(p.sinks, s.lo);
   if (s.sinks == s.lo) s.lo = s.sinks = 0;
+  s.shared = false;
+  if (SHARED && s.lo == 0) {
+    const int shared = shared_of(p, b);
+    if (shared > 0 && shared <= n) s.shared = true, s.lo = shared;
+  }
   s.from = s.lo & ~15;
   s.sink_chunks = (s.sinks + CT - 1) / CT;
   const int chunks = s.sink_chunks + (n - s.from + CT - 1) / CT;
@@ -146,6 +165,9 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int n, bool repor
 // smallest step is 2^-24 of it: of 131071 keys some 17 nats below one other, half
 // a percent of the sum, each would be rounded by up to a half.)
 constexpr float kUp = 15.0f;
+// Sums of the prompt kernel times this are at the same scale.
+constexpr float kFromPrompt = 256.0f;
+static_assert(kUp - kPromptUp == 8.0f, "");
 
 // Stages of a warp's ring.  e4m3: 3 (64 ragged sequences 169.6 us, 172.2 with
 // 2), but 2 where 16 heads' exchange buffer takes the room.  bf16: 2 (131071
@@ -162,7 +184,9 @@ struct Item {
   Span sp;
 };
 
-template <int D, bool E4M3, int NH>
+// SHARED: the keys that a sequence reads together with its group are attended by
+// an earlier launch; its sums are added where a pair's own are complete.
+template <int D, bool E4M3, int NH, bool SHARED = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int ROWB = D * (E4M3 ? 1 : 2);   // bytes of a token's key
   constexpr int CT = kHalf / ROWB;           // tokens per chunk: 16, 32 or 64
@@ -185,13 +209,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring_a = smem_u32(smem + warp * RING);
   float* const exchange = reinterpret_cast<float*>(smem + kWarps * RING);  // [kWarps][HEADS][PAD]
-  pdl_wait();
+  // (The launch before has waited for those that write what this one reads before its own wait.)
+  if (!SHARED) pdl_wait();
 
   // ---- this CTA's range of tiles
   const int HH = p.kv_heads * p.head_blocks;
   // Tiles of the sequences: a sum over all, and a running sum over the first kThreads.
   auto tiles_of = [&](int x, bool report) {
-    return x < p.B ? span_of<CT>(p, __ldg(p.seq_lens + x), report).tiles : 0;
+    return x < p.B ? span_of<CT, SHARED>(p, x, report).tiles : 0;
   };
   auto scan = [&](int x) {  // inclusive, over the warp
 #pragma unroll
@@ -215,7 +240,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
   for (int w = 0; w < kWarps; ++w) total += s_sum[0][w] + s_sum[1][w];
   total *= HH;
   const unsigned int ctas = min(gridDim.x, total), cta = blockIdx.x;
-  if (cta >= ctas) return;  // uniform
+  if (cta >= ctas) {  // uniform
+    if (SHARED) pdl_wait();
+    return;
+  }
   const unsigned int per = total / ctas, extra = total % ctas;  // the first `extra` CTAs take a tile more
   unsigned int u = cta * per + min(cta, extra);
   const unsigned int u_end = u + per + (cta < extra ? 1u : 0u);
@@ -252,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
 
   Item it;
   it.b = b;
-  it.sp = span_of<CT>(p, __ldg(p.seq_lens + b), false);
+  it.sp = span_of<CT, SHARED>(p, b, false);
   // The item that tile u of the launch begins.
   auto place = [&](Item& x) {
     const unsigned int local = u - static_cast<unsigned int>(before) * HH;
@@ -337,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
       if (it.hh == HH - 1) {
         before += it.sp.tiles;
         nx.b = it.b + 1;
-        nx.sp = span_of<CT>(p, __ldg(p.seq_lens + nx.b), false);
+        nx.sp = span_of<CT, SHARED>(p, nx.b, false);
       }
       place(nx);
       fetch_pages(nx, nx.t0 + lane, page_then);
@@ -581,6 +609,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     float* part = p.partials + int64_t(slot) * (HEADS * D);
     float* part_ml = p.partials + int64_t(2) * gridDim.x * (HEADS * D) + int64_t(slot) * (HEADS * 2);
     const float vscale = E4M3 ? p.cache.v_scale[hk] : 1.0f;
+    // The shared tokens' sums of head h, dims d .. d + 3, kAhead pieces at a time.
+    int2 shared_at = make_int2(0, 0);  // {row of the first piece (of all pieces' rows), pieces}
+    if (SHARED) {
+      pdl_wait();
+      if (it.sp.shared) {
+        const int2 at = __ldcg(p.sh.where + b);
+        const int pair = at.x + hk;
+        // (What is out of range can only come from groups that are not in order.)
+        if (at.x >= 0 && pair < p.sh.pairs && at.y >= 0 && at.y + p.group <= 2 * kTileRows) {
+          const int2 pc = __ldcg(p.sh.pieces + pair);
+          if (pc.x >= 0 && pc.y > 0 && pc.y <= p.sh.parts - pc.x)
+            shared_at = make_int2(pc.x * (2 * kTileRows) + at.y + hb * HEADS, pc.y);
+        }
+      }
+    }
+    auto add_shared = [&](int h, int d, float& top, float& sum, float4& acc) {
+      constexpr int kAhead = 8;
+      const float* ml = p.sh.part + int64_t(p.sh.parts) * (2 * kTileRows * D);
+      for (int i0 = 0; i0 < shared_at.y; i0 += kAhead) {
+        float4 v[kAhead];
+        float2 w[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          v[i] = make_float4(0, 0, 0, 0);
+          w[i] = make_float2(-INFINITY, 0.0f);
+          if (i0 + i < shared_at.y) {
+            const int64_t row = shared_at.x + int64_t(i0 + i) * (2 * kTileRows) + h;
+            w[i] = __ldcg(reinterpret_cast<const float2*>(ml + 2 * row));
+            v[i] = __ldcg(reinterpret_cast<const float4*>(p.sh.part + row * D + d));
+          }
+        }
+        float now = top;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) now = fmaxf(now, w[i].x);
+        const float use = now == -INFINITY ? 0.0f : now, keep = ex2(top - use);
+        top = now;
+        sum *= keep;
+        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const float f = ex2(w[i].x - use) * (E4M3 ? kFromPrompt : 1.0f);
+          sum = fmaf(w[i].y, f, sum);
+          acc.x = fmaf(v[i].x, f, acc.x), acc.y = fmaf(v[i].y, f, acc.y);
+          acc.z = fmaf(v[i].z, f, acc.z), acc.w = fmaf(v[i].w, f, acc.w);
+        }
+      }
+    };
     for (int i = tid; i < heads * (D / 4); i += kThreads) {
       const int h = i / (D / 4), d = (i % (D / 4)) * 4;
       float top = -INFINITY, sum = 0.0f;
@@ -600,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
         __stcg(reinterpret_cast<float4*>(part + h * D + d), acc);
         if (d == 0) __stcg(reinterpret_cast<float2*>(part_ml + 2 * h), make_float2(top, sum));
       } else {
+        if (SHARED) add_shared(h, d, top, sum, acc);
         const float f = sum == 0.0f ? 0.0f : vscale / sum;
         *reinterpret_cast<uint2*>(p.y + b * p.ldy + int64_t(h0 + h) * D + d) =
             make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
@@ -656,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
               acc.z = fmaf(v[i].z, f, acc.z), acc.w = fmaf(v[i].w, f, acc.w);
             }
           }
+          if (SHARED) add_shared(h, d, top, sum, acc);
           const float f = sum == 0.0f ? 0.0f : vscale / sum;
           *reinterpret_cast<uint2*>(p.y + b * p.ldy + int64_t(h0 + h) * D + d) =
               make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
@@ -675,18 +752,55 @@ size_t workspace_bytes_for(int ctas, int heads, int D) {
   return control_bytes(ctas) + static_cast<size_t>(2) * ctas * heads * (D + 2) * 4;
 }
 
-template <int D, bool E4M3, int NH>
+template <int D, bool E4M3, int NH, bool SHARED = false>
 sp24_status launch(const DecodeParams& p, const DeviceInfo& dev, int ctas, cudaStream_t s) {
   constexpr int TT = kHalf / (D * (E4M3 ? 1 : 2)) * kWarps;
   // Tile numbers are 32-bit: the host refuses what could pass them.
   const int64_t most = (int64_t(p.table_width) << p.cache.page_shift) / TT + 3;
   if (most * p.B > INT32_MAX / (int64_t(p.kv_heads) * p.head_blocks)) return SP24_ERR_UNSUPPORTED;
   const int smem = kSmem<D, E4M3, NH>;
-  const cudaError_t r = launch_pdl_smem<attention_decode_kernel<D, E4M3, NH>>(dev, dim3(ctas), dim3(kThreads), smem, s, p);
+  const cudaError_t r = 
+      launch_pdl_smem<attention_decode_kernel<D, E4M3, NH, SHARED>>(dev, dim3(ctas), dim3(kThreads), smem, s, p);
   return r == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
 }
 
 }  // namespace
+
+size_t decode_workspace_bytes(const DeviceInfo& dev, int q_heads, int heads, int head_dim) {
+  return workspace_bytes_for(dev.sm_count * kCtasPerSm, heads_per_cta(q_heads / heads), head_dim);
+}
+
+sp24_status launch_own_tokens(const SharedCall& c, const DeviceInfo& dev, cudaStream_t s) {
+  DecodeParams p = {};
+  const int ctas = dev.sm_count * kCtasPerSm, group = c.q_heads / c.cache->heads, hpc = heads_per_cta(group);
+  p.q = static_cast<const __nv_bfloat16*>(c.q);
+  p.ldq = c.ldq;
+  p.B = c.B;
+  p.cache = c.view;
+  p.page_table = c.page_table;
+  p.table_width = c.table_width;
+  p.ld_table = c.ld_table;
+  p.seq_lens = c.seq_lens;
+  p.scale = c.scale;
+  p.window = c.window;
+  p.sinks = c.sinks;
+  p.y = static_cast<__nv_bfloat16*>(c.y);
+  p.ldy = c.ldy;
+  p.kv_heads = c.cache->heads;
+  p.group = group;
+  p.head_blocks = (group + hpc - 1) / hpc;
+  p.counters = static_cast<unsigned int*>(c.decode_workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(c.decode_workspace) + control_bytes(ctas));
+  p.err = dev.err_word;
+  p.sh = c.groups;
+  const bool e4m3 = c.cache->dtype == SP24_E4M3;
+  if (c.cache->head_dim == 128) {
+    if (hpc == 8) return e4m3 ? launch<128, true, 1, true>(p, dev, ctas, s) : launch<128, false, 1, true>(p, dev, ctas, s);
+    return e4m3 ? launch<128, true, 2, true>(p, dev, ctas, s) : launch<128, false, 2, true>(p, dev, ctas, s);
+  }
+  if (hpc == 8) return e4m3 ? launch<64, true, 1, true>(p, dev, ctas, s) : launch<64, false, 1, true>(p, dev, ctas, s);
+  return e4m3 ? launch<64, true, 2, true>(p, dev, ctas, s) : launch<64, false, 2, true>(p, dev, ctas, s);
+}
 }  // namespace sp24
 
 extern "C" size_t sp24_attention_decode_workspace_size(int q_heads, int heads, int head_dim) {

@@ -62,7 +62,7 @@
 namespace sp24 {
 namespace {
 
-constexpr int BM = 128;   // query rows per tile, two tiles per CTA
+constexpr int BM = kTileRows;  // query rows per tile, two tiles per CTA
 constexpr int BN = 128;   // keys per tile
 constexpr int kLeastTiles = 4;  // key tiles of a part, at least, where a block's keys are cut
 
@@ -84,6 +84,7 @@ struct PromptParams {
   float* part;     // splits > 1: of each part, O [2 BM][D], and then of all parts, maxima and sums [2 BM][2]
   int parts;       // how many `part` holds
   unsigned int* err;
+  SharedGroups sh;  // shared first tokens: rows are sequences, of which each has one
 };
 
 template <int D_, bool E4M3_>
@@ -122,7 +123,7 @@ struct Cfg {
   // times that where the maximum has grown by less, so up to 2^15, near f16's end.
   // The row's largest weight is 2^7 at least; f16's smallest step, 2^-24, rounds
   // the smallest weights by 2^-32 of it at most.
-  static constexpr float UP = 7.0f;
+  static constexpr float UP = kPromptUp;
   static constexpr uint32_t P_COL = APART ? 2 * BN : 0, P_STEP = APART ? BN / 2 : BN;  // P of query tile x
   static constexpr uint32_t O_COL = APART ? 3 * BN : 2 * BN;                           // O of query tile x: + x D
 };
@@ -234,6 +235,7 @@ struct Work {
   int first, nst;    // key tiles: 0 .. nst - 1 (sinks), then first, first + 1, ...
   int t0, nt;        // which of them: nt from number t0 on
   int part;          // where this part's sums go (splits > 1)
+  int pair, piece0, pieces;  // (shared tokens) the pair, and all the parts that its keys are cut into
 };
 
 __device__ __forceinline__ int tile_of(const Work& w, int i) {
@@ -324,7 +326,85 @@ __device__ __forceinline__ void find_work(const PromptParams& p, int block, int 
   __syncwarp();
 }
 
-template <class C>
+// The same for shared first tokens.  A pair is a block of a group's sequences and
+// a kv head, a unit a key tile of it; the units of all pairs are dealt out to the
+// CTAs in equal contiguous ranges, so that groups of any sizes and lengths keep
+// all SMs busy alike.
+struct Deal {
+  unsigned int units, ctas, per, extra;  // the first `extra` CTAs take a unit more
+  __device__ __forceinline__ unsigned int begin(unsigned int cta) const { return cta * per + min(cta, extra); }
+  __device__ __forceinline__ unsigned int cta_of(unsigned int u) const {
+    return u < extra * (per + 1) ? u / (per + 1) : extra + (u - extra * (per + 1)) / per;
+  }
+};
+constexpr int kLeastUnits = 4;  // per CTA
+
+// Goes through the groups, 32 at a time: the units of all of them, or (`out`) the
+// work that begins with unit u.  Groups are brought into order: each begins
+// where the one before it ends.
+__device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int lane, bool report, const Deal& deal,
+                                                    unsigned int u, unsigned int u_end, unsigned int cta, Work* out) {
+  const int tok = 2 * p.tile_tokens, most = p.table_width << p.cache.page_shift;
+  const int first = __ldg(p.sh.cu);
+  int carry = min(max(first, 0), p.T);
+  if (report && lane == 0 && first != carry) atomicOr(p.err, DEVERR_INDEX);
+  unsigned int units_before = 0, pairs_before = 0;
+  if (out && lane == 0) out->b = -1;
+  __syncwarp();
+  for (int g0 = 0; g0 < p.sh.G; g0 += 32) {
+    const int g = g0 + lane;
+    int end = 0, raw = 0, shared = 0;
+    if (g < p.sh.G) raw = __ldg(p.sh.cu + g + 1), shared = __ldg(p.sh.lens + g);
+    end = max(min(raw, p.T), carry);
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, end, m);
+      if (lane >= m) end = max(end, x);
+    }
+    int lo = __shfl_up_sync(0xFFFFFFFFu, end, 1);
+    if (lane == 0) lo = carry;
+    if (report && g < p.sh.G && (raw != end || shared < 0 || shared > most)) atomicOr(p.err, DEVERR_INDEX);
+    const int n = g < p.sh.G ? shared_tokens(lo, end, shared, p.seq_lens, most) : 0;
+    const unsigned int tiles = (n + BN - 1) / BN;
+    const unsigned int pairs = tiles ? (end - lo + tok - 1) / tok * p.kv_heads : 0, units = pairs * tiles;
+    unsigned int ui = units, pi = pairs;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const unsigned int x = __shfl_up_sync(0xFFFFFFFFu, ui, m), y = __shfl_up_sync(0xFFFFFFFFu, pi, m);
+      if (lane >= m) ui += x, pi += y;
+    }
+    ui += units_before, pi += pairs_before;
+    if (out && u < u_end && u < ui && u >= ui - units) {
+      Work w;
+      const unsigned int local = u - (ui - units), pair = local / tiles;
+      const int block = pair / p.kv_heads;
+      w.b = lo;
+      w.hk = pair - block * p.kv_heads;
+      w.row0 = lo + block * tok;
+      w.rows = end - w.row0;
+      w.p0 = w.p_hi = n - 1;
+      w.wlo = w.send = w.first = w.nst = 0;
+      w.t0 = local - pair * tiles;
+      w.nt = min(tiles - w.t0, u_end - u);
+      w.pair = pi - pairs + pair;
+      w.part = w.pair + cta;  // (either grows from one piece to the next)
+      const unsigned int u0 = u - w.t0;
+      w.piece0 = w.pair + deal.cta_of(u0);
+      w.pieces = deal.cta_of(u0 + tiles - 1) - deal.cta_of(u0) + 1;
+      if (w.pair >= p.sh.pairs || w.part >= p.sh.parts) w.b = -1;  // (there is room for all that the host expects)
+      *out = w;
+    }
+    units_before = __shfl_sync(0xFFFFFFFFu, ui, 31), pairs_before = __shfl_sync(0xFFFFFFFFu, pi, 31);
+    carry = __shfl_sync(0xFFFFFFFFu, end, 31);
+    if (out && u < units_before) break;
+  }
+  __syncwarp();
+  return units_before;
+}
+
+// SHARED: the shared first tokens of groups of sequences, for one query per
+// sequence; every row sees all of them, and sums go to the workspace.
+template <class C, bool SHARED = false>
 __global__ void __launch_bounds__(C::THREADS, 1)
     attention_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptParams p) {
@@ -397,6 +477,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (SHARED) pdl_trigger();  // sequences' own tokens on SMs that have none of this, and as they get done
   const uint32_t tmem = s_tmem;
   // The work of this CTA's next block, for every role but the one that finds
   // it; done_with says that this warp will not read it again.
@@ -462,7 +543,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // What the loop needs of the block, in registers: shared memory is busy with the MMAs' operands, and a read
         // would take some hundred cycles.
         const int nt = w.nt, nst = w.nst - w.t0, first = w.first * BN;  // nst: sink tiles from here on
-        const int p_min = w.p0 + x * p.tile_tokens, p_max = min(w.p_hi, p_min + p.tile_tokens - 1);
+        const int p_min = SHARED ? w.p_hi : w.p0 + x * p.tile_tokens, p_max = min(w.p_hi, p_min + p.tile_tokens - 1);
         int base = tile_of(w, 0) * BN;
         for (int i = 0; i < nt; ++i, ++sn, base = i == nst && nst > 0 ? first : base + BN) {
           ok = mbar_wait(&s_full[x], sn & 1);
@@ -470,7 +551,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tc_fence_after();
           const int end = base + BN - 1;
           // Columns that this row does not see: past its own position, or before its window and after the sinks.
-          const bool cut_hi = end > p_min, cut_lo = p.window > 0 && base <= p_max - p.window && end >= p.sinks;
+          const bool cut_hi = end > p_min, cut_lo = !SHARED && p.window > 0 && base <= p_max - p.window && end >= p.sinks;
           uint32_t su[BN];
 #pragma unroll
           for (int j = 0; j < BN / 32; ++j) tmem_ld32(ts + 32 * j, su + 32 * j);
@@ -485,7 +566,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // (The position is worked out here, once or twice per block, to leave the registers to S.)
             int rr = r;
             asm volatile("" : "+r"(rr));  // here, not ahead of the loop
-            const int token = token_of(p, rr);
+            const int token = SHARED ? 0 : token_of(p, rr);
             // (rows past the tile's tokens are no one's)
             const int hi = token < p.tile_tokens ? p_min + token - base : BN, lo = hi - p.window, sk = p.sinks - base;
             // Each 32 columns only where some row of the warp does not see them all.
@@ -604,7 +685,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       };
       int rr = r;
       asm volatile("" : "+r"(rr));  // worked out here, not ahead of the loop: S takes the registers there
-      if (p.splits > 1) {
+      if (SHARED) {
+        // As below, but only the rows that are some sequence's; and where the decode kernel finds them.
+        float* const o_part = p.sh.part + static_cast<int64_t>(w.part) * (2 * BM * D) + x * (BM * D);
+        float* const ml = p.sh.part + static_cast<int64_t>(p.sh.parts) * (2 * BM * D) +
+                          static_cast<int64_t>(w.part) * (2 * BM * 2) + x * (BM * 2);
+        const int token = token_of(p, rr), at = x * p.tile_tokens + token;
+        const bool mine = token < p.tile_tokens && at < w.rows;
+        if (mine) *reinterpret_cast<float2*>(ml + 2 * rr) = make_float2(m, l);
+        if (w.t0 == 0) {
+          if (mine && w.hk == 0 && rr == token * p.group) p.sh.where[w.row0 + at] = make_int2(w.pair, x * BM + rr);
+          if (x == 0 && rr == 0) p.sh.pieces[w.pair] = make_int2(w.piece0, w.pieces);
+        }
+        const unsigned int some = __ballot_sync(0xFFFFFFFFu, mine);
+#pragma unroll 1
+        for (int j = 0; j < D && some; j += 16) {
+          uint32_t v[4][4];
+          tmem_ld16(to + j, reinterpret_cast<uint32_t(&)[16]>(v));
+          tmem_ld_wait();
+          exchange(v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (some >> ((lane & ~3) + k) & 1)
+              *reinterpret_cast<uint4*>(o_part + ((rr & ~3) + k) * D + j + (lane & 3) * 4) =
+                  make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        }
+      } else if (p.splits > 1) {
         // This part's O as it is, and its maximum and sum; attention_join_kernel adds the parts up.
         float* const o_part = p.part + static_cast<int64_t>(w.part) * (2 * BM * D) + x * (BM * D);
         float* const ml = p.part + static_cast<int64_t>(p.parts) * (2 * BM * D) + w.part * (2 * BM * 2) + x * (BM * 2);
@@ -810,22 +916,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int ring = 0, last = -1, block = blockIdx.x, total = 0;
       uint32_t qn[2] = {0, 0};
       Rows mine = {0, 0, 0};
-      if (keys) total = count_blocks(p, lane, blockIdx.x == 0, mine);
+      Deal deal = {};
+      unsigned int unit = 0, unit_end = 0;
+      if (SHARED && keys) {
+        deal.units = scan_groups(p, lane, blockIdx.x == 0, deal, 0, 0, 0, nullptr);
+        deal.ctas = min(gridDim.x, max(1u, deal.units / kLeastUnits));
+        deal.per = deal.units / deal.ctas, deal.extra = deal.units % deal.ctas;
+        if (blockIdx.x < deal.ctas) unit = deal.begin(blockIdx.x), unit_end = deal.begin(blockIdx.x + 1);
+      }
+      if (!SHARED && keys) total = count_blocks(p, lane, blockIdx.x == 0, mine);
       int item = 0;
       for (; ok; ++item) {
         Work w;
         if (keys) {
           if (item >= 2) ok = mbar_wait(&work_empty[item & 1], ((item >> 1) - 1) & 1);
           if (!ok) break;
-          find_work(p, block, total, item == 0 ? &mine : nullptr, lane, &s_work[item & 1]);
+          if (SHARED)
+            scan_groups(p, lane, false, deal, unit, unit_end, blockIdx.x, &s_work[item & 1]);
+          else
+            find_work(p, block, total, item == 0 ? &mine : nullptr, lane, &s_work[item & 1]);
           w = s_work[item & 1];
           if (lane == 0) mbar_arrive(&work_full[item & 1]);
           if (w.b < 0) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(stolen, 16);
-            steal_block(&s_response, stolen);
+          if (!SHARED) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(stolen, 16);
+              steal_block(&s_response, stolen);
+            }
+            asked = true;
           }
-          asked = true;
         } else {
           ok = wait_work(item);
           if (!ok) break;
@@ -881,7 +1000,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           __syncwarp();
         }
         ring += 2 * w.nt;
-        if (keys && ok) {
+        if (SHARED && keys) unit += w.nt;
+        if (!SHARED && keys && ok) {
           ok = mbar_wait(stolen, item & 1);
           if (!ok) break;
           asked = false;
@@ -1062,10 +1182,8 @@ inline size_t part_bytes(const Shape& s, int heads, int D) {
 }
 
 template <int D, bool E4M3>
-sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_heads, const sp24_kv_cache& cache,
-                   const DeviceInfo& dev, int64_t blocks, cudaStream_t s) {
-  using C = Cfg<D, E4M3>;
-  CUtensorMap qmap, kmap, vmap;
+sp24_status make_maps(const PromptParams& p, const void* q, int64_t ldq, int q_heads, const sp24_kv_cache& cache,
+                      CUtensorMap& qmap, CUtensorMap& kmap, CUtensorMap& vmap) {
   {
     const uint64_t dims[3] = {uint64_t(D), uint64_t(q_heads), uint64_t(p.T)};
     const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(ldq) * 2};
@@ -1081,7 +1199,15 @@ sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_head
   const auto type = E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto swizzle = E4M3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   if (sp24_status st = make_tmap_nd(&kmap, cache.k, type, 4, dims, strides, box, swizzle)) return st;
-  if (sp24_status st = make_tmap_nd(&vmap, cache.v, type, 4, dims, strides, box, swizzle)) return st;
+  return make_tmap_nd(&vmap, cache.v, type, 4, dims, strides, box, swizzle);
+}
+
+template <int D, bool E4M3>
+sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_heads, const sp24_kv_cache& cache,
+                   const DeviceInfo& dev, int64_t blocks, cudaStream_t s) {
+  using C = Cfg<D, E4M3>;
+  CUtensorMap qmap, kmap, vmap;
+  if (sp24_status st = make_maps<D, E4M3>(p, q, ldq, q_heads, cache, qmap, kmap, vmap)) return st;
   if (launch_pdl_smem<attention_prompt_kernel<C>>(dev, dim3(static_cast<unsigned>(blocks * p.splits * p.kv_heads)),
                                                   dim3(C::THREADS), C::SMEM, s, qmap, kmap, vmap, p) != cudaSuccess)
     return SP24_ERR_CUDA;
@@ -1092,7 +1218,38 @@ sp24_status launch(const PromptParams& p, const void* q, int64_t ldq, int q_head
   return SP24_OK;
 }
 
+template <int D, bool E4M3>
+sp24_status launch_shared(const PromptParams& p, const SharedCall& c, const DeviceInfo& dev, cudaStream_t s) {
+  using C = Cfg<D, E4M3>;
+  CUtensorMap qmap, kmap, vmap;
+  if (sp24_status st = make_maps<D, E4M3>(p, c.q, c.ldq, c.q_heads, *c.cache, qmap, kmap, vmap)) return st;
+  const cudaError_t r = launch_pdl_smem<attention_prompt_kernel<C, true>>(dev, dim3(dev.sm_count), dim3(C::THREADS), C::SMEM, s,
+                                                                          qmap, kmap, vmap, p);
+  return r == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
+}
+
 }  // namespace
+
+sp24_status launch_shared_tokens(const SharedCall& c, const DeviceInfo& dev, cudaStream_t s) {
+  PromptParams p = {};
+  p.T = c.B;
+  p.cache = c.view;
+  p.page_table = c.page_table;
+  p.table_width = c.table_width;
+  p.ld_table = c.ld_table;
+  p.seq_lens = c.seq_lens;
+  p.scale = c.scale;
+  p.kv_heads = c.cache->heads;
+  p.group = c.q_heads / c.cache->heads;
+  p.tile_tokens = BM / p.group;
+  p.inv_group = (65536u + p.group - 1) / p.group;
+  p.splits = 1;
+  p.err = dev.err_word;
+  p.sh = c.groups;
+  if (c.cache->head_dim == 128)
+    return c.cache->dtype == SP24_E4M3 ? launch_shared<128, true>(p, c, dev, s) : launch_shared<128, false>(p, c, dev, s);
+  return c.cache->dtype == SP24_E4M3 ? launch_shared<64, true>(p, c, dev, s) : launch_shared<64, false>(p, c, dev, s);
+}
 }  // namespace sp24
 
 extern "C" size_t sp24_attention_prompt_workspace_size(int64_t T, int64_t B, int q_heads, const sp24_kv_cache* cache,
