@@ -80,21 +80,24 @@ inline sp24_status check_attention(const void* q, int64_t rows, int64_t ldq, int
 }
 
 // ---------------------------------------------------------- shared first tokens
-// sp24_attention_decode_shared in two launches: the prompt kernel attends the
-// shared tokens of each group for all of its sequences' queries at once and
-// leaves sums in the workspace; the decode kernel attends each sequence's own tokens and
-// adds those sums.  What both know of the groups:
+// sp24_attention_decode_shared in three launches: the prompt kernel attends the
+// shared tokens of each group for all of its sequences' queries at once, the
+// decode kernel each sequence's own tokens; both leave maxima, sums and weighted values
+// in the workspace, which the third launch adds up.  What they know of the groups:
 struct SharedGroups {
   const int32_t* cu;    // [G + 1]
   const int32_t* lens;  // [G]
   int G;
-  int2* where;          // [sequences] {pair of its block of rows with kv head 0, row in the block}
-  int2* pieces;         // [pairs] {first piece, how many}: what the pair's keys were cut into
-  float* part;          // [parts][2 kTileRows][D] sums of values, then [parts][2 kTileRows][2] maxima and sums
+  int2* where;          // [sequences][kv heads] {row of its first head in the first piece, how many pieces}
+  float* part;          // [parts][2 kTileRows][D] weighted values, then [parts][2 kTileRows][2] maxima and sums
   int pairs, parts;     // how many there is room for
+  float* own;           // [sequences][query heads][D] and then [2]: the same of a sequence's own tokens, with
+                        // kNotShared for the sum of weights where there is nothing to add
 };
+constexpr float kNotShared = -1.0f;
 constexpr int kTileRows = 128;          // query rows of a tile of the prompt kernel; two tiles are a block
-constexpr float kPromptUp = 7.0f;       // weights of an e4m3 cache are 2^this times exp2(c S - m) there
+// Weights of an e4m3 cache are 2^this times exp2(c S - m) in the kernels for prompts and for decoding.
+constexpr float kPromptUp = 7.0f, kDecodeUp = 15.0f;
 
 // The tokens that a group [lo, hi) of sequences reads together: none if it is
 // one sequence, and no more than the sequence has whose pages they are read through.

@@ -164,10 +164,7 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool repor
 // one is off by 2^-40 of the largest at most.  (With the largest at 1 f16's
 // smallest step is 2^-24 of it: of 131071 keys some 17 nats below one other, half
 // a percent of the sum, each would be rounded by up to a half.)
-constexpr float kUp = 15.0f;
-// Sums of the prompt kernel times this are at the same scale.
-constexpr float kFromPrompt = 256.0f;
-static_assert(kUp - kPromptUp == 8.0f, "");
+constexpr float kUp = kDecodeUp;
 
 // Stages of a warp's ring.  e4m3: 3 (64 ragged sequences 169.6 us, 172.2 with
 // 2), but 2 where 16 heads' exchange buffer takes the room.  bf16: 2 (131071
@@ -185,7 +182,7 @@ struct Item {
 };
 
 // SHARED: the keys that a sequence reads together with its group are attended by
-// an earlier launch; its sums are added where a pair's own are complete.
+// another launch; a row's sums go to the workspace, where a third adds the two up.
 template <int D, bool E4M3, int NH, bool SHARED = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int ROWB = D * (E4M3 ? 1 : 2);   // bytes of a token's key
@@ -609,52 +606,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     float* part = p.partials + int64_t(slot) * (HEADS * D);
     float* part_ml = p.partials + int64_t(2) * gridDim.x * (HEADS * D) + int64_t(slot) * (HEADS * 2);
     const float vscale = E4M3 ? p.cache.v_scale[hk] : 1.0f;
-    // The shared tokens' sums of head h, dims d .. d + 3, kAhead pieces at a time.
-    int2 shared_at = make_int2(0, 0);  // {row of the first piece (of all pieces' rows), pieces}
-    if (SHARED) {
-      pdl_wait();
-      if (it.sp.shared) {
-        const int2 at = __ldcg(p.sh.where + b);
-        const int pair = at.x + hk;
-        // (What is out of range can only come from groups that are not in order.)
-        if (at.x >= 0 && pair < p.sh.pairs && at.y >= 0 && at.y + p.group <= 2 * kTileRows) {
-          const int2 pc = __ldcg(p.sh.pieces + pair);
-          if (pc.x >= 0 && pc.y > 0 && pc.y <= p.sh.parts - pc.x)
-            shared_at = make_int2(pc.x * (2 * kTileRows) + at.y + hb * HEADS, pc.y);
-        }
+    // A row that is complete: out, or, where shared tokens are to be added, to the workspace as it is.
+    auto put = [&](int h, int d, float top, float sum, const float4& acc) {
+      if (SHARED) {
+        const int64_t row = int64_t(b) * (p.kv_heads * p.group) + h0 + h;
+        float* ml = p.sh.own + int64_t(p.B) * (p.kv_heads * p.group) * D + 2 * row;
+        if (it.sp.shared) __stcg(reinterpret_cast<float4*>(p.sh.own + row * D + d), acc);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(ml), make_float2(top, it.sp.shared ? sum : kNotShared));
+        if (it.sp.shared) return;
       }
-    }
-    auto add_shared = [&](int h, int d, float& top, float& sum, float4& acc) {
-      constexpr int kAhead = 8;
-      const float* ml = p.sh.part + int64_t(p.sh.parts) * (2 * kTileRows * D);
-      for (int i0 = 0; i0 < shared_at.y; i0 += kAhead) {
-        float4 v[kAhead];
-        float2 w[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          v[i] = make_float4(0, 0, 0, 0);
-          w[i] = make_float2(-INFINITY, 0.0f);
-          if (i0 + i < shared_at.y) {
-            const int64_t row = shared_at.x + int64_t(i0 + i) * (2 * kTileRows) + h;
-            w[i] = __ldcg(reinterpret_cast<const float2*>(ml + 2 * row));
-            v[i] = __ldcg(reinterpret_cast<const float4*>(p.sh.part + row * D + d));
-          }
-        }
-        float now = top;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) now = fmaxf(now, w[i].x);
-        const float use = now == -INFINITY ? 0.0f : now, keep = ex2(top - use);
-        top = now;
-        sum *= keep;
-        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const float f = ex2(w[i].x - use) * (E4M3 ? kFromPrompt : 1.0f);
-          sum = fmaf(w[i].y, f, sum);
-          acc.x = fmaf(v[i].x, f, acc.x), acc.y = fmaf(v[i].y, f, acc.y);
-          acc.z = fmaf(v[i].z, f, acc.z), acc.w = fmaf(v[i].w, f, acc.w);
-        }
-      }
+      const float f = sum == 0.0f ? 0.0f : vscale / sum;
+      *reinterpret_cast<uint2*>(p.y + b * p.ldy + int64_t(h0 + h) * D + d) =
+          make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
     };
     for (int i = tid; i < heads * (D / 4); i += kThreads) {
       const int h = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -675,10 +638,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
         __stcg(reinterpret_cast<float4*>(part + h * D + d), acc);
         if (d == 0) __stcg(reinterpret_cast<float2*>(part_ml + 2 * h), make_float2(top, sum));
       } else {
-        if (SHARED) add_shared(h, d, top, sum, acc);
-        const float f = sum == 0.0f ? 0.0f : vscale / sum;
-        *reinterpret_cast<uint2*>(p.y + b * p.ldy + int64_t(h0 + h) * D + d) =
-            make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
+        put(h, d, top, sum, acc);
       }
     }
     __syncthreads();  // the exchange buffer is free again; the partial is written
@@ -732,10 +692,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
               acc.z = fmaf(v[i].z, f, acc.z), acc.w = fmaf(v[i].w, f, acc.w);
             }
           }
-          if (SHARED) add_shared(h, d, top, sum, acc);
-          const float f = sum == 0.0f ? 0.0f : vscale / sum;
-          *reinterpret_cast<uint2*>(p.y + b * p.ldy + int64_t(h0 + h) * D + d) =
-              make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
+          put(h, d, top, sum, acc);
         }
       }
     }
@@ -743,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     if (!more) break;
     it = nx;
   }
+  if (SHARED) pdl_wait();  // so that the launch after this one has waited for the one before it
   pdl_trigger();
 }
 

@@ -686,17 +686,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int rr = r;
       asm volatile("" : "+r"(rr));  // worked out here, not ahead of the loop: S takes the registers there
       if (SHARED) {
-        // As below, but only the rows that are some sequence's; and where the decode kernel finds them.
+        // As below, but only the rows that are some sequence's; and where the joining launch finds them.
         float* const o_part = p.sh.part + static_cast<int64_t>(w.part) * (2 * BM * D) + x * (BM * D);
         float* const ml = p.sh.part + static_cast<int64_t>(p.sh.parts) * (2 * BM * D) +
                           static_cast<int64_t>(w.part) * (2 * BM * 2) + x * (BM * 2);
         const int token = token_of(p, rr), at = x * p.tile_tokens + token;
         const bool mine = token < p.tile_tokens && at < w.rows;
         if (mine) *reinterpret_cast<float2*>(ml + 2 * rr) = make_float2(m, l);
-        if (w.t0 == 0) {
-          if (mine && w.hk == 0 && rr == token * p.group) p.sh.where[w.row0 + at] = make_int2(w.pair, x * BM + rr);
-          if (x == 0 && rr == 0) p.sh.pieces[w.pair] = make_int2(w.piece0, w.pieces);
-        }
+        if (w.t0 == 0 && mine && rr == token * p.group)
+          p.sh.where[static_cast<int64_t>(w.row0 + at) * p.kv_heads + w.hk] =
+              make_int2(w.piece0 * (2 * BM) + x * BM + rr, w.pieces);
         const unsigned int some = __ballot_sync(0xFFFFFFFFu, mine);
 #pragma unroll 1
         for (int j = 0; j < D && some; j += 16) {

@@ -7,11 +7,15 @@
 // queries of all its sequences, so that part is a product of matrices: the
 // prompt kernel's tensor-core tiles, with (sequence, head) pairs as rows, each
 // pair of keys' and values' tiles read once for up to 256 of them.  The keys that are
-// a sequence's own have one query per head: the decode kernel streams them, and
-// adds the shared part where a row's own is complete.  The second launch begins
-// on the SMs that the first leaves idle and as it gets done.
+// a sequence's own have one query per head: the decode kernel streams them.  It
+// needs nothing of the first launch, so it begins on the SMs that this leaves
+// idle and as it gets done.  A third launch adds a row's parts up, all loads of
+// a row in one go.  (Added by the decode kernel's CTAs as their rows were complete, 64
+// sequences behind 16000 tokens took 65 us: a chain of four latencies per item.)
 #include <algorithm>
+#include <cuda_bf16.h>
 #include "sp24_attn.cuh"
+#include "sp24_ptx.cuh"
 
 namespace sp24 {
 namespace {
@@ -20,8 +24,12 @@ namespace {
 // filled), times the kv heads: pairs; a pair's keys are cut at most once per CTA.
 struct Room {
   int64_t pairs, parts;
-  size_t where, pieces, part, total;  // offsets behind the decode kernel's workspace
+  size_t where, own, part, total;  // offsets behind the decode kernel's workspace
 };
+// Sums of the prompt kernel times this are at the decode kernel's scale.
+constexpr float kFromPrompt = 256.0f;
+static_assert(kDecodeUp - kPromptUp == 8.0f, "");
+
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 Room room_for(int64_t B, int64_t G, int q_heads, int heads, int D, const DeviceInfo& dev) {
   Room r;
@@ -29,10 +37,92 @@ Room room_for(int64_t B, int64_t G, int q_heads, int heads, int D, const DeviceI
   r.pairs = (B / tokens + std::min(B, G)) * heads;
   r.parts = r.pairs + dev.sm_count;
   r.where = up256(decode_workspace_bytes(dev, q_heads, heads, D));
-  r.pieces = r.where + up256(static_cast<size_t>(B) * sizeof(int2));
-  r.part = r.pieces + up256(static_cast<size_t>(r.pairs) * sizeof(int2));
+  r.own = r.where + up256(static_cast<size_t>(B) * heads * sizeof(int2));
+  r.part = r.own + up256(static_cast<size_t>(B) * q_heads * (D + 2) * sizeof(float));
   r.total = r.part + static_cast<size_t>(r.parts) * (2 * kTileRows) * (D + 2) * sizeof(float);
   return r;
+}
+
+// A row (a sequence's query head) per D / 4 lanes.
+struct JoinParams {
+  SharedGroups sh;
+  int rows, q_heads, group, kv_heads;
+  const float* v_scale;
+  __nv_bfloat16* y;
+  int64_t ldy;
+};
+constexpr int kJoinThreads = 128;
+constexpr int kAhead = 8;  // pieces whose loads are in flight together
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kJoinThreads) attention_shared_join_kernel(const __grid_constant__ JoinParams p) {
+  constexpr int LPR = D / 4;
+  const int row = blockIdx.x * (kJoinThreads / LPR) + threadIdx.x / LPR, d = threadIdx.x % LPR * 4;
+  pdl_wait();
+  if (row < p.rows) {
+    const int b = row / p.q_heads, h = row - b * p.q_heads, hk = h / p.group;
+    const int2 at = __ldcg(p.sh.where + int64_t(b) * p.kv_heads + hk);
+    float4 acc = __ldcg(reinterpret_cast<const float4*>(p.sh.own + int64_t(row) * D + d));
+    const float2 own = __ldcg(reinterpret_cast<const float2*>(p.sh.own + int64_t(p.rows) * D + 2 * int64_t(row)));
+    if (own.y != kNotShared) {
+      float top = own.x, sum = own.y;
+      // (What is out of range can only come from groups that are not in order.)
+      const bool ok = at.x >= 0 && at.y > 0 && int64_t(at.x) + p.group + int64_t(at.y - 1) * (2 * kTileRows) <=
+                                                   int64_t(p.sh.parts) * (2 * kTileRows);
+      const int pieces = ok ? at.y : 0;
+      const float* ml = p.sh.part + int64_t(p.sh.parts) * (2 * kTileRows * D);
+      for (int i0 = 0; i0 < pieces; i0 += kAhead) {
+        float4 v[kAhead];
+        float2 w[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          v[i] = make_float4(0, 0, 0, 0);
+          w[i] = make_float2(-INFINITY, 0.0f);
+          if (i0 + i < pieces) {
+            const int64_t r = at.x + h - hk * p.group + int64_t(i0 + i) * (2 * kTileRows);
+            w[i] = __ldcg(reinterpret_cast<const float2*>(ml + 2 * r));
+            v[i] = __ldcg(reinterpret_cast<const float4*>(p.sh.part + r * D + d));
+          }
+        }
+        float now = top;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) now = fmaxf(now, w[i].x);
+        const float use = now == -INFINITY ? 0.0f : now, keep = ex2(top - use);
+        top = now;
+        sum *= keep;
+        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const float f = ex2(w[i].x - use) * (E4M3 ? kFromPrompt : 1.0f);
+          sum = fmaf(w[i].y, f, sum);
+          acc.x = fmaf(v[i].x, f, acc.x), acc.y = fmaf(v[i].y, f, acc.y);
+          acc.z = fmaf(v[i].z, f, acc.z), acc.w = fmaf(v[i].w, f, acc.w);
+        }
+      }
+      const float f = sum == 0.0f ? 0.0f : (E4M3 ? p.v_scale[hk] : 1.0f) / sum;
+      *reinterpret_cast<uint2*>(p.y + b * p.ldy + int64_t(h) * D + d) =
+          make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
+    }
+  }
+  pdl_trigger();
+}
+
+sp24_status launch_join(const SharedCall& c, cudaStream_t s) {
+  JoinParams p;
+  p.sh = c.groups;
+  p.rows = c.B * c.q_heads;
+  p.q_heads = c.q_heads;
+  p.kv_heads = c.cache->heads;
+  p.group = c.q_heads / c.cache->heads;
+  p.v_scale = c.view.v_scale;
+  p.y = static_cast<__nv_bfloat16*>(c.y);
+  p.ldy = c.ldy;
+  const bool e4m3 = c.cache->dtype == SP24_E4M3;
+  const int per = kJoinThreads / (c.cache->head_dim / 4);
+  auto kern = c.cache->head_dim == 128
+                  ? (e4m3 ? attention_shared_join_kernel<128, true> : attention_shared_join_kernel<128, false>)
+                  : (e4m3 ? attention_shared_join_kernel<64, true> : attention_shared_join_kernel<64, false>);
+  return launch_pdl(kern, dim3((p.rows + per - 1) / per), dim3(kJoinThreads), 0, s, p) == cudaSuccess ? SP24_OK
+                                                                                                   : SP24_ERR_CUDA;
 }
 
 }  // namespace
@@ -70,9 +160,10 @@ extern "C" sp24_status sp24_attention_decode_shared(const void* q, int64_t B, in
   if (G == 0)
     return sp24_attention_decode(q, B, ldq, q_heads, cache, page_table, table_width, ld_table, seq_lens, scale, window, sinks,
                                  Y, ldy, workspace, workspace_bytes, stream);
-  // Numbers of pieces' rows, and of key tiles over all pairs, are 32-bit.
+  // Numbers of rows, of all pieces' rows, and of key tiles over all pairs, are 32-bit.
   const int64_t tiles = ((table_width << c.view.page_shift) + 127) / 128;
-  if (room.parts > INT32_MAX / (2 * kTileRows) || tiles > INT32_MAX / room.pairs) return SP24_ERR_UNSUPPORTED;
+  if (room.parts > INT32_MAX / (2 * kTileRows) || tiles > INT32_MAX / room.pairs || B > INT32_MAX / 128 / q_heads)
+    return SP24_ERR_UNSUPPORTED;
   c.q = q;
   c.ldq = ldq;
   c.B = static_cast<int>(B);
@@ -93,11 +184,12 @@ extern "C" sp24_status sp24_attention_decode_shared(const void* q, int64_t B, in
   c.groups.lens = shared_lens;
   c.groups.G = static_cast<int>(G);
   c.groups.where = reinterpret_cast<int2*>(ws + room.where);
-  c.groups.pieces = reinterpret_cast<int2*>(ws + room.pieces);
+  c.groups.own = reinterpret_cast<float*>(ws + room.own);
   c.groups.part = reinterpret_cast<float*>(ws + room.part);
   c.groups.pairs = static_cast<int>(room.pairs);
   c.groups.parts = static_cast<int>(room.parts);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sp24_status st = launch_shared_tokens(c, *dev, s)) return st;
-  return launch_own_tokens(c, *dev, s);
+  if (sp24_status st = launch_own_tokens(c, *dev, s)) return st;
+  return launch_join(c, s);
 }
