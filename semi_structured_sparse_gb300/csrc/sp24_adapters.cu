@@ -339,40 +339,441 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
   pdl_trigger();
 }
 
-// Many rows, one block each (to be replaced).
-__global__ void __launch_bounds__(kThreads) add_adapters_kernel(const __grid_constant__ AdapterParams p) {
-  __shared__ float h[kMostRank];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x;
+// Many rows.  A tile of 128 rows in a row is a cluster's, whose CTAs cut K and then N
+// among themselves, as above.  Both products are tcgen05.mma with operands by TMA:
+// A x as D1 (128 rows x rank, in tensor memory), whose partial sums each CTA
+// sends to the CTA that owns the row (distributed shared memory); the owner adds
+// them up in order and sends the row's two bf16 parts to all, which is the A
+// operand of D2 = (A x) B^T, 64 columns at a time.  A tile's rows may have
+// several adapters: each is a pass over K, and a product per 64 columns, of
+// which a row takes those of its own (a row's products are its own, so what
+// another adapter makes of it reaches nothing).
+//
+// y's tiles come into the ring that x's came through, beside which the two
+// matrices' tiles have one; the copies run ahead of the products, and so through the
+// exchange.  The sum is formed in y's tile in shared memory, and stored from
+// there.
+constexpr int kTile = 128;          // rows
+constexpr int kCols = 64;           // K, or N, per stage
+constexpr int kRowTile = kTile * kCols * 2;
+constexpr int kMostCluster = 8;
+constexpr int kSumWarps = 8;
+constexpr int kManyThreads = (kSumWarps + 3) * 32;
+template <int KB>  // 64s of the rank
+struct ManyCfg {
+  static constexpr int ROWS = KB == 1 ? 6 : 3, ADS = KB == 1 ? 4 : 2;  // stages
+  static constexpr int AD_TILE = KB * 64 * 128;
+  static constexpr int RP4 = KB * 64 + 4;  // row of the sums' exchange, in floats
+  static constexpr int RECV = (kTile + kMostCluster) * RP4 * 4;
+  static constexpr int H = 2 * KB * kRowTile;  // two parts
+  static constexpr int BARS = 3 * ROWS + 2 * ADS + 2 * 2 + 2 * 4 + 3;
+  static constexpr int SMEM = 1024 + ROWS * kRowTile + ADS * AD_TILE + H + RECV + BARS * 8;
+};
+
+// Arrive, with release, on the mbarrier at p's offset in CTA `rank` of the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank)) : "memory");
+}
+// mbar_wait for what other CTAs of the cluster have written before they arrived.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+      if (ok) return true;
+    }
+    if (globaltimer_ns() - t0 > SP24_WAIT_TIMEOUT_NS) return false;
+  }
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+template <int KB>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    add_adapters_many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
+                             const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap ymap,
+                             const __grid_constant__ CUtensorMap omap, const __grid_constant__ AdapterParams p) {
+  using C = ManyCfg<KB>;
+  constexpr int ROWS = C::ROWS, ADS = C::ADS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_which[kTile];    // of each row: which of the tile's adapters, or -1
+  __shared__ int s_adapter[kTile];  // the tile's adapters
+  __shared__ int s_adapters;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const row_s = smem;
+  uint8_t* const ad_s = row_s + ROWS * kRowTile;
+  uint8_t* const h_s = ad_s + ADS * C::AD_TILE;
+  float* const recv = reinterpret_cast<float*>(h_s + C::H);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(h_s + C::H + C::RECV);
+  uint64_t* const row_full = bars;                // [ROWS]
+  uint64_t* const row_empty = row_full + ROWS;
+  uint64_t* const out_full = row_empty + ROWS;    // [ROWS] the tile holds results
+  uint64_t* const ad_full = out_full + ROWS;      // [ADS]
+  uint64_t* const ad_empty = ad_full + ADS;
+  uint64_t* const d1_full = ad_empty + ADS;       // [2]
+  uint64_t* const d1_empty = d1_full + 2;
+  uint64_t* const d2_full = d1_empty + 2;         // [4]
+  uint64_t* const d2_empty = d2_full + 4;
+  uint64_t* const recv_full = d2_empty + 4;       // all CTAs' sums of this one's rows are there
+  uint64_t* const h_full = recv_full + 1;         // all rows of A x are there
+  uint64_t* const drain = h_full + 1;
+
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const uint32_t rank = cluster_rank(), ctas = cluster_nrank();
+  const int row0 = blockIdx.x / ctas * kTile;
+  if (warp == kSumWarps) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  } else if (warp == kSumWarps + 1 && lane == 0) {
+    for (int i = 0; i < ROWS; ++i) {
+      mbar_init(&row_full[i], 1);
+      mbar_init(&row_empty[i], 1);
+      mbar_init(&out_full[i], kSumWarps);
+    }
+    for (int i = 0; i < ADS; ++i) mbar_init(&ad_full[i], 1), mbar_init(&ad_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&d1_full[i], 1), mbar_init(&d1_empty[i], kSumWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], kSumWarps);
+    mbar_init(recv_full, kSumWarps * ctas);
+    mbar_init(h_full, kSumWarps * ctas);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&xmap), tma_prefetch_desc(&amap), tma_prefetch_desc(&bmap);
+    tma_prefetch_desc(&ymap), tma_prefetch_desc(&omap);
+  }
+  cluster_sync();  // the other CTAs have begun, and their barriers are there
   pdl_wait();
-  int id = p.ids[t];
-  if (id >= p.count) {
-    if (threadIdx.x == 0) atomicOr(p.err, DEVERR_INDEX);
-    id = -1;
-  }
-  if (id >= 0) {
-    const __nv_bfloat16* x = p.x + t * p.ldx;
-    for (int j = warp; j < p.r; j += kThreads / 32) {
-      const __nv_bfloat16* a = p.a + id * p.stride_a + int64_t(j) * p.K;
-      float sum = 0.0f;
-      for (int k = lane; k < p.K; k += 32) sum = fmaf(__bfloat162float(a[k]), __bfloat162float(x[k]), sum);
+  if (warp == 0) {
+    int id[kTile / 32], which[kTile / 32];
 #pragma unroll
-      for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-      if (lane == 0) h[j] = sum * (p.scales ? p.scales[id] : 1.0f);
+    for (int i = 0; i < kTile / 32; ++i) {
+      const int x = row0 + 32 * i + lane;
+      id[i] = x < p.T ? p.ids[x] : -1;
+      if (id[i] >= p.count) {
+        if (rank == 0) atomicOr(p.err, DEVERR_INDEX);
+        id[i] = -1;
+      }
+      which[i] = -1;
     }
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kTile / 32; ++i) {
+      while (true) {  // the first row whose adapter is not on the list yet
+        const unsigned int left = __ballot_sync(0xFFFFFFFFu, id[i] >= 0 && which[i] < 0);
+        if (!left) break;
+        const int now = __shfl_sync(0xFFFFFFFFu, id[i], __ffs(left) - 1);
+#pragma unroll
+        for (int j = 0; j < kTile / 32; ++j)
+          if (id[j] == now) which[j] = n;
+        if (lane == 0) s_adapter[n] = now;
+        ++n;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kTile / 32; ++i) s_which[32 * i + lane] = which[i];
+    if (lane == 0) s_adapters = n;
   }
+  tc_fence_before();
   __syncthreads();
-  for (int n = threadIdx.x; n < p.N; n += kThreads) {
-    float sum = __bfloat162float(p.y[t * p.ldy + n]);
-    if (id >= 0) {
-      const __nv_bfloat16* b = p.b + id * p.stride_b + int64_t(n) * p.r;
-      float add = 0.0f;
-      for (int j = 0; j < p.r; ++j) add = fmaf(__bfloat162float(b[j]), h[j], add);
-      sum += add;
+  tc_fence_after();
+  const uint32_t tmem = s_tmem, d1 = tmem, d2 = tmem + 256;
+  const int passes = s_adapters;
+  const int rp = (p.r + 15) / 16 * 16;
+  const int kbs = (p.K + kCols - 1) / kCols, nbs = (p.N + kCols - 1) / kCols;
+  const int k0 = static_cast<int>(int64_t(kbs) * rank / ctas), nk = static_cast<int>(int64_t(kbs) * (rank + 1) / ctas) - k0;
+  const int n0 = static_cast<int>(int64_t(nbs) * rank / ctas), nn = static_cast<int>(int64_t(nbs) * (rank + 1) / ctas) - n0;
+  bool ok = true;
+
+  if (warp < kSumWarps) {
+    // ------------------------------------------------------------------ sums
+    const int r = tid & (kTile - 1), half = tid / kTile, which = s_which[r];
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int own = (kTile + ctas - 1) / ctas;  // rows that a CTA adds up
+    for (int pass = 0; pass < passes && ok; ++pass) {
+      const int buf = pass & 1;
+      if (nk > 0) ok = mbar_wait(&d1_full[buf], (pass >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t to = cluster_addr(recv + (rank * own + r % own) * C::RP4, r / own);
+      for (int c = half * (rp / 2); c < (half + 1) * (rp / 2); c += 8) {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0;
+        if (nk > 0) {
+          tmem_ld8(d1 + lanes + buf * 128 + c, v);
+          tmem_ld_wait();
+        }
+        if (which == pass) {
+          st_cluster_v4(to + 4 * c, v[0], v[1], v[2], v[3]);
+          st_cluster_v4(to + 4 * c + 16, v[4], v[5], v[6], v[7]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d1_empty[buf]);
     }
-    p.out[t * p.ldo + n] = __float2bfloat16(sum);
+    if (passes > 0 && ok) {
+      __syncwarp();
+      if (lane < static_cast<int>(ctas)) mbar_arrive_cluster(recv_full, lane);
+      ok = mbar_wait_cluster(recv_full, 0);
+      if (ok) {
+        const int pieces = rp / 8;
+        for (int e = tid; e < own * pieces; e += kSumWarps * 32) {
+          const int i = e / pieces, c = e - i * pieces, x = rank * own + i;
+          const int w = x < kTile ? s_which[x] : -1;
+          if (w < 0) continue;
+          float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          for (uint32_t k = 0; k < ctas; ++k) {
+            const float4* v = reinterpret_cast<const float4*>(recv + (k * own + i) * C::RP4 + 8 * c);
+            const float4 lo = v[0], hi = v[1];
+            sum[0] += lo.x, sum[1] += lo.y, sum[2] += lo.z, sum[3] += lo.w;
+            sum[4] += hi.x, sum[5] += hi.y, sum[6] += hi.z, sum[7] += hi.w;
+          }
+          const float scale = p.scales ? p.scales[s_adapter[w]] : 1.0f;
+          uint32_t big[4], rest[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = sum[2 * k] * scale, b = sum[2 * k + 1] * scale;
+            big[k] = bf16x2_rn(a, b);
+            const float ra = a - __uint_as_float(big[k] << 16), rb = b - __uint_as_float(big[k] & 0xFFFF0000u);
+            rest[k] = bf16x2_rn(isfinite(ra) ? ra : 0.0f, isfinite(rb) ? rb : 0.0f);
+          }
+          uint8_t* to = h_s + (c / 8) * kRowTile + x * 128 + (((c & 7) ^ (x & 7)) << 4);
+          for (uint32_t k = 0; k < ctas; ++k) {
+            st_cluster_v4(cluster_addr(to, k), big[0], big[1], big[2], big[3]);
+            st_cluster_v4(cluster_addr(to + KB * kRowTile, k), rest[0], rest[1], rest[2], rest[3]);
+          }
+        }
+        fence_proxy_async_all();
+        __syncwarp();
+        if (lane < static_cast<int>(ctas)) mbar_arrive_cluster(h_full, lane);
+      }
+    }
+    int unit = 0, ring = passes * nk;
+    for (int n = 0; n < nn && ok; ++n, ++ring) {
+      uint32_t v[32];
+      for (int pass = 0; pass < passes; ++pass, ++unit) {
+        ok = mbar_wait(&d2_full[unit & 3], (unit >> 2) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (__any_sync(0xFFFFFFFFu, which == pass)) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            tmem_ld16(d2 + lanes + (unit & 3) * kCols + half * 32 + 16 * k, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (which == pass) v[16 * k + i] = w[i];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d2_empty[unit & 3]);
+      }
+      const int stage = ring % ROWS;
+      if (ok) ok = mbar_wait(&row_full[stage], (ring / ROWS) & 1);
+      if (!ok) break;
+      if (which >= 0) {
+        uint8_t* y = row_s + stage * kRowTile + r * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint4* at = reinterpret_cast<uint4*>(y + (((half * 4 + k) ^ (r & 7)) << 4));
+          const uint4 w = *at;
+          auto add = [&](uint32_t two, int i) {
+            return bf16x2_rn(__uint_as_float(two << 16) + __uint_as_float(v[8 * k + 2 * i]),
+                             __uint_as_float(two & 0xFFFF0000u) + __uint_as_float(v[8 * k + 2 * i + 1]));
+          };
+          *at = make_uint4(add(w.x, 0), add(w.y, 1), add(w.z, 2), add(w.w, 3));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&out_full[stage]);
+    }
+    if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
+  } else if (warp == kSumWarps) {
+    // ---------------------------------------------------------------- copies
+    if (lane == 0) {
+      int row = 0, ad = 0;
+      auto row_tile = [&](const CUtensorMap* map, int x) {
+        if (row >= ROWS) ok = mbar_wait(&row_empty[row % ROWS], (row / ROWS - 1) & 1);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&row_full[row % ROWS], kRowTile);
+        tma_load_2d(row_s + (row % ROWS) * kRowTile, map, &row_full[row % ROWS], x, row0);
+        ++row;
+      };
+      auto ad_stage = [&](uint32_t bytes) {
+        if (ad >= ADS) ok = mbar_wait(&ad_empty[ad % ADS], (ad / ADS - 1) & 1);
+        if (ok) mbar_arrive_expect_tx(&ad_full[ad % ADS], bytes);
+        return ok;
+      };
+      for (int pass = 0; pass < passes && ok; ++pass) {
+        for (int k = 0; k < nk && ok; ++k) {
+          row_tile(&xmap, (k0 + k) * kCols);
+          if (!ok || !ad_stage(rp * 128)) break;
+          tma_load_3d(ad_s + (ad % ADS) * C::AD_TILE, &amap, &ad_full[ad % ADS], (k0 + k) * kCols, 0, s_adapter[pass]);
+          ++ad;
+        }
+      }
+      for (int n = 0; n < nn && ok; ++n) {
+        row_tile(&ymap, (n0 + n) * kCols);
+        for (int pass = 0; pass < passes && ok; ++pass) {
+          if (!ad_stage(KB * 64 * 128)) break;
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+            tma_load_3d(ad_s + (ad % ADS) * C::AD_TILE + k * 64 * 128, &bmap, &ad_full[ad % ADS], 64 * k, (n0 + n) * kCols,
+                        s_adapter[pass]);
+          ++ad;
+        }
+      }
+      if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
+      // Copies in flight have to land before this CTA's shared memory goes.
+      for (int i = max(0, row - ROWS); i < row; ++i) mbar_wait(&row_full[i % ROWS], (i / ROWS) & 1);
+      for (int i = max(0, ad - ADS); i < ad; ++i) mbar_wait(&ad_full[i % ADS], (i / ADS) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kSumWarps + 2) {
+    // ---------------------------------------------------------------- stores
+    if (lane == 0) {
+      const int ring = passes * nk;
+      for (int n = 0; n < nn && ok; ++n) {
+        const int stage = (ring + n) % ROWS;
+        ok = mbar_wait(&out_full[stage], (n / ROWS) & 1);
+        if (!ok) break;
+        tma_store_2d(&omap, row_s + stage * kRowTile, (n0 + n) * kCols, row0);
+        bulk_commit();
+        if (n > 0) {  // the store before has read its tile
+          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          mbar_arrive(&row_empty[(ring + n - 1) % ROWS]);
+        }
+      }
+      bulk_wait_all();
+      if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------- MMA
+    if (lane == 0) {
+      int row = 0, ad = 0;
+      const uint32_t id1 = idesc_bf16(kTile, rp), id2 = idesc_bf16(kTile, kCols);
+      const uint64_t row_d = smem_desc(smem_u32(row_s), 16, 1024, SWZ_128B);
+      const uint64_t ad_d = smem_desc(smem_u32(ad_s), 16, 1024, SWZ_128B);
+      const uint64_t h_d = smem_desc(smem_u32(h_s), 16, 1024, SWZ_128B);
+      for (int pass = 0; pass < passes && ok; ++pass) {
+        if (nk > 0 && pass >= 2) ok = mbar_wait(&d1_empty[pass & 1], ((pass >> 1) - 1) & 1);
+        for (int k = 0; k < nk && ok; ++k, ++row, ++ad) {
+          ok = mbar_wait(&row_full[row % ROWS], (row / ROWS) & 1) && mbar_wait(&ad_full[ad % ADS], (ad / ADS) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = row_d + (row % ROWS) * (kRowTile >> 4), b = ad_d + (ad % ADS) * (C::AD_TILE >> 4);
+#pragma unroll
+          for (int i = 0; i < kCols / 16; ++i) mma_bf16(d1 + (pass & 1) * 128, a + 2 * i, b + 2 * i, id1, k > 0 || i > 0);
+          mma_commit(&row_empty[row % ROWS]);
+          mma_commit(&ad_empty[ad % ADS]);
+        }
+        if (nk > 0 && ok) mma_commit(&d1_full[pass & 1]);
+      }
+      if (passes > 0 && ok) ok = mbar_wait_cluster(h_full, 0);
+      fence_proxy_async_all();
+      int unit = 0;
+      for (int n = 0; n < nn && ok; ++n) {
+        for (int pass = 0; pass < passes && ok; ++pass, ++unit, ++ad) {
+          ok = mbar_wait(&ad_full[ad % ADS], (ad / ADS) & 1) &&
+               (unit < 4 || mbar_wait(&d2_empty[unit & 3], ((unit >> 2) - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b = ad_d + (ad % ADS) * (C::AD_TILE >> 4);
+          for (int x = 0; x < 2; ++x)
+            for (int i = 0; i < rp / 16; ++i) {
+              const uint64_t at = h_d + x * (KB * kRowTile >> 4) + (i / 4) * (kRowTile >> 4) + 2 * (i & 3);
+              mma_bf16(d2 + (unit & 3) * kCols, at, b + (i / 4) * (64 * 128 >> 4) + 2 * (i & 3), id2, x > 0 || i > 0);
+            }
+          mma_commit(&ad_empty[ad % ADS]);
+          mma_commit(&d2_full[unit & 3]);
+        }
+      }
+      if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_MMA);
+      mma_commit(drain);  // every MMA issued must finish before tensor memory is freed
+      mbar_wait(drain, 0);
+    }
+    __syncwarp();
   }
+  tc_fence_before();
+  __syncthreads();
   pdl_trigger();
+  if (warp == kSumWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  cluster_sync();  // no CTA writes to another's shared memory any more
+}
+
+// CTAs per cluster for so many tiles: as many as all of them still run at once with.
+template <int KB>
+unsigned many_cluster(const DeviceInfo& dev, int64_t tiles) {
+  static std::atomic<int> most[64][kMostCluster + 1];  // clusters of each size that fit at once, + 1
+  for (unsigned c = kMostCluster; c > 1; --c) {
+    if (tiles * c > dev.sm_count) continue;
+    std::atomic<int>& known = most[dev.ordinal & 63][c];
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = c;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(c);
+      cfg.blockDim = dim3(kManyThreads);
+      cfg.dynamicSmemBytes = ManyCfg<KB>::SMEM;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int fit = 0;
+      if (cudaFuncSetAttribute(add_adapters_many_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               ManyCfg<KB>::SMEM) != cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&fit, add_adapters_many_kernel<KB>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        fit = 0;
+      }
+      n = fit + 1;
+      known.store(n, std::memory_order_relaxed);
+    }
+    if (tiles <= n - 1) return c;
+  }
+  return 1;
+}
+
+template <int KB>
+sp24_status launch_many(const AdapterParams& p, const DeviceInfo& dev, cudaStream_t s) {
+  using C = ManyCfg<KB>;
+  CUtensorMap x, a, b, y, o;
+  const auto type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint32_t rp = (p.r + 15) / 16 * 16;
+  sp24_status st = make_tmap_2d(&x, p.x, type, p.K, p.T, p.ldx * 2, kCols, kTile, swizzle);
+  if (!st) st = make_tmap_2d(&y, p.y, type, p.N, p.T, p.ldy * 2, kCols, kTile, swizzle);
+  if (!st) st = make_tmap_2d(&o, p.out, type, p.N, p.T, p.ldo * 2, kCols, kTile, swizzle);
+  if (!st) st = make_tmap_3d(&a, p.a, type, p.K, p.r, p.count, uint64_t(p.K) * 2, p.stride_a * 2, kCols, rp, swizzle);
+  if (!st) st = make_tmap_3d(&b, p.b, type, p.r, p.N, p.count, uint64_t(p.r) * 2, p.stride_b * 2, 64, kCols, swizzle);
+  if (st) return st;
+  const int64_t tiles = (p.T + kTile - 1) / kTile;
+  const unsigned c = many_cluster<KB>(dev, tiles);
+  return launch_pdl_clusters_smem<add_adapters_many_kernel<KB>>(dev, c, dim3(static_cast<unsigned>(tiles * c)),
+                                                                dim3(kManyThreads), C::SMEM, s, x, a, b, y, o,
+                                                                p) == cudaSuccess
+             ? SP24_OK
+             : SP24_ERR_CUDA;
 }
 
 template <int MT, int NT>
@@ -380,7 +781,8 @@ cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream
   using C = FewCfg<MT, NT>;
   // Each adapter's last item may be partly filled; rows without an adapter count as one more.
   const int items = std::min<int64_t>(p.T, p.T / C::R + std::min<int64_t>(p.T, int64_t(p.count) + 1));
-  return launch_pdl_smem<add_adapters_few_kernel<MT, NT>, kCluster>(dev, dim3(items * kCluster), dim3(kThreads), C::SMEM, s, p);
+  return launch_pdl_clusters_smem<add_adapters_few_kernel<MT, NT>>(dev, kCluster, dim3(items * kCluster), dim3(kThreads),
+                                                                   C::SMEM, s, p);
 }
 
 }  // namespace
@@ -422,9 +824,8 @@ extern "C" sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void*
   p.err = dev->err_word;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (T > kFewRows)
-    e = launch_pdl(add_adapters_kernel, dim3(static_cast<unsigned>(T)), dim3(kThreads), 0, s, p);
-  else if (r <= 16)
+  if (T > kFewRows) return r <= 64 ? launch_many<1>(p, *dev, s) : launch_many<2>(p, *dev, s);
+  if (r <= 16)
     e = launch_few<1, 1>(p, *dev, s);
   else if (r <= 32)
     e = launch_few<2, 1>(p, *dev, s);

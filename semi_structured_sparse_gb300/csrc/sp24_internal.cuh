@@ -50,34 +50,39 @@ sp24_status make_tmap_nd(CUtensorMap* map, const void* base, CUtensorMapDataType
 
 // Launches `kern` with programmatic stream serialisation: it may begin while
 // the previous kernel in the stream finishes, and must call pdl_wait() (see
-// sp24_ptx.cuh) before its first global-memory access.  CLUSTER: CTAs per
-// cluster along x.
-template <int CLUSTER = 1, typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                              Args&&... args) {
+// sp24_ptx.cuh) before its first global-memory access.  `cluster`: CTAs per
+// cluster, along x.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_clusters(void (*kern)(KArgs...), unsigned cluster, dim3 grid, dim3 block, size_t smem,
+                                       cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CLUSTER;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                              Args&&... args) {
+  return launch_pdl_clusters(kern, 1, grid, block, smem, stream, static_cast<Args&&>(args)...);
 }
 
 // The same for a kernel that needs more shared memory than a kernel has by
 // default: asks for it on each device's first launch (each time would cost a
 // fifth of a microsecond), and again if a launch fails for its sake, as after a reset of
 // the device's context.
-template <auto Kern, int CLUSTER = 1, typename... Args>
-inline cudaError_t launch_pdl_smem(const DeviceInfo& dev, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                   const Args&... args) {
+template <auto Kern, typename... Args>
+inline cudaError_t launch_pdl_clusters_smem(const DeviceInfo& dev, unsigned cluster, dim3 grid, dim3 block, size_t smem,
+                                            cudaStream_t stream, const Args&... args) {
   static std::atomic<uint64_t> asked{0};  // a bit per device
   const uint64_t bit = uint64_t(1) << (dev.ordinal & 63);
   auto ask = [&] {
@@ -89,13 +94,18 @@ inline cudaError_t launch_pdl_smem(const DeviceInfo& dev, dim3 grid, dim3 block,
     if (r != cudaSuccess) return r;
     asked.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaError_t r = launch_pdl<CLUSTER>(Kern, grid, block, smem, stream, args...);
+  cudaError_t r = launch_pdl_clusters(Kern, cluster, grid, block, smem, stream, args...);
   if (r == cudaErrorInvalidValue && before) {
     (void)cudaGetLastError();
     r = ask();
-    if (r == cudaSuccess) r = launch_pdl<CLUSTER>(Kern, grid, block, smem, stream, args...);
+    if (r == cudaSuccess) r = launch_pdl_clusters(Kern, cluster, grid, block, smem, stream, args...);
   }
   return r;
+}
+template <auto Kern, typename... Args>
+inline cudaError_t launch_pdl_smem(const DeviceInfo& dev, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                   const Args&... args) {
+  return launch_pdl_clusters_smem<Kern>(dev, 1, grid, block, smem, stream, args...);
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
