@@ -358,15 +358,18 @@ constexpr int kCols = 64;           // K, or N, per stage
 constexpr int kRowTile = kTile * kCols * 2;
 constexpr int kMostCluster = 8;
 constexpr int kSumWarps = 8;
-constexpr int kManyThreads = (kSumWarps + 3) * 32;
+constexpr int kIssue = 2;           // warps that issue MMAs: a commit holds its thread back until they are done
+constexpr int kManyThreads = (kSumWarps + 2 + kIssue) * 32;
 template <int KB>  // 64s of the rank
 struct ManyCfg {
-  static constexpr int ROWS = KB == 1 ? 6 : 3, ADS = KB == 1 ? 4 : 2;  // stages
+  static constexpr int ROWS = KB == 1 ? 6 : 3, ADS = KB == 1 ? 6 : 2;  // stages
+  static constexpr int D1 = 64 * KB;                   // columns of an adapter's D1
+  static constexpr int PASS = 256 / (kIssue * D1);     // adapters per pass over K
   static constexpr int AD_TILE = KB * 64 * 128;
   static constexpr int RP4 = KB * 64 + 4;  // row of the sums' exchange, in floats
   static constexpr int RECV = (kTile + kMostCluster) * RP4 * 4;
   static constexpr int H = 2 * KB * kRowTile;  // two parts
-  static constexpr int BARS = 3 * ROWS + 2 * ADS + 2 * 2 + 2 * 4 + 3;
+  static constexpr int BARS = 3 * ROWS + 2 * ADS + 2 + 2 * 4 + 2 + kIssue;
   static constexpr int SMEM = 1024 + ROWS * kRowTile + ADS * AD_TILE + H + RECV + BARS * 8;
 };
 
@@ -410,6 +413,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __shared__ int s_which[kTile];    // of each row: which of the tile's adapters, or -1
   __shared__ int s_adapter[kTile];  // the tile's adapters
   __shared__ int s_adapters;
+  __shared__ float s_scale[kTile];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const row_s = smem;
   uint8_t* const ad_s = row_s + ROWS * kRowTile;
@@ -421,13 +425,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   uint64_t* const out_full = row_empty + ROWS;    // [ROWS] the tile holds results
   uint64_t* const ad_full = out_full + ROWS;      // [ADS]
   uint64_t* const ad_empty = ad_full + ADS;
-  uint64_t* const d1_full = ad_empty + ADS;       // [2]
-  uint64_t* const d1_empty = d1_full + 2;
-  uint64_t* const d2_full = d1_empty + 2;         // [4]
+  uint64_t* const d1_full = ad_empty + ADS;
+  uint64_t* const d1_empty = d1_full + 1;
+  uint64_t* const d2_full = d1_empty + 1;         // [4]
   uint64_t* const d2_empty = d2_full + 4;
   uint64_t* const recv_full = d2_empty + 4;       // all CTAs' sums of this one's rows are there
   uint64_t* const h_full = recv_full + 1;         // all rows of A x are there
-  uint64_t* const drain = h_full + 1;
+  uint64_t* const drain = h_full + 1;             // [kIssue]
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -443,17 +447,28 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&out_full[i], kSumWarps);
     }
     for (int i = 0; i < ADS; ++i) mbar_init(&ad_full[i], 1), mbar_init(&ad_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&d1_full[i], 1), mbar_init(&d1_empty[i], kSumWarps);
+    mbar_init(d1_full, kIssue);
+    mbar_init(d1_empty, kSumWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], kSumWarps);
     mbar_init(recv_full, kSumWarps * ctas);
     mbar_init(h_full, kSumWarps * ctas);
-    mbar_init(drain, 1);
+    for (int i = 0; i < kIssue; ++i) mbar_init(&drain[i], 1);
     fence_mbar_init();
     tma_prefetch_desc(&xmap), tma_prefetch_desc(&amap), tma_prefetch_desc(&bmap);
     tma_prefetch_desc(&ymap), tma_prefetch_desc(&omap);
   }
   cluster_sync();  // the other CTAs have begun, and their barriers are there
   pdl_wait();
+  const int kbs = (p.K + kCols - 1) / kCols, nbs = (p.N + kCols - 1) / kCols;
+  const int k0 = static_cast<int>(int64_t(kbs) * rank / ctas), nk = static_cast<int>(int64_t(kbs) * (rank + 1) / ctas) - k0;
+  const int n0 = static_cast<int>(int64_t(nbs) * rank / ctas), nn = static_cast<int>(int64_t(nbs) * (rank + 1) / ctas) - n0;
+  const int ahead = min(ROWS, nk);  // tiles of x that come before it is known which rows have an adapter
+  if (warp == kSumWarps && lane == 0) {
+    for (int i = 0; i < ahead; ++i) {
+      mbar_arrive_expect_tx(&row_full[i], kRowTile);
+      tma_load_2d(row_s + i * kRowTile, &xmap, &row_full[i], (k0 + i) * kCols, row0);
+    }
+  }
   if (warp == 0) {
     int id[kTile / 32], which[kTile / 32];
 #pragma unroll
@@ -488,11 +503,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem, d1 = tmem, d2 = tmem + 256;
-  const int passes = s_adapters;
+  const int adapters = s_adapters, passes = (adapters + C::PASS - 1) / C::PASS;
   const int rp = (p.r + 15) / 16 * 16;
-  const int kbs = (p.K + kCols - 1) / kCols, nbs = (p.N + kCols - 1) / kCols;
-  const int k0 = static_cast<int>(int64_t(kbs) * rank / ctas), nk = static_cast<int>(int64_t(kbs) * (rank + 1) / ctas) - k0;
-  const int n0 = static_cast<int>(int64_t(nbs) * rank / ctas), nn = static_cast<int>(int64_t(nbs) * (rank + 1) / ctas) - n0;
+  const int rows1 = max(passes * nk, ahead);  // tiles of x that come through the ring
   bool ok = true;
 
   if (warp < kSumWarps) {
@@ -500,28 +513,34 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const int r = tid & (kTile - 1), half = tid / kTile, which = s_which[r];
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int own = (kTile + ctas - 1) / ctas;  // rows that a CTA adds up
+    if (tid < adapters) s_scale[tid] = p.scales ? p.scales[s_adapter[tid]] : 1.0f;  // (seen by all after recv_full)
+    const uint32_t to = cluster_addr(recv + (rank * own + r % own) * C::RP4, r / own);
     for (int pass = 0; pass < passes && ok; ++pass) {
-      const int buf = pass & 1;
-      if (nk > 0) ok = mbar_wait(&d1_full[buf], (pass >> 1) & 1);
+      if (nk > 0) ok = mbar_wait(d1_full, pass & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t to = cluster_addr(recv + (rank * own + r % own) * C::RP4, r / own);
-      for (int c = half * (rp / 2); c < (half + 1) * (rp / 2); c += 8) {
-        uint32_t v[8];
+      for (int w = pass * C::PASS; w < min(adapters, (pass + 1) * C::PASS); ++w) {
+        if (!__any_sync(0xFFFFFFFFu, which == w)) continue;
+        for (int c = half * (rp / 2); c < (half + 1) * (rp / 2); c += 8) {
+          uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0;
-        if (nk > 0) {
-          tmem_ld8(d1 + lanes + buf * 128 + c, v);
-          tmem_ld_wait();
-        }
-        if (which == pass) {
-          st_cluster_v4(to + 4 * c, v[0], v[1], v[2], v[3]);
-          st_cluster_v4(to + 4 * c + 16, v[4], v[5], v[6], v[7]);
+          for (int i = 0; i < 8; ++i) v[i] = 0;
+          for (int x = 0; x < min(kIssue, nk); ++x) {  // what each issuing warp's stages came to
+            uint32_t u[8];
+            tmem_ld8(d1 + lanes + ((w - pass * C::PASS) * kIssue + x) * C::D1 + c, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+          }
+          if (which == w) {
+            st_cluster_v4(to + 4 * c, v[0], v[1], v[2], v[3]);
+            st_cluster_v4(to + 4 * c + 16, v[4], v[5], v[6], v[7]);
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&d1_empty[buf]);
+      if (lane == 0) mbar_arrive(d1_empty);
     }
     if (passes > 0 && ok) {
       __syncwarp();
@@ -540,7 +559,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             sum[0] += lo.x, sum[1] += lo.y, sum[2] += lo.z, sum[3] += lo.w;
             sum[4] += hi.x, sum[5] += hi.y, sum[6] += hi.z, sum[7] += hi.w;
           }
-          const float scale = p.scales ? p.scales[s_adapter[w]] : 1.0f;
+          const float scale = s_scale[w];
           uint32_t big[4], rest[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -560,22 +579,23 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (lane < static_cast<int>(ctas)) mbar_arrive_cluster(h_full, lane);
       }
     }
-    int unit = 0, ring = passes * nk;
+    int unit = 0, ring = rows1, ad = adapters * nk;
     for (int n = 0; n < nn && ok; ++n, ++ring) {
       uint32_t v[32];
-      for (int pass = 0; pass < passes; ++pass, ++unit) {
+      for (int w = 0; w < adapters; ++w, ++unit, ++ad) {
         ok = mbar_wait(&d2_full[unit & 3], (unit >> 2) & 1);
         if (!ok) break;
+        if (tid == 0) mbar_arrive(&ad_empty[ad % ADS]);  // the product has been formed
         tc_fence_after();
-        if (__any_sync(0xFFFFFFFFu, which == pass)) {
-          uint32_t w[16];
+        if (__any_sync(0xFFFFFFFFu, which == w)) {
+          uint32_t u[16];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            tmem_ld16(d2 + lanes + (unit & 3) * kCols + half * 32 + 16 * k, w);
+            tmem_ld16(d2 + lanes + (unit & 3) * kCols + half * 32 + 16 * k, u);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (which == pass) v[16 * k + i] = w[i];
+              if (which == w) v[16 * k + i] = u[i];
           }
         }
         tc_fence_before();
@@ -606,35 +626,58 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   } else if (warp == kSumWarps) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
-      int row = 0, ad = 0;
+      int row = ahead, ad = 0;
+      // An adapter's tile, when the one before it in its place has been used.
+      auto ad_free = [&](int use) {  // (a place that has been filled again since has been waited for)
+        return use < 0 || use + ADS < ad || mbar_wait(&ad_empty[use % ADS], (use / ADS) & 1);
+      };
+      auto ad_stage = [&](uint32_t bytes) {
+        ok = ad_free(ad - ADS);
+        if (ok) mbar_arrive_expect_tx(&ad_full[ad % ADS], bytes);
+        return ok;
+      };
       auto row_tile = [&](const CUtensorMap* map, int x) {
-        if (row >= ROWS) ok = mbar_wait(&row_empty[row % ROWS], (row / ROWS - 1) & 1);
-        if (!ok) return;
         mbar_arrive_expect_tx(&row_full[row % ROWS], kRowTile);
         tma_load_2d(row_s + (row % ROWS) * kRowTile, map, &row_full[row % ROWS], x, row0);
         ++row;
       };
-      auto ad_stage = [&](uint32_t bytes) {
-        if (ad >= ADS) ok = mbar_wait(&ad_empty[ad % ADS], (ad / ADS - 1) & 1);
-        if (ok) mbar_arrive_expect_tx(&ad_full[ad % ADS], bytes);
-        return ok;
-      };
+      // A tile of x has been used when the last of its pass's adapters has.
+      int last[ROWS];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) last[i] = -1;
       for (int pass = 0; pass < passes && ok; ++pass) {
+        const int w0 = pass * C::PASS, w1 = min(adapters, w0 + C::PASS);
         for (int k = 0; k < nk && ok; ++k) {
-          row_tile(&xmap, (k0 + k) * kCols);
-          if (!ok || !ad_stage(rp * 128)) break;
-          tma_load_3d(ad_s + (ad % ADS) * C::AD_TILE, &amap, &ad_full[ad % ADS], (k0 + k) * kCols, 0, s_adapter[pass]);
-          ++ad;
+          const int use = pass * nk + k;
+          if (use >= ahead) {
+            ok = ad_free(last[use % ROWS]);
+            if (!ok) break;
+            row_tile(&xmap, (k0 + k) * kCols);
+          }
+          for (int w = w0; w < w1 && ok; ++w) {
+            if (!ad_stage(rp * 128)) break;
+            tma_load_3d(ad_s + (ad % ADS) * C::AD_TILE, &amap, &ad_full[ad % ADS], (k0 + k) * kCols, 0, s_adapter[w]);
+            ++ad;
+          }
+          last[use % ROWS] = ad - 1;
         }
       }
       for (int n = 0; n < nn && ok; ++n) {
+        const int use = row;
+        if (n >= ROWS)
+          ok = mbar_wait(&row_empty[use % ROWS], (n / ROWS - 1) & 1);
+        else if (passes > 0)
+          ok = ad_free(last[use % ROWS]);
+        else if (use >= ROWS || use % ROWS < ahead)  // no row has an adapter: x's tiles have landed, that is all
+          ok = mbar_wait(&row_full[use % ROWS], 0);
+        if (!ok) break;
         row_tile(&ymap, (n0 + n) * kCols);
-        for (int pass = 0; pass < passes && ok; ++pass) {
+        for (int w = 0; w < adapters && ok; ++w) {
           if (!ad_stage(KB * 64 * 128)) break;
 #pragma unroll
           for (int k = 0; k < KB; ++k)
             tma_load_3d(ad_s + (ad % ADS) * C::AD_TILE + k * 64 * 128, &bmap, &ad_full[ad % ADS], 64 * k, (n0 + n) * kCols,
-                        s_adapter[pass]);
+                        s_adapter[w]);
           ++ad;
         }
       }
@@ -647,14 +690,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   } else if (warp == kSumWarps + 2) {
     // ---------------------------------------------------------------- stores
     if (lane == 0) {
-      const int ring = passes * nk;
+      const int ring = rows1;
       for (int n = 0; n < nn && ok; ++n) {
         const int stage = (ring + n) % ROWS;
         ok = mbar_wait(&out_full[stage], (n / ROWS) & 1);
         if (!ok) break;
         tma_store_2d(&omap, row_s + stage * kRowTile, (n0 + n) * kCols, row0);
         bulk_commit();
-        if (n > 0) {  // the store before has read its tile
+        if (n > 0) {  // the store before this one has read its tile
           asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
           mbar_arrive(&row_empty[(ring + n - 1) % ROWS]);
         }
@@ -666,47 +709,51 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   } else {
     // ------------------------------------------------------------------- MMA
     if (lane == 0) {
-      int row = 0, ad = 0;
+      const int x = warp == kSumWarps + 1 ? 0 : 1;  // every other stage and product
       const uint32_t id1 = idesc_bf16(kTile, rp), id2 = idesc_bf16(kTile, kCols);
       const uint64_t row_d = smem_desc(smem_u32(row_s), 16, 1024, SWZ_128B);
       const uint64_t ad_d = smem_desc(smem_u32(ad_s), 16, 1024, SWZ_128B);
       const uint64_t h_d = smem_desc(smem_u32(h_s), 16, 1024, SWZ_128B);
       for (int pass = 0; pass < passes && ok; ++pass) {
-        if (nk > 0 && pass >= 2) ok = mbar_wait(&d1_empty[pass & 1], ((pass >> 1) - 1) & 1);
-        for (int k = 0; k < nk && ok; ++k, ++row, ++ad) {
-          ok = mbar_wait(&row_full[row % ROWS], (row / ROWS) & 1) && mbar_wait(&ad_full[ad % ADS], (ad / ADS) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a = row_d + (row % ROWS) * (kRowTile >> 4), b = ad_d + (ad % ADS) * (C::AD_TILE >> 4);
+        const int w0 = pass * C::PASS, w1 = min(adapters, w0 + C::PASS);
+        if (nk > 0 && pass > 0) ok = mbar_wait(d1_empty, (pass - 1) & 1);
+        for (int k = x; k < nk && ok; k += kIssue) {
+          const int row = pass * nk + k;
+          ok = mbar_wait(&row_full[row % ROWS], (row / ROWS) & 1);
+          const uint64_t a = row_d + (row % ROWS) * (kRowTile >> 4);
+          for (int w = w0; w < w1 && ok; ++w) {
+            const int ad = w0 * nk + k * (w1 - w0) + w - w0;
+            ok = mbar_wait(&ad_full[ad % ADS], (ad / ADS) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b = ad_d + (ad % ADS) * (C::AD_TILE >> 4);
 #pragma unroll
-          for (int i = 0; i < kCols / 16; ++i) mma_bf16(d1 + (pass & 1) * 128, a + 2 * i, b + 2 * i, id1, k > 0 || i > 0);
-          mma_commit(&row_empty[row % ROWS]);
-          mma_commit(&ad_empty[ad % ADS]);
+            for (int i = 0; i < kCols / 16; ++i)
+              mma_bf16(d1 + ((w - w0) * kIssue + x) * C::D1, a + 2 * i, b + 2 * i, id1, k >= kIssue || i > 0);
+            mma_commit(&ad_empty[ad % ADS]);
+          }
         }
-        if (nk > 0 && ok) mma_commit(&d1_full[pass & 1]);
+        if (nk > 0 && ok) mma_commit(d1_full);
       }
       if (passes > 0 && ok) ok = mbar_wait_cluster(h_full, 0);
       fence_proxy_async_all();
-      int unit = 0;
-      for (int n = 0; n < nn && ok; ++n) {
-        for (int pass = 0; pass < passes && ok; ++pass, ++unit, ++ad) {
-          ok = mbar_wait(&ad_full[ad % ADS], (ad / ADS) & 1) &&
-               (unit < 4 || mbar_wait(&d2_empty[unit & 3], ((unit >> 2) - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t b = ad_d + (ad % ADS) * (C::AD_TILE >> 4);
-          for (int x = 0; x < 2; ++x)
-            for (int i = 0; i < rp / 16; ++i) {
-              const uint64_t at = h_d + x * (KB * kRowTile >> 4) + (i / 4) * (kRowTile >> 4) + 2 * (i & 3);
-              mma_bf16(d2 + (unit & 3) * kCols, at, b + (i / 4) * (64 * 128 >> 4) + 2 * (i & 3), id2, x > 0 || i > 0);
-            }
-          mma_commit(&ad_empty[ad % ADS]);
-          mma_commit(&d2_full[unit & 3]);
-        }
+      for (int unit = x; unit < nn * adapters && ok; unit += kIssue) {
+        const int ad = adapters * nk + unit;
+        ok = mbar_wait(&ad_full[ad % ADS], (ad / ADS) & 1) &&
+             (unit < 4 || mbar_wait(&d2_empty[unit & 3], ((unit >> 2) - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t b = ad_d + (ad % ADS) * (C::AD_TILE >> 4);
+        for (int part = 0; part < 2; ++part)
+          for (int i = 0; i < rp / 16; ++i) {
+            const uint64_t at = h_d + part * (KB * kRowTile >> 4) + (i / 4) * (kRowTile >> 4) + 2 * (i & 3);
+            mma_bf16(d2 + (unit & 3) * kCols, at, b + (i / 4) * (64 * 128 >> 4) + 2 * (i & 3), id2, part > 0 || i > 0);
+          }
+        mma_commit(&d2_full[unit & 3]);
       }
       if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_MMA);
-      mma_commit(drain);  // every MMA issued must finish before tensor memory is freed
-      mbar_wait(drain, 0);
+      mma_commit(&drain[x]);  // every MMA issued must finish before tensor memory is freed
+      mbar_wait(&drain[x], 0);
     }
     __syncwarp();
   }
