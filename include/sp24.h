@@ -605,15 +605,25 @@ SP24_API sp24_status sp24_cache_copy(const sp24_kv_cache* src, const int64_t* sr
  *        zeros in the rest.
  *   ids  (device) int32 [T], in any order (rows of one adapter in a row read it
  *        least often); scales (device) fp32 [count], or NULL for 1.
- *   out  (device, out) bf16 [T][N], row stride ldo; may be Y (with ldo = ldy).
+ *   out  (device, out) bf16 [T][N], row stride ldo; may be Y (with ldo = ldy),
+ *        and overlaps nothing else.
+ *   workspace, workspace_bytes: device scratch of at least
+ *        sp24_add_adapters_workspace_size bytes, 16-byte aligned, of any contents
+ *        (may be NULL when that size is 0, as it is for few rows).  Calls that
+ *        overlap on the GPU must not share it.
  * Preconditions: T >= 0; K, N and r positive multiples of 8, r at most 128
  * (SP24_ERR_UNSUPPORTED), K and N at most 2^24; matrices 16-byte aligned, strides
  * multiples of 8 and no shorter than what they step over.
+ * Errors: SP24_ERR_WORKSPACE for a workspace that is missing or too small.
  */
 SP24_API sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void* X, int64_t ldx, int64_t T, int64_t K,
                                        int64_t N, const void* A, int64_t stride_a, const void* B, int64_t stride_b,
                                        int64_t r, int64_t count, const int32_t* ids, const float* scales, void* out,
-                                       int64_t ldo, void* stream);
+                                       int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device scratch bytes sp24_add_adapters needs for a call of this shape on the
+ * current device (0: none). */
+SP24_API size_t sp24_add_adapters_workspace_size(int64_t T, int64_t K, int64_t r);
 
 #ifdef __cplusplus
 }

@@ -72,7 +72,8 @@ SIGNATURES = {
     "sp24_attention_decode_shared_workspace_size": ([_I64, _I64, _I, _I, _I], _SZ),
     "sp24_cache_copy": ([_P, _P, _P, _P, _I64, _P], _I),
     "sp24_add_adapters": ([_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64,
-                           _P], _I),
+                           _P, _SZ, _P], _I),
+    "sp24_add_adapters_workspace_size": ([_I64, _I64, _I64], _SZ),
 }
 
 
@@ -851,12 +852,20 @@ def _adapter_stack(t, shape, name, what, device):
             name, what, list(shape), tuple(t.shape), t.stride()))
 
 
-def add_adapters(y, x, a, b, ids, scales=None, out=None, stream=None):
+def add_adapters_workspace_size(rows: int, k: int, r: int) -> int:
+    """Device scratch bytes add_adapters() needs for `rows` rows of `k` values and rank `r`
+    on the current GPU (0: none)."""
+    return int(load().sp24_add_adapters_workspace_size(rows, k, r))
+
+
+def add_adapters(y, x, a, b, ids, scales=None, out=None, workspace=None, stream=None):
     """Low-rank adapters of many requests beside one projection: to row t of its output y
     bf16 [T, N] the product of the adapter i = ids[t] (int32 [T], in any order; negative:
     none), scales[i] * b[i] (a[i] x[t]), for the projection's input x bf16 [T, K].  a bf16
     [count, r, K] and b bf16 [count, N, r], r a multiple of 8 up to 128; scales fp32 [count],
-    or None for 1.  Returns bf16 [T, N] (in ``out`` if given, which may be y)."""
+    or None for 1.  Returns bf16 [T, N] (in ``out`` if given, which may be y).  `workspace`
+    (uint8, of any contents, at least add_adapters_workspace_size() bytes) is what many rows
+    need; without one, a call that needs it allocates it."""
     lib = _lib or load()
     ok = False
     try:
@@ -904,9 +913,21 @@ def add_adapters(y, x, a, b, ids, scales=None, out=None, stream=None):
             if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
                 raise ValueError("%s must be a contiguous vector of %d values, got %s" % (name, n, tuple(t.shape)))
         raise ValueError("the arguments' layouts are not ones that the library takes")
+    size = 0
+    if workspace is None:
+        need = T > 512 and _on(at, lib.sp24_add_adapters_workspace_size, T, K, r)  # (fewer rows never need any)
+        if need:
+            workspace, size = _new(need, _U8, stream, y.device), need
+    elif isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and workspace.get_device() == at and \
+            workspace.is_contiguous():
+        size = workspace.numel()
+    else:
+        _dev_tensor(workspace, _U8, "workspace", y.device)
+        raise ValueError("workspace must be contiguous")
     s = _raw_stream(at) if stream is None and _raw_stream is not None else _stream(stream, at)
     st = _on(at, lib.sp24_add_adapters, y.data_ptr(), ldy, x.data_ptr(), ldx, T, K, N, a.data_ptr(), stride_a, b.data_ptr(),
-             stride_b, r, count, ids.data_ptr(), None if scales is None else scales.data_ptr(), out.data_ptr(), ldo, s)
+             stride_b, r, count, ids.data_ptr(), None if scales is None else scales.data_ptr(), out.data_ptr(), ldo,
+             None if workspace is None else workspace.data_ptr(), size, s)
     if st:
         _check(st, "sp24_add_adapters")
     return out

@@ -339,227 +339,467 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
   pdl_trigger();
 }
 
-// Many rows.  A tile of 128 rows in a row is a cluster's, whose CTAs cut K and then N
-// among themselves, as above.  Both products are tcgen05.mma with operands by TMA:
-// A x as D1 (128 rows x rank, in tensor memory), whose partial sums each CTA
-// sends to the CTA that owns the row (distributed shared memory); the owner adds
-// them up in order and sends the row's two bf16 parts to all, which is the A
-// operand of D2 = (A x) B^T, 64 columns at a time.  A tile's rows may have
-// several adapters: each is a pass over K, and a product per 64 columns, of
-// which a row takes those of its own (a row's products are its own, so what
-// another adapter makes of it reaches nothing).
+// Many rows, in two launches of tcgen05.mma with operands by TMA.  Rows come in tiles of
+// 128 in a row.  The first launch forms D1 = A x (128 rows x rank), the second D2 =
+// B (A x), 64 columns at a time, and adds y.  A unit of the first is 64 of a tile's
+// K, of the second 64 of its N; each launch deals all units out to one CTA per SM in equal
+// contiguous ranges.  A tile whose K is cut between CTAs has a piece of fp32 sums in the
+// workspace from each, which the second launch adds up in order and takes apart
+// into two bf16 operands.  It needs nothing else of the first launch, so that its
+// CTAs begin as SMs get done with that one, and their first copies run meanwhile.
 //
-// y's tiles come into the ring that x's came through, beside which the two
-// matrices' tiles have one; the copies run ahead of the products, and so through the
-// exchange.  The sum is formed in y's tile in shared memory, and stored from
-// there.
+// A tile's rows may have several adapters: each is a product of its own, of which a row
+// takes that of its own adapter (what another adapter makes of it reaches nothing).
+// A result is formed in y's tile in shared memory, and stored from there.
 constexpr int kTile = 128;          // rows
-constexpr int kCols = 64;           // K, or N, per stage
+constexpr int kCols = 64;           // of K, or N, per unit
 constexpr int kRowTile = kTile * kCols * 2;
-constexpr int kMostCluster = 8;
-constexpr int kSumWarps = 8;
 constexpr int kIssue = 2;           // warps that issue MMAs: a commit holds its thread back until they are done
-constexpr int kManyThreads = (kSumWarps + 2 + kIssue) * 32;
-template <int KB>  // 64s of the rank
-struct ManyCfg {
-  static constexpr int ROWS = KB == 1 ? 6 : 3, ADS = KB == 1 ? 6 : 2;  // stages
-  static constexpr int D1 = 64 * KB;                   // columns of an adapter's D1
-  static constexpr int PASS = 256 / (kIssue * D1);     // adapters per pass over K
-  static constexpr int AD_TILE = KB * 64 * 128;
-  static constexpr int RP4 = KB * 64 + 4;  // row of the sums' exchange, in floats
-  static constexpr int RECV = (kTile + kMostCluster) * RP4 * 4;
-  static constexpr int H = 2 * KB * kRowTile;  // two parts
-  static constexpr int BARS = 3 * ROWS + 2 * ADS + 2 + 2 * 4 + 2 + kIssue;
-  static constexpr int SMEM = 1024 + ROWS * kRowTile + ADS * AD_TILE + H + RECV + BARS * 8;
+constexpr int kLeastK = 8, kLeastN = 4;  // units per CTA
+
+struct Deal {
+  unsigned int ctas, per, extra;  // the first `extra` CTAs take a unit more
+  __host__ __device__ static Deal of(unsigned int units, unsigned int sms, unsigned int least) {
+    Deal d;
+    d.ctas = units / least < 1 ? 1 : units / least < sms ? units / least : sms;
+    d.per = units / d.ctas, d.extra = units % d.ctas;
+    return d;
+  }
+  __device__ unsigned int begin(unsigned int cta) const { return cta * per + min(cta, extra); }
+  __device__ unsigned int cta_of(unsigned int u) const {
+    return u < extra * (per + 1) ? u / (per + 1) : extra + (u - extra * (per + 1)) / per;
+  }
 };
 
-// Arrive, with release, on the mbarrier at p's offset in CTA `rank` of the cluster.
-__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank)) : "memory");
-}
-// mbar_wait for what other CTAs of the cluster have written before they arrived.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
-      uint32_t ok;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity)
-          : "memory");
-      if (ok) return true;
-    }
-    if (globaltimer_ns() - t0 > SP24_WAIT_TIMEOUT_NS) return false;
+struct ManyParams {
+  AdapterParams p;
+  int kbs, nbs, rp;   // units of a tile, and the rank padded to the MMA's multiple of 16
+  Deal k, n;
+  float* part;        // [pieces][kTile][rp]; the piece of a tile that CTA c of the first launch forms is tile + c
+};
+
+// What a CTA does in one go: units of one tile.
+struct Segment {
+  int tile, first, count;     // count 0: nothing more
+  int adapters;
+  int adapter[kTile];         // the tile's adapters
+  int which[kTile];           // of each row: which of them, or -1
+};
+// The segment that begins with unit u, by one warp.
+__device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned int u, unsigned int u_end, int per_tile,
+                                             bool report, Segment* out) {
+  const int lane = threadIdx.x & 31;
+  if (u >= u_end) {
+    if (lane == 0) out->count = 0;
+    __syncwarp();
+    return;
   }
+  const int tile = u / per_tile, first = u - tile * per_tile;
+  int id[kTile / 32], which[kTile / 32];
+#pragma unroll
+  for (int i = 0; i < kTile / 32; ++i) {
+    const int x = tile * kTile + 32 * i + lane;
+    id[i] = x < p.T ? __ldg(p.ids + x) : -1;
+    which[i] = -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kTile / 32; ++i)
+    if (id[i] >= p.count) {
+      if (report) atomicOr(p.err, DEVERR_INDEX);
+      id[i] = -1;
+    }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kTile / 32; ++i) {
+    while (true) {  // the first row whose adapter is not on the list yet
+      const unsigned int left = __ballot_sync(0xFFFFFFFFu, id[i] >= 0 && which[i] < 0);
+      if (!left) break;
+      const int now = __shfl_sync(0xFFFFFFFFu, id[i], __ffs(left) - 1);
+#pragma unroll
+      for (int j = 0; j < kTile / 32; ++j)
+        if (id[j] == now) which[j] = n;
+      if (lane == 0) out->adapter[n] = now;
+      ++n;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTile / 32; ++i) out->which[32 * i + lane] = which[i];
+  if (lane == 0) {
+    out->tile = tile;
+    out->first = first;
+    out->count = min(per_tile - first, static_cast<int>(u_end - u));
+    out->adapters = n;
+  }
+  __syncwarp();
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// ------------------------------------------------------------------ A x
+template <int KB>  // 64s of the rank
+struct DownCfg {
+  static constexpr int ROWS = KB == 1 ? 8 : 6, ADS = KB == 1 ? 8 : 6;  // stages
+  static constexpr int AD_TILE = KB * 64 * 128;
+  static constexpr int D1 = 64 * KB;                  // columns of an adapter's sums
+  static constexpr int PASS = 512 / (kIssue * D1);    // adapters per pass over K
+  static constexpr int BARS = 2 * ROWS + 2 * ADS + 2 + 4 + kIssue;
+  static constexpr int SMEM = 1024 + ROWS * kRowTile + ADS * AD_TILE + BARS * 8;
+};
+constexpr int kDownThreads = (4 + 2 + kIssue) * 32;  // sums, segments, copies, MMAs
 
 template <int KB>
-__global__ void __launch_bounds__(kManyThreads, 1)
-    add_adapters_many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
-                             const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap ymap,
-                             const __grid_constant__ CUtensorMap omap, const __grid_constant__ AdapterParams p) {
-  using C = ManyCfg<KB>;
+__global__ void __launch_bounds__(kDownThreads, 1)
+    adapters_down_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
+                         const __grid_constant__ ManyParams q) {
+  using C = DownCfg<KB>;
   constexpr int ROWS = C::ROWS, ADS = C::ADS;
+  const AdapterParams& p = q.p;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_which[kTile];    // of each row: which of the tile's adapters, or -1
-  __shared__ int s_adapter[kTile];  // the tile's adapters
-  __shared__ int s_adapters;
-  __shared__ float s_scale[kTile];
+  __shared__ Segment s_seg[2];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const row_s = smem;
+  uint8_t* const ad_s = row_s + ROWS * kRowTile;
+  uint64_t* const row_full = reinterpret_cast<uint64_t*>(ad_s + ADS * C::AD_TILE);  // [ROWS]
+  uint64_t* const row_empty = row_full + ROWS;
+  uint64_t* const ad_full = row_empty + ROWS;     // [ADS]
+  uint64_t* const ad_empty = ad_full + ADS;
+  uint64_t* const d1_full = ad_empty + ADS;
+  uint64_t* const d1_empty = d1_full + 1;
+  uint64_t* const seg_full = d1_empty + 1;        // [2]
+  uint64_t* const seg_empty = seg_full + 2;       // [2]
+  uint64_t* const drain = seg_empty + 2;          // [kIssue]
+
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  if (warp == 4) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  } else if (warp == 5 && lane == 0) {
+    for (int i = 0; i < ROWS; ++i) mbar_init(&row_full[i], 1), mbar_init(&row_empty[i], 1);
+    for (int i = 0; i < ADS; ++i) mbar_init(&ad_full[i], 1), mbar_init(&ad_empty[i], 1);
+    mbar_init(d1_full, kIssue);
+    mbar_init(d1_empty, 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_empty[i], 5 + kIssue);
+    for (int i = 0; i < kIssue; ++i) mbar_init(&drain[i], 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&xmap), tma_prefetch_desc(&amap);
+  }
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = s_tmem;
+  bool ok = true;
+  auto wait_segment = [&](int i) { return mbar_wait(&seg_full[i & 1], (i >> 1) & 1); };
+  auto done_with = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[i & 1]);
+  };
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------ sums
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    int passes = 0;  // so far
+    for (int i = 0; ok; ++i) {
+      ok = wait_segment(i);
+      const Segment& s = s_seg[i & 1];
+      if (!ok || s.count == 0) break;
+      const int which = s.which[tid];
+      float* const to = q.part + (int64_t(s.tile + blockIdx.x) * kTile + tid) * q.rp;
+      for (int w0 = 0; w0 < s.adapters && ok; w0 += C::PASS, ++passes) {
+        ok = mbar_wait(d1_full, passes & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (int w = w0; w < min(s.adapters, w0 + C::PASS); ++w) {
+          if (!__any_sync(0xFFFFFFFFu, which == w)) continue;
+          for (int c = 0; c < q.rp; c += 8) {
+            uint32_t u[2][8];
+            float v[8];
+            tmem_ld8(tmem + lanes + (w - w0) * kIssue * C::D1 + c, u[0]);
+            if (s.count > 1) tmem_ld8(tmem + lanes + ((w - w0) * kIssue + 1) * C::D1 + c, u[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = s.count > 1 ? __uint_as_float(u[0][e]) + __uint_as_float(u[1][e]) : __uint_as_float(u[0][e]);
+            if (which == w) {
+              __stcg(reinterpret_cast<float4*>(to + c), make_float4(v[0], v[1], v[2], v[3]));
+              __stcg(reinterpret_cast<float4*>(to + c + 4), make_float4(v[4], v[5], v[6], v[7]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d1_empty);
+      }
+      done_with(i);
+    }
+    if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
+  } else if (warp == 4) {
+    // -------------------------------------------------------------- segments
+    unsigned int u = q.k.begin(blockIdx.x);
+    const unsigned int end = q.k.begin(blockIdx.x + 1);
+    for (int i = 0; ok; ++i) {
+      if (i >= 2) ok = mbar_wait(&seg_empty[i & 1], ((i >> 1) - 1) & 1);
+      if (!ok) break;
+      find_segment(p, u, end, q.kbs, u % q.kbs == 0, &s_seg[i & 1]);
+      const int count = s_seg[i & 1].count;
+      if (lane == 0) mbar_arrive(&seg_full[i & 1]);
+      __syncwarp();
+      if (count == 0) break;
+      u += count;
+    }
+    if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
+  } else if (warp == 5) {
+    // ---------------------------------------------------------------- copies
+    int row = 0, ad = 0;
+    for (int i = 0; ok; ++i) {
+      ok = wait_segment(i);
+      const Segment& s = s_seg[i & 1];
+      if (!ok || s.count == 0) break;
+      if (lane == 0) {
+        for (int w0 = 0; w0 < s.adapters && ok; w0 += C::PASS) {
+          for (int k = 0; k < s.count && ok; ++k, ++row) {
+            const int x = (s.first + k) * kCols, at = row % ROWS;
+            if (row >= ROWS) ok = mbar_wait(&row_empty[at], (row / ROWS - 1) & 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&row_full[at], kRowTile);
+            tma_load_2d(row_s + at * kRowTile, &xmap, &row_full[at], x, s.tile * kTile);
+            for (int w = w0; w < min(s.adapters, w0 + C::PASS) && ok; ++w, ++ad) {
+              const int to = ad % ADS;
+              if (ad >= ADS) ok = mbar_wait(&ad_empty[to], (ad / ADS - 1) & 1);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&ad_full[to], q.rp * 128);
+              tma_load_3d(ad_s + to * C::AD_TILE, &amap, &ad_full[to], x, 0, s.adapter[w]);
+            }
+            if (!ok) {
+              ++row;  // this one is on its way
+              break;
+            }
+          }
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      done_with(i);
+    }
+    if (lane == 0) {
+      if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
+      // Copies in flight have to land before this CTA's shared memory goes.
+      for (int i = max(0, row - ROWS); i < row; ++i) mbar_wait(&row_full[i % ROWS], (i / ROWS) & 1);
+      for (int i = max(0, ad - ADS); i < ad; ++i) mbar_wait(&ad_full[i % ADS], (i / ADS) & 1);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------- MMA
+    const int x = warp - 6;  // every other unit is this warp's
+    const uint32_t id = idesc_bf16(kTile, q.rp);
+    const uint64_t row_d = smem_desc(smem_u32(row_s), 16, 1024, SWZ_128B);
+    const uint64_t ad_d = smem_desc(smem_u32(ad_s), 16, 1024, SWZ_128B);
+    int row0 = 0, ad0 = 0, passes = 0;
+    for (int i = 0; ok; ++i) {
+      ok = wait_segment(i);
+      const Segment& s = s_seg[i & 1];
+      if (!ok || s.count == 0) break;
+      const int count = s.count, adapters = s.adapters;
+      if (lane == 0) {
+        for (int w0 = 0; w0 < adapters && ok; w0 += C::PASS, ++passes) {
+          const int some = min(adapters - w0, C::PASS);
+          if (passes > 0) ok = mbar_wait(d1_empty, (passes - 1) & 1);
+          tc_fence_after();
+          for (int k = x; k < count && ok; k += kIssue) {
+            const int row = row0 + k, at = row % ROWS;
+            ok = mbar_wait(&row_full[at], (row / ROWS) & 1);
+            for (int w = 0; w < some && ok; ++w) {
+              const int ad = ad0 + k * some + w, from = ad % ADS;
+              ok = mbar_wait(&ad_full[from], (ad / ADS) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t a = row_d + at * (kRowTile >> 4), b = ad_d + from * (C::AD_TILE >> 4);
+#pragma unroll
+              for (int e = 0; e < kCols / 16; ++e)
+                mma_bf16(tmem + (w * kIssue + x) * C::D1, a + 2 * e, b + 2 * e, id, k >= kIssue || e > 0);
+              mma_commit(&ad_empty[from]);
+              if (w + 1 == some) mma_commit(&row_empty[at]);
+            }
+          }
+          row0 += count;
+          ad0 += count * some;
+          if (ok) mma_commit(d1_full);
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      done_with(i);
+    }
+    if (lane == 0) {
+      if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_MMA);
+      mma_commit(&drain[x]);  // every MMA issued must finish before tensor memory is freed
+      mbar_wait(&drain[x], 0);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- y + B (A x)
+template <int KB>
+struct UpCfg {
+  static constexpr int ROWS = KB == 1 ? 6 : 4, ADS = KB == 1 ? 6 : 4, HS = KB == 1 ? 2 : 1;  // stages
+  static constexpr int AD_TILE = KB * 64 * 128;
+  static constexpr int H = 2 * KB * kRowTile;  // A x of a tile, in two parts
+  static constexpr int D2S = 512 / kCols;
+  static constexpr int BARS = 3 * ROWS + 2 * ADS + 2 * HS + 2 * D2S + 4 + kIssue;
+  static constexpr int SMEM = 1024 + ROWS * kRowTile + ADS * AD_TILE + HS * H + BARS * 8;
+};
+constexpr int kSumWarps = 8, kHWarps = 4;
+constexpr int kUpThreads = (kSumWarps + kHWarps + 3 + kIssue) * 32;  // ..., segments, copies, stores, MMAs
+
+template <int KB>
+__global__ void __launch_bounds__(kUpThreads, 1)
+    adapters_up_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap ymap,
+                       const __grid_constant__ CUtensorMap omap, const __grid_constant__ ManyParams q) {
+  using C = UpCfg<KB>;
+  constexpr int ROWS = C::ROWS, ADS = C::ADS, HS = C::HS, D2S = C::D2S;
+  constexpr int H0 = kSumWarps, SEG = H0 + kHWarps, COPY = SEG + 1, STORE = COPY + 1, ISSUE = STORE + 1;  // warps
+  const AdapterParams& p = q.p;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ Segment s_seg[2];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const row_s = smem;
   uint8_t* const ad_s = row_s + ROWS * kRowTile;
   uint8_t* const h_s = ad_s + ADS * C::AD_TILE;
-  float* const recv = reinterpret_cast<float*>(h_s + C::H);
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(h_s + C::H + C::RECV);
-  uint64_t* const row_full = bars;                // [ROWS]
+  uint64_t* const row_full = reinterpret_cast<uint64_t*>(h_s + HS * C::H);  // [ROWS]
   uint64_t* const row_empty = row_full + ROWS;
   uint64_t* const out_full = row_empty + ROWS;    // [ROWS] the tile holds results
   uint64_t* const ad_full = out_full + ROWS;      // [ADS]
   uint64_t* const ad_empty = ad_full + ADS;
-  uint64_t* const d1_full = ad_empty + ADS;
-  uint64_t* const d1_empty = d1_full + 1;
-  uint64_t* const d2_full = d1_empty + 1;         // [4]
-  uint64_t* const d2_empty = d2_full + 4;
-  uint64_t* const recv_full = d2_empty + 4;       // all CTAs' sums of this one's rows are there
-  uint64_t* const h_full = recv_full + 1;         // all rows of A x are there
-  uint64_t* const drain = h_full + 1;             // [kIssue]
+  uint64_t* const h_full = ad_empty + ADS;        // [HS]
+  uint64_t* const h_empty = h_full + HS;
+  uint64_t* const d2_full = h_empty + HS;         // [D2S]
+  uint64_t* const d2_empty = d2_full + D2S;
+  uint64_t* const seg_full = d2_empty + D2S;      // [2]
+  uint64_t* const seg_empty = seg_full + 2;       // [2]
+  uint64_t* const drain = seg_empty + 2;          // [kIssue]
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  const uint32_t rank = cluster_rank(), ctas = cluster_nrank();
-  const int row0 = blockIdx.x / ctas * kTile;
-  if (warp == kSumWarps) {
+  if (warp == SEG) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
-  } else if (warp == kSumWarps + 1 && lane == 0) {
+  } else if (warp == COPY && lane == 0) {
     for (int i = 0; i < ROWS; ++i) {
       mbar_init(&row_full[i], 1);
       mbar_init(&row_empty[i], 1);
       mbar_init(&out_full[i], kSumWarps);
     }
     for (int i = 0; i < ADS; ++i) mbar_init(&ad_full[i], 1), mbar_init(&ad_empty[i], 1);
-    mbar_init(d1_full, kIssue);
-    mbar_init(d1_empty, kSumWarps);
-    for (int i = 0; i < 4; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], kSumWarps);
-    mbar_init(recv_full, kSumWarps * ctas);
-    mbar_init(h_full, kSumWarps * ctas);
+    for (int i = 0; i < HS; ++i) mbar_init(&h_full[i], kHWarps), mbar_init(&h_empty[i], kIssue);
+    for (int i = 0; i < D2S; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], kSumWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_empty[i], kSumWarps + kHWarps + 2 + kIssue);
     for (int i = 0; i < kIssue; ++i) mbar_init(&drain[i], 1);
     fence_mbar_init();
-    tma_prefetch_desc(&xmap), tma_prefetch_desc(&amap), tma_prefetch_desc(&bmap);
-    tma_prefetch_desc(&ymap), tma_prefetch_desc(&omap);
-  }
-  cluster_sync();  // the other CTAs have begun, and their barriers are there
-  pdl_wait();
-  const int kbs = (p.K + kCols - 1) / kCols, nbs = (p.N + kCols - 1) / kCols;
-  const int k0 = static_cast<int>(int64_t(kbs) * rank / ctas), nk = static_cast<int>(int64_t(kbs) * (rank + 1) / ctas) - k0;
-  const int n0 = static_cast<int>(int64_t(nbs) * rank / ctas), nn = static_cast<int>(int64_t(nbs) * (rank + 1) / ctas) - n0;
-  const int ahead = min(ROWS, nk);  // tiles of x that come before it is known which rows have an adapter
-  if (warp == kSumWarps && lane == 0) {
-    for (int i = 0; i < ahead; ++i) {
-      mbar_arrive_expect_tx(&row_full[i], kRowTile);
-      tma_load_2d(row_s + i * kRowTile, &xmap, &row_full[i], (k0 + i) * kCols, row0);
-    }
-  }
-  if (warp == 0) {
-    int id[kTile / 32], which[kTile / 32];
-#pragma unroll
-    for (int i = 0; i < kTile / 32; ++i) {
-      const int x = row0 + 32 * i + lane;
-      id[i] = x < p.T ? p.ids[x] : -1;
-      if (id[i] >= p.count) {
-        if (rank == 0) atomicOr(p.err, DEVERR_INDEX);
-        id[i] = -1;
-      }
-      which[i] = -1;
-    }
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kTile / 32; ++i) {
-      while (true) {  // the first row whose adapter is not on the list yet
-        const unsigned int left = __ballot_sync(0xFFFFFFFFu, id[i] >= 0 && which[i] < 0);
-        if (!left) break;
-        const int now = __shfl_sync(0xFFFFFFFFu, id[i], __ffs(left) - 1);
-#pragma unroll
-        for (int j = 0; j < kTile / 32; ++j)
-          if (id[j] == now) which[j] = n;
-        if (lane == 0) s_adapter[n] = now;
-        ++n;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kTile / 32; ++i) s_which[32 * i + lane] = which[i];
-    if (lane == 0) s_adapters = n;
+    tma_prefetch_desc(&bmap), tma_prefetch_desc(&ymap), tma_prefetch_desc(&omap);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem, d1 = tmem, d2 = tmem + 256;
-  const int adapters = s_adapters, passes = (adapters + C::PASS - 1) / C::PASS;
-  const int rp = (p.r + 15) / 16 * 16;
-  const int rows1 = max(passes * nk, ahead);  // tiles of x that come through the ring
+  // (The launch before has waited for those that write what this one reads ahead of its own wait: all but the sums.)
+  const uint32_t tmem = s_tmem;
   bool ok = true;
+  auto wait_segment = [&](int i) { return mbar_wait(&seg_full[i & 1], (i >> 1) & 1); };
+  auto done_with = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[i & 1]);
+  };
 
   if (warp < kSumWarps) {
-    // ------------------------------------------------------------------ sums
-    const int r = tid & (kTile - 1), half = tid / kTile, which = s_which[r];
+    // --------------------------------------------------------------- results
+    const int r = tid & (kTile - 1), half = tid / kTile;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int own = (kTile + ctas - 1) / ctas;  // rows that a CTA adds up
-    if (tid < adapters) s_scale[tid] = p.scales ? p.scales[s_adapter[tid]] : 1.0f;  // (seen by all after recv_full)
-    const uint32_t to = cluster_addr(recv + (rank * own + r % own) * C::RP4, r / own);
-    for (int pass = 0; pass < passes && ok; ++pass) {
-      if (nk > 0) ok = mbar_wait(d1_full, pass & 1);
-      if (!ok) break;
-      tc_fence_after();
-      for (int w = pass * C::PASS; w < min(adapters, (pass + 1) * C::PASS); ++w) {
-        if (!__any_sync(0xFFFFFFFFu, which == w)) continue;
-        for (int c = half * (rp / 2); c < (half + 1) * (rp / 2); c += 8) {
-          uint32_t v[8];
+    int unit = 0, row = 0;
+    for (int i = 0; ok; ++i) {
+      ok = wait_segment(i);
+      const Segment& s = s_seg[i & 1];
+      if (!ok || s.count == 0) break;
+      const int count = s.count, adapters = s.adapters, which = s.which[r];
+      done_with(i);
+      for (int n = 0; n < count && ok; ++n, ++row) {
+        uint32_t v[32];
+        for (int w = 0; w < adapters; ++w, ++unit) {
+          const int at = unit % D2S;
+          ok = mbar_wait(&d2_full[at], (unit / D2S) & 1);
+          if (!ok) break;
+          if (tid == 0) mbar_arrive(&ad_empty[unit % ADS]);  // the product has been formed
+          tc_fence_after();
+          if (__any_sync(0xFFFFFFFFu, which == w)) {
+            uint32_t u[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = 0;
-          for (int x = 0; x < min(kIssue, nk); ++x) {  // what each issuing warp's stages came to
-            uint32_t u[8];
-            tmem_ld8(d1 + lanes + ((w - pass * C::PASS) * kIssue + x) * C::D1 + c, u);
-            tmem_ld_wait();
+            for (int k = 0; k < 2; ++k) {
+              tmem_ld16(tmem + lanes + at * kCols + half * 32 + 16 * k, u);
+              tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+              for (int e = 0; e < 16; ++e)
+                if (which == w) v[16 * k + e] = u[e];
+            }
           }
-          if (which == w) {
-            st_cluster_v4(to + 4 * c, v[0], v[1], v[2], v[3]);
-            st_cluster_v4(to + 4 * c + 16, v[4], v[5], v[6], v[7]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&d2_empty[at]);
+        }
+        const int stage = row % ROWS;
+        if (ok) ok = mbar_wait(&row_full[stage], (row / ROWS) & 1);
+        if (!ok) break;
+        if (which >= 0) {
+          uint8_t* y = row_s + stage * kRowTile + r * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint4* at = reinterpret_cast<uint4*>(y + (((half * 4 + k) ^ (r & 7)) << 4));
+            const uint4 w = *at;
+            auto add = [&](uint32_t two, int e) {
+              return bf16x2_rn(__uint_as_float(two << 16) + __uint_as_float(v[8 * k + 2 * e]),
+                               __uint_as_float(two & 0xFFFF0000u) + __uint_as_float(v[8 * k + 2 * e + 1]));
+            };
+            *at = make_uint4(add(w.x, 0), add(w.y, 1), add(w.z, 2), add(w.w, 3));
           }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&out_full[stage]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(d1_empty);
     }
-    if (passes > 0 && ok) {
-      __syncwarp();
-      if (lane < static_cast<int>(ctas)) mbar_arrive_cluster(recv_full, lane);
-      ok = mbar_wait_cluster(recv_full, 0);
-      if (ok) {
-        const int pieces = rp / 8;
-        for (int e = tid; e < own * pieces; e += kSumWarps * 32) {
-          const int i = e / pieces, c = e - i * pieces, x = rank * own + i;
-          const int w = x < kTile ? s_which[x] : -1;
-          if (w < 0) continue;
+    if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
+  } else if (warp < SEG) {
+    // ------------------------------------------------- A x as two bf16 operands
+    pdl_wait();
+    const int me = tid - H0 * 32, pieces8 = q.rp / 8;
+    int n = 0;  // tiles with adapters so far
+    for (int i = 0; ok; ++i) {
+      ok = wait_segment(i);
+      const Segment& s = s_seg[i & 1];
+      if (!ok || s.count == 0) break;
+      if (s.adapters > 0) {
+        if (n >= HS) ok = mbar_wait(&h_empty[n % HS], (n / HS - 1) & 1);
+        if (!ok) break;
+        const unsigned int u0 = static_cast<unsigned int>(s.tile) * q.kbs;
+        const int c0 = q.k.cta_of(u0), c1 = q.k.cta_of(u0 + q.kbs - 1);
+        const float* from = q.part + int64_t(s.tile + c0) * kTile * q.rp;
+        uint8_t* const h = h_s + n % HS * C::H;
+        for (int e = me; e < kTile * pieces8; e += kHWarps * 32) {
+          const int x = e / pieces8, c = e - x * pieces8, w = s.which[x];
+          if (w < 0) continue;  // (what its row holds reaches no other)
           float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          for (uint32_t k = 0; k < ctas; ++k) {
-            const float4* v = reinterpret_cast<const float4*>(recv + (k * own + i) * C::RP4 + 8 * c);
-            const float4 lo = v[0], hi = v[1];
+          const float* v = from + x * q.rp + 8 * c;
+#pragma unroll 4
+          for (int k = c0; k <= c1; ++k, v += kTile * q.rp) {
+            const float4 lo = __ldcg(reinterpret_cast<const float4*>(v)), hi = __ldcg(reinterpret_cast<const float4*>(v + 4));
             sum[0] += lo.x, sum[1] += lo.y, sum[2] += lo.z, sum[3] += lo.w;
             sum[4] += hi.x, sum[5] += hi.y, sum[6] += hi.z, sum[7] += hi.w;
           }
-          const float scale = s_scale[w];
+          const float scale = p.scales ? __ldg(p.scales + s.adapter[w]) : 1.0f;
           uint32_t big[4], rest[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -568,189 +808,135 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             const float ra = a - __uint_as_float(big[k] << 16), rb = b - __uint_as_float(big[k] & 0xFFFF0000u);
             rest[k] = bf16x2_rn(isfinite(ra) ? ra : 0.0f, isfinite(rb) ? rb : 0.0f);
           }
-          uint8_t* to = h_s + (c / 8) * kRowTile + x * 128 + (((c & 7) ^ (x & 7)) << 4);
-          for (uint32_t k = 0; k < ctas; ++k) {
-            st_cluster_v4(cluster_addr(to, k), big[0], big[1], big[2], big[3]);
-            st_cluster_v4(cluster_addr(to + KB * kRowTile, k), rest[0], rest[1], rest[2], rest[3]);
-          }
+          uint8_t* to = h + (c / 8) * kRowTile + x * 128 + (((c & 7) ^ (x & 7)) << 4);
+          *reinterpret_cast<uint4*>(to) = make_uint4(big[0], big[1], big[2], big[3]);
+          *reinterpret_cast<uint4*>(to + KB * kRowTile) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
         }
-        fence_proxy_async_all();
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane < static_cast<int>(ctas)) mbar_arrive_cluster(h_full, lane);
+        if (lane == 0) mbar_arrive(&h_full[n % HS]);
+        ++n;
       }
-    }
-    int unit = 0, ring = rows1, ad = adapters * nk;
-    for (int n = 0; n < nn && ok; ++n, ++ring) {
-      uint32_t v[32];
-      for (int w = 0; w < adapters; ++w, ++unit, ++ad) {
-        ok = mbar_wait(&d2_full[unit & 3], (unit >> 2) & 1);
-        if (!ok) break;
-        if (tid == 0) mbar_arrive(&ad_empty[ad % ADS]);  // the product has been formed
-        tc_fence_after();
-        if (__any_sync(0xFFFFFFFFu, which == w)) {
-          uint32_t u[16];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            tmem_ld16(d2 + lanes + (unit & 3) * kCols + half * 32 + 16 * k, u);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (which == w) v[16 * k + i] = u[i];
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&d2_empty[unit & 3]);
-      }
-      const int stage = ring % ROWS;
-      if (ok) ok = mbar_wait(&row_full[stage], (ring / ROWS) & 1);
-      if (!ok) break;
-      if (which >= 0) {
-        uint8_t* y = row_s + stage * kRowTile + r * 128;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint4* at = reinterpret_cast<uint4*>(y + (((half * 4 + k) ^ (r & 7)) << 4));
-          const uint4 w = *at;
-          auto add = [&](uint32_t two, int i) {
-            return bf16x2_rn(__uint_as_float(two << 16) + __uint_as_float(v[8 * k + 2 * i]),
-                             __uint_as_float(two & 0xFFFF0000u) + __uint_as_float(v[8 * k + 2 * i + 1]));
-          };
-          *at = make_uint4(add(w.x, 0), add(w.y, 1), add(w.z, 2), add(w.w, 3));
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&out_full[stage]);
+      done_with(i);
     }
     if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
-  } else if (warp == kSumWarps) {
+  } else if (warp == SEG) {
+    // -------------------------------------------------------------- segments
+    unsigned int u = q.n.begin(blockIdx.x);
+    const unsigned int end = q.n.begin(blockIdx.x + 1);
+    for (int i = 0; ok; ++i) {
+      if (i >= 2) ok = mbar_wait(&seg_empty[i & 1], ((i >> 1) - 1) & 1);
+      if (!ok) break;
+      find_segment(p, u, end, q.nbs, false, &s_seg[i & 1]);
+      const int count = s_seg[i & 1].count;
+      if (lane == 0) mbar_arrive(&seg_full[i & 1]);
+      __syncwarp();
+      if (count == 0) break;
+      u += count;
+    }
+    if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
+  } else if (warp == COPY) {
     // ---------------------------------------------------------------- copies
-    if (lane == 0) {
-      int row = ahead, ad = 0;
-      // An adapter's tile, when the one before it in its place has been used.
-      auto ad_free = [&](int use) {  // (a place that has been filled again since has been waited for)
-        return use < 0 || use + ADS < ad || mbar_wait(&ad_empty[use % ADS], (use / ADS) & 1);
-      };
-      auto ad_stage = [&](uint32_t bytes) {
-        ok = ad_free(ad - ADS);
-        if (ok) mbar_arrive_expect_tx(&ad_full[ad % ADS], bytes);
-        return ok;
-      };
-      auto row_tile = [&](const CUtensorMap* map, int x) {
-        mbar_arrive_expect_tx(&row_full[row % ROWS], kRowTile);
-        tma_load_2d(row_s + (row % ROWS) * kRowTile, map, &row_full[row % ROWS], x, row0);
-        ++row;
-      };
-      // A tile of x has been used when the last of its pass's adapters has.
-      int last[ROWS];
-#pragma unroll
-      for (int i = 0; i < ROWS; ++i) last[i] = -1;
-      for (int pass = 0; pass < passes && ok; ++pass) {
-        const int w0 = pass * C::PASS, w1 = min(adapters, w0 + C::PASS);
-        for (int k = 0; k < nk && ok; ++k) {
-          const int use = pass * nk + k;
-          if (use >= ahead) {
-            ok = ad_free(last[use % ROWS]);
+    int row = 0, ad = 0;
+    for (int i = 0; ok; ++i) {
+      ok = wait_segment(i);
+      const Segment& s = s_seg[i & 1];
+      if (!ok || s.count == 0) break;
+      if (lane == 0) {
+        for (int n = 0; n < s.count && ok; ++n) {
+          const int x = (s.first + n) * kCols, at = row % ROWS;
+          if (row >= ROWS) ok = mbar_wait(&row_empty[at], (row / ROWS - 1) & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&row_full[at], kRowTile);
+          tma_load_2d(row_s + at * kRowTile, &ymap, &row_full[at], x, s.tile * kTile);
+          ++row;
+          for (int w = 0; w < s.adapters && ok; ++w) {
+            const int to = ad % ADS;
+            if (ad >= ADS) ok = mbar_wait(&ad_empty[to], (ad / ADS - 1) & 1);
             if (!ok) break;
-            row_tile(&xmap, (k0 + k) * kCols);
-          }
-          for (int w = w0; w < w1 && ok; ++w) {
-            if (!ad_stage(rp * 128)) break;
-            tma_load_3d(ad_s + (ad % ADS) * C::AD_TILE, &amap, &ad_full[ad % ADS], (k0 + k) * kCols, 0, s_adapter[w]);
+            mbar_arrive_expect_tx(&ad_full[to], KB * 64 * 128);
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+              tma_load_3d(ad_s + to * C::AD_TILE + k * 64 * 128, &bmap, &ad_full[to], 64 * k, x, s.adapter[w]);
             ++ad;
           }
-          last[use % ROWS] = ad - 1;
         }
       }
-      for (int n = 0; n < nn && ok; ++n) {
-        const int use = row;
-        if (n >= ROWS)
-          ok = mbar_wait(&row_empty[use % ROWS], (n / ROWS - 1) & 1);
-        else if (passes > 0)
-          ok = ad_free(last[use % ROWS]);
-        else if (use >= ROWS || use % ROWS < ahead)  // no row has an adapter: x's tiles have landed, that is all
-          ok = mbar_wait(&row_full[use % ROWS], 0);
-        if (!ok) break;
-        row_tile(&ymap, (n0 + n) * kCols);
-        for (int w = 0; w < adapters && ok; ++w) {
-          if (!ad_stage(KB * 64 * 128)) break;
-#pragma unroll
-          for (int k = 0; k < KB; ++k)
-            tma_load_3d(ad_s + (ad % ADS) * C::AD_TILE + k * 64 * 128, &bmap, &ad_full[ad % ADS], 64 * k, (n0 + n) * kCols,
-                        s_adapter[w]);
-          ++ad;
-        }
-      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      done_with(i);
+    }
+    if (lane == 0) {
       if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
       // Copies in flight have to land before this CTA's shared memory goes.
       for (int i = max(0, row - ROWS); i < row; ++i) mbar_wait(&row_full[i % ROWS], (i / ROWS) & 1);
       for (int i = max(0, ad - ADS); i < ad; ++i) mbar_wait(&ad_full[i % ADS], (i / ADS) & 1);
     }
     __syncwarp();
-  } else if (warp == kSumWarps + 2) {
+  } else if (warp == STORE) {
     // ---------------------------------------------------------------- stores
-    if (lane == 0) {
-      const int ring = rows1;
-      for (int n = 0; n < nn && ok; ++n) {
-        const int stage = (ring + n) % ROWS;
-        ok = mbar_wait(&out_full[stage], (n / ROWS) & 1);
-        if (!ok) break;
-        tma_store_2d(&omap, row_s + stage * kRowTile, (n0 + n) * kCols, row0);
-        bulk_commit();
-        if (n > 0) {  // the store before this one has read its tile
-          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          mbar_arrive(&row_empty[(ring + n - 1) % ROWS]);
+    int row = 0;
+    for (int i = 0; ok; ++i) {
+      ok = wait_segment(i);
+      const Segment& s = s_seg[i & 1];
+      if (!ok || s.count == 0) break;
+      const int count = s.count, tile = s.tile, first = s.first;
+      done_with(i);
+      if (lane == 0) {
+        for (int n = 0; n < count && ok; ++n, ++row) {
+          const int stage = row % ROWS;
+          ok = mbar_wait(&out_full[stage], (row / ROWS) & 1);
+          if (!ok) break;
+          tma_store_2d(&omap, row_s + stage * kRowTile, (first + n) * kCols, tile * kTile);
+          bulk_commit();
+          if (row > 0) {  // the store before this one has read its tile
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            mbar_arrive(&row_empty[(row - 1) % ROWS]);
+          }
         }
       }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    }
+    if (lane == 0) {
       bulk_wait_all();
       if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------- MMA
-    if (lane == 0) {
-      const int x = warp == kSumWarps + 1 ? 0 : 1;  // every other stage and product
-      const uint32_t id1 = idesc_bf16(kTile, rp), id2 = idesc_bf16(kTile, kCols);
-      const uint64_t row_d = smem_desc(smem_u32(row_s), 16, 1024, SWZ_128B);
-      const uint64_t ad_d = smem_desc(smem_u32(ad_s), 16, 1024, SWZ_128B);
-      const uint64_t h_d = smem_desc(smem_u32(h_s), 16, 1024, SWZ_128B);
-      for (int pass = 0; pass < passes && ok; ++pass) {
-        const int w0 = pass * C::PASS, w1 = min(adapters, w0 + C::PASS);
-        if (nk > 0 && pass > 0) ok = mbar_wait(d1_empty, (pass - 1) & 1);
-        for (int k = x; k < nk && ok; k += kIssue) {
-          const int row = pass * nk + k;
-          ok = mbar_wait(&row_full[row % ROWS], (row / ROWS) & 1);
-          const uint64_t a = row_d + (row % ROWS) * (kRowTile >> 4);
-          for (int w = w0; w < w1 && ok; ++w) {
-            const int ad = w0 * nk + k * (w1 - w0) + w - w0;
-            ok = mbar_wait(&ad_full[ad % ADS], (ad / ADS) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b = ad_d + (ad % ADS) * (C::AD_TILE >> 4);
-#pragma unroll
-            for (int i = 0; i < kCols / 16; ++i)
-              mma_bf16(d1 + ((w - w0) * kIssue + x) * C::D1, a + 2 * i, b + 2 * i, id1, k >= kIssue || i > 0);
-            mma_commit(&ad_empty[ad % ADS]);
-          }
+    const int x = warp - ISSUE;  // every other product is this warp's
+    const uint32_t id = idesc_bf16(kTile, kCols);
+    const uint64_t ad_d = smem_desc(smem_u32(ad_s), 16, 1024, SWZ_128B);
+    const uint64_t h_d = smem_desc(smem_u32(h_s), 16, 1024, SWZ_128B);
+    int unit = 0, tiles = 0;  // so far, tiles: with adapters
+    for (int i = 0; ok; ++i) {
+      ok = wait_segment(i);
+      const Segment& s = s_seg[i & 1];
+      if (!ok || s.count == 0) break;
+      const int units = s.count * s.adapters;
+      done_with(i);
+      if (units == 0) continue;
+      if (lane == 0) {
+        ok = mbar_wait(&h_full[tiles % HS], (tiles / HS) & 1);
+        const uint64_t h = h_d + tiles % HS * (C::H >> 4);
+        for (int k = (unit & 1) == x ? 0 : 1; k < units && ok; k += kIssue) {
+          const int u = unit + k, from = u % ADS, at = u % D2S;
+          ok = mbar_wait(&ad_full[from], (u / ADS) & 1) && (u < D2S || mbar_wait(&d2_empty[at], (u / D2S - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b = ad_d + from * (C::AD_TILE >> 4);
+          for (int part = 0; part < 2; ++part)
+            for (int e = 0; e < q.rp / 16; ++e)
+              mma_bf16(tmem + at * kCols, h + part * (KB * kRowTile >> 4) + (e / 4) * (kRowTile >> 4) + 2 * (e & 3),
+                       b + (e / 4) * (64 * 128 >> 4) + 2 * (e & 3), id, part > 0 || e > 0);
+          mma_commit(&d2_full[at]);
         }
-        if (nk > 0 && ok) mma_commit(d1_full);
+        if (ok) mma_commit(&h_empty[tiles % HS]);
       }
-      if (passes > 0 && ok) ok = mbar_wait_cluster(h_full, 0);
-      fence_proxy_async_all();
-      for (int unit = x; unit < nn * adapters && ok; unit += kIssue) {
-        const int ad = adapters * nk + unit;
-        ok = mbar_wait(&ad_full[ad % ADS], (ad / ADS) & 1) &&
-             (unit < 4 || mbar_wait(&d2_empty[unit & 3], ((unit >> 2) - 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t b = ad_d + (ad % ADS) * (C::AD_TILE >> 4);
-        for (int part = 0; part < 2; ++part)
-          for (int i = 0; i < rp / 16; ++i) {
-            const uint64_t at = h_d + part * (KB * kRowTile >> 4) + (i / 4) * (kRowTile >> 4) + 2 * (i & 3);
-            mma_bf16(d2 + (unit & 3) * kCols, at, b + (i / 4) * (64 * 128 >> 4) + 2 * (i & 3), id2, part > 0 || i > 0);
-          }
-        mma_commit(&d2_full[unit & 3]);
-      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      unit += units;
+      ++tiles;
+    }
+    if (lane == 0) {
       if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_MMA);
       mma_commit(&drain[x]);  // every MMA issued must finish before tensor memory is freed
       mbar_wait(&drain[x], 0);
@@ -760,67 +946,44 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   tc_fence_before();
   __syncthreads();
   pdl_trigger();
-  if (warp == kSumWarps) {
+  if (warp == SEG) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  cluster_sync();  // no CTA writes to another's shared memory any more
 }
 
-// CTAs per cluster for so many tiles: as many as all of them still run at once with.
-template <int KB>
-unsigned many_cluster(const DeviceInfo& dev, int64_t tiles) {
-  static std::atomic<int> most[64][kMostCluster + 1];  // clusters of each size that fit at once, + 1
-  for (unsigned c = kMostCluster; c > 1; --c) {
-    if (tiles * c > dev.sm_count) continue;
-    std::atomic<int>& known = most[dev.ordinal & 63][c];
-    int n = known.load(std::memory_order_relaxed);
-    if (n == 0) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = c;
-      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(c);
-      cfg.blockDim = dim3(kManyThreads);
-      cfg.dynamicSmemBytes = ManyCfg<KB>::SMEM;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int fit = 0;
-      if (cudaFuncSetAttribute(add_adapters_many_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               ManyCfg<KB>::SMEM) != cudaSuccess ||
-          cudaOccupancyMaxActiveClusters(&fit, add_adapters_many_kernel<KB>, &cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        fit = 0;
-      }
-      n = fit + 1;
-      known.store(n, std::memory_order_relaxed);
-    }
-    if (tiles <= n - 1) return c;
-  }
-  return 1;
+inline Deal deal_k(int64_t T, int64_t K, int sms) {
+  return Deal::of(static_cast<unsigned int>((T + kTile - 1) / kTile * ((K + kCols - 1) / kCols)), sms, kLeastK);
+}
+inline size_t many_bytes(int64_t T, int64_t K, int64_t r, int sms) {
+  return T <= kFewRows ? 0 : static_cast<size_t>((T + kTile - 1) / kTile + deal_k(T, K, sms).ctas) * kTile *
+                                 static_cast<size_t>((r + 15) / 16 * 16) * sizeof(float);
 }
 
 template <int KB>
-sp24_status launch_many(const AdapterParams& p, const DeviceInfo& dev, cudaStream_t s) {
-  using C = ManyCfg<KB>;
+sp24_status launch_many(const AdapterParams& p, float* part, const DeviceInfo& dev, cudaStream_t s) {
   CUtensorMap x, a, b, y, o;
   const auto type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
-  const uint32_t rp = (p.r + 15) / 16 * 16;
+  ManyParams q;
+  q.p = p;
+  q.kbs = (p.K + kCols - 1) / kCols, q.nbs = (p.N + kCols - 1) / kCols;
+  q.rp = (p.r + 15) / 16 * 16;
+  q.k = deal_k(p.T, p.K, dev.sm_count);
+  q.n = Deal::of(static_cast<unsigned int>((p.T + kTile - 1) / kTile) * q.nbs, dev.sm_count, kLeastN);
+  q.part = part;
   sp24_status st = make_tmap_2d(&x, p.x, type, p.K, p.T, p.ldx * 2, kCols, kTile, swizzle);
   if (!st) st = make_tmap_2d(&y, p.y, type, p.N, p.T, p.ldy * 2, kCols, kTile, swizzle);
   if (!st) st = make_tmap_2d(&o, p.out, type, p.N, p.T, p.ldo * 2, kCols, kTile, swizzle);
-  if (!st) st = make_tmap_3d(&a, p.a, type, p.K, p.r, p.count, uint64_t(p.K) * 2, p.stride_a * 2, kCols, rp, swizzle);
+  if (!st) st = make_tmap_3d(&a, p.a, type, p.K, p.r, p.count, uint64_t(p.K) * 2, p.stride_a * 2, kCols, q.rp, swizzle);
   if (!st) st = make_tmap_3d(&b, p.b, type, p.r, p.N, p.count, uint64_t(p.r) * 2, p.stride_b * 2, 64, kCols, swizzle);
   if (st) return st;
-  const int64_t tiles = (p.T + kTile - 1) / kTile;
-  const unsigned c = many_cluster<KB>(dev, tiles);
-  return launch_pdl_clusters_smem<add_adapters_many_kernel<KB>>(dev, c, dim3(static_cast<unsigned>(tiles * c)),
-                                                                dim3(kManyThreads), C::SMEM, s, x, a, b, y, o,
-                                                                p) == cudaSuccess
-             ? SP24_OK
-             : SP24_ERR_CUDA;
+  if (launch_pdl_smem<adapters_down_kernel<KB>>(dev, dim3(q.k.ctas), dim3(kDownThreads), DownCfg<KB>::SMEM, s, x, a, q) !=
+          cudaSuccess ||
+      launch_pdl_smem<adapters_up_kernel<KB>>(dev, dim3(q.n.ctas), dim3(kUpThreads), UpCfg<KB>::SMEM, s, b, y, o, q) !=
+          cudaSuccess)
+    return SP24_ERR_CUDA;
+  return SP24_OK;
 }
 
 template <int MT, int NT>
@@ -835,10 +998,18 @@ cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream
 }  // namespace
 }  // namespace sp24
 
+extern "C" size_t sp24_add_adapters_workspace_size(int64_t T, int64_t K, int64_t r) {
+  using namespace sp24;
+  const int64_t most = int64_t(1) << 24;
+  const DeviceInfo* dev = nullptr;
+  if (T <= kFewRows || T > INT32_MAX / 2 || K < 8 || K > most || r < 1 || r > kMostRank || current_device(&dev)) return 0;
+  return many_bytes(T, K, r, dev->sm_count);
+}
+
 extern "C" sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void* X, int64_t ldx, int64_t T, int64_t K,
                                          int64_t N, const void* A, int64_t stride_a, const void* B, int64_t stride_b,
                                          int64_t r, int64_t count, const int32_t* ids, const float* scales, void* out,
-                                         int64_t ldo, void* stream) {
+                                         int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
   using namespace sp24;
   const int64_t most = int64_t(1) << 24;
   if (T < 0 || T > INT32_MAX / 2 || K < 8 || N < 8 || K > most || N > most || r < 1 || count < 1 || count > INT32_MAX)
@@ -857,6 +1028,12 @@ extern "C" sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void*
   const DeviceInfo* dev = nullptr;
   if (sp24_status st = current_device(&dev)) return st;
   if (T == 0) return SP24_OK;
+  if (const size_t need = many_bytes(T, K, r, dev->sm_count)) {
+    if (!workspace || workspace_bytes < need) return SP24_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SP24_ERR_ALIGNMENT;
+    const int64_t tiles = (T + kTile - 1) / kTile, most = INT32_MAX / tiles;
+    if ((K + kCols - 1) / kCols > most || (N + kCols - 1) / kCols > most) return SP24_ERR_UNSUPPORTED;  // 32-bit units
+  }
   AdapterParams p;
   p.y = static_cast<const __nv_bfloat16*>(Y);
   p.x = static_cast<const __nv_bfloat16*>(X);
@@ -871,7 +1048,9 @@ extern "C" sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void*
   p.err = dev->err_word;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (T > kFewRows) return r <= 64 ? launch_many<1>(p, *dev, s) : launch_many<2>(p, *dev, s);
+  if (T > kFewRows)
+    return r <= 64 ? launch_many<1>(p, static_cast<float*>(workspace), *dev, s)
+                   : launch_many<2>(p, static_cast<float*>(workspace), *dev, s);
   if (r <= 16)
     e = launch_few<1, 1>(p, *dev, s);
   else if (r <= 32)

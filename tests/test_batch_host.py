@@ -64,7 +64,7 @@ def test_copy_arguments(lib):
 def test_adapter_arguments(lib):
     def call(**kw):
         a = dict(y=P, ldy=64, x=P, ldx=128, T=2, K=128, N=64, a=P, sa=1024, b=P, sb=512, r=8, count=3, ids=P, scales=P, out=P,
-                 ldo=64)
+                 ldo=64, ws=None, bytes=0)
         a.update(kw)
         return lib.sp24_add_adapters(*a.values(), None)
 
