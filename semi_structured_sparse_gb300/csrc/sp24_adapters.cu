@@ -384,10 +384,11 @@ struct Segment {
   int adapters;
   int adapter[kTile];         // the tile's adapters
   int which[kTile];           // of each row: which of them, or -1
+  float scale[kTile];         // of each row
 };
 // The segment that begins with unit u, by one warp.
 __device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned int u, unsigned int u_end, int per_tile,
-                                             bool report, Segment* out) {
+                                             bool report, bool scales, Segment* out) {
   const int lane = threadIdx.x & 31;
   if (u >= u_end) {
     if (lane == 0) out->count = 0;
@@ -423,7 +424,10 @@ __device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned in
     }
   }
 #pragma unroll
-  for (int i = 0; i < kTile / 32; ++i) out->which[32 * i + lane] = which[i];
+  for (int i = 0; i < kTile / 32; ++i) {
+    out->which[32 * i + lane] = which[i];
+    if (scales) out->scale[32 * i + lane] = p.scales && id[i] >= 0 ? __ldg(p.scales + id[i]) : 1.0f;
+  }
   if (lane == 0) {
     out->tile = tile;
     out->first = first;
@@ -436,12 +440,13 @@ __device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned in
 // ------------------------------------------------------------------ A x
 template <int KB>  // 64s of the rank
 struct DownCfg {
-  static constexpr int ROWS = KB == 1 ? 8 : 6, ADS = KB == 1 ? 8 : 6;  // stages
+  static constexpr int ROWS = KB == 1 ? 8 : 6, ADS = KB == 1 ? 11 : 7;  // stages
   static constexpr int AD_TILE = KB * 64 * 128;
   static constexpr int D1 = 64 * KB;                  // columns of an adapter's sums
   static constexpr int PASS = 512 / (kIssue * D1);    // adapters per pass over K
   static constexpr int BARS = 2 * ROWS + 2 * ADS + 2 + 4 + kIssue;
   static constexpr int SMEM = 1024 + ROWS * kRowTile + ADS * AD_TILE + BARS * 8;
+  static_assert(SMEM + 2 * sizeof(Segment) + 64 <= 227 * 1024, "shared memory");
 };
 constexpr int kDownThreads = (4 + 2 + kIssue) * 32;  // sums, segments, copies, MMAs
 
@@ -541,7 +546,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     for (int i = 0; ok; ++i) {
       if (i >= 2) ok = mbar_wait(&seg_empty[i & 1], ((i >> 1) - 1) & 1);
       if (!ok) break;
-      find_segment(p, u, end, q.kbs, u % q.kbs == 0, &s_seg[i & 1]);
+      find_segment(p, u, end, q.kbs, u % q.kbs == 0, false, &s_seg[i & 1]);
       const int count = s_seg[i & 1].count;
       if (lane == 0) mbar_arrive(&seg_full[i & 1]);
       __syncwarp();
@@ -653,8 +658,10 @@ struct UpCfg {
   static constexpr int D2S = 512 / kCols;
   static constexpr int BARS = 3 * ROWS + 2 * ADS + 2 * HS + 2 * D2S + 4 + kIssue;
   static constexpr int SMEM = 1024 + ROWS * kRowTile + ADS * AD_TILE + HS * H + BARS * 8;
+  static_assert(SMEM + 2 * sizeof(Segment) + 64 <= 227 * 1024, "shared memory");
 };
-constexpr int kSumWarps = 8, kHWarps = 4;
+constexpr int kGroups = 2, kSumWarps = 4 * kGroups;  // groups of warps that take every other unit's results
+constexpr int kHWarps = 8;
 constexpr int kUpThreads = (kSumWarps + kHWarps + 3 + kIssue) * 32;  // ..., segments, copies, stores, MMAs
 
 template <int KB>
@@ -694,11 +701,11 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     for (int i = 0; i < ROWS; ++i) {
       mbar_init(&row_full[i], 1);
       mbar_init(&row_empty[i], 1);
-      mbar_init(&out_full[i], kSumWarps);
+      mbar_init(&out_full[i], 4);
     }
     for (int i = 0; i < ADS; ++i) mbar_init(&ad_full[i], 1), mbar_init(&ad_empty[i], 1);
     for (int i = 0; i < HS; ++i) mbar_init(&h_full[i], kHWarps), mbar_init(&h_empty[i], kIssue);
-    for (int i = 0; i < D2S; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], kSumWarps);
+    for (int i = 0; i < D2S; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], 4);
     for (int i = 0; i < 2; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_empty[i], kSumWarps + kHWarps + 2 + kIssue);
     for (int i = 0; i < kIssue; ++i) mbar_init(&drain[i], 1);
     fence_mbar_init();
@@ -718,58 +725,62 @@ __global__ void __launch_bounds__(kUpThreads, 1)
 
   if (warp < kSumWarps) {
     // --------------------------------------------------------------- results
-    const int r = tid & (kTile - 1), half = tid / kTile;
+    const int r = tid & (kTile - 1), group = tid / kTile;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int unit = 0, row = 0;
+    int unit0 = 0, row0 = 0;  // of the segment
     for (int i = 0; ok; ++i) {
       ok = wait_segment(i);
       const Segment& s = s_seg[i & 1];
       if (!ok || s.count == 0) break;
       const int count = s.count, adapters = s.adapters, which = s.which[r];
       done_with(i);
-      for (int n = 0; n < count && ok; ++n, ++row) {
-        uint32_t v[32];
-        for (int w = 0; w < adapters; ++w, ++unit) {
-          const int at = unit % D2S;
+      for (int n = (row0 + group) % kGroups; n < count && ok; n += kGroups) {
+        const int row = row0 + n, stage = row % ROWS;
+        ok = mbar_wait(&row_full[stage], (row / ROWS) & 1);
+        if (!ok) break;
+        uint8_t* const y = row_s + stage * kRowTile + r * 128;
+        for (int w = 0; w < adapters; ++w) {
+          const int unit = unit0 + n * adapters + w, at = unit % D2S;
           ok = mbar_wait(&d2_full[at], (unit / D2S) & 1);
           if (!ok) break;
-          if (tid == 0) mbar_arrive(&ad_empty[unit % ADS]);  // the product has been formed
+          if (r == 0) mbar_arrive(&ad_empty[unit % ADS]);  // the product has been formed
           tc_fence_after();
           if (__any_sync(0xFFFFFFFFu, which == w)) {
-            uint32_t u[16];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              tmem_ld16(tmem + lanes + at * kCols + half * 32 + 16 * k, u);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t u[2][16];
+              uint4 v[4];
+              tmem_ld16(tmem + lanes + at * kCols + 32 * h, u[0]);
+              tmem_ld16(tmem + lanes + at * kCols + 32 * h + 16, u[1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(y + (((h * 4 + k) ^ (r & 7)) << 4));
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (which == w) v[16 * k + e] = u[e];
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t* a = &u[k / 2][8 * (k & 1)];
+                auto add = [&](uint32_t two, int e) {
+                  return bf16x2_rn(__uint_as_float(two << 16) + __uint_as_float(a[2 * e]),
+                                   __uint_as_float(two & 0xFFFF0000u) + __uint_as_float(a[2 * e + 1]));
+                };
+                v[k] = make_uint4(add(v[k].x, 0), add(v[k].y, 1), add(v[k].z, 2), add(v[k].w, 3));
+              }
+              if (which == w) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(y + (((h * 4 + k) ^ (r & 7)) << 4)) = v[k];
+              }
             }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&d2_empty[at]);
         }
-        const int stage = row % ROWS;
-        if (ok) ok = mbar_wait(&row_full[stage], (row / ROWS) & 1);
         if (!ok) break;
-        if (which >= 0) {
-          uint8_t* y = row_s + stage * kRowTile + r * 128;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4* at = reinterpret_cast<uint4*>(y + (((half * 4 + k) ^ (r & 7)) << 4));
-            const uint4 w = *at;
-            auto add = [&](uint32_t two, int e) {
-              return bf16x2_rn(__uint_as_float(two << 16) + __uint_as_float(v[8 * k + 2 * e]),
-                               __uint_as_float(two & 0xFFFF0000u) + __uint_as_float(v[8 * k + 2 * e + 1]));
-            };
-            *at = make_uint4(add(w.x, 0), add(w.y, 1), add(w.z, 2), add(w.w, 3));
-          }
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&out_full[stage]);
       }
+      unit0 += count * adapters;
+      row0 += count;
     }
     if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
   } else if (warp < SEG) {
@@ -788,29 +799,52 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         const int c0 = q.k.cta_of(u0), c1 = q.k.cta_of(u0 + q.kbs - 1);
         const float* from = q.part + int64_t(s.tile + c0) * kTile * q.rp;
         uint8_t* const h = h_s + n % HS * C::H;
-        for (int e = me; e < kTile * pieces8; e += kHWarps * 32) {
-          const int x = e / pieces8, c = e - x * pieces8, w = s.which[x];
-          if (w < 0) continue;  // (what its row holds reaches no other)
-          float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          const float* v = from + x * q.rp + 8 * c;
-#pragma unroll 4
-          for (int k = c0; k <= c1; ++k, v += kTile * q.rp) {
-            const float4 lo = __ldcg(reinterpret_cast<const float4*>(v)), hi = __ldcg(reinterpret_cast<const float4*>(v + 4));
-            sum[0] += lo.x, sum[1] += lo.y, sum[2] += lo.z, sum[3] += lo.w;
-            sum[4] += hi.x, sum[5] += hi.y, sum[6] += hi.z, sum[7] += hi.w;
-          }
-          const float scale = p.scales ? __ldg(p.scales + s.adapter[w]) : 1.0f;
-          uint32_t big[4], rest[4];
+        // Two tasks of 8 values at a time, and four pieces of each: their loads are under way together.  (A row without
+        // an adapter has whatever is there: it reaches no other row, and is not used.)
+        constexpr int STEP = kHWarps * 32;
+        for (int e0 = me; e0 < kTile * pieces8; e0 += 2 * STEP) {
+          float sum[2][8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float a = sum[2 * k] * scale, b = sum[2 * k + 1] * scale;
-            big[k] = bf16x2_rn(a, b);
-            const float ra = a - __uint_as_float(big[k] << 16), rb = b - __uint_as_float(big[k] & 0xFFFF0000u);
-            rest[k] = bf16x2_rn(isfinite(ra) ? ra : 0.0f, isfinite(rb) ? rb : 0.0f);
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[j][k] = 0.0f;
+          for (int k0 = c0; k0 <= c1; k0 += 4) {
+            float4 v[2][4][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                v[j][k][0] = v[j][k][1] = make_float4(0, 0, 0, 0);
+                if (e0 + j * STEP < kTile * pieces8 && k0 + k <= c1) {  // (8 values: a task's place is its number's)
+                  const float4* f = reinterpret_cast<const float4*>(from + int64_t(k0 + k - c0) * kTile * q.rp) + 2 * (e0 + j * STEP);
+                  v[j][k][0] = __ldcg(f), v[j][k][1] = __ldcg(f + 1);
+                }
+              }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                sum[j][0] += v[j][k][0].x, sum[j][1] += v[j][k][0].y, sum[j][2] += v[j][k][0].z, sum[j][3] += v[j][k][0].w;
+                sum[j][4] += v[j][k][1].x, sum[j][5] += v[j][k][1].y, sum[j][6] += v[j][k][1].z, sum[j][7] += v[j][k][1].w;
+              }
           }
-          uint8_t* to = h + (c / 8) * kRowTile + x * 128 + (((c & 7) ^ (x & 7)) << 4);
-          *reinterpret_cast<uint4*>(to) = make_uint4(big[0], big[1], big[2], big[3]);
-          *reinterpret_cast<uint4*>(to + KB * kRowTile) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int e = e0 + j * STEP, x = e / pieces8, c = e - x * pieces8;
+            if (x >= kTile) break;
+            const float scale = s.scale[x];
+            uint32_t big[4], rest[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = sum[j][2 * k] * scale, b = sum[j][2 * k + 1] * scale;
+              big[k] = bf16x2_rn(a, b);
+              const float ra = a - __uint_as_float(big[k] << 16), rb = b - __uint_as_float(big[k] & 0xFFFF0000u);
+              rest[k] = bf16x2_rn(isfinite(ra) ? ra : 0.0f, isfinite(rb) ? rb : 0.0f);
+            }
+            uint8_t* to = h + (c / 8) * kRowTile + x * 128 + (((c & 7) ^ (x & 7)) << 4);
+            *reinterpret_cast<uint4*>(to) = make_uint4(big[0], big[1], big[2], big[3]);
+            *reinterpret_cast<uint4*>(to + KB * kRowTile) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -827,7 +861,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     for (int i = 0; ok; ++i) {
       if (i >= 2) ok = mbar_wait(&seg_empty[i & 1], ((i >> 1) - 1) & 1);
       if (!ok) break;
-      find_segment(p, u, end, q.nbs, false, &s_seg[i & 1]);
+      find_segment(p, u, end, q.nbs, false, true, &s_seg[i & 1]);
       const int count = s_seg[i & 1].count;
       if (lane == 0) mbar_arrive(&seg_full[i & 1]);
       __syncwarp();
