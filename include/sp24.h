@@ -532,13 +532,14 @@ SP24_API size_t sp24_attention_prompt_workspace_size(int64_t T, int64_t B, int q
  *           sequences cu_shared[g] .. cu_shared[g + 1] - 1.  Sequences before the
  *           first group and after the last have nothing in common.
  *   shared_lens (device) int32 [G]: the first shared_lens[g] tokens of the
- *           group's sequences are the same, and are read through the pages of
- *           its first sequence.  (Any number of tokens: where it is no multiple
- *           of the page size, each sequence has the page in which they end as a
- *           copy of its own, sp24_cache_copy.)  A sequence that does not see all
- *           of them, because it is shorter or its window begins later, is
- *           attended by itself, through its own pages, as in
- *           sp24_attention_decode.
+ *           group's sequences are the same.  They are read through the pages of
+ *           its first sequence (at most as many as that one has).  Any number of
+ *           tokens: where it is no multiple of the page size, each sequence has
+ *           the page in which they end as a copy of its own, sp24_cache_copy.  A
+ *           sequence that does not see all of them, because it is shorter or its
+ *           window begins later, is attended by itself, through its own pages, as
+ *           in sp24_attention_decode; so are all sequences of a call whose tables
+ *           are so narrow that sharing could not pay.
  *   workspace: device scratch of sp24_attention_decode_shared_workspace_size
  *           bytes, 16-byte aligned, zeroed once before its first use and then
  *           consistent from call to call, whatever their shapes; calls that

@@ -852,6 +852,16 @@ def _adapter_stack(t, shape, name, what, device):
             name, what, list(shape), tuple(t.shape), t.stride()))
 
 
+def _stack_stride(t, rows, cols):
+    """The distance of [count, rows, cols] matrices that are contiguous each (0: they are not)."""
+    if t.is_contiguous():
+        return rows * cols
+    count, (s0, s1, s2) = t.shape[0], t.stride()
+    if s2 != 1 or (rows > 1 and s1 != cols) or (count > 1 and s0 < rows * cols):
+        return 0
+    return s0 if count > 1 else rows * cols
+
+
 def add_adapters_workspace_size(rows: int, k: int, r: int) -> int:
     """Device scratch bytes add_adapters() needs for `rows` rows of `k` values and rank `r`
     on the current GPU (0: none)."""
@@ -870,23 +880,28 @@ def add_adapters(y, x, a, b, ids, scales=None, out=None, workspace=None, stream=
     ok = False
     try:
         at = y.get_device()
-        T, N = y.shape
+        shape = T, N = y.shape
         count, r, K = a.shape
-        ldy, ldx = _row_stride(y, N), _row_stride(x, K)
+        ldy = N if y.is_contiguous() else _row_stride(y, N)
+        ldx = K if x.is_contiguous() else _row_stride(x, K)
         if out is None:
-            out, ldo = _new((T, N), _BF16, stream, y.device), N
+            out, ldo = _new(shape, _BF16, stream, y.device), N
+        elif out is y:
+            ldo = ldy
         else:
-            ldo = _row_stride(out, N)
-        stride_a, stride_b = (a.stride(0), b.stride(0)) if count > 1 else (r * K, N * r)
-        ok = (y.dtype is _BF16 and y.is_cuda and ldy and x.dtype is _BF16 and ldx and x.shape == (T, K) and
-              x.get_device() == at and out.dtype is _BF16 and ldo and out.shape == (T, N) and out.get_device() == at and
-              a.dtype is _BF16 and a.get_device() == at and a.stride(2) == 1 and a.stride(1) == K and stride_a >= r * K and
-              b.dtype is _BF16 and b.get_device() == at and b.shape == (count, N, r) and b.stride(2) == 1 and
-              b.stride(1) == r and stride_b >= N * r and ids.dtype is _I32 and ids.shape == (T,) and
-              ids.is_contiguous() and ids.get_device() == at)
+            ldo = N if out.is_contiguous() else _row_stride(out, N)
+            ok = out.dtype is _BF16 and out.shape == shape and out.get_device() == at
+            ldo = ldo if ok else 0
+        stride_a, stride_b = _stack_stride(a, r, K), _stack_stride(b, N, r)
+        ok = (ldy and ldx and ldo and stride_a and stride_b and at >= 0 and y.dtype is _BF16 and x.dtype is _BF16 and
+              x.shape == (T, K) and x.get_device() == at and a.dtype is _BF16 and a.get_device() == at and
+              b.dtype is _BF16 and b.get_device() == at and b.shape == (count, N, r) and ids.dtype is _I32 and
+              ids.shape == (T,) and ids.is_contiguous() and ids.get_device() == at)
+        sp = None
         if scales is not None:
             ok = (ok and scales.dtype is _F32 and scales.shape == (count,) and scales.is_contiguous() and
                   scales.get_device() == at)
+            sp = scales.data_ptr()
     except (AttributeError, IndexError, ValueError, TypeError):
         ok = False
     if not ok:
@@ -926,7 +941,7 @@ def add_adapters(y, x, a, b, ids, scales=None, out=None, workspace=None, stream=
         raise ValueError("workspace must be contiguous")
     s = _raw_stream(at) if stream is None and _raw_stream is not None else _stream(stream, at)
     st = _on(at, lib.sp24_add_adapters, y.data_ptr(), ldy, x.data_ptr(), ldx, T, K, N, a.data_ptr(), stride_a, b.data_ptr(),
-             stride_b, r, count, ids.data_ptr(), None if scales is None else scales.data_ptr(), out.data_ptr(), ldo,
+             stride_b, r, count, ids.data_ptr(), sp, out.data_ptr(), ldo,
              None if workspace is None else workspace.data_ptr(), size, s)
     if st:
         _check(st, "sp24_add_adapters")

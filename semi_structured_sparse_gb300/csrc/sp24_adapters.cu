@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCluster = 8;        // CTAs that share a few rows' work
+constexpr int kMostCluster = 8;    // CTAs that share a few rows' work, at most
 constexpr int kMostRank = 128;
 constexpr int kFewRows = 512;      // rows of a call that are sorted by adapter
 
@@ -54,7 +54,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
 }
 
 // Few rows.  An item is one adapter and up to R = 8 NT rows that have it, wherever they
-// are in the batch; a cluster of 8 CTAs works on it.  Their 64 warps cut K for
+// are in the batch; a cluster of 2 to 8 CTAs works on it.  Their warps cut K for
 // A x, a warp's sums meet in shared memory and the CTAs' in all CTAs of the cluster
 // (distributed shared memory, always added in the same order), and the warps
 // cut N for B (A x).
@@ -70,11 +70,12 @@ struct FewCfg {
   static constexpr int R = 8 * NT, RP = 16 * MT;         // rows and rank, padded
   static constexpr int KS = MT < 2 ? 1 : MT / 2;         // 32s of the rank
   static constexpr int LOADS = 2 * MT + NT;              // 16-byte pieces per lane and 32 of K
-  static constexpr int STAGES = MT <= 2 ? 4 : 2;
+  static constexpr int STAGES = LOADS <= 5 ? 4 : LOADS <= 10 ? 3 : 2;
+  static constexpr int AHEAD = KS == 1 ? 3 : KS == 2 ? 2 : 1;  // 32s of N whose operands are under way
   static constexpr int HLD = 32 * KS + 8;                // row of A x, in bf16
   static constexpr int RING = kWarps * STAGES * LOADS * 512, PART = kWarps * R * RP * 4;
   static constexpr int FIRST = RING > PART ? RING : PART;  // the ring, and then the warps' sums
-  static constexpr int RECV = kCluster * R * RP * 4, H = 2 * R * HLD * 2;
+  static constexpr int RECV = kMostCluster * R * RP * 4, H = 2 * R * HLD * 2;
   static constexpr int SMEM = FIRST + RECV + H;
 };
 template <int MT, int NT>
@@ -83,14 +84,13 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
   constexpr int R = C::R, RP = C::RP, KS = C::KS, ST = C::STAGES, MH = (NT + 1) / 2;  // 16-row tiles of tokens
   extern __shared__ __align__(128) uint8_t smem[];
   float* const part = reinterpret_cast<float*>(smem);                       // [kWarps][R][RP]
-  float* const recv = reinterpret_cast<float*>(smem + C::FIRST);            // [kCluster][R][RP]
+  float* const recv = reinterpret_cast<float*>(smem + C::FIRST);            // [CTAs][R][RP]
   uint8_t* const h_s = smem + C::FIRST + C::RECV;                           // [2][R][HLD] bf16
   __shared__ __align__(16) int s_id[kFewRows];
   __shared__ int s_count[kFewRows / 32], s_item[2], s_row[R];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const uint32_t rank = cluster_rank();
-  const int item = blockIdx.x / kCluster, gw = rank * kWarps + warp;
-  constexpr int GW = kCluster * kWarps;
+  const uint32_t rank = cluster_rank(), ctas = cluster_nrank();
+  const int item = blockIdx.x / ctas, gw = rank * kWarps + warp, GW = ctas * kWarps;
   pdl_wait();
 
   // ---- this cluster's item: rows are numbered within their adapter; every R-th begins one
@@ -115,12 +115,12 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
   if (tid < R) s_row[tid] = -1;
   if (tid == 0) s_item[0] = -1;
   __syncthreads();
-  const int scan = min(p.T, kFewRows);
-  for (int x = 0; x < scan; x += 4) {
-    const int4 v = *reinterpret_cast<const int4*>(s_id + x);
 #pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-      const int me = tid + i * kThreads;
+  for (int i = 0; i < MINE; ++i) {  // how many rows before this one have its adapter
+    const int me = tid + i * kThreads, end = i * kThreads + (warp + 1) * 32;  // (of the warp)
+    if (end - 32 >= p.T) break;
+    for (int x = 0; x < end; x += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(s_id + x);
       nth[i] += (v.x == id[i] && x < me) + (v.y == id[i] && x + 1 < me) + (v.z == id[i] && x + 2 < me) +
                 (v.w == id[i] && x + 3 < me);
     }
@@ -236,26 +236,30 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
   int row[2 * MH];
 #pragma unroll
   for (int i = 0; i < 2 * MH; ++i) row[i] = i < NT ? s_row[8 * i + g] : -1;
-  uint4 bv[KS][4], yv[2 * MH];
-  auto load = [&](int block) {
+  uint4 bv[C::AHEAD][KS][4], yv[C::AHEAD][2 * MH];
+  const __nv_bfloat16* const b_lane = b + (8 * (g >> 1) + (g & 1)) * p.r + 8 * t;
+  const __nv_bfloat16* y_row[NT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = 32 * block + 8 * (g >> 1) + 2 * j + (g & 1);
+  for (int i = 0; i < NT; ++i) y_row[i] = p.y + max(row[i], 0) * p.ldy + 8 * t;
+  auto load = [&](int block, uint4 (&bv)[KS][4], uint4 (&yv)[2 * MH]) {
+    const __nv_bfloat16* from = b_lane + int64_t(32 * block) * p.r;
+    const int left = block < n1 ? p.N - 32 * block : 0;  // columns from here on
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         bv[s][j] = make_uint4(0, 0, 0, 0);
-        if (n < p.N && 32 * s + 8 * t < p.r)
-          bv[s][j] = *reinterpret_cast<const uint4*>(b + int64_t(n) * p.r + 32 * s + 8 * t);
+        if (8 * (g >> 1) + 2 * j + (g & 1) < left && 32 * s + 8 * t < p.r)
+          bv[s][j] = *reinterpret_cast<const uint4*>(from + 2 * j * p.r + 32 * s);
       }
-    }
 #pragma unroll
     for (int i = 0; i < 2 * MH; ++i) {
       yv[i] = make_uint4(0, 0, 0, 0);
-      if (row[i] >= 0 && 32 * block + 8 * t < p.N)
-        yv[i] = *reinterpret_cast<const uint4*>(p.y + row[i] * p.ldy + 32 * block + 8 * t);
+      if (i < NT && row[i] >= 0 && 8 * t < left) yv[i] = *reinterpret_cast<const uint4*>(y_row[i < NT ? i : 0] + 32 * block);
     }
   };
-  if (n0 < n1) load(n0);
+#pragma unroll
+  for (int a = 0; a < C::AHEAD; ++a) load(n0 + a, bv[a], yv[a]);
 
   // ---- the warps' sums, then the CTAs'
   __syncthreads();  // the ring has been read
@@ -273,7 +277,8 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += part[w * (R * RP) + e];
 #pragma unroll
-    for (uint32_t c = 0; c < kCluster; ++c) st_cluster(cluster_addr(recv + rank * (R * RP) + e, c), sum);
+    for (uint32_t c = 0; c < kMostCluster; ++c)
+      if (c < ctas) st_cluster(cluster_addr(recv + rank * (R * RP) + e, c), sum);
   }
   cluster_sync();
   const float scale = p.scales ? p.scales[adapter] : 1.0f;
@@ -285,7 +290,8 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
     float sum = 0.0f;
     if (j < RP) {
 #pragma unroll
-      for (int c = 0; c < kCluster; ++c) sum += recv[c * (R * RP) + i * RP + j];
+      for (int c = 0; c < kMostCluster; ++c)
+        if (c < static_cast<int>(ctas)) sum += recv[c * (R * RP) + i * RP + j];
       sum *= scale;
     }
     const __nv_bfloat16 hi = __float2bfloat16(sum);
@@ -296,44 +302,49 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
   __syncthreads();
 
   // ---- B (A x), this warp's columns, 32 at a time
-  for (int block = n0; block < n1; ++block) {
-    float o[MH][4][4];
+  for (int block0 = n0; block0 < n1; block0 += C::AHEAD) {
 #pragma unroll
-    for (int m = 0; m < MH; ++m)
+    for (int a = 0; a < C::AHEAD; ++a) {
+      const int block = block0 + a;
+      if (block >= n1) break;
+      float o[MH][4][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[m][j][0] = o[m][j][1] = o[m][j][2] = o[m][j][3] = 0.0f;
+      for (int m = 0; m < MH; ++m)
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
+        for (int j = 0; j < 4; ++j) o[m][j][0] = o[m][j][1] = o[m][j][2] = o[m][j][3] = 0.0f;
 #pragma unroll
-      for (int m = 0; m < MH; ++m) {
+      for (int s = 0; s < KS; ++s) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const __nv_bfloat16* h = (x ? h_lo : h_hi) + 32 * s + 8 * t;
-          const uint4 lo = *reinterpret_cast<const uint4*>(h + (16 * m + g) * C::HLD);
-          uint4 hi = make_uint4(0, 0, 0, 0);
-          if (2 * m + 1 < NT) hi = *reinterpret_cast<const uint4*>(h + (16 * m + 8 + g) * C::HLD);
+        for (int m = 0; m < MH; ++m) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mma16816(o[m][j], lo.x, hi.x, lo.y, hi.y, bv[s][j].x, bv[s][j].y);
-            mma16816(o[m][j], lo.z, hi.z, lo.w, hi.w, bv[s][j].z, bv[s][j].w);
+          for (int x = 0; x < 2; ++x) {
+            const __nv_bfloat16* h = (x ? h_lo : h_hi) + 32 * s + 8 * t;
+            const uint4 lo = *reinterpret_cast<const uint4*>(h + (16 * m + g) * C::HLD);
+            uint4 hi = make_uint4(0, 0, 0, 0);
+            if (2 * m + 1 < NT) hi = *reinterpret_cast<const uint4*>(h + (16 * m + 8 + g) * C::HLD);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma16816(o[m][j], lo.x, hi.x, lo.y, hi.y, bv[a][s][j].x, bv[a][s][j].y);
+              mma16816(o[m][j], lo.z, hi.z, lo.w, hi.w, bv[a][s][j].z, bv[a][s][j].w);
+            }
           }
         }
       }
-    }
-    uint4 y[2 * MH];
+      uint4 y[2 * MH];
 #pragma unroll
-    for (int i = 0; i < 2 * MH; ++i) y[i] = yv[i];
-    if (block + 1 < n1) load(block + 1);
+      for (int i = 0; i < 2 * MH; ++i) y[i] = yv[a][i];
+      load(block + C::AHEAD, bv[a], yv[a]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      if (row[i] < 0 || 32 * block + 8 * t >= p.N) continue;
-      const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
-      uint32_t r[4];
+      for (int i = 0; i < NT; ++i) {
+        if (row[i] < 0 || 32 * block + 8 * t >= p.N) continue;
+        const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+        uint32_t r[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        r[j] = bf16x2_rn(__uint_as_float(w[j] << 16) + o[i / 2][j][2 * (i & 1)],
-                         __uint_as_float(w[j] & 0xFFFF0000u) + o[i / 2][j][2 * (i & 1) + 1]);
-      *reinterpret_cast<uint4*>(p.out + row[i] * p.ldo + 32 * block + 8 * t) = make_uint4(r[0], r[1], r[2], r[3]);
+        for (int j = 0; j < 4; ++j)
+          r[j] = bf16x2_rn(__uint_as_float(w[j] << 16) + o[i / 2][j][2 * (i & 1)],
+                           __uint_as_float(w[j] & 0xFFFF0000u) + o[i / 2][j][2 * (i & 1) + 1]);
+        *reinterpret_cast<uint4*>(p.out + row[i] * p.ldo + 32 * block + 8 * t) = make_uint4(r[0], r[1], r[2], r[3]);
+      }
     }
   }
   pdl_trigger();
@@ -354,7 +365,11 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
 constexpr int kTile = 128;          // rows
 constexpr int kCols = 64;           // of K, or N, per unit
 constexpr int kRowTile = kTile * kCols * 2;
-constexpr int kIssue = 2;           // warps that issue MMAs: a commit holds its thread back until they are done
+// Warps that issue MMAs, every other unit each: a commit holds its thread back until they are done.  Each has stages of
+// its own in every ring that it reads (as the two groups of warps that take the results have).  A wait tells a phase
+// from the one before it only, so whoever waits on a stage has to see all its phases; with stages that change hands, a
+// warp that is ahead would take a use that it has not waited for, and is not there yet, for its own.
+constexpr int kIssue = 2;
 constexpr int kLeastK = 8, kLeastN = 4;  // units per CTA
 
 struct Deal {
@@ -440,7 +455,8 @@ __device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned in
 // ------------------------------------------------------------------ A x
 template <int KB>  // 64s of the rank
 struct DownCfg {
-  static constexpr int ROWS = KB == 1 ? 8 : 6, ADS = KB == 1 ? 11 : 7;  // stages
+  static constexpr int ROWS = KB == 1 ? 8 : 6, ADS = KB == 1 ? 10 : 6;  // stages
+  static constexpr int R = ROWS / kIssue, A = ADS / kIssue;              // of each issuing warp
   static constexpr int AD_TILE = KB * 64 * 128;
   static constexpr int D1 = 64 * KB;                  // columns of an adapter's sums
   static constexpr int PASS = 512 / (kIssue * D1);    // adapters per pass over K
@@ -556,32 +572,33 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
   } else if (warp == 5) {
     // ---------------------------------------------------------------- copies
-    int row = 0, ad = 0;
+    int rows[kIssue] = {}, ads[kIssue] = {};  // so far, of each issuing warp's
     for (int i = 0; ok; ++i) {
       ok = wait_segment(i);
       const Segment& s = s_seg[i & 1];
       if (!ok || s.count == 0) break;
       if (lane == 0) {
-        for (int w0 = 0; w0 < s.adapters && ok; w0 += C::PASS) {
-          for (int k = 0; k < s.count && ok; ++k, ++row) {
-            const int x = (s.first + k) * kCols, at = row % ROWS;
-            if (row >= ROWS) ok = mbar_wait(&row_empty[at], (row / ROWS - 1) & 1);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&row_full[at], kRowTile);
-            tma_load_2d(row_s + at * kRowTile, &xmap, &row_full[at], x, s.tile * kTile);
-            for (int w = w0; w < min(s.adapters, w0 + C::PASS) && ok; ++w, ++ad) {
-              const int to = ad % ADS;
-              if (ad >= ADS) ok = mbar_wait(&ad_empty[to], (ad / ADS - 1) & 1);
-              if (!ok) break;
-              mbar_arrive_expect_tx(&ad_full[to], q.rp * 128);
-              tma_load_3d(ad_s + to * C::AD_TILE, &amap, &ad_full[to], x, 0, s.adapter[w]);
-            }
-            if (!ok) {
-              ++row;  // this one is on its way
-              break;
-            }
+        auto load = [&](int w0, int k, int x, int& row, int& ad) {
+          const int col = (s.first + k) * kCols, at = x * C::R + row % C::R;
+          if (row >= C::R) ok = mbar_wait(&row_empty[at], (row / C::R - 1) & 1);
+          if (!ok) return;
+          mbar_arrive_expect_tx(&row_full[at], kRowTile);
+          tma_load_2d(row_s + at * kRowTile, &xmap, &row_full[at], col, s.tile * kTile);
+          ++row;
+          for (int w = w0; w < min(s.adapters, w0 + C::PASS); ++w, ++ad) {
+            const int to = x * C::A + ad % C::A;
+            if (ad >= C::A) ok = mbar_wait(&ad_empty[to], (ad / C::A - 1) & 1);
+            if (!ok) return;
+            mbar_arrive_expect_tx(&ad_full[to], q.rp * 128);
+            tma_load_3d(ad_s + to * C::AD_TILE, &amap, &ad_full[to], col, 0, s.adapter[w]);
           }
-        }
+        };
+        for (int w0 = 0; w0 < s.adapters && ok; w0 += C::PASS)
+          for (int k = 0; k < s.count && ok; k += kIssue) {
+#pragma unroll
+            for (int x = 0; x < kIssue; ++x)
+              if (k + x < s.count && ok) load(w0, k + x, x, rows[x], ads[x]);
+          }
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       done_with(i);
@@ -589,8 +606,11 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     if (lane == 0) {
       if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
       // Copies in flight have to land before this CTA's shared memory goes.
-      for (int i = max(0, row - ROWS); i < row; ++i) mbar_wait(&row_full[i % ROWS], (i / ROWS) & 1);
-      for (int i = max(0, ad - ADS); i < ad; ++i) mbar_wait(&ad_full[i % ADS], (i / ADS) & 1);
+#pragma unroll
+      for (int x = 0; x < kIssue; ++x) {
+        for (int i = max(0, rows[x] - C::R); i < rows[x]; ++i) mbar_wait(&row_full[x * C::R + i % C::R], (i / C::R) & 1);
+        for (int i = max(0, ads[x] - C::A); i < ads[x]; ++i) mbar_wait(&ad_full[x * C::A + i % C::A], (i / C::A) & 1);
+      }
     }
     __syncwarp();
   } else {
@@ -599,7 +619,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     const uint32_t id = idesc_bf16(kTile, q.rp);
     const uint64_t row_d = smem_desc(smem_u32(row_s), 16, 1024, SWZ_128B);
     const uint64_t ad_d = smem_desc(smem_u32(ad_s), 16, 1024, SWZ_128B);
-    int row0 = 0, ad0 = 0, passes = 0;
+    int row = 0, ad = 0, passes = 0;  // so far, of this warp's
     for (int i = 0; ok; ++i) {
       ok = wait_segment(i);
       const Segment& s = s_seg[i & 1];
@@ -610,12 +630,12 @@ __global__ void __launch_bounds__(kDownThreads, 1)
           const int some = min(adapters - w0, C::PASS);
           if (passes > 0) ok = mbar_wait(d1_empty, (passes - 1) & 1);
           tc_fence_after();
-          for (int k = x; k < count && ok; k += kIssue) {
-            const int row = row0 + k, at = row % ROWS;
-            ok = mbar_wait(&row_full[at], (row / ROWS) & 1);
-            for (int w = 0; w < some && ok; ++w) {
-              const int ad = ad0 + k * some + w, from = ad % ADS;
-              ok = mbar_wait(&ad_full[from], (ad / ADS) & 1);
+          for (int k = x; k < count && ok; k += kIssue, ++row) {
+            const int at = x * C::R + row % C::R;
+            ok = mbar_wait(&row_full[at], (row / C::R) & 1);
+            for (int w = 0; w < some && ok; ++w, ++ad) {
+              const int from = x * C::A + ad % C::A;
+              ok = mbar_wait(&ad_full[from], (ad / C::A) & 1);
               if (!ok) break;
               tc_fence_after();
               const uint64_t a = row_d + at * (kRowTile >> 4), b = ad_d + from * (C::AD_TILE >> 4);
@@ -626,8 +646,6 @@ __global__ void __launch_bounds__(kDownThreads, 1)
               if (w + 1 == some) mma_commit(&row_empty[at]);
             }
           }
-          row0 += count;
-          ad0 += count * some;
           if (ok) mma_commit(d1_full);
         }
       }
@@ -656,11 +674,13 @@ struct UpCfg {
   static constexpr int AD_TILE = KB * 64 * 128;
   static constexpr int H = 2 * KB * kRowTile;  // A x of a tile, in two parts
   static constexpr int D2S = 512 / kCols;
+  static constexpr int A = ADS / kIssue, D2 = D2S / kIssue;  // of each issuing warp, and group of those for results
+  static_assert(ROWS % kIssue == 0, "a row tile's stage is always the same warp's");
   static constexpr int BARS = 3 * ROWS + 2 * ADS + 2 * HS + 2 * D2S + 4 + kIssue;
   static constexpr int SMEM = 1024 + ROWS * kRowTile + ADS * AD_TILE + HS * H + BARS * 8;
   static_assert(SMEM + 2 * sizeof(Segment) + 64 <= 227 * 1024, "shared memory");
 };
-constexpr int kGroups = 2, kSumWarps = 4 * kGroups;  // groups of warps that take every other unit's results
+constexpr int kGroups = kIssue, kSumWarps = 4 * kGroups;  // groups of warps that take every other unit's results
 constexpr int kHWarps = 8;
 constexpr int kUpThreads = (kSumWarps + kHWarps + 3 + kIssue) * 32;  // ..., segments, copies, stores, MMAs
 
@@ -727,7 +747,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     // --------------------------------------------------------------- results
     const int r = tid & (kTile - 1), group = tid / kTile;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int unit0 = 0, row0 = 0;  // of the segment
+    int unit = 0, row0 = 0;  // products of this group so far, and units of all before this segment
     for (int i = 0; ok; ++i) {
       ok = wait_segment(i);
       const Segment& s = s_seg[i & 1];
@@ -739,11 +759,11 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         ok = mbar_wait(&row_full[stage], (row / ROWS) & 1);
         if (!ok) break;
         uint8_t* const y = row_s + stage * kRowTile + r * 128;
-        for (int w = 0; w < adapters; ++w) {
-          const int unit = unit0 + n * adapters + w, at = unit % D2S;
-          ok = mbar_wait(&d2_full[at], (unit / D2S) & 1);
+        for (int w = 0; w < adapters; ++w, ++unit) {
+          const int at = group * C::D2 + unit % C::D2;
+          ok = mbar_wait(&d2_full[at], (unit / C::D2) & 1);
           if (!ok) break;
-          if (r == 0) mbar_arrive(&ad_empty[unit % ADS]);  // the product has been formed
+          if (r == 0) mbar_arrive(&ad_empty[group * C::A + unit % C::A]);  // the product has been formed
           tc_fence_after();
           if (__any_sync(0xFFFFFFFFu, which == w)) {
 #pragma unroll
@@ -779,7 +799,6 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&out_full[stage]);
       }
-      unit0 += count * adapters;
       row0 += count;
     }
     if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
@@ -871,29 +890,30 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     if (!ok && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
   } else if (warp == COPY) {
     // ---------------------------------------------------------------- copies
-    int row = 0, ad = 0;
+    int row = 0, ads[kIssue] = {};  // so far: tiles of y, and of B for each issuing warp
     for (int i = 0; ok; ++i) {
       ok = wait_segment(i);
       const Segment& s = s_seg[i & 1];
       if (!ok || s.count == 0) break;
       if (lane == 0) {
         for (int n = 0; n < s.count && ok; ++n) {
-          const int x = (s.first + n) * kCols, at = row % ROWS;
+          const int col = (s.first + n) * kCols, at = row % ROWS, x = row % kIssue;
           if (row >= ROWS) ok = mbar_wait(&row_empty[at], (row / ROWS - 1) & 1);
           if (!ok) break;
           mbar_arrive_expect_tx(&row_full[at], kRowTile);
-          tma_load_2d(row_s + at * kRowTile, &ymap, &row_full[at], x, s.tile * kTile);
+          tma_load_2d(row_s + at * kRowTile, &ymap, &row_full[at], col, s.tile * kTile);
           ++row;
-          for (int w = 0; w < s.adapters && ok; ++w) {
-            const int to = ad % ADS;
-            if (ad >= ADS) ok = mbar_wait(&ad_empty[to], (ad / ADS - 1) & 1);
+          int ad = x ? ads[1] : ads[0];
+          for (int w = 0; w < s.adapters; ++w, ++ad) {
+            const int to = x * C::A + ad % C::A;
+            if (ad >= C::A) ok = mbar_wait(&ad_empty[to], (ad / C::A - 1) & 1);
             if (!ok) break;
             mbar_arrive_expect_tx(&ad_full[to], KB * 64 * 128);
 #pragma unroll
             for (int k = 0; k < KB; ++k)
-              tma_load_3d(ad_s + to * C::AD_TILE + k * 64 * 128, &bmap, &ad_full[to], 64 * k, x, s.adapter[w]);
-            ++ad;
+              tma_load_3d(ad_s + to * C::AD_TILE + k * 64 * 128, &bmap, &ad_full[to], 64 * k, col, s.adapter[w]);
           }
+          (x ? ads[1] : ads[0]) = ad;
         }
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -903,7 +923,9 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_PRODUCER);
       // Copies in flight have to land before this CTA's shared memory goes.
       for (int i = max(0, row - ROWS); i < row; ++i) mbar_wait(&row_full[i % ROWS], (i / ROWS) & 1);
-      for (int i = max(0, ad - ADS); i < ad; ++i) mbar_wait(&ad_full[i % ADS], (i / ADS) & 1);
+#pragma unroll
+      for (int x = 0; x < kIssue; ++x)
+        for (int i = max(0, ads[x] - C::A); i < ads[x]; ++i) mbar_wait(&ad_full[x * C::A + i % C::A], (i / C::A) & 1);
     }
     __syncwarp();
   } else if (warp == STORE) {
@@ -941,34 +963,36 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     const uint32_t id = idesc_bf16(kTile, kCols);
     const uint64_t ad_d = smem_desc(smem_u32(ad_s), 16, 1024, SWZ_128B);
     const uint64_t h_d = smem_desc(smem_u32(h_s), 16, 1024, SWZ_128B);
-    int unit = 0, tiles = 0;  // so far, tiles: with adapters
+    int unit = 0, row0 = 0, tiles = 0;  // products of this warp so far, units before this segment, tiles with adapters
     for (int i = 0; ok; ++i) {
       ok = wait_segment(i);
       const Segment& s = s_seg[i & 1];
       if (!ok || s.count == 0) break;
-      const int units = s.count * s.adapters;
+      const int count = s.count, adapters = s.adapters;
       done_with(i);
-      if (units == 0) continue;
-      if (lane == 0) {
+      if (lane == 0 && adapters > 0) {
         ok = mbar_wait(&h_full[tiles % HS], (tiles / HS) & 1);
         const uint64_t h = h_d + tiles % HS * (C::H >> 4);
-        for (int k = (unit & 1) == x ? 0 : 1; k < units && ok; k += kIssue) {
-          const int u = unit + k, from = u % ADS, at = u % D2S;
-          ok = mbar_wait(&ad_full[from], (u / ADS) & 1) && (u < D2S || mbar_wait(&d2_empty[at], (u / D2S - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t b = ad_d + from * (C::AD_TILE >> 4);
-          for (int part = 0; part < 2; ++part)
-            for (int e = 0; e < q.rp / 16; ++e)
-              mma_bf16(tmem + at * kCols, h + part * (KB * kRowTile >> 4) + (e / 4) * (kRowTile >> 4) + 2 * (e & 3),
-                       b + (e / 4) * (64 * 128 >> 4) + 2 * (e & 3), id, part > 0 || e > 0);
-          mma_commit(&d2_full[at]);
+        for (int n = (row0 + x) % kIssue; n < count && ok; n += kIssue) {
+          for (int w = 0; w < adapters && ok; ++w, ++unit) {
+            const int from = x * C::A + unit % C::A, at = x * C::D2 + unit % C::D2;
+            ok = mbar_wait(&ad_full[from], (unit / C::A) & 1) &&
+                 (unit < C::D2 || mbar_wait(&d2_empty[at], (unit / C::D2 - 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b = ad_d + from * (C::AD_TILE >> 4);
+            for (int part = 0; part < 2; ++part)
+              for (int e = 0; e < q.rp / 16; ++e)
+                mma_bf16(tmem + at * kCols, h + part * (KB * kRowTile >> 4) + (e / 4) * (kRowTile >> 4) + 2 * (e & 3),
+                         b + (e / 4) * (64 * 128 >> 4) + 2 * (e & 3), id, part > 0 || e > 0);
+            mma_commit(&d2_full[at]);
+          }
         }
         if (ok) mma_commit(&h_empty[tiles % HS]);
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      unit += units;
-      ++tiles;
+      row0 += count;
+      if (adapters > 0) ++tiles;
     }
     if (lane == 0) {
       if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_MMA);
@@ -1023,10 +1047,48 @@ sp24_status launch_many(const AdapterParams& p, float* part, const DeviceInfo& d
 template <int MT, int NT>
 cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream_t s) {
   using C = FewCfg<MT, NT>;
+  constexpr auto kern = add_adapters_few_kernel<MT, NT>;
   // Each adapter's last item may be partly filled; rows without an adapter count as one more.
-  const int items = std::min<int64_t>(p.T, p.T / C::R + std::min<int64_t>(p.T, int64_t(p.count) + 1));
-  return launch_pdl_clusters_smem<add_adapters_few_kernel<MT, NT>>(dev, kCluster, dim3(items * kCluster), dim3(kThreads),
-                                                                   C::SMEM, s, p);
+  const int64_t adapters = std::min<int64_t>(p.T, p.count), items = std::min<int64_t>(p.T, p.T / C::R + adapters + 1);
+  // As many CTAs per item as run at once, for as many items as rows spread evenly over the adapters come to.  (200 rows
+  // of 20 adapters, rank 64, K 14336, 1 CTA per SM: 14 clusters of 8 fit, 24 of 6; 26 us with 8 and 17 with 6.)
+  const int64_t likely = std::min(items, adapters * ((p.T / adapters + C::R - 1) / C::R) + 1);
+  static std::atomic<int> most[64][kMostCluster + 1];  // clusters of each size that fit at once, + 1
+  unsigned cluster = kMostCluster;
+  for (; cluster > 2; --cluster) {
+    std::atomic<int>& known = most[dev.ordinal & 63][cluster];
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = cluster;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(cluster);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = C::SMEM;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int fit = 0;
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        fit = 0;
+      }
+      n = fit + 1;
+      known.store(n, std::memory_order_relaxed);
+    }
+    if (likely <= n - 1) break;
+  }
+  return launch_pdl_clusters_smem<kern>(dev, cluster, dim3(static_cast<unsigned>(items * cluster)), dim3(kThreads), C::SMEM, s,
+                                        p);
+}
+// Rows per item: enough that an adapter is rarely read more than once.
+template <int MT>
+cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream_t s) {
+  const int64_t each = p.T / std::min<int64_t>(p.T, p.count);
+  if (MT <= 4 && each > 12) return launch_few<MT, MT <= 4 ? 4 : 2>(p, dev, s);
+  return each > 4 ? launch_few<MT, 2>(p, dev, s) : launch_few<MT, 1>(p, dev, s);
 }
 
 }  // namespace
@@ -1086,12 +1148,12 @@ extern "C" sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void*
     return r <= 64 ? launch_many<1>(p, static_cast<float*>(workspace), *dev, s)
                    : launch_many<2>(p, static_cast<float*>(workspace), *dev, s);
   if (r <= 16)
-    e = launch_few<1, 1>(p, *dev, s);
+    e = launch_few<1>(p, *dev, s);
   else if (r <= 32)
-    e = launch_few<2, 1>(p, *dev, s);
+    e = launch_few<2>(p, *dev, s);
   else if (r <= 64)
-    e = launch_few<4, 1>(p, *dev, s);
+    e = launch_few<4>(p, *dev, s);
   else
-    e = launch_few<8, 1>(p, *dev, s);
+    e = launch_few<8>(p, *dev, s);
   return e == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
 }

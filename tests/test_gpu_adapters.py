@@ -180,3 +180,37 @@ def test_no_rows(sp24):
     got = sp24.add_adapters(y.cuda()[:0], x.cuda()[:0], a.cuda(), b.cuda(), torch.zeros(0, dtype=torch.int32, device="cuda"))
     sp24.last_device_error()
     assert got.shape == (0, 72)
+
+
+@pytest.mark.parametrize("T,K,N,r,count", [(2300, 1088, 1600, 64, 9), (4000, 512, 2112, 24, 5), (1700, 2112, 1024, 128, 7)])
+def test_tiles_of_several_adapters_again_and_again(sp24, T, K, N, r, count):
+    """Runs that end inside a tile, so that its rows have two, three and more adapters, beside tiles of one and of none:
+    the same bits every time."""
+    y, x, a, b, scales = inputs(T, K, N, r, count, seed=r)
+    g = torch.Generator().manual_seed(r)
+    ids = torch.cat([torch.randint(-1, count, (1,), generator=g).repeat(n) for n in (3, 500, 37, 41, 600, 50, 1, 2, 60, 300,
+                                                                                     90, 45, 30, 25, 700, 2000)])
+    ids = ids[:T].to(torch.int32)
+    args = [t.cuda() for t in (y, x, a, b, ids, scales)]
+    first = sp24.add_adapters(*args)
+    out, size = reference(y, x, a, b, ids, scales)
+    assert_adapted(first, out, size, "several adapters")
+    workspace = torch.empty(sp24.add_adapters_workspace_size(T, K, r), dtype=torch.uint8, device="cuda")
+    for _ in range(30):
+        again = sp24.add_adapters(*args, workspace=workspace)
+        assert torch.equal(first, again)
+    sp24.last_device_error()
+
+
+def test_workspace(sp24):
+    y, x, a, b, scales = (t.cuda() for t in inputs(600, 256, 136, 16, 2, seed=1))
+    ids = torch.zeros(600, dtype=torch.int32, device="cuda")
+    need = sp24.add_adapters_workspace_size(600, 256, 16)
+    assert need > 0 and sp24.add_adapters_workspace_size(512, 256, 16) == 0
+    short = torch.empty(need - 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(sp24.Sp24Error, match="WORKSPACE"):
+        sp24.add_adapters(y, x, a, b, ids, workspace=short)
+    with pytest.raises(ValueError, match="unit stride"):
+        sp24.add_adapters(y, x, a, b, ids, workspace=torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2])
+    with pytest.raises(ValueError, match="alignment|ALIGNMENT"):
+        sp24.add_adapters(y, x, a, b, ids, workspace=torch.empty(need + 16, dtype=torch.uint8, device="cuda")[1:])

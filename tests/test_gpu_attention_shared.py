@@ -7,7 +7,18 @@ from attention_util import Setup, assert_attention, attend, sees
 pytestmark = pytest.mark.gpu
 
 
-def batch(sp24, cu, shared, lens, hkv, d, page, e4m3, token_major, window, sinks, seed):
+def widened(table, page, hkv, d, e4m3, seed=1):
+    """The table with more columns, of pages that are not to be read: a call whose tables could hold so much that
+    sharing may save more than 32 MB (fewer, and the sequences are attended one by one)."""
+    B = table.shape[0]
+    tokens = (32 << 20) // (max(1, B - 1) * hkv * 2 * d * (1 if e4m3 else 2)) + 1
+    width = max(table.shape[1], -(-tokens // page))
+    out = torch.full((B, width), 1 << 28, dtype=torch.int32)
+    out[:, :table.shape[1]] = table
+    return out
+
+
+def batch(sp24, cu, shared, lens, hkv, d, page, e4m3, token_major, window, sinks, seed, one_by_one=False):
     """A cache in which the groups' shared tokens are in the pages of each group's first sequence: whole pages in all
     the group's tables, the page that they end in as a copy.  All that is not to be read is NaN.  Returns the setup and
     each sequence's keys and values in 64 bits."""
@@ -15,7 +26,7 @@ def batch(sp24, cu, shared, lens, hkv, d, page, e4m3, token_major, window, sinks
     by_itself = [True] * len(lens)
     for g, n in enumerate(shared):
         for b in range(cu[g], cu[g + 1]):
-            by_itself[b] = lens[b] < n or (window > 0 and lens[b] > window)
+            by_itself[b] = one_by_one or lens[b] < n or (window > 0 and lens[b] > window)
             lead = cu[g]
             m = min(n, lens[b])
             full = min(m, lens[lead]) // page
@@ -41,14 +52,15 @@ def batch(sp24, cu, shared, lens, hkv, d, page, e4m3, token_major, window, sinks
 
 
 def run(sp24, cu, shared, lens, hq, hkv, d, page, e4m3=False, token_major=False, window=0, sinks=0, seed=0, q=None,
-        scale=None, **kw):
-    s, tokens = batch(sp24, cu, shared, lens, hkv, d, page, e4m3, token_major, window, sinks, seed)
+        scale=None, wide=True, **kw):
+    s, tokens = batch(sp24, cu, shared, lens, hkv, d, page, e4m3, token_major, window, sinks, seed, not wide)
+    table = widened(s.table, page, hkv, d, e4m3) if wide else s.table
     cache = s.upload()
     g = torch.Generator().manual_seed(seed + 1)
     if q is None:
         q = (2 * torch.randn(len(lens), hq, d, generator=g)).to(torch.bfloat16)
     i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
-    y = sp24.attention_decode_shared(q.cuda(), cache, s.table.cuda(), i32(lens), i32(cu), i32(shared), scale=scale,
+    y = sp24.attention_decode_shared(q.cuda(), cache, table.cuda(), i32(lens), i32(cu), i32(shared), scale=scale,
                                      window=window, sinks=sinks, **kw)
     sp24.last_device_error()
     want, size = torch.zeros(len(lens), hq, d, dtype=torch.float64), torch.zeros(len(lens), hq, d, dtype=torch.float64)
@@ -93,6 +105,13 @@ def test_shared(sp24, case):
     run(sp24, cu, shared, lens, hq, hkv, d, page, e4m3, token_major, window, sinks, seed=len(lens) + d)
 
 
+@pytest.mark.parametrize("case", CASES[1:9:2] + CASES[14:16], ids=str)
+def test_little_to_share(sp24, case):
+    """The same sizes where the tables could not hold much: one by one, through each sequence's own pages."""
+    cu, shared, lens, hq, hkv, d, page, e4m3, token_major, window, sinks = case
+    run(sp24, cu, shared, lens, hq, hkv, d, page, e4m3, token_major, window, sinks, seed=len(lens) + d, wide=False)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 def test_every_visible_key_counts_once(sp24, d, e4m3):
@@ -106,7 +125,8 @@ def test_every_visible_key_counts_once(sp24, d, e4m3):
             s.store[x][int(s.table[b, 37]), :, :8] = s.store[x][int(s.table[0, 37]), :, :8]
     cache = s.upload()
     i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
-    y = sp24.attention_decode_shared(torch.zeros(9, 4, d, device="cuda").bfloat16(), cache, s.table.cuda(), i32(*lens),
+    table = widened(s.table, 16, 2, d, e4m3).cuda()
+    y = sp24.attention_decode_shared(torch.zeros(9, 4, d, device="cuda").bfloat16(), cache, table, i32(*lens),
                                      i32(0, 9), i32(600))
     sp24.last_device_error()
     for b in range(9):
@@ -120,8 +140,6 @@ def test_every_visible_key_counts_once(sp24, d, e4m3):
 def test_agrees_with_decode_and_is_the_same_every_time(sp24):
     """The same call again, with the same workspace, after calls of other shapes: the same bits."""
     cu, shared, lens = [1, 30], [3000], [40] + [3001 + 17 * i for i in range(29)]
-    s, _ = batch(sp24, cu, shared, lens, 2, 128, 64, False, False, 0, 0, 7)
-    # (not poisoned for the comparison: every sequence reads its own copies there)
     s = Setup(sp24, lens, 2, 128, 64, False, False, 7)
     for b in range(1, 30):
         s.table[b, :46] = s.table[1, :46]
@@ -133,7 +151,7 @@ def test_agrees_with_decode_and_is_the_same_every_time(sp24):
     size = max(sp24.attention_decode_shared_workspace_size(cache, 8, 30, 1),
                sp24.attention_decode_shared_workspace_size(cache, 8, 30, 3))
     ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
-    args = (q, cache, s.table.cuda(), i32(lens))
+    args = (q, cache, widened(s.table, 64, 2, 128, False).cuda(), i32(lens))
     first = sp24.attention_decode_shared(*args, i32(cu), i32(shared), workspace=ws)
     other = sp24.attention_decode_shared(*args, i32([1, 4, 20, 30]), i32([3000, 100, 2999]), workspace=ws)
     plain = sp24.attention_decode(*args)
@@ -154,7 +172,7 @@ def test_graph_replays_follow_the_lengths(sp24):
         s.table[b, :20] = s.table[0, :20]
     cache = s.upload()
     q = torch.randn(4, 4, 64, generator=torch.Generator().manual_seed(2)).bfloat16()
-    qd, table = q.cuda(), s.table.cuda()
+    qd, table = q.cuda(), widened(s.table, 16, 1, 64, False).cuda()
     i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
     n, cu, sh = i32(*lens), i32(0, 4), i32(320)
     ws = torch.zeros(sp24.attention_decode_shared_workspace_size(cache, 4, 4, 1), dtype=torch.uint8, device="cuda")
@@ -202,13 +220,13 @@ def test_index_errors(sp24):
                                  (i32(0, 3), i32(1 << 30), good, i32(*lens)), (i32(0, 3), i32(64), bad, i32(*lens)),
                                  (i32(0, 3), i32(64), worse, i32(*lens)), (i32(0, 3), i32(64), good, i32(64, -1, 80)),
                                  (i32(0, 3), i32(64), good, i32(64, 1 << 30, 80))):
-        y = sp24.attention_decode_shared(q.cuda(), cache, table.cuda(), n, cu, shared)
+        y = sp24.attention_decode_shared(q.cuda(), cache, widened(table, 16, 1, 64, False).cuda(), n, cu, shared)
         with pytest.raises(sp24.Sp24Error) as e:
             sp24.last_device_error()
         assert e.value.status == 8
         assert torch.isfinite(y.float()).all()
     # and all is well afterwards
-    y = sp24.attention_decode_shared(q.cuda(), cache, good.cuda(), i32(*lens), i32(0, 3), i32(64))
+    y = sp24.attention_decode_shared(q.cuda(), cache, widened(good, 16, 1, 64, False).cuda(), i32(*lens), i32(0, 3), i32(64))
     sp24.last_device_error()
     for b in range(3):
         want, size = attend(q[b:b + 1].double(), s.tokens("k", b), s.tokens("v", b),
@@ -225,15 +243,16 @@ def test_layouts_and_empty_calls(sp24):
     cache = s.upload()
     q = torch.randn(3, 4 * 64 + 24, generator=torch.Generator().manual_seed(3)).bfloat16()
     i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
-    wide = torch.full((3, 20), 1 << 20, dtype=torch.int32)
-    wide[:, :s.table.shape[1]] = s.table
+    wide = widened(s.table, 16, 2, 64, False)
+    columns = wide.shape[1]
+    wide = torch.cat((wide, wide[:, :7]), 1)            # rows further apart than their length
     out = torch.zeros(3, 4 * 64 + 8, device="cuda").bfloat16()
     qd, wd, n, cu, sh = q.cuda(), wide.cuda(), i32(*lens), i32(0, 3), i32(64)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    y = sp24.attention_decode_shared(qd[:, 8:264], cache, wd[:, :9], n, cu, sh, scale=0.3, out=out[:, :256], stream=side)
+    y = sp24.attention_decode_shared(qd[:, 8:264], cache, wd[:, :columns], n, cu, sh, scale=0.3, out=out[:, :256], stream=side)
     sp24.last_device_error(side)
-    none = sp24.attention_decode_shared(qd[:, 8:264], cache, wd[:, :9], n, i32(0), i32(), scale=0.3)
+    none = sp24.attention_decode_shared(qd[:, 8:264], cache, wd[:, :columns], n, i32(0), i32(), scale=0.3)
     sp24.last_device_error()
     for b in range(3):
         want, size = attend(q[b:b + 1, 8:264].double().view(1, 4, 64), s.tokens("k", b), s.tokens("v", b),
