@@ -91,6 +91,7 @@ struct SharedGroups {
   int2* where;          // [sequences][kv heads] {row of its first head in the first piece, how many pieces}
   float* part;          // [parts][2 kTileRows][D] weighted values, then [parts][2 kTileRows][2] maxima and sums
   int pairs, parts;     // how many there is room for
+  int window;           // of the call
   float* own;           // [sequences][query heads][D] and then [2]: the same of a sequence's own tokens, with
                         // kNotShared for the sum of weights where there is nothing to add
 };

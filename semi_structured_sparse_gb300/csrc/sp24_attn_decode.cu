@@ -237,10 +237,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
   for (int w = 0; w < kWarps; ++w) total += s_sum[0][w] + s_sum[1][w];
   total *= HH;
   const unsigned int ctas = min(gridDim.x, total), cta = blockIdx.x;
-  if (cta >= ctas) {  // uniform
-    if (SHARED) pdl_wait();
-    return;
-  }
+  if (cta >= ctas) return;  // uniform; never the first
   const unsigned int per = total / ctas, extra = total % ctas;  // the first `extra` CTAs take a tile more
   unsigned int u = cta * per + min(cta, extra);
   const unsigned int u_end = u + per + (cta < extra ? 1u : 0u);
@@ -700,7 +697,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     if (!more) break;
     it = nx;
   }
-  if (SHARED) pdl_wait();  // so that the launch after this one has waited for the one before it
+  // So that the launch after this one has waited for the one before it, too; one CTA does, and the others make room.
+  if (SHARED && blockIdx.x == 0) pdl_wait();
   pdl_trigger();
 }
 

@@ -339,67 +339,110 @@ struct Deal {
 };
 constexpr int kLeastUnits = 4;  // per CTA
 
-// Goes through the groups, 32 at a time: the units of all of them, or (`out`) the
-// work that begins with unit u.  Groups are brought into order: each begins
-// where the one before it ends.
-__device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int lane, bool report, const Deal& deal,
-                                                    unsigned int u, unsigned int u_end, unsigned int cta, Work* out) {
+// 32 groups, one per lane, with the units and pairs up to and with each.  Groups
+// are brought into order: each begins where the one before it ends.
+struct Groups {
+  int lo, end, n;                    // sequences, and the tokens that they read together
+  unsigned int tiles, units, pairs;  // of this one
+  unsigned int units_to, pairs_to;
+};
+__device__ __forceinline__ Groups load_groups(const PromptParams& p, int g, int lane, bool report, int before,
+                                              unsigned int units_before, unsigned int pairs_before) {
   const int tok = 2 * p.tile_tokens, most = p.table_width << p.cache.page_shift;
-  const int first = __ldg(p.sh.cu);
-  int carry = min(max(first, 0), p.T);
-  if (report && lane == 0 && first != carry) atomicOr(p.err, DEVERR_INDEX);
-  unsigned int units_before = 0, pairs_before = 0;
+  Groups s;
+  int raw = 0, shared = 0;
+  if (g < p.sh.G) raw = __ldg(p.sh.cu + g + 1), shared = __ldg(p.sh.lens + g);
+  s.end = max(min(raw, p.T), before);
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int x = __shfl_up_sync(0xFFFFFFFFu, s.end, m);
+    if (lane >= m) s.end = max(s.end, x);
+  }
+  s.lo = __shfl_up_sync(0xFFFFFFFFu, s.end, 1);
+  if (lane == 0) s.lo = before;
+  if (report && g < p.sh.G && (raw != s.end || shared < 0 || shared > most)) atomicOr(p.err, DEVERR_INDEX);
+  s.n = g < p.sh.G ? shared_tokens(s.lo, s.end, shared, p.seq_lens, most) : 0;
+  s.tiles = (s.n + BN - 1) / BN;
+  s.pairs = s.tiles ? (s.end - s.lo + tok - 1) / tok * p.kv_heads : 0;
+  s.units = s.pairs * s.tiles;
+  s.units_to = s.units, s.pairs_to = s.pairs;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const unsigned int x = __shfl_up_sync(0xFFFFFFFFu, s.units_to, m), y = __shfl_up_sync(0xFFFFFFFFu, s.pairs_to, m);
+    if (lane >= m) s.units_to += x, s.pairs_to += y;
+  }
+  s.units_to += units_before, s.pairs_to += pairs_before;
+  return s;
+}
+// The work that begins with unit u, if it is one of these groups'.
+__device__ __forceinline__ void place_unit(const PromptParams& p, const Groups& s, const Deal& deal, unsigned int u,
+                                           unsigned int u_end, unsigned int cta, Work* out) {
+  if (u >= u_end || u >= s.units_to || u < s.units_to - s.units) return;
+  Work w;
+  const unsigned int local = u - (s.units_to - s.units), pair = local / s.tiles;
+  const int block = pair / p.kv_heads;
+  w.b = s.lo;
+  w.hk = pair - block * p.kv_heads;
+  w.row0 = s.lo + block * 2 * p.tile_tokens;
+  w.rows = s.end - w.row0;
+  w.p0 = w.p_hi = s.n - 1;
+  w.wlo = w.send = w.first = w.nst = 0;
+  w.t0 = local - pair * s.tiles;
+  w.nt = min(s.tiles - w.t0, u_end - u);
+  w.pair = s.pairs_to - s.pairs + pair;
+  w.part = w.pair + cta;  // (either grows from one piece to the next)
+  const unsigned int u0 = u - w.t0, first = deal.cta_of(u0);
+  w.piece0 = w.pair + first;
+  w.pieces = deal.cta_of(u0 + s.tiles - 1) - first + 1;
+  if (w.pair >= p.sh.pairs || w.part >= p.sh.parts) w.b = -1;  // (there is room for all that the host expects)
+  *out = w;
+}
+// Goes through the groups: the units of all, and how often their tokens would be
+// read one by one; or (`out`) the work that begins with unit u.  `few`: the groups,
+// where they are 32 at most and known.
+__device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int lane, bool report, const Deal& deal,
+                                                    unsigned int u, unsigned int u_end, unsigned int cta, Work* out,
+                                                    Groups* few, float* times) {
   if (out && lane == 0) out->b = -1;
   __syncwarp();
-  for (int g0 = 0; g0 < p.sh.G; g0 += 32) {
-    const int g = g0 + lane;
-    int end = 0, raw = 0, shared = 0;
-    if (g < p.sh.G) raw = __ldg(p.sh.cu + g + 1), shared = __ldg(p.sh.lens + g);
-    end = max(min(raw, p.T), carry);
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int x = __shfl_up_sync(0xFFFFFFFFu, end, m);
-      if (lane >= m) end = max(end, x);
+  unsigned int units = 0, pairs = 0;
+  if (out && p.sh.G <= 32) {
+    place_unit(p, *few, deal, u, u_end, cta, out);
+  } else {
+    const int first = __ldg(p.sh.cu);
+    int before = min(max(first, 0), p.T);
+    if (report && lane == 0 && first != before) atomicOr(p.err, DEVERR_INDEX);
+    float sum = 0.0f;
+    for (int g0 = 0; g0 < p.sh.G; g0 += 32) {
+      const Groups s = load_groups(p, g0 + lane, lane, report, before, units, pairs);
+      if (out)
+        place_unit(p, s, deal, u, u_end, cta, out);
+      else
+        *few = s, sum += static_cast<float>(s.end - s.lo) * s.n;
+      units = __shfl_sync(0xFFFFFFFFu, s.units_to, 31), pairs = __shfl_sync(0xFFFFFFFFu, s.pairs_to, 31);
+      before = __shfl_sync(0xFFFFFFFFu, s.end, 31);
+      if (out && u < units) break;
     }
-    int lo = __shfl_up_sync(0xFFFFFFFFu, end, 1);
-    if (lane == 0) lo = carry;
-    if (report && g < p.sh.G && (raw != end || shared < 0 || shared > most)) atomicOr(p.err, DEVERR_INDEX);
-    const int n = g < p.sh.G ? shared_tokens(lo, end, shared, p.seq_lens, most) : 0;
-    const unsigned int tiles = (n + BN - 1) / BN;
-    const unsigned int pairs = tiles ? (end - lo + tok - 1) / tok * p.kv_heads : 0, units = pairs * tiles;
-    unsigned int ui = units, pi = pairs;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const unsigned int x = __shfl_up_sync(0xFFFFFFFFu, ui, m), y = __shfl_up_sync(0xFFFFFFFFu, pi, m);
-      if (lane >= m) ui += x, pi += y;
-    }
-    ui += units_before, pi += pairs_before;
-    if (out && u < u_end && u < ui && u >= ui - units) {
-      Work w;
-      const unsigned int local = u - (ui - units), pair = local / tiles;
-      const int block = pair / p.kv_heads;
-      w.b = lo;
-      w.hk = pair - block * p.kv_heads;
-      w.row0 = lo + block * tok;
-      w.rows = end - w.row0;
-      w.p0 = w.p_hi = n - 1;
-      w.wlo = w.send = w.first = w.nst = 0;
-      w.t0 = local - pair * tiles;
-      w.nt = min(tiles - w.t0, u_end - u);
-      w.pair = pi - pairs + pair;
-      w.part = w.pair + cta;  // (either grows from one piece to the next)
-      const unsigned int u0 = u - w.t0;
-      w.piece0 = w.pair + deal.cta_of(u0);
-      w.pieces = deal.cta_of(u0 + tiles - 1) - deal.cta_of(u0) + 1;
-      if (w.pair >= p.sh.pairs || w.part >= p.sh.parts) w.b = -1;  // (there is room for all that the host expects)
-      *out = w;
-    }
-    units_before = __shfl_sync(0xFFFFFFFFu, ui, 31), pairs_before = __shfl_sync(0xFFFFFFFFu, pi, 31);
-    carry = __shfl_sync(0xFFFFFFFFu, end, 31);
-    if (out && u < units_before) break;
+    if (times) *times = sum;
   }
   __syncwarp();
-  return units_before;
+  return units;
+}
+// How many SMs should do the shared tokens: the others begin with the sequences'
+// own at once, so that one's idle memory is the other's.  The shares of the SMs are
+// those of the work: key tiles, which the chain of products and exponentials bounds, and
+// bytes that an SM's decode CTAs read.  `tokens`: this lane's part of all sequences', `times`: of those that are read
+// together.
+template <class C>
+__device__ __forceinline__ unsigned int shared_sms(const PromptParams& p, unsigned int units, float tokens, float times,
+                                                   unsigned int sms) {
+  constexpr float UNIT_NS = C::D == 128 ? (C::E4M3 ? 1650.0f : 1350.0f) : (C::E4M3 ? 1400.0f : 1150.0f);
+  constexpr float BYTES_PER_NS = 34.0f;
+  tokens -= times;
+#pragma unroll
+  for (int m = 16; m; m >>= 1) tokens += __shfl_xor_sync(0xFFFFFFFFu, tokens, m);
+  const float own = fmaxf(0.0f, tokens) * (p.kv_heads * C::D * (C::E4M3 ? 2 : 4)) / BYTES_PER_NS, shared = units * UNIT_NS;
+  return max(1u, min(sms, static_cast<unsigned int>(sms * (shared / (shared + own)) + 0.999f)));
 }
 
 // SHARED: the shared first tokens of groups of sequences, for one query per
@@ -916,10 +959,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint32_t qn[2] = {0, 0};
       Rows mine = {0, 0, 0};
       Deal deal = {};
+      Groups groups = {};
       unsigned int unit = 0, unit_end = 0;
       if (SHARED && keys) {
-        deal.units = scan_groups(p, lane, blockIdx.x == 0, deal, 0, 0, 0, nullptr);
-        deal.ctas = min(gridDim.x, max(1u, deal.units / kLeastUnits));
+        float tokens = 0.0f, times = 0.0f;
+        for (int b = lane; b < p.T; b += 32) {
+          const int n = max(0, __ldg(p.seq_lens + b));
+          tokens += static_cast<float>(p.sh.window > 0 ? min(n, p.sh.window) : n);
+        }
+        deal.units = scan_groups(p, lane, blockIdx.x == 0, deal, 0, 0, 0, nullptr, &groups, &times);
+        deal.ctas = min(shared_sms<C>(p, deal.units, tokens, times, gridDim.x), max(1u, deal.units / kLeastUnits));
         deal.per = deal.units / deal.ctas, deal.extra = deal.units % deal.ctas;
         if (blockIdx.x < deal.ctas) unit = deal.begin(blockIdx.x), unit_end = deal.begin(blockIdx.x + 1);
       }
@@ -931,7 +980,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (item >= 2) ok = mbar_wait(&work_empty[item & 1], ((item >> 1) - 1) & 1);
           if (!ok) break;
           if (SHARED)
-            scan_groups(p, lane, false, deal, unit, unit_end, blockIdx.x, &s_work[item & 1]);
+            scan_groups(p, lane, false, deal, unit, unit_end, blockIdx.x, &s_work[item & 1], &groups, nullptr);
           else
             find_work(p, block, total, item == 0 ? &mine : nullptr, lane, &s_work[item & 1]);
           w = s_work[item & 1];
