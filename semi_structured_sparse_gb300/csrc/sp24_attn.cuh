@@ -97,13 +97,36 @@ struct SharedGroups {
 };
 constexpr float kNotShared = -1.0f;
 constexpr int kTileRows = 128;          // query rows of a tile of the prompt kernel; two tiles are a block
+constexpr int kKeyTile = 128;           // keys of one of its tiles
 // Weights of an e4m3 cache are 2^this times exp2(c S - m) in the kernels for prompts and for decoding.
 constexpr float kPromptUp = 7.0f, kDecodeUp = 15.0f;
+
+// Tokens of a sequence that count as read one by one, shared ones among them.
+__device__ __forceinline__ int counted_tokens(int n, int window) { return max(0, window > 0 ? min(n, window) : n); }
 
 // The tokens that a group [lo, hi) of sequences reads together: none if it is
 // one sequence, and no more than the sequence has whose pages they are read through.
 __device__ __forceinline__ int shared_tokens(int lo, int hi, int shared, const int32_t* seq_lens, int most) {
   return hi - lo < 2 ? 0 : max(0, min(min(shared, most), __ldg(seq_lens + lo)));
+}
+
+// How many of the SMs should do the shared tokens: the others begin with the
+// sequences' own at once, so that one's idle memory is the other's.  Both launches
+// ask, and get the same answer: shares of the SMs as those of the work, of units
+// (key tiles of up to 256 query rows), which the chain of products and
+// exponentials bounds, and of the bytes of own keys and values.  `tokens`: those of all sequences (as far
+// as a window reaches), less those that are read together.
+#ifndef SP24_OWN_RATE
+#define SP24_OWN_RATE 32.0f
+#endif
+template <int D, bool E4M3>
+__device__ __forceinline__ unsigned int shared_sms(unsigned int units, long long tokens, int kv_heads, unsigned int sms) {
+  constexpr float UNIT_NS = D == 128 ? (E4M3 ? 1650.0f : 1350.0f) : (E4M3 ? 1400.0f : 1150.0f);
+  constexpr float BYTES_PER_NS = SP24_OWN_RATE;  // that an SM's decode CTAs read
+  if (units == 0) return 0;
+  const float bytes = static_cast<float>(max(tokens, 0ll)) * (kv_heads * D * (E4M3 ? 2 : 4));
+  const float shared = units * UNIT_NS, own = bytes / BYTES_PER_NS;
+  return max(1u, min(sms, static_cast<unsigned int>(sms * (shared / (shared + own)) + 0.999f)));
 }
 
 // A call, as the entry point hands it to both launches.

@@ -35,6 +35,9 @@
 // which the keys take 1: launch, lengths, pages, keys and the join of 16 pieces
 // are a chain of seven memory latencies; 128 of up to 9000 tokens under a
 // window of 2000 with 4 sinks, 28/4 heads of 64, 45.8 us, 5.1 TB/s (75 %).
+#ifndef SP24_LEAST_OWN
+#define SP24_LEAST_OWN 40
+#endif
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "sp24_attn.cuh"
@@ -199,6 +202,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_sum[2][kWarps];
   __shared__ int s_found[2];
+  __shared__ int s_units[kWarps];
+  __shared__ long long s_tokens[kWarps];
   __shared__ float s_m[kWarps][HEADS], s_l[kWarps][HEADS];
   __shared__ unsigned int s_last;
 
@@ -231,12 +236,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     for (int m = 16; m; m >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, m);
   }
   if (lane == 31) s_sum[0][warp] = incl, s_sum[1][warp] = rest;
+  if (SHARED) {  // what the launch before has to do, and what is left
+    int units = 0;
+    long long tokens = 0;
+    for (int x = tid; x < p.B; x += kThreads) tokens += counted_tokens(__ldg(p.seq_lens + x), p.sh.window);
+    for (int x = tid; x < p.sh.G; x += kThreads) {
+      const int lo = min(max(__ldg(p.sh.cu + x), 0), p.B), hi = min(max(__ldg(p.sh.cu + x + 1), lo), p.B);
+      const int n = shared_tokens(lo, hi, __ldg(p.sh.lens + x), p.seq_lens, p.table_width << p.cache.page_shift);
+      const int rows = 2 * (kTileRows / p.group);
+      units += (n + kKeyTile - 1) / kKeyTile * ((hi - lo + rows - 1) / rows);
+      tokens -= static_cast<long long>(hi - lo) * n;
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+      units += __shfl_xor_sync(0xFFFFFFFFu, units, m);
+      tokens += __shfl_xor_sync(0xFFFFFFFFu, tokens, m);
+    }
+    if (lane == 0) s_units[warp] = units, s_tokens[warp] = tokens;
+  }
   __syncthreads();
   unsigned int total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += s_sum[0][w] + s_sum[1][w];
   total *= HH;
-  const unsigned int ctas = min(gridDim.x, total), cta = blockIdx.x;
+  unsigned int most = gridDim.x;
+  if (SHARED) {  // as many CTAs as run at once beside that
+    int units = 0;
+    long long tokens = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) units += s_units[w], tokens += s_tokens[w];
+    const unsigned int sms = gridDim.x / kCtasPerSm, busy = shared_sms<D, E4M3>(units * p.kv_heads, tokens, p.kv_heads, sms);
+    if (sms - busy >= SP24_LEAST_OWN) most = kCtasPerSm * (sms - busy);
+  }
+  const unsigned int ctas = min(most, total), cta = blockIdx.x;
   if (cta >= ctas) return;  // uniform; never the first
   const unsigned int per = total / ctas, extra = total % ctas;  // the first `extra` CTAs take a tile more
   unsigned int u = cta * per + min(cta, extra);

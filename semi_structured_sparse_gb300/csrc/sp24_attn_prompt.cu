@@ -55,6 +55,9 @@
 // (exactly) between the copy and the MMA; the softmax warps scale each query
 // row by a power of two, so that bf16 queries fit f16's range.
 #include <algorithm>
+#ifndef SP24_TURNS
+#define SP24_TURNS (D == 128 && !E4M3)
+#endif
 #include <cuda_bf16.h>
 #include "sp24_attn.cuh"
 #include "sp24_ptx.cuh"
@@ -63,7 +66,7 @@ namespace sp24 {
 namespace {
 
 constexpr int BM = kTileRows;  // query rows per tile, two tiles per CTA
-constexpr int BN = 128;   // keys per tile
+constexpr int BN = kKeyTile;   // keys per tile
 constexpr int kLeastTiles = 4;  // key tiles of a part, at least, where a block's keys are cut
 
 struct PromptParams {
@@ -97,7 +100,7 @@ struct Cfg {
   static constexpr int RAW_TILE = BN * D;                 // e4m3 codes
   static constexpr int RAW = E4M3 ? (D == 128 ? 2 : 4) : 0;
   static constexpr int SLOTS = D == 128 ? (E4M3 ? 4 : 5) : 8;
-  static constexpr int BARS = 23 + 2 * SLOTS + 2 * RAW;
+  static constexpr int BARS = 25 + 2 * SLOTS + 2 * RAW;
   static constexpr int SMEM = 1024 + 2 * Q_TILE + SLOTS * KV_TILE + RAW * RAW_TILE + BARS * 8;
   // Registers after the split: the warpgroups' shares stay within the launch's
   // (168 x 384 or 128 x 512).
@@ -119,6 +122,7 @@ struct Cfg {
   // cache (579 us against 555: the registers do not reach), nor with P apart
   // (P V of the last key tile is still reading P then).
   static constexpr bool AHEAD = D == 128 && !E4M3;
+  static constexpr bool TURNS = SP24_TURNS;
   // With an e4m3 cache P, and its sums, are 2^UP times exp2(c S - m): up to 2^8
   // times that where the maximum has grown by less, so up to 2^15, near f16's end.
   // The row's largest weight is 2^7 at least; f16's smallest step, 2^-24, rounds
@@ -402,7 +406,7 @@ __device__ __forceinline__ void place_unit(const PromptParams& p, const Groups& 
 // where they are 32 at most and known.
 __device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int lane, bool report, const Deal& deal,
                                                     unsigned int u, unsigned int u_end, unsigned int cta, Work* out,
-                                                    Groups* few, float* times) {
+                                                    Groups* few, long long* times) {
   if (out && lane == 0) out->b = -1;
   __syncwarp();
   unsigned int units = 0, pairs = 0;
@@ -412,13 +416,13 @@ __device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int l
     const int first = __ldg(p.sh.cu);
     int before = min(max(first, 0), p.T);
     if (report && lane == 0 && first != before) atomicOr(p.err, DEVERR_INDEX);
-    float sum = 0.0f;
+    long long sum = 0;
     for (int g0 = 0; g0 < p.sh.G; g0 += 32) {
       const Groups s = load_groups(p, g0 + lane, lane, report, before, units, pairs);
       if (out)
         place_unit(p, s, deal, u, u_end, cta, out);
       else
-        *few = s, sum += static_cast<float>(s.end - s.lo) * s.n;
+        *few = s, sum += static_cast<long long>(s.end - s.lo) * s.n;
       units = __shfl_sync(0xFFFFFFFFu, s.units_to, 31), pairs = __shfl_sync(0xFFFFFFFFu, s.pairs_to, 31);
       before = __shfl_sync(0xFFFFFFFFu, s.end, 31);
       if (out && u < units) break;
@@ -428,23 +432,6 @@ __device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int l
   __syncwarp();
   return units;
 }
-// How many SMs should do the shared tokens: the others begin with the sequences'
-// own at once, so that one's idle memory is the other's.  The shares of the SMs are
-// those of the work: key tiles, which the chain of products and exponentials bounds, and
-// bytes that an SM's decode CTAs read.  `tokens`: this lane's part of all sequences', `times`: of those that are read
-// together.
-template <class C>
-__device__ __forceinline__ unsigned int shared_sms(const PromptParams& p, unsigned int units, float tokens, float times,
-                                                   unsigned int sms) {
-  constexpr float UNIT_NS = C::D == 128 ? (C::E4M3 ? 1650.0f : 1350.0f) : (C::E4M3 ? 1400.0f : 1150.0f);
-  constexpr float BYTES_PER_NS = 34.0f;
-  tokens -= times;
-#pragma unroll
-  for (int m = 16; m; m >>= 1) tokens += __shfl_xor_sync(0xFFFFFFFFu, tokens, m);
-  const float own = fmaxf(0.0f, tokens) * (p.kv_heads * C::D * (C::E4M3 ? 2 : 4)) / BYTES_PER_NS, shared = units * UNIT_NS;
-  return max(1u, min(sms, static_cast<unsigned int>(sms * (shared / (shared + own)) + 0.999f)));
-}
-
 // SHARED: the shared first tokens of groups of sequences, for one query per
 // sequence; every row sees all of them, and sums go to the workspace.
 template <class C, bool SHARED = false>
@@ -476,7 +463,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t* work_empty = bars + 18;   // [2]
   uint64_t* stolen = bars + 20;
   uint64_t* s_read = bars + 21;       // [2] S is in the softmax warps' registers (APART)
-  uint64_t* kv_full = bars + 23;      // [SLOTS]
+  uint64_t* turn = bars + 23;         // [2] the other query tile has formed its P (TURNS)
+  uint64_t* kv_full = bars + 25;      // [SLOTS]
   uint64_t* kv_empty = kv_full + SLOTS;
   uint64_t* raw_full = kv_empty + SLOTS;  // [RAW]
   uint64_t* raw_empty = raw_full + RAW;
@@ -498,6 +486,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
       mbar_init(&drain[x], 1);
+      mbar_init(&turn[x], 4);
       mbar_init(&work_full[x], 1);
       mbar_init(&work_empty[x], E4M3 ? 15 : 11);  // the warps that read the work
     }
@@ -539,6 +528,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t ts = tmem + lanes + x * BN, tp = tmem + lanes + C::P_COL + x * C::P_STEP;
     const uint32_t to = tmem + lanes + C::O_COL + x * D;
     uint32_t sn = 0, on = 0;  // key tiles and blocks so far, for the barriers' parities
+    uint32_t tn = 0;          // turns so far
     bool ok = true;
     for (int item = 0; ok; ++item) {
       ok = wait_work(item);
@@ -588,8 +578,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int nt = w.nt, nst = w.nst - w.t0, first = w.first * BN;  // nst: sink tiles from here on
         const int p_min = SHARED ? w.p_hi : w.p0 + x * p.tile_tokens, p_max = min(w.p_hi, p_min + p.tile_tokens - 1);
         int base = tile_of(w, 0) * BN;
+        const bool turns = SHARED && C::TURNS && tiles_of(w) == 2;
         for (int i = 0; i < nt; ++i, ++sn, base = i == nst && nst > 0 ? first : base + BN) {
           ok = mbar_wait(&s_full[x], sn & 1);
+          if (turns && ok && (x == 1 || tn > 0)) ok = mbar_wait(&turn[x], (x == 1 ? tn : tn - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const int end = base + BN - 1;
@@ -703,7 +695,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[x]);
+          if (lane == 0) {
+            mbar_arrive(&p_full[x]);
+            if (turns) mbar_arrive(&turn[1 - x]);
+          }
+          if (turns) ++tn;
         }
         if (ok) ok = mbar_wait(&o_full[x], (C::APART ? sn - 1 : on) & 1);
         if (!ok) break;
@@ -962,13 +958,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       Groups groups = {};
       unsigned int unit = 0, unit_end = 0;
       if (SHARED && keys) {
-        float tokens = 0.0f, times = 0.0f;
-        for (int b = lane; b < p.T; b += 32) {
-          const int n = max(0, __ldg(p.seq_lens + b));
-          tokens += static_cast<float>(p.sh.window > 0 ? min(n, p.sh.window) : n);
-        }
+        long long tokens = 0, times = 0;
+        for (int b = lane; b < p.T; b += 32) tokens += counted_tokens(__ldg(p.seq_lens + b), p.sh.window);
         deal.units = scan_groups(p, lane, blockIdx.x == 0, deal, 0, 0, 0, nullptr, &groups, &times);
-        deal.ctas = min(shared_sms<C>(p, deal.units, tokens, times, gridDim.x), max(1u, deal.units / kLeastUnits));
+        tokens -= times;
+#pragma unroll
+        for (int m = 16; m; m >>= 1) tokens += __shfl_xor_sync(0xFFFFFFFFu, tokens, m);
+        deal.ctas = max(1u, min(shared_sms<D, E4M3>(deal.units, tokens, p.kv_heads, gridDim.x), deal.units / kLeastUnits));
         deal.per = deal.units / deal.ctas, deal.extra = deal.units % deal.ctas;
         if (blockIdx.x < deal.ctas) unit = deal.begin(blockIdx.x), unit_end = deal.begin(blockIdx.x + 1);
       }
