@@ -116,13 +116,10 @@ __device__ __forceinline__ int shared_tokens(int lo, int hi, int shared, const i
 // (key tiles of up to 256 query rows), which the chain of products and
 // exponentials bounds, and of the bytes of own keys and values.  `tokens`: those of all sequences (as far
 // as a window reaches), less those that are read together.
-#ifndef SP24_OWN_RATE
-#define SP24_OWN_RATE 32.0f
-#endif
 template <int D, bool E4M3>
 __device__ __forceinline__ unsigned int shared_sms(unsigned int units, long long tokens, int kv_heads, unsigned int sms) {
   constexpr float UNIT_NS = D == 128 ? (E4M3 ? 1650.0f : 1350.0f) : (E4M3 ? 1400.0f : 1150.0f);
-  constexpr float BYTES_PER_NS = SP24_OWN_RATE;  // that an SM's decode CTAs read
+  constexpr float BYTES_PER_NS = 32.0f;  // that an SM's decode CTAs read (28: 44.6 us, 34: 43.6, 44: 44.9, see sp24_attn_shared.cu)
   if (units == 0) return 0;
   const float bytes = static_cast<float>(max(tokens, 0ll)) * (kv_heads * D * (E4M3 ? 2 : 4));
   const float shared = units * UNIT_NS, own = bytes / BYTES_PER_NS;

@@ -35,9 +35,6 @@
 // which the keys take 1: launch, lengths, pages, keys and the join of 16 pieces
 // are a chain of seven memory latencies; 128 of up to 9000 tokens under a
 // window of 2000 with 4 sinks, 28/4 heads of 64, 45.8 us, 5.1 TB/s (75 %).
-#ifndef SP24_LEAST_OWN
-#define SP24_LEAST_OWN 40
-#endif
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "sp24_attn.cuh"
@@ -50,6 +47,7 @@ constexpr int kWarps = 4;           // per CTA (2, and twice the CTAs: 131071 to
                                     // us against 170)
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
+constexpr int kLeastOwnSms = 40;    // fewer are left by shared tokens: own tokens to as many CTAs as without them
 constexpr int kHalf = 4096;         // bytes of keys (and of values) per chunk and stage
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kPieces = 16;         // of a pair, that a thread joins in one round of loads
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) units += s_units[w], tokens += s_tokens[w];
     const unsigned int sms = gridDim.x / kCtasPerSm, busy = shared_sms<D, E4M3>(units * p.kv_heads, tokens, p.kv_heads, sms);
-    if (sms - busy >= SP24_LEAST_OWN) most = kCtasPerSm * (sms - busy);
+    if (sms - busy >= kLeastOwnSms) most = kCtasPerSm * (sms - busy);
   }
   const unsigned int ctas = min(most, total), cta = blockIdx.x;
   if (cta >= ctas) return;  // uniform; never the first
