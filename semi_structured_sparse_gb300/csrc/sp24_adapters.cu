@@ -455,7 +455,7 @@ __device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned in
 // ------------------------------------------------------------------ A x
 template <int KB>  // 64s of the rank
 struct DownCfg {
-  static constexpr int ROWS = KB == 1 ? 8 : 6, ADS = KB == 1 ? 10 : 6;  // stages
+  static constexpr int ROWS = 6, ADS = KB == 1 ? 14 : 6;  // stages
   static constexpr int R = ROWS / kIssue, A = ADS / kIssue;              // of each issuing warp
   static constexpr int AD_TILE = KB * 64 * 128;
   static constexpr int D1 = 64 * KB;                  // columns of an adapter's sums
