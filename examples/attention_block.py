@@ -3,11 +3,18 @@ QKV and output projections, and between them the norm and rotation of queries
 and keys, the paged cache and attention over it.
 
     python examples/attention_block.py [--cache bf16|e4m3] [--steps 32]
+    python examples/attention_block.py --shared [--cache bf16|e4m3] [--steps 32]
 
 Serves a ragged batch of prompts with random weights: one call for the prompts,
 then decode steps of one token per sequence, replayed as a CUDA graph.  At the
 end one sequence is run again as a single prompt over all its tokens, and the
 rows of its decoded tokens are compared: the two ways must agree.
+
+With --shared a batch of requests goes on from one instruction: its tokens run
+once, are copied (quantised, for an e4m3 cache) to pages that all requests' tables
+name, and are attended once for all of them in each decode step; each request has a
+low-rank adapter of its own on both projections.  Compared with the same steps in
+which every sequence is attended by itself.
 """
 import argparse
 import os
@@ -79,6 +86,20 @@ class AttentionBlock:
         q = self._heads(x, cache, positions, slots)
         return self.out(sp24.attention_decode(q, cache, table, lens, workspace=workspace, **mask).flatten(1))
 
+    def decode_shared(self, x, cache, table, lens, positions, slots, groups, adapters, ids, workspace):
+        """A decode step of requests behind shared tokens (`groups`: cu_shared and shared_lens, or None for one by one),
+        with each row's adapters (A, B) beside the two projections."""
+        qkv, out = adapters
+        rows = self.qkv(x)
+        sp24.add_adapters(rows, x, *qkv, ids, out=rows)
+        q = sp24.qk_norm_rope(rows, self.heads, cache, positions, slots, self.cos_sin, self.q_norm, self.k_norm)
+        if groups is None:
+            y = sp24.attention_decode(q, cache, table, lens, workspace=workspace).flatten(1)
+        else:
+            y = sp24.attention_decode_shared(q, cache, table, lens, *groups, workspace=workspace).flatten(1)
+        rows = self.out(y)
+        return sp24.add_adapters(rows, y, *out, ids, out=rows)
+
 
 def run(cache_type="bf16", steps=32, prompts=(700, 33, 256, 1200), window=512, sinks=4, width=4096, heads=32,
         kv_heads=8, head_dim=128, report=print):
@@ -149,10 +170,87 @@ def run(cache_type="bf16", steps=32, prompts=(700, 33, 256, 1200), window=512, s
     return off
 
 
+def run_shared(cache_type="bf16", steps=32, requests=24, instruction=3000, rank=16, width=4096, heads=32, kv_heads=8,
+               head_dim=128, page_size=64, report=print):
+    torch.manual_seed(2)
+    B, e4m3 = requests, cache_type == "e4m3"
+    block = AttentionBlock(width, heads, kv_heads, head_dim, most_positions=instruction + steps + 64)
+    wide = lambda n, k: (torch.randn(B, n, k, device="cuda") * k ** -0.5).bfloat16()  # noqa: E731
+    rows = (heads + 2 * kv_heads) * head_dim
+    adapters = ((wide(rank, width), wide(rows, rank)), (wide(rank, heads * head_dim), wide(width, rank)))
+    ids = torch.randperm(B, device="cuda").to(torch.int32)
+    hidden = torch.randn(instruction, width, device="cuda").bfloat16()
+    steps_in = torch.randn(steps, B, width, device="cuda").bfloat16()
+
+    # the instruction, once, in a bf16 cache of its own
+    once = PagedCache(1, instruction, kv_heads, head_dim, page_size)
+    at = torch.arange(instruction, device="cuda")
+    first = torch.zeros(instruction, dtype=torch.int64, device="cuda")
+    from_slots = once.slots(first, at)
+    block.prompt(hidden, torch.tensor([0, instruction], dtype=torch.int32, device="cuda"), once.cache, once.table,
+                 torch.tensor([instruction], dtype=torch.int32, device="cuda"), at.to(torch.int32), from_slots)
+
+    # whole pages of it in all tables, the page that it ends in as a copy for each request
+    def serve(shared):
+        pages = PagedCache(B, instruction + steps, kv_heads, head_dim, page_size, e4m3)
+        full = instruction // page_size
+        if shared:
+            pages.table[:, :full] = pages.table[:1, :full]
+        tail = at[full * page_size:] if shared else at
+        whole = at[:full * page_size] if shared else at[:0]
+        sequence = torch.arange(B, device="cuda")
+        to_slots = torch.cat((pages.slots(first[:len(whole)], whole),
+                              pages.slots(sequence.repeat_interleave(len(tail)), tail.repeat(B))))
+        of = torch.cat((from_slots[:len(whole)], from_slots[len(at) - len(tail):].repeat(B)))
+        sp24.cache_copy(once.cache, of, pages.cache, to_slots)
+        lens = torch.full((B,), instruction, dtype=torch.int32, device="cuda")
+        i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        groups = (i32(0, B), i32(instruction)) if shared else None
+        size = sp24.attention_decode_shared_workspace_size(pages.cache, heads, B, 1) if shared else \
+            sp24.attention_decode_workspace_size(pages.cache, heads)
+        workspace = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        x = torch.empty(B, width, dtype=torch.bfloat16, device="cuda")
+
+        def step():
+            positions = lens.clone()
+            lens.add_(1)
+            return block.decode_shared(x, pages.cache, pages.table, lens, positions, pages.slots(sequence, positions),
+                                       groups, adapters, ids, workspace)
+
+        x.copy_(steps_in[0])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = step()
+        lens.fill_(instruction)
+        got, start, stop = [], torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        for i in range(steps):
+            x.copy_(steps_in[i])
+            graph.replay()
+            got.append(y.clone())
+        stop.record()
+        stop.synchronize()
+        sp24.last_device_error()
+        report("%d decode steps of %d requests behind %d tokens, %s: %.1f us each" % (
+            steps, B, instruction, "read once" if shared else "read by each", start.elapsed_time(stop) * 1e3 / steps))
+        return torch.stack(got)
+
+    got, want = serve(True), serve(False)
+    off = float((got.float() - want.float()).norm() / want.float().norm())
+    report("rows against the same steps one by one: relative difference %.2g" % off)
+    return off
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--cache", choices=("bf16", "e4m3"), default="bf16")
     ap.add_argument("--steps", type=int, default=32)
+    ap.add_argument("--shared", action="store_true")
     a = ap.parse_args()
     # e4m3 activations differ in a last place where attention's rounding differs: a few times 2^-4 / sqrt(width) apart
-    assert run(a.cache, a.steps) < 0.03
+    assert (run_shared if a.shared else run)(a.cache, a.steps) < 0.03

@@ -65,10 +65,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
 
 
 # A fault-test copy of the library for the tests of the give-up path: bounded
-# waits give up after 1 ms, and the one-CTA GEMM kernel and the attention prompt
-# kernel issue nothing for each CTA's first pipeline stage
-# (SP24_FAULT_WITHHOLD_FIRST_STAGE), so that the waits for it run out and the
-# launch reports a device timeout.
+# waits give up after 1 ms, and the one-CTA GEMM kernel, the attention prompt
+# kernel and the kernels for many rows' adapters issue nothing for each CTA's first
+# pipeline stage (SP24_FAULT_WITHHOLD_FIRST_STAGE), so that the waits for it run
+# out and the launch reports a device timeout.
 # Built into _build/fault/, separate from libsp24.so, whose build never
 # defines either macro.
 FAULT_DIR = os.path.join(BUILD, "fault")

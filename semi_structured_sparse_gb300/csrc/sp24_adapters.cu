@@ -580,6 +580,12 @@ __global__ void __launch_bounds__(kDownThreads, 1)
       if (lane == 0) {
         auto load = [&](int w0, int k, int x, int& row, int& ad) {
           const int col = (s.first + k) * kCols, at = x * C::R + row % C::R;
+#ifdef SP24_FAULT_WITHHOLD_FIRST_STAGE
+          if (x == 0 && row == 0) {  // the fault-test build: each CTA's first tile never comes
+            ++row;
+            return;
+          }
+#endif
           if (row >= C::R) ok = mbar_wait(&row_empty[at], (row / C::R - 1) & 1);
           if (!ok) return;
           mbar_arrive_expect_tx(&row_full[at], kRowTile);
@@ -898,6 +904,12 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       if (lane == 0) {
         for (int n = 0; n < s.count && ok; ++n) {
           const int col = (s.first + n) * kCols, at = row % ROWS, x = row % kIssue;
+#ifdef SP24_FAULT_WITHHOLD_FIRST_STAGE
+          if (row == 0) {
+            ++row;
+            continue;
+          }
+#endif
           if (row >= ROWS) ok = mbar_wait(&row_empty[at], (row / ROWS - 1) & 1);
           if (!ok) break;
           mbar_arrive_expect_tx(&row_full[at], kRowTile);

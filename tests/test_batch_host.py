@@ -86,3 +86,56 @@ def test_python_refuses_what_is_not_on_a_gpu():
         s.add_adapters(t, t, t[None], t[None], torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError, match="y must be a CUDA tensor"):
         s.add_adapters(None, t, t[None], t[None], torch.zeros(2, dtype=torch.int32))
+
+
+def fake_gpu_tensors(monkeypatch):
+    """Tensors of the CPU that say that they are GPU 0's: what the binding checks of shapes, types and strides."""
+    import semi_structured_sparse_gb300 as s
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda self: True))
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail("the library was called")
+    monkeypatch.setattr(s, "_lib", Library())
+    return s
+
+
+def test_adapter_shapes_are_refused(monkeypatch):
+    s = fake_gpu_tensors(monkeypatch)
+    z = lambda *shape, t=torch.bfloat16: torch.zeros(shape, dtype=t)  # noqa: E731
+    good = dict(y=z(4, 16), x=z(4, 24), a=z(3, 8, 24), b=z(3, 16, 8), ids=z(4, t=torch.int32), scales=z(3, t=torch.float32),
+                out=z(4, 16))
+    bad = [dict(y=z(4, 16, t=torch.float16)), dict(y=z(5, 16)), dict(y=z(4, 32)[:, ::2]), dict(y=z(4)), dict(x=z(3, 24)),
+           dict(x=z(4, 32)), dict(x=z(24, 4).T), dict(x=z(4, 24, t=torch.float32)), dict(a=z(3, 8, 16)), dict(a=z(2, 8, 24)),
+           dict(a=z(3, 24, 8).transpose(1, 2)), dict(a=z(8, 24)), dict(a=z(1, 8, 24).expand(3, 8, 24)), dict(b=z(3, 16, 16)),
+           dict(b=z(3, 8, 8)), dict(b=z(3, 8, 16).transpose(1, 2)), dict(ids=z(4, t=torch.int64)), dict(ids=z(3, t=torch.int32)),
+           dict(ids=z(8, t=torch.int32)[::2]), dict(scales=z(2, t=torch.float32)), dict(scales=z(3)), dict(out=z(4, 24)),
+           dict(out=z(4, 16, t=torch.float32)), dict(out=z(16, 4).T), dict(y=None), dict(a=None), dict(ids=None)]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            s.add_adapters(**dict(good, **kw))
+
+
+def test_shared_and_copy_shapes_are_refused(monkeypatch):
+    s = fake_gpu_tensors(monkeypatch)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    c, other = s.KVCache(k, k), s.KVCache(k[:, :1], k[:, :1])
+    q, table, lens = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 3, dtype=torch.int32), i32(1, 1)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    for cu, shared in ((i32(0), i32(1)), (i32(0, 1, 2), i32(1)), (i32(0, 1).long(), i32(1)), (i32(0, 1), i32(1).float()),
+                       (i32(0, 9, 1)[::2], i32(1)), (i32(0, 1)[None], i32(1)), (None, i32(1)), (i32(0, 1), None)):
+        with pytest.raises(ValueError):
+            s.attention_decode_shared(q, c, table, lens, cu, shared, workspace=ws)
+    with pytest.raises(ValueError, match="sequences"):
+        s.attention_decode_shared(q[:1], c, table, lens, i32(0, 2), i32(1), workspace=ws)
+    with pytest.raises(ValueError):
+        s.attention_decode_shared(q, c, table, lens, i32(0, 2), i32(1), workspace=ws.float())
+    slots = torch.zeros(2, dtype=torch.int64)
+    for i, j in ((slots, slots[:1]), (slots.int(), slots), (slots, slots.int()), (slots[None], slots[None]), (None, slots),
+                 (slots, torch.zeros(4, dtype=torch.int64)[::2])):
+        with pytest.raises(ValueError):
+            s.cache_copy(c, i, c, j)
+    with pytest.raises(ValueError, match="same heads"):
+        s.cache_copy(c, slots, other, slots)
