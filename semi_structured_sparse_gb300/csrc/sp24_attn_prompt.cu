@@ -97,7 +97,7 @@ struct Cfg {
   static constexpr int RAW_TILE = BN * D;                 // e4m3 codes
   static constexpr int RAW = E4M3 ? (D == 128 ? 2 : 4) : 0;
   static constexpr int SLOTS = D == 128 ? (E4M3 ? 4 : 5) : 8;
-  static constexpr int BARS = 25 + 2 * SLOTS + 2 * RAW;
+  static constexpr int BARS = 23 + 2 * SLOTS + 2 * RAW;
   static constexpr int SMEM = 1024 + 2 * Q_TILE + SLOTS * KV_TILE + RAW * RAW_TILE + BARS * 8;
   // Registers after the split: the warpgroups' shares stay within the launch's
   // (168 x 384 or 128 x 512).
@@ -239,7 +239,9 @@ struct Work {
   int first, nst;    // key tiles: 0 .. nst - 1 (sinks), then first, first + 1, ...
   int t0, nt;        // which of them: nt from number t0 on
   int part;          // where this part's sums go (splits > 1)
-  int pair, piece0, pieces;  // (shared tokens) the pair, and all the parts that its keys are cut into
+};
+struct Pieces {      // shared tokens: all the parts that a pair's keys are cut into
+  int first, count;
 };
 
 __device__ __forceinline__ int tile_of(const Work& w, int i) {
@@ -380,7 +382,7 @@ __device__ __forceinline__ Groups load_groups(const PromptParams& p, int g, int 
 }
 // The work that begins with unit u, if it is one of these groups'.
 __device__ __forceinline__ void place_unit(const PromptParams& p, const Groups& s, const Deal& deal, unsigned int u,
-                                           unsigned int u_end, unsigned int cta, Work* out) {
+                                           unsigned int u_end, unsigned int cta, Work* out, Pieces* pieces) {
   if (u >= u_end || u >= s.units_to || u < s.units_to - s.units) return;
   Work w;
   const unsigned int local = u - (s.units_to - s.units), pair = local / s.tiles;
@@ -393,12 +395,12 @@ __device__ __forceinline__ void place_unit(const PromptParams& p, const Groups& 
   w.wlo = w.send = w.first = w.nst = 0;
   w.t0 = local - pair * s.tiles;
   w.nt = min(s.tiles - w.t0, u_end - u);
-  w.pair = s.pairs_to - s.pairs + pair;
-  w.part = w.pair + cta;  // (either grows from one piece to the next)
+  const int number = s.pairs_to - s.pairs + pair;
+  w.part = number + cta;  // (either grows from one piece to the next)
   const unsigned int u0 = u - w.t0, first = deal.cta_of(u0);
-  w.piece0 = w.pair + first;
-  w.pieces = deal.cta_of(u0 + s.tiles - 1) - first + 1;
-  if (w.pair >= p.sh.pairs || w.part >= p.sh.parts) w.b = -1;  // (there is room for all that the host expects)
+  pieces->first = number + first;
+  pieces->count = deal.cta_of(u0 + s.tiles - 1) - first + 1;
+  if (number >= p.sh.pairs || w.part >= p.sh.parts) w.b = -1;  // (there is room for all that the host expects)
   *out = w;
 }
 // Goes through the groups: the units of all, and how often their tokens would be
@@ -406,12 +408,12 @@ __device__ __forceinline__ void place_unit(const PromptParams& p, const Groups& 
 // where they are 32 at most and known.
 __device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int lane, bool report, const Deal& deal,
                                                     unsigned int u, unsigned int u_end, unsigned int cta, Work* out,
-                                                    Groups* few, long long* times) {
+                                                    Pieces* pieces, Groups* few, long long* times) {
   if (out && lane == 0) out->b = -1;
   __syncwarp();
   unsigned int units = 0, pairs = 0;
   if (out && p.sh.G <= 32) {
-    place_unit(p, *few, deal, u, u_end, cta, out);
+    place_unit(p, *few, deal, u, u_end, cta, out, pieces);
   } else {
     const int first = __ldg(p.sh.cu);
     int before = min(max(first, 0), p.T);
@@ -420,7 +422,7 @@ __device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int l
     for (int g0 = 0; g0 < p.sh.G; g0 += 32) {
       const Groups s = load_groups(p, g0 + lane, lane, report, before, units, pairs);
       if (out)
-        place_unit(p, s, deal, u, u_end, cta, out);
+        place_unit(p, s, deal, u, u_end, cta, out, pieces);
       else
         *few = s, sum += static_cast<long long>(s.end - s.lo) * s.n;
       units = __shfl_sync(0xFFFFFFFFu, s.units_to, 31), pairs = __shfl_sync(0xFFFFFFFFu, s.pairs_to, 31);
@@ -442,6 +444,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   constexpr bool E4M3 = C::E4M3;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Work s_work[2];
+  __shared__ Pieces s_pieces[2];   // (shared tokens)
+  __shared__ uint64_t turn[2];     // (TURNS) the other query tile has formed its P
   __shared__ __align__(16) uint4 s_response;
   __shared__ uint32_t s_tmem;
   __shared__ int s_last[2];  // position in the ring of the last copy of keys, and of values
@@ -463,8 +467,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t* work_empty = bars + 18;   // [2]
   uint64_t* stolen = bars + 20;
   uint64_t* s_read = bars + 21;       // [2] S is in the softmax warps' registers (APART)
-  uint64_t* turn = bars + 23;         // [2] the other query tile has formed its P (TURNS)
-  uint64_t* kv_full = bars + 25;      // [SLOTS]
+  uint64_t* kv_full = bars + 23;      // [SLOTS]
   uint64_t* kv_empty = kv_full + SLOTS;
   uint64_t* raw_full = kv_empty + SLOTS;  // [RAW]
   uint64_t* raw_empty = raw_full + RAW;
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
       mbar_init(&drain[x], 1);
-      mbar_init(&turn[x], 4);
+      if (SHARED && C::TURNS) mbar_init(&turn[x], 4);
       mbar_init(&work_full[x], 1);
       mbar_init(&work_empty[x], E4M3 ? 15 : 11);  // the warps that read the work
     }
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (mine) *reinterpret_cast<float2*>(ml + 2 * rr) = make_float2(m, l);
         if (w.t0 == 0 && mine && rr == token * p.group)
           p.sh.where[static_cast<int64_t>(w.row0 + at) * p.kv_heads + w.hk] =
-              make_int2(w.piece0 * (2 * BM) + x * BM + rr, w.pieces);
+              make_int2(s_pieces[item & 1].first * (2 * BM) + x * BM + rr, s_pieces[item & 1].count);
         const unsigned int some = __ballot_sync(0xFFFFFFFFu, mine);
 #pragma unroll 1
         for (int j = 0; j < D && some; j += 16) {
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (SHARED && keys) {
         long long tokens = 0, times = 0;
         for (int b = lane; b < p.T; b += 32) tokens += counted_tokens(__ldg(p.seq_lens + b), p.sh.window);
-        deal.units = scan_groups(p, lane, blockIdx.x == 0, deal, 0, 0, 0, nullptr, &groups, &times);
+        deal.units = scan_groups(p, lane, blockIdx.x == 0, deal, 0, 0, 0, nullptr, nullptr, &groups, &times);
         tokens -= times;
 #pragma unroll
         for (int m = 16; m; m >>= 1) tokens += __shfl_xor_sync(0xFFFFFFFFu, tokens, m);
@@ -976,7 +979,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (item >= 2) ok = mbar_wait(&work_empty[item & 1], ((item >> 1) - 1) & 1);
           if (!ok) break;
           if (SHARED)
-            scan_groups(p, lane, false, deal, unit, unit_end, blockIdx.x, &s_work[item & 1], &groups, nullptr);
+            scan_groups(p, lane, false, deal, unit, unit_end, blockIdx.x, &s_work[item & 1], &s_pieces[item & 1], &groups,
+                        nullptr);
           else
             find_work(p, block, total, item == 0 ? &mine : nullptr, lane, &s_work[item & 1]);
           w = s_work[item & 1];
