@@ -116,6 +116,7 @@ __device__ __forceinline__ int shared_tokens(int lo, int hi, int shared, const i
 // (key tiles of up to 256 query rows), which the chain of products and
 // exponentials bounds, and of the bytes of own keys and values.  `tokens`: those of all sequences (as far
 // as a window reaches), less those that are read together.
+constexpr unsigned int kLeastOwnSms = 40;  // fewer, and the shared tokens take them all first
 template <int D, bool E4M3>
 __device__ __forceinline__ unsigned int shared_sms(unsigned int units, long long tokens, int kv_heads, unsigned int sms) {
   constexpr float UNIT_NS = D == 128 ? (E4M3 ? 1650.0f : 1350.0f) : (E4M3 ? 1400.0f : 1150.0f);
@@ -123,7 +124,8 @@ __device__ __forceinline__ unsigned int shared_sms(unsigned int units, long long
   if (units == 0) return 0;
   const float bytes = static_cast<float>(max(tokens, 0ll)) * (kv_heads * D * (E4M3 ? 2 : 4));
   const float shared = units * UNIT_NS, own = bytes / BYTES_PER_NS;
-  return max(1u, min(sms, static_cast<unsigned int>(sms * (shared / (shared + own)) + 0.999f)));
+  const unsigned int busy = max(1u, min(sms, static_cast<unsigned int>(sms * (shared / (shared + own)) + 0.999f)));
+  return sms - busy < kLeastOwnSms ? sms : busy;
 }
 
 // A call, as the entry point hands it to both launches.

@@ -47,7 +47,6 @@ constexpr int kWarps = 4;           // per CTA (2, and twice the CTAs: 131071 to
                                     // us against 170)
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kLeastOwnSms = 40;    // fewer are left by shared tokens: own tokens to as many CTAs as without them
 constexpr int kHalf = 4096;         // bytes of keys (and of values) per chunk and stage
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kPieces = 16;         // of a pair, that a thread joins in one round of loads
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) units += s_units[w], tokens += s_tokens[w];
     const unsigned int sms = gridDim.x / kCtasPerSm, busy = shared_sms<D, E4M3>(units * p.kv_heads, tokens, p.kv_heads, sms);
-    if (sms - busy >= kLeastOwnSms) most = kCtasPerSm * (sms - busy);
+    if (busy < sms) most = kCtasPerSm * (sms - busy);
   }
   const unsigned int ctas = min(most, total), cta = blockIdx.x;
   if (cta >= ctas) return;  // uniform; never the first
