@@ -79,7 +79,7 @@ struct FewCfg {
   static constexpr int SMEM = FIRST + RECV + H;
 };
 template <int MT, int NT>
-__global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid_constant__ AdapterParams p) {
+__global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kernel(const __grid_constant__ AdapterParams p) {
   using C = FewCfg<MT, NT>;
   constexpr int R = C::R, RP = C::RP, KS = C::KS, ST = C::STAGES, MH = (NT + 1) / 2;  // 16-row tiles of tokens
   extern __shared__ __align__(128) uint8_t smem[];
@@ -233,15 +233,15 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
   // ---- the first columns' operands of B (A x), ahead of the wait for A x
   const int n0 = static_cast<int>(int64_t(blocks) * gw / GW), n1 = static_cast<int>(int64_t(blocks) * (gw + 1) / GW);
   const __nv_bfloat16* const b = p.b + adapter * p.stride_b;
-  int row[2 * MH];
+  int row[NT];
 #pragma unroll
-  for (int i = 0; i < 2 * MH; ++i) row[i] = i < NT ? s_row[8 * i + g] : -1;
-  uint4 bv[C::AHEAD][KS][4], yv[C::AHEAD][2 * MH];
+  for (int i = 0; i < NT; ++i) row[i] = s_row[8 * i + g];
+  uint4 bv[C::AHEAD][KS][4], yv[C::AHEAD][NT];
   const __nv_bfloat16* const b_lane = b + (8 * (g >> 1) + (g & 1)) * p.r + 8 * t;
   const __nv_bfloat16* y_row[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) y_row[i] = p.y + max(row[i], 0) * p.ldy + 8 * t;
-  auto load = [&](int block, uint4 (&bv)[KS][4], uint4 (&yv)[2 * MH]) {
+  auto load = [&](int block, uint4 (&bv)[KS][4], uint4 (&yv)[NT]) {
     const __nv_bfloat16* from = b_lane + int64_t(32 * block) * p.r;
     const int left = block < n1 ? p.N - 32 * block : 0;  // columns from here on
 #pragma unroll
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
           bv[s][j] = *reinterpret_cast<const uint4*>(from + 2 * j * p.r + 32 * s);
       }
 #pragma unroll
-    for (int i = 0; i < 2 * MH; ++i) {
+    for (int i = 0; i < NT; ++i) {
       yv[i] = make_uint4(0, 0, 0, 0);
-      if (i < NT && row[i] >= 0 && 8 * t < left) yv[i] = *reinterpret_cast<const uint4*>(y_row[i < NT ? i : 0] + 32 * block);
+      if (row[i] >= 0 && 8 * t < left) yv[i] = *reinterpret_cast<const uint4*>(y_row[i] + 32 * block);
     }
   };
 #pragma unroll
@@ -330,9 +330,9 @@ __global__ void __launch_bounds__(kThreads) add_adapters_few_kernel(const __grid
           }
         }
       }
-      uint4 y[2 * MH];
+      uint4 y[NT];
 #pragma unroll
-      for (int i = 0; i < 2 * MH; ++i) y[i] = yv[a][i];
+      for (int i = 0; i < NT; ++i) y[i] = yv[a][i];
       load(block + C::AHEAD, bv[a], yv[a]);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
