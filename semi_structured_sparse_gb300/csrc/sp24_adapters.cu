@@ -19,6 +19,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMostCluster = 8;    // CTAs that share a few rows' work, at most
 constexpr int kMostRank = 128;
 constexpr int kFewRows = 512;      // rows of a call that are sorted by adapter
+// So many adapters that up to so many rows have few of each: in blocks of kFewRows.  (1024 rows of 4096 values, rank 16,
+// 256 adapters: 54 us in blocks, 139 in tiles of 128 rows; of 8 adapters 26 and 19.)
+constexpr int kScattered = 32, kFewScattered = 1024;
 
 struct AdapterParams {
   const __nv_bfloat16* y;
@@ -79,7 +82,8 @@ struct FewCfg {
   static constexpr int SMEM = FIRST + RECV + H;
 };
 template <int MT, int NT>
-__global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kernel(const __grid_constant__ AdapterParams p) {
+__global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kernel(
+    const __grid_constant__ AdapterParams p, int items) {
   using C = FewCfg<MT, NT>;
   constexpr int R = C::R, RP = C::RP, KS = C::KS, ST = C::STAGES, MH = (NT + 1) / 2;  // 16-row tiles of tokens
   extern __shared__ __align__(128) uint8_t smem[];
@@ -90,7 +94,8 @@ __global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kern
   __shared__ int s_count[kFewRows / 32], s_item[2], s_row[R];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t rank = cluster_rank(), ctas = cluster_nrank();
-  const int item = blockIdx.x / ctas, gw = rank * kWarps + warp, GW = ctas * kWarps;
+  const int gw = rank * kWarps + warp, GW = ctas * kWarps, block = blockIdx.x / ctas / items;
+  const int item = blockIdx.x / ctas - block * items, t0 = block * kFewRows, T = min(kFewRows, p.T - t0);
   pdl_wait();
 
   // ---- this cluster's item: rows are numbered within their adapter; every R-th begins one
@@ -101,10 +106,10 @@ __global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kern
   for (int i = 0; i < MINE; ++i) {
     const int x = tid + i * kThreads;
     id[i] = -2;
-    if (x < p.T) {
-      id[i] = p.ids[x];
+    if (x < T) {
+      id[i] = p.ids[t0 + x];
       if (id[i] >= p.count) {
-        if (blockIdx.x == 0) atomicOr(p.err, DEVERR_INDEX);
+        if (item == 0) atomicOr(p.err, DEVERR_INDEX);
         id[i] = -1;
       }
       id[i] = max(id[i], -1);
@@ -118,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kern
 #pragma unroll
   for (int i = 0; i < MINE; ++i) {  // how many rows before this one have its adapter
     const int me = tid + i * kThreads, end = i * kThreads + (warp + 1) * 32;  // (of the warp)
-    if (end - 32 >= p.T) break;
+    if (end - 32 >= T) break;
     for (int x = 0; x < end; x += 4) {
       const int4 v = *reinterpret_cast<const int4*>(s_id + x);
       nth[i] += (v.x == id[i] && x < me) + (v.y == id[i] && x + 1 < me) + (v.z == id[i] && x + 2 < me) +
@@ -152,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kern
   const int adapter = s_item[0], from = s_item[1];
 #pragma unroll
   for (int i = 0; i < MINE; ++i)
-    if (id[i] == adapter && nth[i] >= from && nth[i] < from + R) s_row[nth[i] - from] = tid + i * kThreads;
+    if (id[i] == adapter && nth[i] >= from && nth[i] < from + R) s_row[nth[i] - from] = t0 + tid + i * kThreads;
   __syncthreads();
   if (adapter < 0) {
     for (int i = gw; i < R * ((p.N + 255) / 256); i += GW) {
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kern
   for (int e = tid; e < R * 32 * KS; e += kThreads) {
     const int i = e / (32 * KS), j = e % (32 * KS);
     float sum = 0.0f;
-    if (j < RP) {
+    if (j < p.r) {  // (behind the rank, an infinite x has made zeros into what is not a number)
 #pragma unroll
       for (int c = 0; c < kMostCluster; ++c)
         if (c < static_cast<int>(ctas)) sum += recv[c * (R * RP) + i * RP + j];
@@ -388,22 +393,128 @@ struct Deal {
 
 struct ManyParams {
   AdapterParams p;
+  int32_t* order;     // the rows, sorted by adapter in windows of kWindow (null: as they are)
+  int32_t* sorted;    // of each window: whether it has been (otherwise its rows stay as they are)
   int kbs, nbs, rp;   // units of a tile, and the rank padded to the MMA's multiple of 16
   Deal k, n;
   float* part;        // [pieces][kTile][rp]; the piece of a tile that CTA c of the first launch forms is tile + c
 };
 
+// Rows whose adapters are in no order would make every tile a tile of many adapters, so a launch before the two
+// sorts them by adapter in windows, unless an adapter's rows mostly stand in runs.  A tile is then 128 rows in that
+// order, fetched and stored four rows per copy where they are apart.  A radix sort that counts a digit's rows by
+// warp, each warp's in order, keeps equal ones as they were and needs no atomics, so the results are the same
+// every time.  (4096 rows of 4096 values, rank 16, 64 adapters, in no order: 90 us, 555 without the sort, 48 if each
+// adapter's rows stand together.  Fetching all tiles row by row: 8192 rows with one adapter 116 us instead of 45.)
+constexpr int kWindow = 8192, kSortThreads = 1024, kDigits = 256, kSortWarps = kSortThreads / 32;
+constexpr int kEach = kWindow / kSortThreads, kHistRow = kSortWarps + 1;
+constexpr int kLongRuns = 2;  // changes of adapter per tile up to which rows stay as they are
+struct SortSmem {
+  unsigned int key[kWindow];
+  unsigned int count[kDigits * kHistRow];  // of a digit: of each warp's rows, and then where they go
+  unsigned short at[kWindow];
+  unsigned int warp_sum[kSortWarps], changes;
+};
+__global__ void __launch_bounds__(kSortThreads) adapters_sort_kernel(const __grid_constant__ ManyParams q, int bits) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SortSmem& sm = *reinterpret_cast<SortSmem*>(smem_raw);
+  const AdapterParams& p = q.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int x0 = blockIdx.x * kWindow, n = min(kWindow, p.T - x0);
+  if (tid == 0) sm.changes = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int mine = warp * (32 * kEach) + lane;  // and every 32nd behind it
+  unsigned int key[kEach], at[kEach], rank[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int x = mine + 32 * i;
+    at[i] = x;
+    key[i] = 0xFFFFFFFFu;  // behind the last row: stays there
+    if (x < n) {
+      const int id = __ldg(p.ids + x0 + x);
+      key[i] = id < 0 || id >= p.count ? 0 : id + 1;
+    }
+  }
+  __syncthreads();
+  int changes = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const unsigned int before = __shfl_up_sync(0xFFFFFFFFu, key[i], 1);
+    changes += __popc(__ballot_sync(0xFFFFFFFFu, lane > 0 && mine + 32 * i < n && key[i] != before));
+  }
+  if (lane == 0 && changes) atomicAdd(&sm.changes, changes);
+  __syncthreads();
+  const bool sort = sm.changes > kLongRuns * ((n + kTile - 1) / kTile);
+  if (tid == 0) q.sorted[blockIdx.x] = sort;
+  if (!sort) return;
+  for (int shift = 0; shift < bits; shift += 8) {
+    for (int i = tid; i < kDigits * kHistRow; i += kSortThreads) sm.count[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const unsigned int digit = key[i] >> shift & (kDigits - 1);
+      const unsigned int same = __match_any_sync(0xFFFFFFFFu, digit);
+      const unsigned int before = __popc(same & ((1u << lane) - 1));
+      unsigned int* const c = &sm.count[digit * kHistRow + warp];
+      const unsigned int base = *c;
+      rank[i] = base + before;
+      __syncwarp();
+      if (before == 0) *c = base + __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    {  // sums of what comes before, digits first, warps in order
+      constexpr int PER = kDigits * kSortWarps / kSortThreads;
+      static_assert(kSortWarps % PER == 0, "a thread's counts are of one digit");
+      unsigned int* const c = &sm.count[tid * PER / kSortWarps * kHistRow + tid * PER % kSortWarps];
+      unsigned int v[PER], sum = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = sum, sum += c[i];
+      unsigned int upto = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const unsigned int x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += x;
+      }
+      if (lane == 31) sm.warp_sum[warp] = upto;
+      __syncthreads();
+      unsigned int base = upto - sum;
+      for (int w = 0; w < warp; ++w) base += sm.warp_sum[w];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = base + v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const unsigned int to = sm.count[(key[i] >> shift & (kDigits - 1)) * kHistRow + warp] + rank[i];
+      sm.key[to] = key[i];
+      sm.at[to] = static_cast<unsigned short>(at[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) key[i] = sm.key[mine + 32 * i], at[i] = sm.at[mine + 32 * i];
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (mine + 32 * i < n) q.order[x0 + mine + 32 * i] = x0 + at[i];
+}
+
 // What a CTA does in one go: units of one tile.
 struct Segment {
   int tile, first, count;     // count 0: nothing more
   int adapters;
+  int apart;                  // whether its rows are not in a row
   int adapter[kTile];         // the tile's adapters
+  __align__(16) int row[kTile];
   int which[kTile];           // of each row: which of them, or -1
   float scale[kTile];         // of each row
 };
 // The segment that begins with unit u, by one warp.
-__device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned int u, unsigned int u_end, int per_tile,
+__device__ __forceinline__ void find_segment(const ManyParams& q, unsigned int u, unsigned int u_end, int per_tile,
                                              bool report, bool scales, Segment* out) {
+  const AdapterParams& p = q.p;
   const int lane = threadIdx.x & 31;
   if (u >= u_end) {
     if (lane == 0) out->count = 0;
@@ -411,13 +522,22 @@ __device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned in
     return;
   }
   const int tile = u / per_tile, first = u - tile * per_tile;
+  const bool sorted = q.order && __ldcg(q.sorted + tile / (kWindow / kTile));
   int id[kTile / 32], which[kTile / 32];
+  bool apart = false;
 #pragma unroll
   for (int i = 0; i < kTile / 32; ++i) {
-    const int x = tile * kTile + 32 * i + lane;
-    id[i] = x < p.T ? __ldg(p.ids + x) : -1;
+    int x = min(tile * kTile + 32 * i + lane, p.T - 1);  // (behind the last row: that row again, with the same result)
+    if (sorted) {
+      const int from = __ldcg(q.order + x);
+      apart |= from != x;
+      x = from;
+    }
+    out->row[32 * i + lane] = x;
+    id[i] = __ldg(p.ids + x);
     which[i] = -1;
   }
+  apart = __any_sync(0xFFFFFFFFu, apart);
 #pragma unroll
   for (int i = 0; i < kTile / 32; ++i)
     if (id[i] >= p.count) {
@@ -446,10 +566,33 @@ __device__ __forceinline__ void find_segment(const AdapterParams& p, unsigned in
   if (lane == 0) {
     out->tile = tile;
     out->first = first;
+    out->apart = apart;
     out->count = min(per_tile - first, static_cast<int>(u_end - u));
     out->adapters = n;
   }
   __syncwarp();
+}
+
+// A tile's rows, 64 columns of them, by one thread.  `rows` is the same matrix in boxes of one row.
+__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* tiles, const CUtensorMap* rows, uint64_t* bar,
+                                          int col, const Segment& s) {
+  if (s.apart) {
+#pragma unroll 4
+    for (int i = 0; i < kTile / 4; ++i)
+      tma_gather4(dst + i * (4 * kCols * 2), rows, bar, col, *reinterpret_cast<const int4*>(s.row + 4 * i));
+  } else {
+    tma_load_2d(dst, tiles, bar, col, s.tile * kTile);
+  }
+}
+__device__ __forceinline__ void store_rows(const uint8_t* src, const CUtensorMap* tiles, const CUtensorMap* rows, int col,
+                                           const Segment& s) {
+  if (s.apart) {
+#pragma unroll 4
+    for (int i = 0; i < kTile / 4; ++i)
+      tma_scatter4(rows, src + i * (4 * kCols * 2), col, *reinterpret_cast<const int4*>(s.row + 4 * i));
+  } else {
+    tma_store_2d(tiles, src, col, s.tile * kTile);
+  }
 }
 
 // ------------------------------------------------------------------ A x
@@ -468,7 +611,8 @@ constexpr int kDownThreads = (4 + 2 + kIssue) * 32;  // sums, segments, copies, 
 
 template <int KB>
 __global__ void __launch_bounds__(kDownThreads, 1)
-    adapters_down_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
+    adapters_down_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xrows,
+                         const __grid_constant__ CUtensorMap amap,
                          const __grid_constant__ ManyParams q) {
   using C = DownCfg<KB>;
   constexpr int ROWS = C::ROWS, ADS = C::ADS;
@@ -562,7 +706,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     for (int i = 0; ok; ++i) {
       if (i >= 2) ok = mbar_wait(&seg_empty[i & 1], ((i >> 1) - 1) & 1);
       if (!ok) break;
-      find_segment(p, u, end, q.kbs, u % q.kbs == 0, false, &s_seg[i & 1]);
+      find_segment(q, u, end, q.kbs, u % q.kbs == 0, false, &s_seg[i & 1]);
       const int count = s_seg[i & 1].count;
       if (lane == 0) mbar_arrive(&seg_full[i & 1]);
       __syncwarp();
@@ -589,7 +733,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
           if (row >= C::R) ok = mbar_wait(&row_empty[at], (row / C::R - 1) & 1);
           if (!ok) return;
           mbar_arrive_expect_tx(&row_full[at], kRowTile);
-          tma_load_2d(row_s + at * kRowTile, &xmap, &row_full[at], col, s.tile * kTile);
+          load_rows(row_s + at * kRowTile, &xmap, &xrows, &row_full[at], col, s);
           ++row;
           for (int w = w0; w < min(s.adapters, w0 + C::PASS); ++w, ++ad) {
             const int to = x * C::A + ad % C::A;
@@ -693,7 +837,8 @@ constexpr int kUpThreads = (kSumWarps + kHWarps + 3 + kIssue) * 32;  // ..., seg
 template <int KB>
 __global__ void __launch_bounds__(kUpThreads, 1)
     adapters_up_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap ymap,
-                       const __grid_constant__ CUtensorMap omap, const __grid_constant__ ManyParams q) {
+                       const __grid_constant__ CUtensorMap yrows, const __grid_constant__ CUtensorMap omap,
+                       const __grid_constant__ CUtensorMap orows, const __grid_constant__ ManyParams q) {
   using C = UpCfg<KB>;
   constexpr int ROWS = C::ROWS, ADS = C::ADS, HS = C::HS, D2S = C::D2S;
   constexpr int H0 = kSumWarps, SEG = H0 + kHWarps, COPY = SEG + 1, STORE = COPY + 1, ISSUE = STORE + 1;  // warps
@@ -858,6 +1003,10 @@ __global__ void __launch_bounds__(kUpThreads, 1)
             const int e = e0 + j * STEP, x = e / pieces8, c = e - x * pieces8;
             if (x >= kTile) break;
             const float scale = s.scale[x];
+            if (8 * c >= p.r) {  // (behind the rank, an infinite x has made zeros into what is not a number)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) sum[j][k] = 0.0f;
+            }
             uint32_t big[4], rest[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -886,7 +1035,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     for (int i = 0; ok; ++i) {
       if (i >= 2) ok = mbar_wait(&seg_empty[i & 1], ((i >> 1) - 1) & 1);
       if (!ok) break;
-      find_segment(p, u, end, q.nbs, false, true, &s_seg[i & 1]);
+      find_segment(q, u, end, q.nbs, false, true, &s_seg[i & 1]);
       const int count = s_seg[i & 1].count;
       if (lane == 0) mbar_arrive(&seg_full[i & 1]);
       __syncwarp();
@@ -913,7 +1062,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
           if (row >= ROWS) ok = mbar_wait(&row_empty[at], (row / ROWS - 1) & 1);
           if (!ok) break;
           mbar_arrive_expect_tx(&row_full[at], kRowTile);
-          tma_load_2d(row_s + at * kRowTile, &ymap, &row_full[at], col, s.tile * kTile);
+          load_rows(row_s + at * kRowTile, &ymap, &yrows, &row_full[at], col, s);
           ++row;
           int ad = x ? ads[1] : ads[0];
           for (int w = 0; w < s.adapters; ++w, ++ad) {
@@ -947,14 +1096,12 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       ok = wait_segment(i);
       const Segment& s = s_seg[i & 1];
       if (!ok || s.count == 0) break;
-      const int count = s.count, tile = s.tile, first = s.first;
-      done_with(i);
       if (lane == 0) {
-        for (int n = 0; n < count && ok; ++n, ++row) {
+        for (int n = 0; n < s.count && ok; ++n, ++row) {
           const int stage = row % ROWS;
           ok = mbar_wait(&out_full[stage], (row / ROWS) & 1);
           if (!ok) break;
-          tma_store_2d(&omap, row_s + stage * kRowTile, (first + n) * kCols, tile * kTile);
+          store_rows(row_s + stage * kRowTile, &omap, &orows, (s.first + n) * kCols, s);
           bulk_commit();
           if (row > 0) {  // the store before this one has read its tile
             asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
@@ -963,6 +1110,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         }
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      done_with(i);
     }
     if (lane == 0) {
       bulk_wait_all();
@@ -1025,14 +1173,17 @@ __global__ void __launch_bounds__(kUpThreads, 1)
 inline Deal deal_k(int64_t T, int64_t K, int sms) {
   return Deal::of(static_cast<unsigned int>((T + kTile - 1) / kTile * ((K + kCols - 1) / kCols)), sms, kLeastK);
 }
-inline size_t many_bytes(int64_t T, int64_t K, int64_t r, int sms) {
-  return T <= kFewRows ? 0 : static_cast<size_t>((T + kTile - 1) / kTile + deal_k(T, K, sms).ctas) * kTile *
-                                 static_cast<size_t>((r + 15) / 16 * 16) * sizeof(float);
+inline size_t part_bytes(int64_t T, int64_t K, int64_t r, int sms) {
+  return static_cast<size_t>((T + kTile - 1) / kTile + deal_k(T, K, sms).ctas) * kTile *
+         static_cast<size_t>((r + 15) / 16 * 16) * sizeof(float);
+}
+inline size_t many_bytes(int64_t T, int64_t K, int64_t r, int sms) {  // sums, whether sorted, the rows
+  return T <= kFewRows ? 0 : part_bytes(T, K, r, sms) + static_cast<size_t>((T + kWindow - 1) / kWindow + T) * sizeof(int32_t);
 }
 
 template <int KB>
 sp24_status launch_many(const AdapterParams& p, float* part, const DeviceInfo& dev, cudaStream_t s) {
-  CUtensorMap x, a, b, y, o;
+  CUtensorMap x, a, b, y, o, x1, y1, o1;
   const auto type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
   ManyParams q;
@@ -1042,15 +1193,28 @@ sp24_status launch_many(const AdapterParams& p, float* part, const DeviceInfo& d
   q.k = deal_k(p.T, p.K, dev.sm_count);
   q.n = Deal::of(static_cast<unsigned int>((p.T + kTile - 1) / kTile) * q.nbs, dev.sm_count, kLeastN);
   q.part = part;
+  q.order = q.sorted = nullptr;
+  const unsigned windows = static_cast<unsigned>((p.T + kWindow - 1) / kWindow);
+  if (p.count > 1) {
+    q.sorted = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(part) + part_bytes(p.T, p.K, p.r, dev.sm_count));
+    q.order = q.sorted + windows;
+  }
   sp24_status st = make_tmap_2d(&x, p.x, type, p.K, p.T, p.ldx * 2, kCols, kTile, swizzle);
   if (!st) st = make_tmap_2d(&y, p.y, type, p.N, p.T, p.ldy * 2, kCols, kTile, swizzle);
   if (!st) st = make_tmap_2d(&o, p.out, type, p.N, p.T, p.ldo * 2, kCols, kTile, swizzle);
+  if (!st) st = make_tmap_2d(&x1, p.x, type, p.K, p.T, p.ldx * 2, kCols, 1, swizzle);
+  if (!st) st = make_tmap_2d(&y1, p.y, type, p.N, p.T, p.ldy * 2, kCols, 1, swizzle);
+  if (!st) st = make_tmap_2d(&o1, p.out, type, p.N, p.T, p.ldo * 2, kCols, 1, swizzle);
   if (!st) st = make_tmap_3d(&a, p.a, type, p.K, p.r, p.count, uint64_t(p.K) * 2, p.stride_a * 2, kCols, q.rp, swizzle);
   if (!st) st = make_tmap_3d(&b, p.b, type, p.r, p.N, p.count, uint64_t(p.r) * 2, p.stride_b * 2, 64, kCols, swizzle);
   if (st) return st;
-  if (launch_pdl_smem<adapters_down_kernel<KB>>(dev, dim3(q.k.ctas), dim3(kDownThreads), DownCfg<KB>::SMEM, s, x, a, q) !=
+  int bits = 0;
+  while (int64_t(p.count) >> bits) ++bits;  // of ids + 1
+  if ((q.order && launch_pdl_smem<adapters_sort_kernel>(dev, dim3(windows), dim3(kSortThreads), sizeof(SortSmem), s, q,
+                                                        bits) != cudaSuccess) ||
+      launch_pdl_smem<adapters_down_kernel<KB>>(dev, dim3(q.k.ctas), dim3(kDownThreads), DownCfg<KB>::SMEM, s, x, x1, a, q) !=
           cudaSuccess ||
-      launch_pdl_smem<adapters_up_kernel<KB>>(dev, dim3(q.n.ctas), dim3(kUpThreads), UpCfg<KB>::SMEM, s, b, y, o, q) !=
+      launch_pdl_smem<adapters_up_kernel<KB>>(dev, dim3(q.n.ctas), dim3(kUpThreads), UpCfg<KB>::SMEM, s, b, y, y1, o, o1, q) !=
           cudaSuccess)
     return SP24_ERR_CUDA;
   return SP24_OK;
@@ -1061,10 +1225,11 @@ cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream
   using C = FewCfg<MT, NT>;
   constexpr auto kern = add_adapters_few_kernel<MT, NT>;
   // Each adapter's last item may be partly filled; rows without an adapter count as one more.
-  const int64_t adapters = std::min<int64_t>(p.T, p.count), items = std::min<int64_t>(p.T, p.T / C::R + adapters + 1);
+  const int64_t T = std::min(p.T, kFewRows), blocks = (p.T + kFewRows - 1) / kFewRows;
+  const int64_t adapters = std::min<int64_t>(T, p.count), items = std::min<int64_t>(T, T / C::R + adapters + 1);
   // As many CTAs per item as run at once, for as many items as rows spread evenly over the adapters come to.  (200 rows
   // of 20 adapters, rank 64, K 14336, 1 CTA per SM: 14 clusters of 8 fit, 24 of 6; 26 us with 8 and 17 with 6.)
-  const int64_t likely = std::min(items, adapters * ((p.T / adapters + C::R - 1) / C::R) + 1);
+  const int64_t likely = blocks * std::min(items, adapters * ((T / adapters + C::R - 1) / C::R) + 1);
   static std::atomic<int> most[64][kMostCluster + 1];  // clusters of each size that fit at once, + 1
   unsigned cluster = kMostCluster;
   for (; cluster > 2; --cluster) {
@@ -1092,13 +1257,13 @@ cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream
     }
     if (likely <= n - 1) break;
   }
-  return launch_pdl_clusters_smem<kern>(dev, cluster, dim3(static_cast<unsigned>(items * cluster)), dim3(kThreads), C::SMEM, s,
-                                        p);
+  return launch_pdl_clusters_smem<kern>(dev, cluster, dim3(static_cast<unsigned>(blocks * items * cluster)), dim3(kThreads),
+                                        C::SMEM, s, p, static_cast<int>(items));
 }
 // Rows per item: enough that an adapter is rarely read more than once.
 template <int MT>
 cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream_t s) {
-  const int64_t each = p.T / std::min<int64_t>(p.T, p.count);
+  const int64_t T = std::min(p.T, kFewRows), each = T / std::min<int64_t>(T, p.count);
   if (MT <= 4 && each > 12) return launch_few<MT, MT <= 4 ? 4 : 2>(p, dev, s);
   return each > 4 ? launch_few<MT, 2>(p, dev, s) : launch_few<MT, 1>(p, dev, s);
 }
@@ -1156,7 +1321,7 @@ extern "C" sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void*
   p.err = dev->err_word;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (T > kFewRows)
+  if (T > kFewRows && (T > kFewScattered || count < kScattered))
     return r <= 64 ? launch_many<1>(p, static_cast<float*>(workspace), *dev, s)
                    : launch_many<2>(p, static_cast<float*>(workspace), *dev, s);
   if (r <= 16)

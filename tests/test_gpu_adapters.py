@@ -214,3 +214,78 @@ def test_workspace(sp24):
         sp24.add_adapters(y, x, a, b, ids, workspace=torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2])
     with pytest.raises(ValueError, match="alignment|ALIGNMENT"):
         sp24.add_adapters(y, x, a, b, ids, workspace=torch.empty(need + 16, dtype=torch.uint8, device="cuda")[1:])
+
+
+@pytest.mark.parametrize("T,K,N,r,count", [
+    (513, 264, 136, 24, 31),       # the last row's tile has no other
+    (1023, 520, 264, 16, 300),     # two bytes of ids
+    (1100, 1032, 1096, 40, 90),
+    (2175, 256, 328, 72, 2),       # two adapters in turn
+    (8191, 72, 200, 8, 20),
+    (8193, 64, 136, 16, 6),        # one row in a window of its own
+    (20000, 64, 72, 8, 70000),     # three bytes, most adapters nobody's
+])
+def test_many_rows_in_no_order(sp24, T, K, N, r, count):
+    """Adapters scattered over the rows, some rows without one and one id out of range; in place and not, the same bits
+    every time."""
+    y, x, a, b, scales = inputs(T, K, N, r, min(count, 300), seed=T)
+    used = torch.randint(0, count, (300,), generator=torch.Generator().manual_seed(T))
+    if count > 300:                                     # 300 different ones
+        a = a[torch.arange(count) % 300]
+        b = b[torch.arange(count) % 300]
+        scales = scales[torch.arange(count) % 300]
+    ids = ids_of(T, count, "any", T)
+    if count == 2:
+        ids = (torch.arange(T) % 2).to(torch.int32)
+    if count == 70000:
+        ids = torch.where(ids < 0, ids, used[torch.arange(T) % 300].to(torch.int32))
+    ids[T // 2] = count
+    args = [t.cuda() for t in (y, x, a, b, ids, scales)]
+    first = sp24.add_adapters(*args)
+    with pytest.raises(sp24.Sp24Error) as e:
+        sp24.last_device_error()
+    assert e.value.status == 8
+    out, size = reference(y, x, a, b, torch.where(ids == count, -1, ids), scales)
+    assert_adapted(first, out, size, "scattered")
+    bare = (ids < 0) | (ids == count)
+    assert torch.equal(first.cpu()[bare], y[bare])
+    for _ in range(5):
+        again = args[0].clone()
+        sp24.add_adapters(again, *args[1:], out=again)
+        assert torch.equal(first, again)
+    with pytest.raises(sp24.Sp24Error):
+        sp24.last_device_error()
+
+
+@pytest.mark.parametrize("first", [True, False])
+def test_rows_in_order_beside_rows_in_none(sp24, first):
+    """Tiles that stay as they are beside tiles put together from everywhere, and windows that are sorted beside ones
+    that are not."""
+    T, K, N, r, count = 9300, 136, 200, 16, 460
+    g = torch.Generator().manual_seed(5)
+    short = torch.arange(2000) // 5                       # in order, but in short runs
+    mixed = torch.randint(400, count, (6192,), generator=g)
+    runs = torch.arange(T - 8192) // 300
+    ids = torch.cat((short, mixed, runs) if first else (mixed, short, runs)).to(torch.int32)
+    y, x, a, b, scales = inputs(T, K, N, r, count, seed=6)
+    args = [t.cuda() for t in (y, x, a, b, ids, scales)]
+    got = sp24.add_adapters(*args)
+    sp24.last_device_error()
+    out, size = reference(y, x, a, b, ids, scales)
+    assert_adapted(got, out, size, "in order and in none")
+    again = args[0].clone()
+    assert torch.equal(got, sp24.add_adapters(again, *args[1:], out=again))
+
+
+def test_an_infinite_value_has_the_sign_of_its_products(sp24):
+    """Ranks that are no multiple of 16: what pads them adds nothing, not even to a row with an infinite value."""
+    for T in (20, 800):
+        y, x, a, b, _ = inputs(T, 64, 136, 8, 2, seed=T)
+        a, b = a.abs() + 0.5, b.abs() + 0.5
+        x[7, 3], x[11, 3] = float("inf"), float("-inf")
+        got = sp24.add_adapters(y.cuda(), x.cuda(), a.cuda(), b.cuda(), torch.zeros(T, dtype=torch.int32, device="cuda"))
+        sp24.last_device_error()
+        assert (got[7] == float("inf")).all() and (got[11] == float("-inf")).all()
+        rest = torch.ones(T, dtype=torch.bool)
+        rest[7], rest[11] = False, False
+        assert torch.isfinite(got.cpu()[rest].float()).all()
