@@ -522,21 +522,27 @@ __device__ __forceinline__ void find_segment(const ManyParams& q, unsigned int u
     return;
   }
   const int tile = u / per_tile, first = u - tile * per_tile;
-  const bool sorted = q.order && __ldcg(q.sorted + tile / (kWindow / kTile));
+  const int sorted = q.order ? __ldcg(q.sorted + tile / (kWindow / kTile)) : 0;
   int id[kTile / 32], which[kTile / 32];
   bool apart = false;
+  int x[kTile / 32];
 #pragma unroll
   for (int i = 0; i < kTile / 32; ++i) {
-    int x = min(tile * kTile + 32 * i + lane, p.T - 1);  // (behind the last row: that row again, with the same result)
-    if (sorted) {
-      const int from = __ldcg(q.order + x);
-      apart |= from != x;
-      x = from;
-    }
-    out->row[32 * i + lane] = x;
-    id[i] = __ldg(p.ids + x);
+    x[i] = min(tile * kTile + 32 * i + lane, p.T - 1);  // (behind the last row: that row again, with the same result)
+    id[i] = __ldg(p.ids + x[i]);                        // (on its way together with whether rows have been sorted)
     which[i] = -1;
   }
+  if (sorted) {
+#pragma unroll
+    for (int i = 0; i < kTile / 32; ++i) {
+      const int from = __ldcg(q.order + x[i]);
+      apart |= from != x[i];
+      x[i] = from;
+      id[i] = __ldg(p.ids + from);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTile / 32; ++i) out->row[32 * i + lane] = x[i];
   apart = __any_sync(0xFFFFFFFFu, apart);
 #pragma unroll
   for (int i = 0; i < kTile / 32; ++i)
