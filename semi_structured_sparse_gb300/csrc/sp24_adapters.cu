@@ -588,24 +588,26 @@ __device__ __forceinline__ void find_segment(const ManyParams& q, unsigned int u
   __syncwarp();
 }
 
-// A tile's rows, 64 columns of them, by one thread.  `rows` is the same matrix in boxes of one row.
+__device__ __forceinline__ bool all_of(bool x) { return __all_sync(0xFFFFFFFFu, x); }
+// A tile's rows, 64 columns of them, by a warp: four rows per lane where they are apart.  `rows` is the same matrix in
+// boxes of one row.
 __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* tiles, const CUtensorMap* rows, uint64_t* bar,
                                           int col, const Segment& s) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) mbar_arrive_expect_tx(bar, kRowTile);
+  __syncwarp();
   if (s.apart) {
-#pragma unroll 4
-    for (int i = 0; i < kTile / 4; ++i)
-      tma_gather4(dst + i * (4 * kCols * 2), rows, bar, col, *reinterpret_cast<const int4*>(s.row + 4 * i));
-  } else {
+    tma_gather4(dst + lane * (4 * kCols * 2), rows, bar, col, *reinterpret_cast<const int4*>(s.row + 4 * lane));
+  } else if (lane == 0) {
     tma_load_2d(dst, tiles, bar, col, s.tile * kTile);
   }
 }
 __device__ __forceinline__ void store_rows(const uint8_t* src, const CUtensorMap* tiles, const CUtensorMap* rows, int col,
                                            const Segment& s) {
+  const int lane = threadIdx.x & 31;
   if (s.apart) {
-#pragma unroll 4
-    for (int i = 0; i < kTile / 4; ++i)
-      tma_scatter4(rows, src + i * (4 * kCols * 2), col, *reinterpret_cast<const int4*>(s.row + 4 * i));
-  } else {
+    tma_scatter4(rows, src + lane * (4 * kCols * 2), col, *reinterpret_cast<const int4*>(s.row + 4 * lane));
+  } else if (lane == 0) {
     tma_store_2d(tiles, src, col, s.tile * kTile);
   }
 }
@@ -733,39 +735,37 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     // ---------------------------------------------------------------- copies
     int rows[kIssue] = {}, ads[kIssue] = {};  // so far, of each issuing warp's
     for (int i = 0; ok; ++i) {
-      ok = wait_segment(i);
+      ok = all_of(wait_segment(i));
       const Segment& s = s_seg[i & 1];
       if (!ok || s.count == 0) break;
-      if (lane == 0) {
-        auto load = [&](int w0, int k, int x, int& row, int& ad) {
-          const int col = (s.first + k) * kCols, at = x * C::R + row % C::R;
+      auto load = [&](int w0, int k, int x, int& row, int& ad) {
+        const int col = (s.first + k) * kCols, at = x * C::R + row % C::R;
 #ifdef SP24_FAULT_WITHHOLD_FIRST_STAGE
-          if (x == 0 && row == 0) {  // the fault-test build: each CTA's first tile never comes
-            ++row;
-            return;
-          }
-#endif
-          if (row >= C::R) ok = mbar_wait(&row_empty[at], (row / C::R - 1) & 1);
-          if (!ok) return;
-          mbar_arrive_expect_tx(&row_full[at], kRowTile);
-          load_rows(row_s + at * kRowTile, &xmap, &xrows, &row_full[at], col, s);
+        if (x == 0 && row == 0) {  // the fault-test build: each CTA's first tile never comes
           ++row;
-          for (int w = w0; w < min(s.adapters, w0 + C::PASS); ++w, ++ad) {
-            const int to = x * C::A + ad % C::A;
-            if (ad >= C::A) ok = mbar_wait(&ad_empty[to], (ad / C::A - 1) & 1);
-            if (!ok) return;
+          return;
+        }
+#endif
+        if (row >= C::R) ok = all_of(mbar_wait(&row_empty[at], (row / C::R - 1) & 1));
+        if (!ok) return;
+        load_rows(row_s + at * kRowTile, &xmap, &xrows, &row_full[at], col, s);
+        ++row;
+        for (int w = w0; w < min(s.adapters, w0 + C::PASS); ++w, ++ad) {
+          const int to = x * C::A + ad % C::A;
+          if (ad >= C::A) ok = all_of(mbar_wait(&ad_empty[to], (ad / C::A - 1) & 1));
+          if (!ok) return;
+          if (lane == 0) {
             mbar_arrive_expect_tx(&ad_full[to], q.rp * 128);
             tma_load_3d(ad_s + to * C::AD_TILE, &amap, &ad_full[to], col, 0, s.adapter[w]);
           }
-        };
-        for (int w0 = 0; w0 < s.adapters && ok; w0 += C::PASS)
-          for (int k = 0; k < s.count && ok; k += kIssue) {
+        }
+      };
+      for (int w0 = 0; w0 < s.adapters && ok; w0 += C::PASS)
+        for (int k = 0; k < s.count && ok; k += kIssue) {
 #pragma unroll
-            for (int x = 0; x < kIssue; ++x)
-              if (k + x < s.count && ok) load(w0, k + x, x, rows[x], ads[x]);
-          }
-      }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+          for (int x = 0; x < kIssue; ++x)
+            if (k + x < s.count && ok) load(w0, k + x, x, rows[x], ads[x]);
+        }
       done_with(i);
     }
     if (lane == 0) {
@@ -1062,37 +1062,35 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     // ---------------------------------------------------------------- copies
     int row = 0, ads[kIssue] = {};  // so far: tiles of y, and of B for each issuing warp
     for (int i = 0; ok; ++i) {
-      ok = wait_segment(i);
+      ok = all_of(wait_segment(i));
       const Segment& s = s_seg[i & 1];
       if (!ok || s.count == 0) break;
-      if (lane == 0) {
-        for (int n = 0; n < s.count && ok; ++n) {
-          const int col = (s.first + n) * kCols, at = row % ROWS, x = row % kIssue;
+      for (int n = 0; n < s.count && ok; ++n) {
+        const int col = (s.first + n) * kCols, at = row % ROWS, x = row % kIssue;
 #ifdef SP24_FAULT_WITHHOLD_FIRST_STAGE
-          if (row == 0) {
-            ++row;
-            continue;
-          }
-#endif
-          if (row >= ROWS) ok = mbar_wait(&row_empty[at], (row / ROWS - 1) & 1);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&row_full[at], kRowTile);
-          load_rows(row_s + at * kRowTile, &ymap, &yrows, &row_full[at], col, s);
+        if (row == 0) {
           ++row;
-          int ad = x ? ads[1] : ads[0];
-          for (int w = 0; w < s.adapters; ++w, ++ad) {
-            const int to = x * C::A + ad % C::A;
-            if (ad >= C::A) ok = mbar_wait(&ad_empty[to], (ad / C::A - 1) & 1);
-            if (!ok) break;
+          continue;
+        }
+#endif
+        if (row >= ROWS) ok = all_of(mbar_wait(&row_empty[at], (row / ROWS - 1) & 1));
+        if (!ok) break;
+        load_rows(row_s + at * kRowTile, &ymap, &yrows, &row_full[at], col, s);
+        ++row;
+        int ad = x ? ads[1] : ads[0];
+        for (int w = 0; w < s.adapters; ++w, ++ad) {
+          const int to = x * C::A + ad % C::A;
+          if (ad >= C::A) ok = all_of(mbar_wait(&ad_empty[to], (ad / C::A - 1) & 1));
+          if (!ok) break;
+          if (lane == 0) {
             mbar_arrive_expect_tx(&ad_full[to], KB * 64 * 128);
 #pragma unroll
             for (int k = 0; k < KB; ++k)
               tma_load_3d(ad_s + to * C::AD_TILE + k * 64 * 128, &bmap, &ad_full[to], 64 * k, col, s.adapter[w]);
           }
-          (x ? ads[1] : ads[0]) = ad;
         }
+        (x ? ads[1] : ads[0]) = ad;
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       done_with(i);
     }
     if (lane == 0) {
@@ -1108,27 +1106,25 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     // ---------------------------------------------------------------- stores
     int row = 0;
     for (int i = 0; ok; ++i) {
-      ok = wait_segment(i);
+      ok = all_of(wait_segment(i));
       const Segment& s = s_seg[i & 1];
       if (!ok || s.count == 0) break;
-      if (lane == 0) {
-        for (int n = 0; n < s.count && ok; ++n, ++row) {
-          const int stage = row % ROWS;
-          ok = mbar_wait(&out_full[stage], (row / ROWS) & 1);
-          if (!ok) break;
-          store_rows(row_s + stage * kRowTile, &omap, &orows, (s.first + n) * kCols, s);
-          bulk_commit();
-          if (row > 0) {  // the store before this one has read its tile
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            mbar_arrive(&row_empty[(row - 1) % ROWS]);
-          }
+      for (int n = 0; n < s.count && ok; ++n, ++row) {
+        const int stage = row % ROWS;
+        ok = all_of(mbar_wait(&out_full[stage], (row / ROWS) & 1));
+        if (!ok) break;
+        store_rows(row_s + stage * kRowTile, &omap, &orows, (s.first + n) * kCols, s);
+        bulk_commit();
+        if (row > 0) {  // the store before this one has read its tile
+          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&row_empty[(row - 1) % ROWS]);
         }
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       done_with(i);
     }
+    bulk_wait_all();
     if (lane == 0) {
-      bulk_wait_all();
       if (!ok) atomicOr(p.err, DEVERR_TIMEOUT_EPILOGUE);
     }
     __syncwarp();
