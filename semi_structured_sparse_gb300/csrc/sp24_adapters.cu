@@ -12,8 +12,8 @@
 //
 // Measured (GB300, in a graph): 1 row of 4096 values, rank 16, N 4096 4.9 us; 64 rows with an
 // adapter each, N 6144 9.1 us; 200 rows of 20 adapters in no order, K 14336, rank 64,
-// N 4096 18.1 us; 3000 rows of 16 adapters in runs, rank 32, N 14336 50 us (58 % of the measured
-// copy rate); 8192 rows of 8 in runs, rank 64, K = N = 4096 55 us, of one 45 us (56 and 68 %).
+// N 4096 18.1 us; 3000 rows of 16 adapters in runs, rank 32, N 14336 48 us (60 % of the measured
+// copy rate); 8192 rows of 8 in runs, rank 64, K = N = 4096 54 us, of one 44 us (57 and 70 %).
 #include <cuda_bf16.h>
 #include <algorithm>
 #include <cmath>
@@ -413,8 +413,9 @@ struct ManyParams {
 // sorts them by adapter in windows, unless an adapter's rows mostly stand in runs.  A tile is then 128 rows in that
 // order, fetched and stored four rows per copy where they are apart.  A radix sort that counts a digit's rows by
 // warp, each warp's in order, keeps equal ones as they were and needs no atomics, so the results are the same
-// every time.  (4096 rows of 4096 values, rank 16, 64 adapters, in no order: 90 us, 555 without the sort, 48 if each
-// adapter's rows stand together.  Fetching all tiles row by row: 8192 rows with one adapter 116 us instead of 45.)
+// every time.  (4096 rows of 4096 values, rank 16, 64 adapters, in no order: 74 us, 555 without the sort, 45 if each
+// adapter's rows stand together.  Fetching all tiles row by row: 8192 rows with one adapter 116 us instead of 45, all
+// copies issued by one thread.)
 constexpr int kWindow = 8192, kSortThreads = 1024, kDigits = 256, kSortWarps = kSortThreads / 32;
 constexpr int kEach = kWindow / kSortThreads, kHistRow = kSortWarps + 1;
 constexpr int kLongRuns = 2;  // changes of adapter per tile up to which rows stay as they are
@@ -589,8 +590,8 @@ __device__ __forceinline__ void find_segment(const ManyParams& q, unsigned int u
 }
 
 __device__ __forceinline__ bool all_of(bool x) { return __all_sync(0xFFFFFFFFu, x); }
-// A tile's rows, 64 columns of them, by a warp: four rows per lane where they are apart.  `rows` is the same matrix in
-// boxes of one row.
+// A tile's rows, 64 columns of them, by a warp: four rows per lane where they are apart (by one lane, 4096 rows of 64
+// adapters in no order took 89 us, 74 so).  `rows` is the same matrix in boxes of one row.
 __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* tiles, const CUtensorMap* rows, uint64_t* bar,
                                           int col, const Segment& s) {
   const int lane = threadIdx.x & 31;

@@ -277,6 +277,28 @@ def test_rows_in_order_beside_rows_in_none(sp24, first):
     assert torch.equal(got, sp24.add_adapters(again, *args[1:], out=again))
 
 
+@pytest.mark.parametrize("K", [64, 1000])
+@pytest.mark.parametrize("r", [16, 104])
+def test_tiles_of_very_different_cost(sp24, K, r):
+    """One tile of 128 adapters, some of few, some of none: every part of every sum is there."""
+    T, N, count = 8192 + 640, 136, 140
+    ids = torch.full((T,), 3)
+    ids[1280:1408] = torch.arange(128)
+    ids[2000:4000] = -1
+    ids[4100:4110] = torch.arange(10) + 128
+    ids[8000:8300] = 139
+    ids = ids.to(torch.int32)
+    y, x, a, b, scales = inputs(T, K, N, r, count, seed=r + K)
+    args = [t.cuda() for t in (y, x, a, b, ids, scales)]
+    need = sp24.add_adapters_workspace_size(T, K, r)
+    workspace = torch.full((need,), 255, dtype=torch.uint8, device="cuda")   # parts that nobody writes are no numbers
+    got = sp24.add_adapters(*args, workspace=workspace)
+    sp24.last_device_error()
+    out, size = reference(y, x, a, b, ids, scales)
+    assert_adapted(got, out, size, "tiles of different cost")
+    assert torch.equal(got, sp24.add_adapters(*args, workspace=workspace))
+
+
 def test_an_infinite_value_has_the_sign_of_its_products(sp24):
     """Ranks that are no multiple of 16: what pads them adds nothing, not even to a row with an infinite value."""
     for T in (20, 800):
