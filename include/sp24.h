@@ -582,7 +582,7 @@ SP24_API size_t sp24_attention_decode_shared_workspace_size(int64_t B, int64_t G
  *           reported by sp24_last_device_error (SP24_ERR_DEVICE_INDEX).  Places
  *           that a call both reads and writes, or writes twice, hold a mixture
  *           afterwards.
- * Preconditions: T >= 0; the caches have the same heads (at most 65536) and
+ * Preconditions: T >= 0; the caches have the same heads (at most 65535) and
  * head_dim.
  */
 SP24_API sp24_status sp24_cache_copy(const sp24_kv_cache* src, const int64_t* src_slots, const sp24_kv_cache* dst,
@@ -608,6 +608,8 @@ SP24_API sp24_status sp24_cache_copy(const sp24_kv_cache* src, const int64_t* sr
  *        least often); scales (device) fp32 [count], or NULL for 1.
  *   out  (device, out) bf16 [T][N], row stride ldo; may be Y (with ldo = ldy),
  *        and overlaps nothing else.
+ * Values of the adapters in use are finite: an infinite one makes not-a-numbers of
+ * the results it reaches.
  *   workspace, workspace_bytes: device scratch of at least
  *        sp24_add_adapters_workspace_size bytes, 16-byte aligned, of any contents
  *        (may be NULL when that size is 0, as it is for few rows).  Calls that

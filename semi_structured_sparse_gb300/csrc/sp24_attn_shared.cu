@@ -167,7 +167,7 @@ extern "C" sp24_status sp24_attention_decode_shared(const void* q, int64_t B, in
   // Sharing saves at most the groups' tokens but for one time each.  Where that takes less time than the two launches
   // more (2 sequences behind 1000 tokens, 4 MB: 14.2 us shared, 8.5 one by one), the sequences are attended one by one.
   const int64_t e = cache->dtype == SP24_E4M3 ? 1 : 2;
-  const int64_t saved = (table_width << c.view.page_shift) * (B - 1) * cache->heads * (2 * cache->head_dim * e);
+  const double saved = double(table_width << c.view.page_shift) * (B - 1) * cache->heads * (2 * cache->head_dim * e);
   if (G == 0 || saved < kLeastSaved)
     return sp24_attention_decode(q, B, ldq, q_heads, cache, page_table, table_width, ld_table, seq_lens, scale, window, sinks,
                                  Y, ldy, workspace, workspace_bytes, stream);

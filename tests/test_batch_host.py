@@ -139,3 +139,12 @@ def test_shared_and_copy_shapes_are_refused(monkeypatch):
             s.cache_copy(c, i, c, j)
     with pytest.raises(ValueError, match="same heads"):
         s.cache_copy(c, slots, other, slots)
+
+
+def test_copy_takes_as_many_heads_as_a_grid_has(lib):
+    n = 1 << 16
+    a = cache(heads=n, page_stride=n * 16 * 64)
+    assert lib.sp24_cache_copy(ctypes.addressof(a), P, ctypes.addressof(a), P, 1, None) == INVALID
+    n -= 1
+    a = cache(heads=n, page_stride=n * 16 * 64)
+    assert lib.sp24_cache_copy(ctypes.addressof(a), P, ctypes.addressof(a), P, 0, None) != INVALID
