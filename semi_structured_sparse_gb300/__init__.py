@@ -930,7 +930,7 @@ def add_adapters(y, x, a, b, ids, scales=None, out=None, workspace=None, stream=
         raise ValueError("the arguments' layouts are not ones that the library takes")
     size = 0
     if workspace is None:
-        need = T > 512 and _on(at, lib.sp24_add_adapters_workspace_size, T, K, r)  # (fewer rows never need any)
+        need = T > 1024 and _on(at, lib.sp24_add_adapters_workspace_size, T, K, r)  # (fewer rows never need any)
         if need:
             workspace, size = _new(need, _U8, stream, y.device), need
     elif isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and workspace.get_device() == at and \

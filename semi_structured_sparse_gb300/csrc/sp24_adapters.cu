@@ -27,10 +27,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMostCluster = 8;    // CTAs that share a few rows' work, at most
 constexpr int kMostRank = 128;
+constexpr int kNobody = -3;        // (ids are -1 and up, -2 behind the last row)
+constexpr int kSlots = 1024, kBitsRow = 20;  // (words; 16 are used, 20 keep banks apart)
 constexpr int kFewRows = 512;      // rows of a call that are sorted by adapter
-// So many adapters that up to so many rows have few of each: in blocks of kFewRows.  (1024 rows of 4096 values, rank 16,
-// 256 adapters: 54 us in blocks, 139 in tiles of 128 rows; of 8 adapters 26 and 19.)
-constexpr int kScattered = 32, kFewScattered = 1024;
+constexpr int kFew = 1024;         // rows up to which the form for few takes all, in blocks of kFewRows (4096 values, rank 16, 8
+                                   // adapters in runs: 1024 rows 11.5 us, in tiles 17.4; 2048 rows 22 and 20)
 
 struct AdapterParams {
   const __nv_bfloat16* y;
@@ -99,7 +100,6 @@ __global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kern
   float* const part = reinterpret_cast<float*>(smem);                       // [kWarps][R][RP]
   float* const recv = reinterpret_cast<float*>(smem + C::FIRST);            // [CTAs][R][RP]
   uint8_t* const h_s = smem + C::FIRST + C::RECV;                           // [2][R][HLD] bf16
-  __shared__ __align__(16) int s_id[kFewRows];
   __shared__ int s_count[kFewRows / 32], s_item[2], s_row[R];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t rank = cluster_rank(), ctas = cluster_nrank();
@@ -110,35 +110,77 @@ __global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kern
   // ---- this cluster's item: rows are numbered within their adapter; every R-th begins one
   constexpr int MINE = kFewRows / kThreads;
   int id[MINE], nth[MINE];
+  unsigned int same[MINE];
   bool first[MINE];
 #pragma unroll
   for (int i = 0; i < MINE; ++i) {
     const int x = tid + i * kThreads;
     id[i] = -2;
     if (x < T) {
-      id[i] = p.ids[t0 + x];
+      id[i] = __ldg(p.ids + t0 + x);
       if (id[i] >= p.count) {
         if (item == 0) atomicOr(p.err, DEVERR_INDEX);
         id[i] = -1;
       }
       id[i] = max(id[i], -1);
     }
-    s_id[x] = id[i];
-    nth[i] = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {  // how many rows of these 32 before this one have its adapter
+    same[i] = __match_any_sync(0xFFFFFFFFu, id[i]);
+    nth[i] = __popc(same[i] & ((1u << lane) - 1));
+  }
+  // ... and of those before them.
+  if (T > 32) {
+    // Each adapter has a slot in a table, there its first row, and at that row the bits of all its rows.
+    // (Slots depend on who comes first, the rest on the ids alone: all CTAs find the same.)
+    int* const key = reinterpret_cast<int*>(smem);
+    int* const head = key + kSlots;
+    unsigned int* const bits = reinterpret_cast<unsigned int*>(head + kSlots);  // [rows][kBitsRow]
+    static_assert(C::FIRST >= (2 * kSlots + kFewRows * kBitsRow) * 4, "the table is where the ring will be");
+    const int slot_bits = T <= kSlots / 8 ? 8 : 10, slots = 1 << slot_bits;
+    for (int j = tid; j < slots; j += kThreads) key[j] = kNobody, head[j] = kFewRows;
+    for (int j = tid; j < T * (kBitsRow / 4); j += kThreads) reinterpret_cast<uint4*>(bits)[j] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    int slot[MINE];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      slot[i] = 0;
+      if (nth[i] || id[i] < -1) continue;  // (the first of its 32 speaks for the others)
+      slot[i] = (static_cast<unsigned int>(id[i]) * 2654435769u) >> (32 - slot_bits);
+      while (true) {  // at most half of the slots are taken
+        const int who = atomicCAS(&key[slot[i]], kNobody, id[i]);
+        if (who == kNobody || who == id[i]) break;
+        slot[i] = (slot[i] + 1) & (slots - 1);
+      }
+      atomicMin(&head[slot[i]], tid + i * kThreads);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MINE; ++i)
+      if (!nth[i] && id[i] >= -1) bits[head[slot[i]] * kBitsRow + i * kWarps + warp] = same[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      int before = 0;
+      if (!nth[i] && id[i] >= -1) {
+        const unsigned int* const mine = bits + head[slot[i]] * kBitsRow;
+        const int upto = i * kWarps + warp;
+#pragma unroll
+        for (int w = 0; w < kFewRows / 32; w += 4) {
+          if (w >= upto) break;
+          const uint4 v = *reinterpret_cast<const uint4*>(mine + w);
+          before += __popc(v.x);
+          if (w + 1 < upto) before += __popc(v.y);
+          if (w + 2 < upto) before += __popc(v.z);
+          if (w + 3 < upto) before += __popc(v.w);
+        }
+      }
+      nth[i] += __shfl_sync(0xFFFFFFFFu, before, __ffs(same[i]) - 1);
+    }
   }
   if (tid < R) s_row[tid] = -1;
   if (tid == 0) s_item[0] = -1;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < MINE; ++i) {  // how many rows before this one have its adapter
-    const int me = tid + i * kThreads, end = i * kThreads + (warp + 1) * 32;  // (of the warp)
-    if (end - 32 >= T) break;
-    for (int x = 0; x < end; x += 4) {
-      const int4 v = *reinterpret_cast<const int4*>(s_id + x);
-      nth[i] += (v.x == id[i] && x < me) + (v.y == id[i] && x + 1 < me) + (v.z == id[i] && x + 2 < me) +
-                (v.w == id[i] && x + 3 < me);
-    }
-  }
   unsigned int votes[MINE];
 #pragma unroll
   for (int i = 0; i < MINE; ++i) {
@@ -1190,7 +1232,7 @@ inline size_t part_bytes(int64_t T, int64_t K, int64_t r, int sms) {
          static_cast<size_t>((r + 15) / 16 * 16) * sizeof(float);
 }
 inline size_t many_bytes(int64_t T, int64_t K, int64_t r, int sms) {  // sums, whether sorted, the rows
-  return T <= kFewRows ? 0 : part_bytes(T, K, r, sms) + static_cast<size_t>((T + kWindow - 1) / kWindow + T) * sizeof(int32_t);
+  return T <= kFew ? 0 : part_bytes(T, K, r, sms) + static_cast<size_t>((T + kWindow - 1) / kWindow + T) * sizeof(int32_t);
 }
 
 template <int KB>
@@ -1272,12 +1314,13 @@ cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream
   return launch_pdl_clusters_smem<kern>(dev, cluster, dim3(static_cast<unsigned>(blocks * items * cluster)), dim3(kThreads),
                                         C::SMEM, s, p, static_cast<int>(items));
 }
-// Rows per item: enough that an adapter is rarely read more than once.
+// Rows per item: 8 or 16, so that an adapter is rarely read more than once if its rows are few.  (200 rows of 20, K 14336,
+// rank 64: 21 us with 8, 17.6 with 16; 40 rows of 8, K 4096, rank 16: 5.4 and 6.2.  With 32, fewer CTAs have more to do:
+// 512 rows in runs, K = N = 4096, rank 64 14.6 us, 12.6 with 16.)
 template <int MT>
 cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream_t s) {
   const int64_t T = std::min(p.T, kFewRows), each = T / std::min<int64_t>(T, p.count);
-  if (MT <= 4 && each > 12) return launch_few<MT, MT <= 4 ? 4 : 2>(p, dev, s);
-  return each > 4 ? launch_few<MT, 2>(p, dev, s) : launch_few<MT, 1>(p, dev, s);
+  return each > 7 ? launch_few<MT, 2>(p, dev, s) : launch_few<MT, 1>(p, dev, s);
 }
 
 }  // namespace
@@ -1287,7 +1330,7 @@ extern "C" size_t sp24_add_adapters_workspace_size(int64_t T, int64_t K, int64_t
   using namespace sp24;
   const int64_t most = int64_t(1) << 24;
   const DeviceInfo* dev = nullptr;
-  if (T <= kFewRows || T > INT32_MAX / 2 || K < 8 || K > most || r < 1 || r > kMostRank || current_device(&dev)) return 0;
+  if (T <= kFew || T > INT32_MAX / 2 || K < 8 || K > most || r < 1 || r > kMostRank || current_device(&dev)) return 0;
   return many_bytes(T, K, r, dev->sm_count);
 }
 
@@ -1333,7 +1376,7 @@ extern "C" sp24_status sp24_add_adapters(const void* Y, int64_t ldy, const void*
   p.err = dev->err_word;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (T > kFewRows && (T > kFewScattered || count < kScattered))
+  if (T > kFew)
     return r <= 64 ? launch_many<1>(p, static_cast<float*>(workspace), *dev, s)
                    : launch_many<2>(p, static_cast<float*>(workspace), *dev, s);
   if (r <= 16)

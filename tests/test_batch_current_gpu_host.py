@@ -15,9 +15,9 @@ def calls(c):
     table, lens = torch.zeros(2, 100, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
     cu, shared = torch.tensor([0, 2], dtype=torch.int32), torch.ones(1, dtype=torch.int32)
     slots = torch.zeros(2, dtype=torch.int64)
-    y, x = torch.zeros(600, 16, dtype=torch.bfloat16), torch.zeros(600, 8, dtype=torch.bfloat16)
+    y, x = torch.zeros(1100, 16, dtype=torch.bfloat16), torch.zeros(1100, 8, dtype=torch.bfloat16)
     a, b = torch.zeros(3, 8, 8, dtype=torch.bfloat16), torch.zeros(3, 16, 8, dtype=torch.bfloat16)
-    ids = torch.zeros(600, dtype=torch.int32)
+    ids = torch.zeros(1100, dtype=torch.int32)
     return {
         "sp24_attention_decode_shared": lambda **kw: s.attention_decode_shared(q, c, table, lens, cu, shared, **kw),
         "sp24_cache_copy": lambda **kw: s.cache_copy(c, slots, c, slots, **kw),

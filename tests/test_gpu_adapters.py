@@ -70,7 +70,12 @@ def ids_of(T, count, kind, seed):
     (100, 1024, 1024, 128, 7, "runs"),
     (257, 512, 776, 56, 9, "any"),
     (300, 2048, 512, 64, 1, "one"),
-    (700, 1032, 1032, 16, 6, "runs"),     # the many-row form
+    (700, 1032, 1032, 16, 6, "runs"),     # two blocks of rows
+    (513, 136, 200, 128, 30, "any"),
+    (1024, 520, 264, 48, 12, "any"),
+    (1025, 520, 264, 48, 12, "any"),      # the many-row form
+    (1100, 1032, 1032, 16, 6, "runs"),
+    (1200, 64, 64, 32, 2, "none"),
     (1030, 256, 2048, 104, 40, "any"),
     (1500, 3000, 640, 8, 3, "runs"),
     (2049, 640, 1000, 128, 5, "runs"),
@@ -90,7 +95,7 @@ def test_add_adapters(sp24, T, K, N, r, count, kind, scaled):
     assert torch.equal(got.cpu()[bare], y[bare])        # rows without an adapter keep every bit
 
 
-@pytest.mark.parametrize("T", [5, 40, 900])
+@pytest.mark.parametrize("T", [5, 40, 900, 1300])
 def test_strides_in_place_and_bounds(sp24, T):
     """Rows and adapters further apart than their length; the result in place; nothing else is written, and NaN in what
     belongs to no row's adapter, or lies between, reaches no result."""
@@ -121,7 +126,7 @@ def test_strides_in_place_and_bounds(sp24, T):
 
 
 def test_a_row_that_is_not_finite_keeps_to_itself(sp24):
-    for T in (20, 800):
+    for T in (20, 800, 1200):
         y, x, a, b, scales = inputs(T, 256, 136, 16, 2, seed=T)
         ids = torch.zeros(T, dtype=torch.int32)
         ids[1::3] = 1
@@ -136,7 +141,7 @@ def test_a_row_that_is_not_finite_keeps_to_itself(sp24):
         assert torch.equal(got.cpu()[keep], clean.cpu()[keep])
 
 
-@pytest.mark.parametrize("T", [1, 48, 700])
+@pytest.mark.parametrize("T", [1, 48, 700, 1100])
 def test_the_same_every_time_streams_and_graphs(sp24, T):
     y, x, a, b, scales = inputs(T, 1024, 520, 32, 5, seed=T)
     ids = ids_of(T, 5, "any", 1)
@@ -162,7 +167,7 @@ def test_the_same_every_time_streams_and_graphs(sp24, T):
 
 
 def test_ids_out_of_range(sp24):
-    for T in (6, 600):
+    for T in (6, 600, 1100):
         y, x, a, b, _ = inputs(T, 64, 72, 8, 2, seed=T)
         ids = torch.zeros(T, dtype=torch.int32)
         ids[3], ids[4] = 2, 2 ** 31 - 1
@@ -203,10 +208,10 @@ def test_tiles_of_several_adapters_again_and_again(sp24, T, K, N, r, count):
 
 
 def test_workspace(sp24):
-    y, x, a, b, scales = (t.cuda() for t in inputs(600, 256, 136, 16, 2, seed=1))
-    ids = torch.zeros(600, dtype=torch.int32, device="cuda")
-    need = sp24.add_adapters_workspace_size(600, 256, 16)
-    assert need > 0 and sp24.add_adapters_workspace_size(512, 256, 16) == 0
+    y, x, a, b, scales = (t.cuda() for t in inputs(1100, 256, 136, 16, 2, seed=1))
+    ids = torch.zeros(1100, dtype=torch.int32, device="cuda")
+    need = sp24.add_adapters_workspace_size(1100, 256, 16)
+    assert need > 0 and sp24.add_adapters_workspace_size(1024, 256, 16) == 0
     short = torch.empty(need - 16, dtype=torch.uint8, device="cuda")
     with pytest.raises(sp24.Sp24Error, match="WORKSPACE"):
         sp24.add_adapters(y, x, a, b, ids, workspace=short)
@@ -217,8 +222,10 @@ def test_workspace(sp24):
 
 
 @pytest.mark.parametrize("T,K,N,r,count", [
-    (513, 264, 136, 24, 31),       # the last row's tile has no other
-    (1023, 520, 264, 16, 300),     # two bytes of ids
+    (513, 264, 136, 24, 31),       # the last row's block has no other
+    (1023, 520, 264, 16, 300),
+    (1025, 264, 136, 24, 31),      # the last row's tile has no other
+    (1300, 520, 264, 16, 300),     # two bytes of ids
     (1100, 1032, 1096, 40, 90),
     (2175, 256, 328, 72, 2),       # two adapters in turn
     (8191, 72, 200, 8, 20),
@@ -301,7 +308,7 @@ def test_tiles_of_very_different_cost(sp24, K, r):
 
 def test_an_infinite_value_has_the_sign_of_its_products(sp24):
     """Ranks that are no multiple of 16: what pads them adds nothing, not even to a row with an infinite value."""
-    for T in (20, 800):
+    for T in (20, 800, 1200):
         y, x, a, b, _ = inputs(T, 64, 136, 8, 2, seed=T)
         a, b = a.abs() + 0.5, b.abs() + 0.5
         x[7, 3], x[11, 3] = float("inf"), float("-inf")

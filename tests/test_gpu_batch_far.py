@@ -7,7 +7,7 @@ pytestmark = pytest.mark.gpu
 FAR = (1 << 31) + 64  # elements
 
 
-@pytest.mark.parametrize("T", [5, 300, 600])
+@pytest.mark.parametrize("T", [5, 300, 600, 1100])
 def test_adapters_and_rows_far_apart(sp24, T):
     """Adapters FAR apart, and rows so far apart that the last begin behind 2^31 elements: the same bits as packed ones."""
     K, N, r, count = 136, 72, 24, 2

@@ -30,7 +30,7 @@ def status():
 
 out = []
 for r in (16, 64, 128):
-    for T in (600, 5000):
+    for T in (1100, 5000):
         z = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
         ids = (torch.arange(T, device="cuda") // 100 % 3).to(torch.int32)
         s.add_adapters(z(T, 512), z(T, 1024), z(3, r, 1024), z(3, 512, r), ids)
@@ -63,8 +63,8 @@ def test_waits_that_run_out_are_reported(sp24):
     assert out["context_ok"]
 
     from test_gpu_adapters import assert_adapted, inputs, reference
-    y, x, a, b_, scales = inputs(600, 256, 136, 16, 2, seed=1)
-    ids = torch.arange(600, dtype=torch.int32) // 100 % 2
+    y, x, a, b_, scales = inputs(1100, 256, 136, 16, 2, seed=1)
+    ids = torch.arange(1100, dtype=torch.int32) // 100 % 2
     got = sp24.add_adapters(*(t.cuda() for t in (y, x, a, b_, ids, scales)))
     sp24.last_device_error()
     assert_adapted(got, *reference(y, x, a, b_, ids, scales), "library proper")

@@ -47,7 +47,7 @@ sp24.last_device_error()
 """
 
 
-@pytest.mark.parametrize("what", ["shared", "copy", "7", "300", "700"])
+@pytest.mark.parametrize("what", ["shared", "copy", "7", "300", "1100"])
 def test_first_call_in_a_capture(what):
     root = Path(__file__).resolve().parents[1]
     r = subprocess.run([sys.executable, "-c", CHILD, what], cwd=root, capture_output=True, text=True, timeout=240)
