@@ -10,9 +10,9 @@
 // Two forms.  Few rows: the rows of one adapter, wherever they are, to a cluster of
 // CTAs, by mma.sync.  Many rows: tiles of 128 rows by tcgen05.mma, in two launches.
 //
-// Measured (GB300, in a graph): 1 row of 4096 values, rank 16, N 4096 4.9 us; 64 rows with an
-// adapter each, N 6144 9.1 us; 200 rows of 20 adapters in no order, K 14336, rank 64,
-// N 4096 18.1 us; 3000 rows of 16 adapters in runs, rank 32, N 14336 48 us (60 % of the measured
+// Measured (GB300, in a graph): 1 row of 4096 values, rank 16, N 4096 4.8 us; 64 rows with an
+// adapter each, N 6144 9.3 us; 200 rows of 20 adapters in no order, K 14336, rank 64,
+// N 4096 17.5 us; 512 rows of one adapter, rank 64, K = N = 4096 12.5 us; 3000 rows of 16 adapters in runs, rank 32, N 14336 48 us (60 % of the measured
 // copy rate); 8192 rows of 8 in runs, rank 64, K = N = 4096 54 us, of one 44 us (57 and 70 %).
 #include <cuda_bf16.h>
 #include <algorithm>
@@ -29,7 +29,7 @@ constexpr int kMostCluster = 8;    // CTAs that share a few rows' work, at most
 constexpr int kMostRank = 128;
 constexpr int kNobody = -3;        // (ids are -1 and up, -2 behind the last row)
 constexpr int kSlots = 1024, kBitsRow = 20;  // (words; 16 are used, 20 keep banks apart)
-constexpr int kFewRows = 512;      // rows of a call that are sorted by adapter
+constexpr int kFewRows = 512;      // rows that are brought together by adapter
 constexpr int kFew = 1024;         // rows up to which the form for few takes all, in blocks of kFewRows (4096 values, rank 16, 8
                                    // adapters in runs: 1024 rows 11.5 us, in tiles 17.4; 2048 rows 22 and 20)
 
