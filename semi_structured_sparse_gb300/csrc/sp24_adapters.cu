@@ -67,7 +67,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
 }
 
 // Few rows.  An item is one adapter and up to R = 8 NT rows that have it, wherever they
-// are in the batch; a cluster of 2 to 8 CTAs works on it.  Their warps cut K for
+// are in the batch; a cluster of 1 to 8 CTAs works on it.  Their warps cut K for
 // A x, a warp's sums meet in shared memory and the CTAs' in all CTAs of the cluster
 // (distributed shared memory, always added in the same order), and the warps
 // cut N for B (A x).
@@ -1284,11 +1284,12 @@ cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream
   const int64_t T = std::min(p.T, kFewRows), blocks = (p.T + kFewRows - 1) / kFewRows;
   const int64_t adapters = std::min<int64_t>(T, p.count), items = std::min<int64_t>(T, T / C::R + adapters + 1);
   // As many CTAs per item as run at once, for as many items as rows spread evenly over the adapters come to.  (200 rows
-  // of 20 adapters, rank 64, K 14336, 1 CTA per SM: 14 clusters of 8 fit, 24 of 6; 26 us with 8 and 17 with 6.)
+  // of 20 adapters, rank 64, K 14336, 1 CTA per SM: 14 clusters of 8 fit, 24 of 6; 26 us with 8 and 17 with 6.  512 rows with an
+  // adapter each, rank 16, K = N = 1024: 30 us in twos, 18 with one CTA for each.)
   const int64_t likely = blocks * std::min(items, adapters * ((T / adapters + C::R - 1) / C::R) + 1);
   static std::atomic<int> most[64][kMostCluster + 1];  // clusters of each size that fit at once, + 1
   unsigned cluster = kMostCluster;
-  for (; cluster > 2; --cluster) {
+  for (; cluster > 1; --cluster) {
     std::atomic<int>& known = most[dev.ordinal & 63][cluster];
     int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
