@@ -264,11 +264,12 @@ def test_many_rows_in_no_order(sp24, T, K, N, r, count):
         sp24.last_device_error()
 
 
+@pytest.mark.parametrize("r", [16, 80])
 @pytest.mark.parametrize("first", [True, False])
-def test_rows_in_order_beside_rows_in_none(sp24, first):
+def test_rows_in_order_beside_rows_in_none(sp24, first, r):
     """Tiles that stay as they are beside tiles put together from everywhere, and windows that are sorted beside ones
     that are not."""
-    T, K, N, r, count = 9300, 136, 200, 16, 460
+    T, K, N, count = 9300, 136, 200, 460
     g = torch.Generator().manual_seed(5)
     short = torch.arange(2000) // 5                       # in order, but in short runs
     mixed = torch.randint(400, count, (6192,), generator=g)
