@@ -251,18 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kern
   };
 #pragma unroll
   for (int i = 0; i < ST - 1; ++i) issue(k0 + i);
-  // this CTA's rows of B on their way to L2 meanwhile
   const int blocks = (p.N + 31) / 32;
-  {
-    const int b0 = static_cast<int>(int64_t(blocks) * (rank * kWarps) / GW) * 32;
-    const int b1 = min(p.N, static_cast<int>(int64_t(blocks) * ((rank + 1) * kWarps) / GW) * 32);
-    const __nv_bfloat16* b = p.b + adapter * p.stride_b;
-    constexpr int PIECE = 8192;
-    const int64_t bytes = int64_t(b1 - b0) * p.r * 2;
-    for (int64_t i = int64_t(tid) * PIECE; i < bytes; i += int64_t(kThreads) * PIECE)
-      bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(b + int64_t(b0) * p.r) + i,
-                       static_cast<uint32_t>(min(int64_t(PIECE), bytes - i)));
-  }
   float acc[MT][NT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
