@@ -10,9 +10,9 @@
 // Two forms.  Few rows: the rows of one adapter, wherever they are, to a cluster of
 // CTAs, by mma.sync.  Many rows: tiles of 128 rows by tcgen05.mma, in two launches.
 //
-// Measured (GB300, in a graph): 1 row of 4096 values, rank 16, N 4096 4.8 us; 64 rows with an
-// adapter each, N 6144 9.3 us; 200 rows of 20 adapters in no order, K 14336, rank 64,
-// N 4096 17.5 us; 512 rows of one adapter, rank 64, K = N = 4096 12.5 us; 3000 rows of 16 adapters in runs, rank 32, N 14336 48 us (60 % of the measured
+// Measured (GB300, in a graph): 1 row of 4096 values, rank 16, N 4096 4.4 us; 64 rows with an
+// adapter each, N 6144 8.9 us; 200 rows of 20 adapters in no order, K 14336, rank 64,
+// N 4096 16.8 us; 512 rows of one adapter, rank 64, K = N = 4096 12.0 us; 3000 rows of 16 adapters in runs, rank 32, N 14336 48 us (60 % of the measured
 // copy rate); 8192 rows of 8 in runs, rank 64, K = N = 4096 54 us, of one 44 us (57 and 70 %).
 #include <cuda_bf16.h>
 #include <algorithm>
@@ -84,9 +84,11 @@ struct FewCfg {
   static constexpr int KS = MT < 2 ? 1 : MT / 2;         // 32s of the rank
   static constexpr int LOADS = 2 * MT + NT;              // 16-byte pieces per lane and 32 of K
   // (Items of 8 rows are the form for many adapters, of which an SM holds two: 512 rows of 100 adapters, rank 64, K = N =
-  // 4096 33.7 us, 40.1 with three stages and one CTA.)
+  // 4096 29.5 us; with three stages and one CTA 6 us more.)
   static constexpr int STAGES = LOADS <= 5 ? 4 : NT == 1 || LOADS > 10 ? 2 : 3;
-  static constexpr int AHEAD = KS == 1 ? 3 : KS == 2 ? 2 : 1;  // 32s of N whose operands are under way
+  // 32s of N whose operands are under way.  (512 rows with an adapter each, rank 16, K = N = 4096: 42 us with two, 47 with
+  // one or four, 44 with three; with B sent for to L2 beside A, 49.)
+  static constexpr int AHEAD = KS <= 2 ? 2 : 1;
   static constexpr int HLD = 32 * KS + 8;                // row of A x, in bf16
   static constexpr int RING = kWarps * STAGES * LOADS * 512, PART = kWarps * R * RP * 4;
   static constexpr int FIRST = RING > PART ? RING : PART;  // the ring, and then the warps' sums
@@ -1307,7 +1309,7 @@ cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream
                                         C::SMEM, s, p, static_cast<int>(items));
 }
 // Rows per item: 8 or 16, so that an adapter is rarely read more than once if its rows are few.  (200 rows of 20, K 14336,
-// rank 64: 21 us with 8, 17.6 with 16; 40 rows of 8, K 4096, rank 16: 5.4 and 6.2.  With 32, fewer CTAs have more to do:
+// rank 64: 21 us with 8, 17.6 with 16; 40 rows of 8, K 4096, rank 16: 5.4 and 6.2, all at the time.  With 32, fewer CTAs have more to do:
 // 512 rows in runs, K = N = 4096, rank 64 14.6 us, 12.6 with 16.)
 template <int MT>
 cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream_t s) {
