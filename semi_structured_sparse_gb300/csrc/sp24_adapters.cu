@@ -1274,10 +1274,17 @@ cudaError_t launch_few(const AdapterParams& p, const DeviceInfo& dev, cudaStream
   // Each adapter's last item may be partly filled; rows without an adapter count as one more.
   const int64_t T = std::min(p.T, kFewRows), blocks = (p.T + kFewRows - 1) / kFewRows;
   const int64_t adapters = std::min<int64_t>(T, p.count), items = std::min<int64_t>(T, T / C::R + adapters + 1);
-  // As many CTAs per item as run at once, for as many items as rows spread evenly over the adapters come to.  (200 rows
+  // As many CTAs per item as run at once, for as many items as rows spread over the adapters come to, evenly or by chance
+  // (each adapter's last item is half full then).  More items than that take a second wave: 512 rows of 8 adapters by chance,
+  // rank 64, N 14336 23 us, 32 with clusters for rows spread evenly (which take 19 for rows of one adapter, and these 23).  (200 rows
   // of 20 adapters, rank 64, K 14336, 1 CTA per SM: 14 clusters of 8 fit, 24 of 6; 26 us with 8 and 17 with 6.  512 rows with an
   // adapter each, rank 16, K = N = 1024: 30 us in twos, 18 with one CTA for each.)
-  const int64_t likely = blocks * std::min(items, adapters * ((T / adapters + C::R - 1) / C::R) + 1);
+  auto expect = [&](int64_t rows) {
+    const int64_t some = std::min<int64_t>(rows, p.count);
+    return std::min(items, std::max(some * ((rows / some + C::R - 1) / C::R), rows / C::R + some / 2) + 1);
+  };
+  const int64_t likely = expect(T) + (p.T > kFewRows ? expect(p.T - kFewRows) : 0);
+  static_assert(kFew <= 2 * kFewRows, "two blocks");
   static std::atomic<int> most[64][kMostCluster + 1];  // clusters of each size that fit at once, + 1
   unsigned cluster = kMostCluster;
   for (; cluster > 1; --cluster) {
