@@ -545,9 +545,10 @@ SP24_API size_t sp24_attention_prompt_workspace_size(int64_t T, int64_t B, int q
  *           consistent from call to call, whatever their shapes; calls that
  *           overlap on the GPU must not share it.
  *   Others as for sp24_attention_decode.
- * cu_shared out of order or out of [0, B] is brought into it, shared_lens out of
- * [0, table_width * page_size] as well; sp24_last_device_error then reports
- * SP24_ERR_DEVICE_INDEX.
+ * With cu_shared out of order or out of [0, B] no sequence has anything in common
+ * with others; shared_lens out of [0, table_width * page_size] is brought into it;
+ * sp24_last_device_error then reports SP24_ERR_DEVICE_INDEX (except in a call that attends
+ * all sequences by themselves anyway, which does not look).
  * Values of the shared tokens are finite: a weight of zero times an infinite
  * value is not a number.
  * Preconditions: G >= 0; cu_shared given (shared_lens may be NULL with G = 0).

@@ -134,8 +134,9 @@ __device__ __forceinline__ int shared_of(const DecodeParams& p, int b) {
   return b < lo || b >= hi ? 0 : shared_tokens(lo, hi, __ldg(p.sh.lens + g), p.seq_lens, p.table_width << p.cache.page_shift);
 }
 
+// `share`: the groups are in order.
 template <int CT, bool SHARED>
-__device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool report) {
+__device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool report, bool share) {
   Span s;
   int n = __ldg(p.seq_lens + b);
   const int most = p.table_width << p.cache.page_shift;
@@ -148,7 +149,7 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool repor
   s.sinks = min(p.sinks, s.lo);
   if (s.sinks == s.lo) s.lo = s.sinks = 0;
   s.shared = false;
-  if (SHARED && s.lo == 0) {
+  if (SHARED && share && s.lo == 0) {
     const int shared = shared_of(p, b);
     if (shared > 0 && shared <= n) s.shared = true, s.lo = shared;
   }
@@ -214,8 +215,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
   // ---- this CTA's range of tiles
   const int HH = p.kv_heads * p.head_blocks;
   // Tiles of the sequences: a sum over all, and a running sum over the first kThreads.
+  bool share = SHARED;
   auto tiles_of = [&](int x, bool report) {
-    return x < p.B ? span_of<CT, SHARED>(p, x, report).tiles : 0;
+    return x < p.B ? span_of<CT, SHARED>(p, x, report, share).tiles : 0;
   };
   auto scan = [&](int x) {  // inclusive, over the warp
 #pragma unroll
@@ -225,20 +227,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     }
     return x;
   };
-  int own = tiles_of(tid, blockIdx.x == 0), rest = 0;
-  for (int x = tid + kThreads; x < p.B; x += kThreads) rest += tiles_of(x, blockIdx.x == 0);
-  int incl = scan(own);
-  if (p.B > kThreads) {
+  int own = 0, incl = 0;
+  auto count_tiles = [&](bool report) {
+    int rest = 0;
+    own = tiles_of(tid, report);
+    for (int x = tid + kThreads; x < p.B; x += kThreads) rest += tiles_of(x, report);
+    incl = scan(own);
+    if (p.B > kThreads) {
 #pragma unroll
-    for (int m = 16; m; m >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, m);
-  }
-  if (lane == 31) s_sum[0][warp] = incl, s_sum[1][warp] = rest;
+      for (int m = 16; m; m >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, m);
+    }
+    if (lane == 31) s_sum[0][warp] = incl, s_sum[1][warp] = rest;
+  };
+  count_tiles(blockIdx.x == 0);
   if (SHARED) {  // what the launch before has to do, and what is left
+    bool in_order = true;
     int units = 0;
     long long tokens = 0;
     for (int x = tid; x < p.B; x += kThreads) tokens += counted_tokens(__ldg(p.seq_lens + x), p.sh.window);
     for (int x = tid; x < p.sh.G; x += kThreads) {
-      const int lo = min(max(__ldg(p.sh.cu + x), 0), p.B), hi = min(max(__ldg(p.sh.cu + x + 1), lo), p.B);
+      const int lo = __ldg(p.sh.cu + x), hi = __ldg(p.sh.cu + x + 1);
+      in_order = lo >= 0 && lo <= hi && hi <= p.B;
+      if (!in_order) break;
       const int n = shared_tokens(lo, hi, __ldg(p.sh.lens + x), p.seq_lens, p.table_width << p.cache.page_shift);
       const int rows = 2 * (kTileRows / p.group);
       units += (n + kKeyTile - 1) / kKeyTile * ((hi - lo + rows - 1) / rows);
@@ -250,8 +260,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
       tokens += __shfl_xor_sync(0xFFFFFFFFu, tokens, m);
     }
     if (lane == 0) s_units[warp] = units, s_tokens[warp] = tokens;
+    share = __syncthreads_and(in_order);
+    if (!share) {  // groups out of order, which the launch before leaves alone: all tokens are a sequence's own
+      count_tiles(false);
+      if (lane == 0) s_units[warp] = 0;
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
   }
-  __syncthreads();
   unsigned int total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += s_sum[0][w] + s_sum[1][w];
@@ -303,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
 
   Item it;
   it.b = b;
-  it.sp = span_of<CT, SHARED>(p, b, false);
+  it.sp = span_of<CT, SHARED>(p, b, false, share);
   // The item that tile u of the launch begins.
   auto place = [&](Item& x) {
     const unsigned int local = u - static_cast<unsigned int>(before) * HH;
@@ -388,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
       if (it.hh == HH - 1) {
         before += it.sp.tiles;
         nx.b = it.b + 1;
-        nx.sp = span_of<CT, SHARED>(p, nx.b, false);
+        nx.sp = span_of<CT, SHARED>(p, nx.b, false, share);
       }
       place(nx);
       fetch_pages(nx, nx.t0 + lane, page_then);
@@ -744,7 +761,7 @@ sp24_status launch(const DecodeParams& p, const DeviceInfo& dev, int ctas, cudaS
   const int64_t most = (int64_t(p.table_width) << p.cache.page_shift) / TT + 3;
   if (most * p.B > INT32_MAX / (int64_t(p.kv_heads) * p.head_blocks)) return SP24_ERR_UNSUPPORTED;
   const int smem = kSmem<D, E4M3, NH>;
-  const cudaError_t r = 
+  const cudaError_t r =
       launch_pdl_smem<attention_decode_kernel<D, E4M3, NH, SHARED>>(dev, dim3(ctas), dim3(kThreads), smem, s, p);
   return r == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
 }

@@ -345,10 +345,10 @@ struct Deal {
 };
 constexpr int kLeastUnits = 4;  // per CTA
 
-// 32 groups, one per lane, with the units and pairs up to and with each.  Groups
-// are brought into order: each begins where the one before it ends.
+// 32 groups, one per lane, with the units and pairs up to and with each.
 struct Groups {
   int lo, end, n;                    // sequences, and the tokens that they read together
+  bool in_order;                     // each begins where the one before it ends, within the batch
   unsigned int tiles, units, pairs;  // of this one
   unsigned int units_to, pairs_to;
 };
@@ -366,7 +366,8 @@ __device__ __forceinline__ Groups load_groups(const PromptParams& p, int g, int 
   }
   s.lo = __shfl_up_sync(0xFFFFFFFFu, s.end, 1);
   if (lane == 0) s.lo = before;
-  if (report && g < p.sh.G && (raw != s.end || shared < 0 || shared > most)) atomicOr(p.err, DEVERR_INDEX);
+  s.in_order = g >= p.sh.G || raw == s.end;
+  if (report && g < p.sh.G && (!s.in_order || shared < 0 || shared > most)) atomicOr(p.err, DEVERR_INDEX);
   s.n = g < p.sh.G ? shared_tokens(s.lo, s.end, shared, p.seq_lens, most) : 0;
   s.tiles = (s.n + BN - 1) / BN;
   s.pairs = s.tiles ? (s.end - s.lo + tok - 1) / tok * p.kv_heads : 0;
@@ -403,8 +404,9 @@ __device__ __forceinline__ void place_unit(const PromptParams& p, const Groups& 
   if (number >= p.sh.pairs || w.part >= p.sh.parts) w.b = -1;  // (there is room for all that the host expects)
   *out = w;
 }
-// Goes through the groups: the units of all, and how often their tokens would be
-// read one by one; or (`out`) the work that begins with unit u.  `few`: the groups,
+// Goes through the groups: the units of all (none if groups are out of order: the
+// launch for sequences' own tokens sees that as well, and attends all of them one by one),
+// and how often their tokens would be read one by one; or (`out`) the work that begins with unit u.  `few`: the groups,
 // where they are 32 at most and known.
 __device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int lane, bool report, const Deal& deal,
                                                     unsigned int u, unsigned int u_end, unsigned int cta, Work* out,
@@ -419,17 +421,20 @@ __device__ __forceinline__ unsigned int scan_groups(const PromptParams& p, int l
     int before = min(max(first, 0), p.T);
     if (report && lane == 0 && first != before) atomicOr(p.err, DEVERR_INDEX);
     long long sum = 0;
+    bool in_order = first == before;
     for (int g0 = 0; g0 < p.sh.G; g0 += 32) {
       const Groups s = load_groups(p, g0 + lane, lane, report, before, units, pairs);
       if (out)
         place_unit(p, s, deal, u, u_end, cta, out, pieces);
       else
         *few = s, sum += static_cast<long long>(s.end - s.lo) * s.n;
+      in_order &= s.in_order;
       units = __shfl_sync(0xFFFFFFFFu, s.units_to, 31), pairs = __shfl_sync(0xFFFFFFFFu, s.pairs_to, 31);
       before = __shfl_sync(0xFFFFFFFFu, s.end, 31);
       if (out && u < units) break;
     }
     if (times) *times = sum;
+    if (!__all_sync(0xFFFFFFFFu, in_order)) units = 0;
   }
   __syncwarp();
   return units;

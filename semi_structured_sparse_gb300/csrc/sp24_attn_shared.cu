@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_shared_join_kernel(con
     const float2 own = __ldcg(reinterpret_cast<const float2*>(p.sh.own + int64_t(p.rows) * D + 2 * int64_t(row)));
     if (own.y != kNotShared) {
       float top = own.x, sum = own.y;
-      // (What is out of range can only come from groups that are not in order.)
+      // (Out of range is only what a first launch that gave up has not written.)
       const bool ok = at.x >= 0 && at.y > 0 && int64_t(at.x) + p.group + int64_t(at.y - 1) * (2 * kTileRows) <=
                                                    int64_t(p.sh.parts) * (2 * kTileRows);
       const int pieces = ok ? at.y : 0;

@@ -262,3 +262,36 @@ def test_layouts_and_empty_calls(sp24):
     assert (out[:, 256:] == 0).all()
     empty = sp24.attention_decode_shared(qd[:0, 8:264], cache, wd[:0], n[:0], i32(0), i32())
     assert empty.shape == (0, 256)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("cu", [[0, 7, 3, 8], [5, 2, 8, 8], [0, 3, 3, 9], [-1, 4, 6, 8], [2, 1, 0, 8], [0, 8, 0, 8]], ids=str)
+def test_groups_out_of_order(sp24, cu, e4m3):
+    """Groups that are not in order share nothing and are reported: no row takes what an earlier call has left in the
+    workspace, or loses its first tokens."""
+    lens = [113, 150, 200, 260, 170, 121, 300, 240]
+    s = Setup(sp24, lens, 2, 64, 16, e4m3, False, 11)
+    for b in range(8):
+        s.table[b, :7] = s.table[0, :7]      # the first 112 tokens are everyone's
+    cache = s.upload()
+    g = torch.Generator().manual_seed(12)
+    q, other = ((2 * torch.randn(8, 6, 64, generator=g)).bfloat16() for _ in range(2))
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    table, n = widened(s.table, 16, 2, 64, e4m3).cuda(), i32(*lens)
+    ws = torch.zeros(sp24.attention_decode_shared_workspace_size(cache, 6, 8, 3), dtype=torch.uint8, device="cuda")
+    wants = []
+    for x in (q, other):
+        rows = [attend(x[b:b + 1].double(), s.tokens("k", b), s.tokens("v", b), torch.ones(1, lens[b], dtype=torch.bool), 0.125)
+                for b in range(8)]
+        wants.append([torch.cat([r[i] for r in rows]) for i in range(2)])
+    y = sp24.attention_decode_shared(other.cuda(), cache, table, n, i32(0, 8, 8, 8), i32(112, 0, 0), workspace=ws)
+    sp24.last_device_error()
+    assert_attention(y, *wants[1], "a call before")
+    y = sp24.attention_decode_shared(q.cuda(), cache, table, n, i32(*cu), i32(112, 96, 112), workspace=ws)
+    with pytest.raises(sp24.Sp24Error) as e:
+        sp24.last_device_error()
+    assert e.value.status == 8
+    assert_attention(y, *wants[0], "groups %s" % cu)
+    y = sp24.attention_decode_shared(q.cuda(), cache, table, n, i32(0, 3, 3, 8), i32(112, 96, 112), workspace=ws)
+    sp24.last_device_error()
+    assert_attention(y, *wants[0], "a call after")
