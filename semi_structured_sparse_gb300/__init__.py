@@ -784,7 +784,8 @@ def attention_decode_shared(q, cache: KVCache, page_table, seq_lens, cu_shared, 
     - 1 are group g (cu_shared int32 [G + 1]; those before the first and after the last are
     in none), and their first shared_lens[g] tokens (int32 [G]) are those in the pages of the
     group's first sequence.  A sequence that does not see all of them (shorter, or under a
-    window that begins later) is attended by itself.  The others as for attention_decode();
+    window that begins later) is attended by itself, and so is a group whose first sequence
+    is longer than window + sinks.  The others as for attention_decode();
     `workspace` (uint8, attention_decode_shared_workspace_size() bytes, zeroed once) may be
     kept for all later calls on one stream; without one, each call allocates a zeroed one."""
     lib = _lib or load()

@@ -91,7 +91,7 @@ struct SharedGroups {
   int2* where;          // [sequences][kv heads] {row of its first head in the first piece, how many pieces}
   float* part;          // [parts][2 kTileRows][D] weighted values, then [parts][2 kTileRows][2] maxima and sums
   int pairs, parts;     // how many there is room for
-  int window;           // of the call
+  int window, sinks;    // of the call
   float* own;           // [sequences][query heads][D] and then [2]: the same of a sequence's own tokens, with
                         // kNotShared for the sum of weights where there is nothing to add
 };
@@ -105,9 +105,13 @@ constexpr float kPromptUp = 7.0f, kDecodeUp = 15.0f;
 __device__ __forceinline__ int counted_tokens(int n, int window) { return max(0, window > 0 ? min(n, window) : n); }
 
 // The tokens that a group [lo, hi) of sequences reads together: none if it is
-// one sequence, and no more than the sequence has whose pages they are read through.
-__device__ __forceinline__ int shared_tokens(int lo, int hi, int shared, const int32_t* seq_lens, int most) {
-  return hi - lo < 2 ? 0 : max(0, min(min(shared, most), __ldg(seq_lens + lo)));
+// one sequence, or if its first, through whose pages they are read, does not see all of its
+// own (the entries of pages before its window may be anything); and no more than that one has.
+__device__ __forceinline__ int shared_tokens(const SharedGroups& s, int lo, int hi, int shared, const int32_t* seq_lens,
+                                             int most) {
+  if (hi - lo < 2) return 0;
+  const int n = min(__ldg(seq_lens + lo), most);
+  return s.window > 0 && n > s.window && n - s.window > s.sinks ? 0 : max(0, min(shared, n));
 }
 
 // How many of the SMs should do the shared tokens: the others begin with the

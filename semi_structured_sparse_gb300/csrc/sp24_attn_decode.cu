@@ -131,7 +131,9 @@ __device__ __forceinline__ int shared_of(const DecodeParams& p, int b) {
     if (__ldg(p.sh.cu + mid) <= b) g = mid; else end = mid;
   }
   const int lo = max(__ldg(p.sh.cu + g), 0), hi = min(__ldg(p.sh.cu + g + 1), p.B);
-  return b < lo || b >= hi ? 0 : shared_tokens(lo, hi, __ldg(p.sh.lens + g), p.seq_lens, p.table_width << p.cache.page_shift);
+  return b < lo || b >= hi
+             ? 0
+             : shared_tokens(p.sh, lo, hi, __ldg(p.sh.lens + g), p.seq_lens, p.table_width << p.cache.page_shift);
 }
 
 // `share`: the groups are in order.
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
       const int lo = __ldg(p.sh.cu + x), hi = __ldg(p.sh.cu + x + 1);
       in_order = lo >= 0 && lo <= hi && hi <= p.B;
       if (!in_order) break;
-      const int n = shared_tokens(lo, hi, __ldg(p.sh.lens + x), p.seq_lens, p.table_width << p.cache.page_shift);
+      const int n = shared_tokens(p.sh, lo, hi, __ldg(p.sh.lens + x), p.seq_lens, p.table_width << p.cache.page_shift);
       const int rows = 2 * (kTileRows / p.group);
       units += (n + kKeyTile - 1) / kKeyTile * ((hi - lo + rows - 1) / rows);
       tokens -= static_cast<long long>(hi - lo) * n;

@@ -368,7 +368,7 @@ __device__ __forceinline__ Groups load_groups(const PromptParams& p, int g, int 
   if (lane == 0) s.lo = before;
   s.in_order = g >= p.sh.G || raw == s.end;
   if (report && g < p.sh.G && (!s.in_order || shared < 0 || shared > most)) atomicOr(p.err, DEVERR_INDEX);
-  s.n = g < p.sh.G ? shared_tokens(s.lo, s.end, shared, p.seq_lens, most) : 0;
+  s.n = g < p.sh.G ? shared_tokens(p.sh, s.lo, s.end, shared, p.seq_lens, most) : 0;
   s.tiles = (s.n + BN - 1) / BN;
   s.pairs = s.tiles ? (s.end - s.lo + tok - 1) / tok * p.kv_heads : 0;
   s.units = s.pairs * s.tiles;

@@ -200,6 +200,7 @@ extern "C" sp24_status sp24_attention_decode_shared(const void* q, int64_t B, in
   c.groups.pairs = static_cast<int>(room.pairs);
   c.groups.parts = static_cast<int>(room.parts);
   c.groups.window = c.window;
+  c.groups.sinks = sinks;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sp24_status st = launch_shared_tokens(c, *dev, s)) return st;
   if (sp24_status st = launch_own_tokens(c, *dev, s)) return st;

@@ -295,3 +295,36 @@ def test_groups_out_of_order(sp24, cu, e4m3):
     y = sp24.attention_decode_shared(q.cuda(), cache, table, n, i32(0, 3, 3, 8), i32(112, 96, 112), workspace=ws)
     sp24.last_device_error()
     assert_attention(y, *wants[0], "a call after")
+
+
+@pytest.mark.parametrize("shared,lens,window,sinks,one_by_one", [
+    (700, [1100 + 6 * i for i in range(70)], 500, 0, True),            # nobody sees all shared tokens
+    (700, [701 + 6 * i for i in range(70)], 500, 20, True),
+    (300, [900] + [301 + 3 * i for i in range(69)], 500, 20, True),    # the first sequence does not, others would
+    (300, [560] + [301 + 3 * i for i in range(69)], 500, 20, True),    # ... by three pages
+    (480, [520] + [481 + 2 * i for i in range(69)], 500, 20, False),   # the first does, some do not
+    (480, [485] + [481 + 9 * i for i in range(69)], 500, 40, False),
+    (0, [900] + [301 + 3 * i for i in range(69)], 500, 20, True),
+])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_pages_before_a_window(sp24, shared, lens, window, sinks, one_by_one, e4m3):
+    """Neither a page without a visible key nor its entry in the table is read, whoever else is in the group."""
+    hq, hkv, d, page, B = 16, 8, 64, 16, len(lens)
+    s, tokens = batch(sp24, [0, B], [shared], lens, hkv, d, page, e4m3, False, window, sinks, 21, one_by_one)
+    table = widened(s.table, page, hkv, d, e4m3)
+    see = [sees([n - 1], n, window, sinks) for n in lens]
+    hidden = 0
+    for b, n in enumerate(lens):
+        for i in range(-(-n // page)):
+            if not see[b][0, i * page:(i + 1) * page].any():
+                table[b, i] = -1 if (b + i) % 2 else 1 << 28
+                hidden += 1
+    assert hidden
+    cache = s.upload()
+    q = (2 * torch.randn(B, hq, d, generator=torch.Generator().manual_seed(22))).bfloat16()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    y = sp24.attention_decode_shared(q.cuda(), cache, table.cuda(), i32(lens), i32([0, B]), i32([shared]), window=window,
+                                     sinks=sinks)
+    sp24.last_device_error()
+    rows = [attend(q[b:b + 1].double(), *tokens[b], see[b], d ** -0.5) for b in range(B)]
+    assert_attention(y, torch.cat([r[0] for r in rows]), torch.cat([r[1] for r in rows]), "window")
