@@ -101,9 +101,6 @@ constexpr int kKeyTile = 128;           // keys of one of its tiles
 // Weights of an e4m3 cache are 2^this times exp2(c S - m) in the kernels for prompts and for decoding.
 constexpr float kPromptUp = 7.0f, kDecodeUp = 15.0f;
 
-// Tokens of a sequence that count as read one by one, shared ones among them.
-__device__ __forceinline__ int counted_tokens(int n, int window) { return max(0, window > 0 ? min(n, window) : n); }
-
 // The tokens that a group [lo, hi) of sequences reads together: none if it is
 // one sequence, or if its first, through whose pages they are read, does not see all of its
 // own (the entries of pages before its window may be anything); and no more than that one has.
@@ -113,13 +110,37 @@ __device__ __forceinline__ int shared_tokens(const SharedGroups& s, int lo, int 
   const int n = min(__ldg(seq_lens + lo), most);
   return s.window > 0 && n > s.window && n - s.window > s.sinks ? 0 : max(0, min(shared, n));
 }
+// How many first tokens sequence b of B reads together with its group.
+__device__ __forceinline__ int shared_of(const SharedGroups& s, int b, int B, const int32_t* seq_lens, int most) {
+  int g = 0, end = s.G;
+  while (end - g > 1) {  // the last group that begins at b or before
+    const int mid = (g + end) / 2;
+    if (__ldg(s.cu + mid) <= b) g = mid; else end = mid;
+  }
+  const int lo = max(__ldg(s.cu + g), 0), hi = min(__ldg(s.cu + g + 1), B);
+  return b < lo || b >= hi ? 0 : shared_tokens(s, lo, hi, __ldg(s.lens + g), seq_lens, most);
+}
+// Tokens that sequence b reads one by one, as far as they take a share of the SMs.  Without a window those that its group
+// reads together are among them: they are taken off for a group at once, which takes fewer loads (and only a sequence
+// shorter than them does not share them).  Under a window some of a group may see all of them and others not: what the
+// latter read of them is in L2, at 76 bytes per ns and SM (attention_decode of 64 sequences behind the same 16000 tokens,
+// 363 us), and counts 7/16.  (Window 16384, of those 64 2 share: 373 us, 716 with a count of 1, 520 without any; 32 share:
+// 219, 485, 330; 62: 54, 60, 86.)
+__device__ __forceinline__ int counted_tokens(const SharedGroups& s, int b, int B, const int32_t* seq_lens, int most) {
+  const int n = max(0, min(__ldg(seq_lens + b), most));
+  if (s.window == 0) return n;
+  const int shared = shared_of(s, b, B, seq_lens, most);
+  if (n <= s.window || n - s.window <= s.sinks) return shared <= n ? n - shared : n;
+  const int near = max(0, shared - (n - s.window)) + min(s.sinks, shared);
+  return s.window + s.sinks - near + near / 16 * 7;  // (less than n)
+}
 
 // How many of the SMs should do the shared tokens: the others begin with the
 // sequences' own at once, so that one's idle memory is the other's.  Both launches
 // ask, and get the same answer: shares of the SMs as those of the work, of units
 // (key tiles of up to 256 query rows), which the chain of products and
-// exponentials bounds, and of the bytes of own keys and values.  `tokens`: those of all sequences (as far
-// as a window reaches), less those that are read together.
+// exponentials bounds, and of the bytes of own keys and values.  `tokens`: the counted ones of all sequences, without a
+// window less those that their groups read together.
 constexpr unsigned int kLeastOwnSms = 40;  // fewer, and the shared tokens take them all first
 template <int D, bool E4M3>
 __device__ __forceinline__ unsigned int shared_sms(unsigned int units, long long tokens, int kv_heads, unsigned int sms) {

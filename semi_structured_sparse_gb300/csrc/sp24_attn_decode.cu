@@ -123,19 +123,6 @@ struct Span {
   bool shared;       // the keys before lo are in the workspace already
 };
 
-// How many first tokens sequence b reads together with its group.
-__device__ __forceinline__ int shared_of(const DecodeParams& p, int b) {
-  int g = 0, end = p.sh.G;
-  while (end - g > 1) {  // the last group that begins at b or before
-    const int mid = (g + end) / 2;
-    if (__ldg(p.sh.cu + mid) <= b) g = mid; else end = mid;
-  }
-  const int lo = max(__ldg(p.sh.cu + g), 0), hi = min(__ldg(p.sh.cu + g + 1), p.B);
-  return b < lo || b >= hi
-             ? 0
-             : shared_tokens(p.sh, lo, hi, __ldg(p.sh.lens + g), p.seq_lens, p.table_width << p.cache.page_shift);
-}
-
 // `share`: the groups are in order.
 template <int CT, bool SHARED>
 __device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool report, bool share) {
@@ -152,7 +139,7 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int b, bool repor
   if (s.sinks == s.lo) s.lo = s.sinks = 0;
   s.shared = false;
   if (SHARED && share && s.lo == 0) {
-    const int shared = shared_of(p, b);
+    const int shared = shared_of(p.sh, b, p.B, p.seq_lens, most);
     if (shared > 0 && shared <= n) s.shared = true, s.lo = shared;
   }
   s.from = s.lo & ~15;
@@ -246,15 +233,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_decode_kernel(
     bool in_order = true;
     int units = 0;
     long long tokens = 0;
-    for (int x = tid; x < p.B; x += kThreads) tokens += counted_tokens(__ldg(p.seq_lens + x), p.sh.window);
+    const int room = p.table_width << p.cache.page_shift;
+    for (int x = tid; x < p.B; x += kThreads) tokens += counted_tokens(p.sh, x, p.B, p.seq_lens, room);
     for (int x = tid; x < p.sh.G; x += kThreads) {
       const int lo = __ldg(p.sh.cu + x), hi = __ldg(p.sh.cu + x + 1);
       in_order = lo >= 0 && lo <= hi && hi <= p.B;
       if (!in_order) break;
-      const int n = shared_tokens(p.sh, lo, hi, __ldg(p.sh.lens + x), p.seq_lens, p.table_width << p.cache.page_shift);
+      const int n = shared_tokens(p.sh, lo, hi, __ldg(p.sh.lens + x), p.seq_lens, room);
       const int rows = 2 * (kTileRows / p.group);
       units += (n + kKeyTile - 1) / kKeyTile * ((hi - lo + rows - 1) / rows);
-      tokens -= static_cast<long long>(hi - lo) * n;
+      if (p.sh.window == 0) tokens -= static_cast<long long>(hi - lo) * n;
     }
 #pragma unroll
     for (int m = 16; m; m >>= 1) {

@@ -967,9 +967,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       unsigned int unit = 0, unit_end = 0;
       if (SHARED && keys) {
         long long tokens = 0, times = 0;
-        for (int b = lane; b < p.T; b += 32) tokens += counted_tokens(__ldg(p.seq_lens + b), p.sh.window);
+        const int most = p.table_width << p.cache.page_shift;
+        for (int b = lane; b < p.T; b += 32) tokens += counted_tokens(p.sh, b, p.T, p.seq_lens, most);
         deal.units = scan_groups(p, lane, blockIdx.x == 0, deal, 0, 0, 0, nullptr, nullptr, &groups, &times);
-        tokens -= times;
+        if (p.sh.window == 0) tokens -= times;
 #pragma unroll
         for (int m = 16; m; m >>= 1) tokens += __shfl_xor_sync(0xFFFFFFFFu, tokens, m);
         deal.ctas = max(1u, min(shared_sms<D, E4M3>(deal.units, tokens, p.kv_heads, gridDim.x), deal.units / kLeastUnits));
