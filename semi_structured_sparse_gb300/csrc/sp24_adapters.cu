@@ -83,8 +83,8 @@ struct FewCfg {
   static constexpr int R = 8 * NT, RP = 16 * MT;         // rows and rank, padded
   static constexpr int KS = MT < 2 ? 1 : MT / 2;         // 32s of the rank
   static constexpr int LOADS = 2 * MT + NT;              // 16-byte pieces per lane and 32 of K
-  // (Items of 8 rows are the form for many adapters, of which an SM holds two: 512 rows of 100 adapters, rank 64, K = N =
-  // 4096 29.5 us; with three stages and one CTA 6 us more.)
+  // (Items of 8 rows are the form for many adapters, of which an SM holds two up to rank 64: 512 rows of 100 adapters, rank
+  // 64, K = N = 4096 29.5 us; with three stages and one CTA 6 us more.)
   static constexpr int STAGES = LOADS <= 5 ? 4 : NT == 1 || LOADS > 10 ? 2 : 3;
   // 32s of N whose operands are under way.  (512 rows with an adapter each, rank 16, K = N = 4096: 42 us with two, 47 with
   // one or four, 44 with three; with B sent for to L2 beside A, 49.)
@@ -94,9 +94,10 @@ struct FewCfg {
   static constexpr int FIRST = RING > PART ? RING : PART;  // the ring, and then the warps' sums
   static constexpr int RECV = kMostCluster * R * RP * 4, H = 2 * R * HLD * 2;
   static constexpr int SMEM = FIRST + RECV + H;
+  static constexpr int CTAS = NT == 1 && 2 * (SMEM + 2048) <= 227 * 1024 ? 2 : 1;  // per SM, that registers are to allow
 };
 template <int MT, int NT>
-__global__ void __launch_bounds__(kThreads, 1 + (NT == 1)) add_adapters_few_kernel(
+__global__ void __launch_bounds__(kThreads, FewCfg<MT, NT>::CTAS) add_adapters_few_kernel(
     const __grid_constant__ AdapterParams p, int items) {
   using C = FewCfg<MT, NT>;
   constexpr int R = C::R, RP = C::RP, KS = C::KS, ST = C::STAGES, MH = (NT + 1) / 2;  // 16-row tiles of tokens
