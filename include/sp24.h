@@ -526,7 +526,11 @@ SP24_API size_t sp24_attention_prompt_workspace_size(int64_t T, int64_t B, int q
  * sp24_attention_decode_shared -- sp24_attention_decode for a batch in which
  * groups of sequences have their first tokens in common (one instruction
  * before many requests): those keys and values are read once for the group, not
- * once per sequence.  The result is the same.
+ * once per sequence.  The result is the same but for roundings: the weights of shared
+ * keys enter the tensor core relative to a maximum that may lag by a factor of 2^8, as in
+ * sp24_attention_prompt, so that with a bf16 cache the largest is rounded too (against
+ * 64 bits 2.2e-3 of the norm, where sp24_attention_decode has 1.8e-3 and the rounding of Y alone
+ * 1.65e-3; with an e4m3 cache 1.7e-3 each).
  *
  *   cu_shared (device) int32 [G + 1], ascending within [0, B]: group g is the
  *           sequences cu_shared[g] .. cu_shared[g + 1] - 1.  Sequences before the

@@ -787,7 +787,8 @@ def attention_decode_shared(q, cache: KVCache, page_table, seq_lens, cu_shared, 
     window that begins later) is attended by itself, and so is a group whose first sequence
     is longer than window + sinks.  The others as for attention_decode();
     `workspace` (uint8, attention_decode_shared_workspace_size() bytes, zeroed once) may be
-    kept for all later calls on one stream; without one, each call allocates a zeroed one."""
+    kept for all later calls on one stream; without one, each call allocates and zeroes one (26 MB
+    for 64 sequences and 32 query and 8 kv heads of 128)."""
     lib = _lib or load()
     rows, ldq, heads, B, width, ld_table, lens_p, scale, out, ldy = _attention_args(
         q, cache, page_table, seq_lens, scale, out, stream)

@@ -141,11 +141,17 @@ __device__ __forceinline__ int counted_tokens(const SharedGroups& s, int b, int 
 // (key tiles of up to 256 query rows), which the chain of products and
 // exponentials bounds, and of the bytes of own keys and values.  `tokens`: the counted ones of all sequences, without a
 // window less those that their groups read together.
-constexpr unsigned int kLeastOwnSms = 40;  // fewer, and the shared tokens take them all first
+// Fewer, and the shared tokens take them all first.  (200 sequences behind 20000 tokens, 28/4 heads of 64, e4m3: up to 1000
+// of their own 74 us, 81 with 25; up to 100 59 us, 289 with 1.  64 behind 16000, up to 130, 32/8 heads of 128: 36.6 us, 42.5 with 60.)
+constexpr unsigned int kLeastOwnSms = 40;
 template <int D, bool E4M3>
 __device__ __forceinline__ unsigned int shared_sms(unsigned int units, long long tokens, int kv_heads, unsigned int sms) {
+  // (e4m3, heads of 64: those 200 with up to 1000 and 3000 of their own 73.9 and 84.2 us, with 1150 69.5 and 86.0, with 1700
+  // 74.1 and 90.6.)
   constexpr float UNIT_NS = D == 128 ? (E4M3 ? 1650.0f : 1350.0f) : (E4M3 ? 1400.0f : 1150.0f);
-  constexpr float BYTES_PER_NS = 32.0f;  // that an SM's decode CTAs read (28: 44.6 us, 34: 43.6, 44: 44.9, see sp24_attn_shared.cu)
+  // That an SM's decode CTAs read.  (64 sequences behind 16000 tokens with up to 512 and 250 of their own, 96 in 6 groups with an
+  // e4m3 cache: 44.3, 38.1 and 89.0 us; with 28 45.5, 38.3 and 93.0, with 36 43.6, 41.3 and 89.1, with 40 44.4, 41.3 and 92.9.)
+  constexpr float BYTES_PER_NS = 32.0f;
   if (units == 0) return 0;
   const float bytes = static_cast<float>(max(tokens, 0ll)) * (kv_heads * D * (E4M3 ? 2 : 4));
   const float shared = units * UNIT_NS, own = bytes / BYTES_PER_NS;

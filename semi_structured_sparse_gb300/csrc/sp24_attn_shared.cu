@@ -14,8 +14,8 @@
 // sequences behind 16000 tokens took 65 us: a chain of four latencies per item.)
 //
 // Measured (GB300, in a graph; 32/8 heads of 128): 64 sequences behind 16000 tokens, up to 512 of their
-// own, bf16 43.8 us (132 MB: 3.0 TB/s; one by one 361 us); 96 in 6 groups behind up to 16000, e4m3 89.7 us;
-// 200 behind 50001, 28/4 heads of 64 100.7 us.  Bound by the softmax warps of the shared tokens' launch, and by
+// own, bf16 43.9 us (132 MB: 3.0 TB/s; one by one 363 us); 96 in 6 groups behind up to 16000, e4m3 88.8 us;
+// 200 behind 50001, 28/4 heads of 64 100.5 us.  Bound by the softmax warps of the shared tokens' launch, and by
 // the own tokens' latencies on the other SMs.
 #include <algorithm>
 #include <cuda_bf16.h>
