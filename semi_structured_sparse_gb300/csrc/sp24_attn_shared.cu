@@ -165,7 +165,9 @@ extern "C" sp24_status sp24_attention_decode_shared(const void* q, int64_t B, in
   if (!aligned16(workspace)) return SP24_ERR_ALIGNMENT;
   if (B == 0) return SP24_OK;
   // Sharing saves at most the groups' tokens but for one time each.  Where that takes less time than the two launches
-  // more (2 sequences behind 1000 tokens, 4 MB: 14.2 us shared, 8.5 one by one), the sequences are attended one by one.
+  // more, the sequences are attended one by one.  (In wide tables, shared and one by one: 2 sequences behind 1000 tokens, 4 MB,
+  // 14.4 and 7.5 us; 2 behind 4000, 16 MB, 16.1 and 11.3; 8 behind 1000, 29 MB, 14.6 and 11.1; 8 behind 4000, 115 MB, 16.5 and
+  // 19.2; 32 behind 1000, 127 MB, 15.1 and 19.7.)
   const int64_t e = cache->dtype == SP24_E4M3 ? 1 : 2;
   const double saved = double(table_width << c.view.page_shift) * (B - 1) * cache->heads * (2 * cache->head_dim * e);
   if (G == 0 || saved < kLeastSaved)
